@@ -254,6 +254,130 @@ int il_centroid_head(const float* x, int64_t h, const il_weight* centroids, cons
                      const uint32_t* ordering, int64_t top_k, uint32_t* token_out, float* score_out,
                      uint32_t* selected_out, float* scores_out, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged K/V cache: what a decode step does between its q/k/v batch and its
+ * output projection.  The pages leave attention outside the matmul backend;
+ * these entry points take the batch's fp32 results (q, k, v) and give the fp32
+ * x of the next batch, on the same stream, without a copy or a host round trip:
+ *     il_kv_extend  block tables and slot maps from the sequences' lengths
+ *     il_kv_append  k and v rows into the cache (and il_kv_read back)
+ *     il_kv_attend  one new token's attention over each sequence's cache
+ * The cache is the caller's memory, described by value: n_pages pages of
+ * page_size tokens.  A token's slot is page * page_size + its index in the page;
+ * a sequence's block table lists its pages, so that its position p is in page
+ * table[p / page_size].  All pointers are DEVICE pointers; every call is one
+ * kernel launch (none for an empty call), asynchronous on `stream`, and can be
+ * captured in a CUDA graph.  Lengths, tables and slots live on the device and may
+ * change between the replays of a graph.  Arguments that only the device can
+ * see are checked there: a page or slot outside the cache is never accessed;
+ * it is skipped and flagged, and il_check_device_status then returns IL_ERR_ARG.
+ * These calls count in il_stats only where they return an error.
+ * ------------------------------------------------------------------------- */
+
+/* A paged cache.
+ *   format   : IL_BF16, or IL_Q8 as the weights have it: int8 q and one fp32 scale
+ *              d per 32 elements of head_dim, value fp32(d*q).
+ *   page_size: tokens per page, 1 .. 2^20.      n_pages: 1 .., n_pages * page_size < 2^31.
+ *   n_heads  : K/V heads, 1 .. 1024.
+ *   head_dim : 8 .. 256, a multiple of 8 (IL_BF16) or of 32 (IL_Q8).
+ *   k, v     : bf16 or int8 elements; (page, token, head, i) is at
+ *              page*page_stride + token*token_stride + head*head_stride + i.  Any order of
+ *              the three strides (64-bit offsets); 16-byte aligned rows: base
+ *              address and strides times the element size are multiples of 16.
+ *   k_scale, v_scale : IL_Q8: fp32 scales, (page, token, head, i / 32) likewise with
+ *              the scale_ strides, in floats (4-byte alignment); NULL for IL_BF16.
+ * Strides of a dimension of extent 1 are not used; the others are at least
+ * head_dim (scales: head_dim / 32).  Elements must not overlap. */
+typedef struct {
+  int32_t format;
+  int32_t page_size;
+  int64_t n_pages;
+  int32_t n_heads;
+  int32_t head_dim;
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t page_stride, token_stride, head_stride;
+  int64_t scale_page_stride, scale_token_stride, scale_head_stride;
+} il_kv;
+
+/*
+ * il_kv_extend -- one scheduler step: sequence r of length lens[r] grows by
+ * add[r] tokens, or loses its last -add[r] tokens where add[r] < 0 (rejected draft
+ * tokens; add = -lens or less: a finished sequence).  Pages come from and go back to
+ * a ring of free pages: cursor = {head, tail} counts the pages ever taken and ever
+ * given; entry p is ring[p % ring_size] and the tail - head entries from head are free.
+ * Pages are taken in order of sequence, then of position; pages given back follow
+ * at the tail in that order, and are free from the next call on.  The table keeps its
+ * entries beyond a sequence's pages as they are.
+ *   n_seq, page_size : 0 <= n_seq <= 65536; 0 is a successful no-op.
+ *   lens, add        : int32 [n_seq] (negative lens count as 0).
+ *   table            : int32 [n_seq][table_width], rows table_stride apart; updated.
+ *   ring, ring_size  : int32 [ring_size], at least as many as there are pages; updated.
+ *   cursor           : int64 [2].
+ *   lens_out, cursor_out : the state after the call; may be lens and cursor.
+ *   slots            : int32 [max_slots]: slots of the new tokens, sequence by sequence;
+ *                      -1 behind the last.      positions: their positions, likewise, or NULL.
+ *   first            : int32 [n_seq + 1] or NULL: index in slots of each sequence's first new
+ *                      token, and their number.
+ *   info             : int64 [4] or NULL: {code, new tokens, pages taken, pages given}.
+ * All or nothing: where there are too few free pages (code bit 0), a sequence
+ * would need more pages than table_width (bit 1), the new tokens are more than
+ * max_slots (bit 2) or the ring's state is impossible (bit 3), nothing changes: table and ring stay,
+ * lens_out = lens, cursor_out = cursor, slots, positions are -1, first is 0, and info
+ * has the numbers that were asked for.  The outputs must not overlap each other or
+ * an input, except lens_out == lens and cursor_out == cursor.
+ */
+int il_kv_extend(int64_t n_seq, int64_t page_size, const int32_t* lens, const int32_t* add, int32_t* table,
+                 int64_t table_stride, int64_t table_width, int32_t* ring, int64_t ring_size, const int64_t* cursor,
+                 int32_t* lens_out, int64_t* cursor_out, int32_t* slots, int64_t max_slots, int32_t* positions,
+                 int32_t* first, int64_t* info, void* stream);
+
+/*
+ * il_kv_append -- writes n tokens' K and V rows into the cache.
+ *   k, v   : fp32, row (token, head) at token*k_stride (v_stride) + head*head_dim; 16-byte
+ *            aligned, strides multiples of 4 and at least n_heads*head_dim (e.g. the y
+ *            of a k job, or columns of a wider y).
+ *   slots  : int32 [n]; a negative slot is skipped.  Slots of one call must differ.
+ * bf16 rounds to nearest even.  Q8: d = max|w| / 127 over the 32 elements, q = w / d
+ * rounded to nearest even (IEEE divisions, as the weights' test quantiser); a block of
+ * zeros has d = 0, q = 0; a block with a NaN or an infinity reads back as NaN.
+ */
+int il_kv_append(const il_kv* kv, const float* k, int64_t k_stride, const float* v, int64_t v_stride,
+                 const int32_t* slots, int64_t n, void* stream);
+
+/*
+ * il_kv_read -- the inverse of il_kv_append: the cached values of n slots as fp32 (exact
+ * for bf16, fp32(d*q) for Q8), rows of a negative slot as zeros.  k, v as above, written.
+ */
+int il_kv_read(const il_kv* kv, const int32_t* slots, int64_t n, float* k, int64_t k_stride, float* v,
+               int64_t v_stride, void* stream);
+
+/*
+ * il_kv_attend -- attention of one token per sequence over its cached tokens:
+ *     s_t = scale * q_h . k_t,   out_h = sum_t softmax(s)_t v_t,   lse_h = ln sum_t exp(s_t)
+ * over t in [max(0, len - window), len), query head h reading K/V head
+ * h / (n_q_heads / n_heads).  The new token itself is one of the len (append it first).
+ *   q      : fp32 [n_seq][n_q_heads][head_dim], sequences q_stride apart; 16-byte aligned,
+ *            q_stride a multiple of 4.         out: likewise with out_stride, overwritten.
+ *   lse    : fp32 [n_seq][n_q_heads] or NULL.
+ *   table, table_stride, table_width, lens : as il_kv_extend leaves them.  A length is cut to
+ *            0 .. table_width * page_size.
+ *   n_q_heads : a multiple of the cache's n_heads, at most 32768.    n_seq: 0 .. 65536.
+ *   window : tokens seen, counted from the end; 0: all.
+ * A sequence of length 0 gives out = 0 and lse = -inf.  Cached values outside the
+ * attended range are never used, NaN or not.  q is kept to 21 or more of its 24 bits,
+ * sums and softmax statistics are fp32.  q, K and V that are attended must be finite:
+ * where one is not, that sequence's heads that read it give NaN or infinity.  Work is split
+ * over the length and joined in an order that depends on the lengths only, so that equal
+ * calls give equal bits.  The library's split workspace for `stream` holds the parts (see
+ * il_matmul_batch for its growth and stream capture).
+ */
+int il_kv_attend(const il_kv* kv, const float* q, int64_t q_stride, const int32_t* table, int64_t table_stride,
+                 int64_t table_width, const int32_t* lens, int64_t n_seq, int64_t n_q_heads, float scale,
+                 int64_t window, float* out, int64_t out_stride, float* lse, void* stream);
+
 /* 1 if the handle came from il_upload_gate_up, 0 if from il_upload_weight,
  * -1 for an invalid handle. */
 int il_weight_is_gate_up(const il_weight* w);
@@ -288,7 +412,8 @@ int il_dequantize_weight(const il_weight* w, float* dev_out, void* stream);
  * wait timed out since the last call; in that case it also waits for the
  * device and clears the library's split-K workspaces on it, so that later
  * batches start from a clean state.  Returns IL_ERR_ARG if no wait timed out
- * but il_centroid_head met an ordering entry >= vocab. */
+ * but il_centroid_head met an ordering entry >= vocab, or an il_kv_* call a page
+ * or slot outside its cache. */
 int il_check_device_status(void* stream);
 
 /* Frees the scratch the library keeps for `stream` on the current device (the

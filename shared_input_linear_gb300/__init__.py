@@ -20,7 +20,7 @@ import numpy as np
 __all__ = ["ILError", "Weight", "FORMATS", "IL_BF16", "IL_Q8", "IL_Q4", "load", "build",
            "upload_weight", "matmul_batch", "matmul_batch_ptr", "matmul_batch_noalloc_ptr", "free_weight", "weight_bytes",
            "dequantize_weight", "check_device_status", "release_scratch", "get_stats", "reset_stats", "last_error",
-           "version", "LIB_PATH", "STATUS"]
+           "version", "LIB_PATH", "STATUS", "KVCache", "kv_cache", "kv_extend", "kv_append", "kv_read", "kv_attend"]
 
 IL_BF16, IL_Q8, IL_Q4 = 0, 1, 2
 FORMATS = {"bf16": IL_BF16, "q8": IL_Q8, "q4": IL_Q4}
@@ -48,6 +48,14 @@ class _Stats(ctypes.Structure):
     _fields_ = [(n, ctypes.c_uint64) for n in
                 ("uploads", "upload_bytes", "batches", "jobs", "launches", "weight_bytes",
                  "flops", "errors", "profiled_batches", "device_ns")]
+
+
+class _KV(ctypes.Structure):
+    _fields_ = ([("format", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int64),
+                 ("n_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+                + [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
+                + [(n, ctypes.c_int64) for n in ("page_stride", "token_stride", "head_stride", "scale_page_stride",
+                                                 "scale_token_stride", "scale_head_stride")])
 
 
 _lib = None
@@ -83,6 +91,14 @@ def load() -> ctypes.CDLL:
         lib.il_upload_gate_up.restype = vp
         lib.il_centroid_head.argtypes = [vp, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp]
         lib.il_centroid_head.restype = ci
+        lib.il_kv_extend.argtypes = [i64, i64, vp, vp, vp, i64, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, vp, vp]
+        lib.il_kv_extend.restype = ci
+        lib.il_kv_append.argtypes = [vp, vp, i64, vp, i64, vp, i64, vp]
+        lib.il_kv_append.restype = ci
+        lib.il_kv_read.argtypes = [vp, vp, i64, vp, i64, vp, i64, vp]
+        lib.il_kv_read.restype = ci
+        lib.il_kv_attend.argtypes = [vp, vp, i64, vp, i64, i64, vp, i64, i64, ctypes.c_float, i64, vp, i64, vp, vp]
+        lib.il_kv_attend.restype = ci
         lib.il_weight_is_gate_up.argtypes = [vp]
         lib.il_weight_is_gate_up.restype = ci
         lib.il_free_weight.argtypes = [vp]
@@ -314,6 +330,165 @@ def dequantize_weight(w: Weight, out, stream=None) -> None:
     """Test hook: every element of ``w`` as fp32 into ``out`` ([n_out][n_in], CUDA;
     [2*n_out][n_in] with gate/up rows interleaved for a gate+up weight)."""
     _check(load().il_dequantize_weight(w.handle, out.data_ptr(), _stream_ptr(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Paged K/V cache
+# ---------------------------------------------------------------------------
+class KVCache:
+    """A paged K/V cache in the caller's tensors (``il_kv``); holds references to them.
+
+    ``k``, ``v``: CUDA ``[n_pages][page_size][n_heads][head_dim]`` of one shape and one set of
+    strides, the last dimension contiguous; pass ``pool.transpose(1, 2)`` of a pool stored
+    head-major.  ``torch.bfloat16`` is IL_BF16; ``torch.int8`` is IL_Q8 with fp32 ``k_scale``,
+    ``v_scale`` ``[n_pages][page_size][n_heads][head_dim / 32]``.  :func:`kv_cache` allocates one.
+    """
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+            raise ILError(-1, "k and v must be [n_pages][page_size][n_heads][head_dim] of one shape, stride and dtype")
+        if k.dtype not in (torch.bfloat16, torch.int8):
+            raise ILError(-3, "the cache must be bfloat16 or int8")
+        if k.stride(3) != 1:
+            raise ILError(-1, "the last dimension of k and v must be contiguous")
+        if not (k.is_cuda and v.is_cuda):
+            raise ILError(-1, "k and v must be CUDA tensors")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.page_size, self.n_heads, self.head_dim = k.shape
+        self.format = IL_BF16 if k.dtype == torch.bfloat16 else IL_Q8
+        c = self._c = _KV(self.format, self.page_size, self.n_pages, self.n_heads, self.head_dim, k.data_ptr(),
+                          v.data_ptr(), None, None, *k.stride()[:3], 0, 0, 0)
+        if (self.format == IL_Q8) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+            raise ILError(-1, "an int8 cache needs k_scale and v_scale, a bfloat16 cache has none")
+        if k_scale is not None:
+            shape = (*k.shape[:3], self.head_dim // 32)
+            for t in (k_scale, v_scale):
+                if (tuple(t.shape) != shape or t.dtype != torch.float32 or not t.is_cuda
+                        or (shape[3] > 1 and t.stride(3) != 1)):
+                    raise ILError(-1, f"scales must be CUDA float32 {list(shape)}, the last dimension contiguous")
+            if k_scale.stride()[:3] != v_scale.stride()[:3]:
+                raise ILError(-1, "k_scale and v_scale must have the same strides")
+            c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+            c.scale_page_stride, c.scale_token_stride, c.scale_head_stride = k_scale.stride()[:3]
+        self._ref = ctypes.addressof(c)
+
+    @property
+    def bytes(self) -> int:
+        """Bytes of the cache's elements and scales."""
+        return sum(t.numel() * t.element_size() for t in (self.k, self.v, self.k_scale, self.v_scale) if t is not None)
+
+
+def kv_cache(fmt, n_pages: int, page_size: int, n_heads: int, head_dim: int, device="cuda") -> KVCache:
+    """A zeroed :class:`KVCache`, stored head-major within a page: a head's tokens of one page
+    are one contiguous run."""
+    import torch
+    q8 = _fmt(fmt) == IL_Q8
+    if not q8 and _fmt(fmt) != IL_BF16:
+        raise ILError(-3, "the cache must be bf16 or q8")
+
+    def pool(last, dtype):
+        return torch.zeros((n_pages, n_heads, page_size, last), dtype=dtype, device=device).transpose(1, 2)
+    kv = [pool(head_dim, torch.int8 if q8 else torch.bfloat16) for _ in range(2)]
+    return KVCache(*kv, *([pool(head_dim // 32, torch.float32) for _ in range(2)] if q8 else []))
+
+
+def _ptr(t, dtype, numel=None, what="an argument"):
+    """Address of a contiguous CUDA tensor of ``dtype`` (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or (numel is not None and t.numel() != numel):
+        raise ILError(-1, f"{what} must be a contiguous CUDA {dtype} tensor" + (f" of {numel}" if numel is not None else ""))
+    return t.data_ptr()
+
+
+def _rows(t, heads: int, dim: int, what: str):
+    """(address, row stride) of fp32 ``[n][heads][dim]`` (or ``[n][heads*dim]``) whose rows are contiguous."""
+    import torch
+    shape, st = t.shape, t.stride()
+    if len(shape) == 3:
+        ok = shape[1] == heads and shape[2] == dim and st[2] == 1 and (heads == 1 or st[1] == dim)
+    else:
+        ok = len(shape) == 2 and shape[1] == heads * dim and st[1] == 1
+    if not ok or t.dtype is not torch.float32 or not t.is_cuda:
+        raise ILError(-1, f"{what} must be CUDA float32 [n][{heads}][{dim}] with contiguous rows")
+    return t.data_ptr(), st[0]
+
+
+def _table(t, n_seq: int):
+    """(address, row stride, width) of an int32 block table."""
+    import torch
+    if t.dim() != 2 or t.dtype is not torch.int32 or not t.is_cuda or t.shape[0] != n_seq or t.stride(1) != 1:
+        raise ILError(-1, f"table must be CUDA int32 [{n_seq}][width] with contiguous rows")
+    return t.data_ptr(), t.stride(0), t.shape[1]
+
+
+def kv_extend(lens, add, table, ring, cursor, page_size: int, slots, lens_out=None, cursor_out=None, positions=None,
+              first=None, info=None, stream=None) -> None:
+    """``il_kv_extend``: sequences of ``lens`` grow by ``add`` tokens (or lose ``-add``): pages move
+    between the free ``ring`` and ``table``, ``slots`` (and ``positions``) get the new tokens' places.
+
+    All tensors are CUDA and contiguous (``table`` rows may be apart): ``lens``, ``add`` int32
+    ``[n_seq]``; ``table`` int32 ``[n_seq][width]``; ``ring`` int32; ``cursor`` int64 ``[2]``; ``slots``,
+    ``positions`` int32 ``[max_slots]``; ``first`` int32 ``[n_seq + 1]``; ``info`` int64 ``[4]``.
+    ``lens_out`` and ``cursor_out`` default to ``lens`` and ``cursor`` themselves.
+    """
+    import torch
+    i32, i64 = torch.int32, torch.int64
+    n = lens.numel()
+    tp, ts, tw = _table(table, n)
+    most = slots.numel()
+    lp, cp = _ptr(lens, i32, None, "lens"), _ptr(cursor, i64, 2, "cursor")
+    _check(load().il_kv_extend(
+        n, page_size, lp, _ptr(add, i32, n, "add"), tp, ts, tw, _ptr(ring, i32, None, "ring"), ring.numel(), cp,
+        lp if lens_out is None else _ptr(lens_out, i32, n, "lens_out"),
+        cp if cursor_out is None else _ptr(cursor_out, i64, 2, "cursor_out"),
+        _ptr(slots, i32, None, "slots"), most, _ptr(positions, i32, most, "positions"), _ptr(first, i32, n + 1, "first"),
+        _ptr(info, i64, 4, "info"), _stream_ptr(stream)))
+
+
+def kv_append(cache: KVCache, k, v, slots, stream=None) -> None:
+    """``il_kv_append``: fp32 rows ``k``, ``v`` ``[n][n_heads][head_dim]`` into the cache's ``slots``
+    (int32 ``[n]``; a negative one is skipped).  The rows may be columns of a wider tensor."""
+    import torch
+    n = slots.numel()
+    kp, ks = _rows(k, cache.n_heads, cache.head_dim, "k")
+    vp, vs = _rows(v, cache.n_heads, cache.head_dim, "v")
+    if k.shape[0] != n or v.shape[0] != n:
+        raise ILError(-2, "k, v and slots must have the same number of tokens")
+    _check(load().il_kv_append(cache._ref, kp, ks, vp, vs, _ptr(slots, torch.int32, n, "slots"), n, _stream_ptr(stream)))
+
+
+def kv_read(cache: KVCache, slots, k, v, stream=None) -> None:
+    """``il_kv_read``: the cached values of ``slots`` as fp32 into ``k`` and ``v`` (as for :func:`kv_append`)."""
+    import torch
+    n = slots.numel()
+    kp, ks = _rows(k, cache.n_heads, cache.head_dim, "k")
+    vp, vs = _rows(v, cache.n_heads, cache.head_dim, "v")
+    if k.shape[0] != n or v.shape[0] != n:
+        raise ILError(-2, "k, v and slots must have the same number of tokens")
+    _check(load().il_kv_read(cache._ref, _ptr(slots, torch.int32, n, "slots"), n, kp, ks, vp, vs, _stream_ptr(stream)))
+
+
+def kv_attend(cache: KVCache, q, table, lens, out, lse=None, scale=None, window: int = 0, stream=None) -> None:
+    """``il_kv_attend``: attention of one token per sequence over its cached tokens.
+
+    ``q``, ``out``: fp32 ``[n_seq][n_q_heads][head_dim]`` (sequences may be apart); ``table``, ``lens`` as
+    :func:`kv_extend` leaves them; ``lse``: fp32 ``[n_seq][n_q_heads]`` or None; ``scale`` defaults
+    to ``head_dim ** -0.5``; ``window``: tokens seen, counted from the end (0: all)."""
+    import torch
+    if q.dim() != 3:
+        raise ILError(-1, "q must be [n_seq][n_q_heads][head_dim]")
+    n, heads = q.shape[0], q.shape[1]
+    dim = cache.head_dim
+    qp, qs = _rows(q, heads, dim, "q")
+    op, os_ = _rows(out, heads, dim, "out")
+    if out.shape[0] != n:
+        raise ILError(-2, "q and out must have the same number of sequences")
+    tp, ts, tw = _table(table, n)
+    _check(load().il_kv_attend(cache._ref, qp, qs, tp, ts, tw, _ptr(lens, torch.int32, n, "lens"), n, heads,
+                               dim ** -0.5 if scale is None else scale, window, op, os_,
+                               _ptr(lse, torch.float32, n * heads, "lse"), _stream_ptr(stream)))
 
 
 def check_device_status(stream=None) -> None:

@@ -649,6 +649,9 @@ int il_check_device_status(void* stream) {
   if (e != cudaSuccess) return cuda_fail(e, "il_check_device_status");
   word |= noalloc_word;
   if (word == kStatusBadToken) return fail(IL_ERR_ARG, "il_centroid_head met an ordering entry >= vocab");
+  if (word == kStatusBadSlot) return fail(IL_ERR_ARG, "an il_kv_* call met a page or slot outside its cache");
+  if (word == (kStatusBadToken | kStatusBadSlot))
+    return fail(IL_ERR_ARG, "il_centroid_head met an ordering entry >= vocab, and an il_kv_* call a page or slot outside its cache");
   if (word != 0) {
     // a kernel that gave up may have left split-K arrival counters behind: clear
     // this device's workspaces, once no stream still uses them, so the next
@@ -1010,6 +1013,19 @@ cudaError_t prepare_batch(const BatchPlan& plan, const float* x, int64_t t, int6
 }
 
 void api_clear_error() { clear_error(); }
+
+int api_device(int* num_sms, unsigned** status) {
+  DeviceState* ds = nullptr;
+  const int dev = current_device(&ds);
+  if (dev < 0) return dev;
+  *num_sms = ds->num_sms;
+  *status = ds->status;
+  return dev;
+}
+
+int api_workspace(int dev, cudaStream_t stream, size_t bytes, void** ws, size_t* got) {
+  return get_workspace(dev, stream, bytes, ws, got);
+}
 
 int api_fail(int code, const char* msg) { return fail(code, "%s", msg); }
 

@@ -340,4 +340,68 @@ cudaError_t prepare_lmhead(const float* x, int h, const float* cl, int n_cent, i
                            unsigned long long* best_key, unsigned* done, uint32_t* token_out, float* score_out,
                            unsigned* status, int num_sms, std::vector<Launch>* out);
 
+// ---------------------------------------------------------------------------
+// Paged K/V cache
+// ---------------------------------------------------------------------------
+constexpr unsigned kStatusBadSlot = 0x200;  // status word: a page or slot outside the cache was skipped
+constexpr int kMaxKvSeqs = 65536;
+constexpr int kMaxKvDim = 256;
+
+// The cache as the kernels see it: il_kv checked, the strides of dimensions of extent 1 set to 0.
+struct KvView {
+  int format, page_size, n_heads, head_dim;
+  int64_t n_slots;  // n_pages * page_size
+  int64_t n_pages;
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;
+  int64_t page, token, head;     // strides in elements
+  int64_t spage, stoken, shead;  // strides of the scales in floats
+};
+
+struct KvExtendArgs {
+  int n_seq, page_size;
+  const int32_t *lens, *add;
+  int32_t* table;
+  int64_t table_stride, table_width;
+  int32_t* ring;
+  int64_t ring_size;
+  const int64_t* cursor;
+  int32_t* lens_out;
+  int64_t* cursor_out;
+  int32_t* slots;
+  int64_t max_slots;
+  int32_t *positions, *first;
+  int64_t* info;
+  unsigned* arrived;  // zero before and after: the last CTA writes the state that others read
+};
+
+struct KvAttendArgs {
+  KvView kv;
+  const float* q;
+  int64_t q_stride;
+  const int32_t* table;
+  int64_t table_stride, table_width;
+  const int32_t* lens;
+  int n_seq, n_q_heads;
+  float scale;
+  int64_t window;
+  float* out;
+  int64_t out_stride;
+  float* lse;
+  unsigned* status;
+};
+
+cudaError_t prepare_kv_extend(const KvExtendArgs& a, int num_sms, Launch* out);
+// write: fp32 rows into the cache; otherwise the cached values into the rows.
+cudaError_t prepare_kv_rows(bool write, const KvView& kv, float* k, int64_t k_stride, float* v, int64_t v_stride,
+                            const int32_t* slots, int64_t n, unsigned* status, int num_sms, Launch* out);
+// Split workspace that il_kv_attend wants (0: none).
+size_t kv_attend_workspace_bytes(const KvAttendArgs& a, int num_sms);
+cudaError_t prepare_kv_attend(const KvAttendArgs& a, int num_sms, void* ws, size_t ws_bytes, Launch* out);
+
+// Helpers of entry points defined in other translation units: the calling thread's device
+// (negative: an il_status, error set) and the split workspace of a stream.
+int api_device(int* num_sms, unsigned** status);
+int api_workspace(int dev, cudaStream_t stream, size_t bytes, void** ws, size_t* got);
+
 }  // namespace il
