@@ -1,0 +1,48 @@
+// kv_attend_bf16.cu -- il_kv_attend over a bf16 cache (see kv_attend.cuh), and the plan of a
+// call for either format.
+#include "kv_attend.cuh"
+
+namespace il {
+
+cudaError_t prepare_kv_attend_bf16(const KvAttendPlan& p, int dim, bool wide, int ctas, Launch* out) {
+  return attend::prepare_format<false>(p, dim, wide, ctas, out);
+}
+
+namespace {
+
+int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
+bool wide_block(const KvAttendArgs& a) { return a.n_q_heads / a.kv.n_heads > 8 && a.kv.head_dim <= 128; }
+
+}  // namespace
+
+// A counter and two parts for each CTA of the grid, one CTA per SM.
+size_t kv_attend_workspace_bytes(const KvAttendArgs& a, int num_sms) {
+  const int rows = wide_block(a) ? 16 : 8;
+  return kSplitCounterBytes + (size_t)num_sms * 2 * rows * (padded_dim(a.kv.head_dim) + 2) * sizeof(float);
+}
+
+cudaError_t prepare_kv_attend(const KvAttendArgs& a, int num_sms, void* ws, size_t ws_bytes, Launch* out) {
+  if (num_sms > kSplitCounters || ws_bytes < kv_attend_workspace_bytes(a, num_sms)) return cudaErrorInvalidValue;
+  const bool wide = wide_block(a);
+  KvAttendPlan p;
+  memset(&p, 0, sizeof p);
+  p.a = a;
+  p.cap = (int)std::min<int64_t>(a.table_width * a.kv.page_size, INT32_MAX);
+  p.window = (int)std::min<int64_t>(a.window, INT32_MAX);
+  // exact division of t < 2^31 by page_size: with l = ceil(log2 d), floor(t / d) is the high
+  // word of t * (2^32 + m) shifted by l, m = floor(2^32 (2^l - d) / d) + 1 (Granlund and Montgomery)
+  const uint64_t d = (uint64_t)a.kv.page_size;
+  while ((1ull << p.div_s) < d) ++p.div_s;
+  p.div_m = (uint32_t)((((1ull << p.div_s) - d) << 32) / d + 1);
+  p.group = a.n_q_heads / a.kv.n_heads;
+  p.blocks = (p.group + (wide ? 15 : 7)) / (wide ? 16 : 8);
+  p.q_scale = a.scale * 1.4426950408889634f;
+  p.arrived = static_cast<unsigned*>(ws);
+  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kSplitCounterBytes);
+  const int dim = padded_dim(a.kv.head_dim);
+  return a.kv.format == IL_Q8 ? prepare_kv_attend_q8(p, dim, wide, num_sms, out)
+                              : prepare_kv_attend_bf16(p, dim, wide, num_sms, out);
+}
+
+}  // namespace il
