@@ -17,7 +17,10 @@
 //
 // Stream.  Every warp owns a ring of stages, one tile of K and V each, filled with 16-byte
 // cp.async (any strides, any page size: a lane looks up its token's page one tile ahead) and zeros for
-// tokens outside the attended range.  No barrier other than the warp's own sits in the stream.
+// tokens outside the attended range.  Where pages hold whole tiles the addresses of a tile are one base and
+// constants of the lane.  No barrier other than the warp's own sits in the stream.  A head of more than 128
+// elements takes a pair of warps, half of its columns each: they trade their halves of s
+// through shared memory, with a barrier of the two.
 //
 // Arithmetic.  Query heads are the rows of m16n8k16 MMAs and tokens (then elements of V) the
 // columns; a softmax row lives in the four lanes of a quad.  q and p are fp32 and are split
@@ -48,6 +51,7 @@ struct KvAttendPlan {
   int group;              // query heads of a K/V head
   int blocks;             // blocks of 8 R query heads of a K/V head
   float q_scale;          // scale * log2(e)
+  int simple;             // pages hold whole tiles and (Q8) scales allow the widest copies
   unsigned* arrived;      // one counter a CTA, zero before and after
   float* parts;           // two parts a CTA
 };
@@ -57,36 +61,46 @@ namespace attend {
 constexpr int kTile = 16;
 constexpr int kSmemLimit = 232448;  // 227 KB
 
-template <bool Q8, int DP, int R>
+// W columns of a head in a warp, H warps a head (H * W >= head_dim), R blocks of 8 query heads.
+template <bool Q8, int W, int R, int H>
 struct Config {
-  static constexpr int kRows = 8 * R;         // query heads of a block
-  static constexpr int kBlocks = DP / 32;     // 32-element blocks of a row
-  static constexpr int kPart = kRows * (DP + 2);  // floats of a part: sums, maxima, sums of p
-  static constexpr int kRowBytes = Q8 ? DP : 2 * DP;
+  static constexpr int kRows = 8 * R;            // query heads of a block
+  static constexpr int kBlocks = W / 32;         // 32-element blocks of a warp's columns
+  static constexpr int kPart = kRows * (W + 2);  // floats of a part: sums, maxima, sums of p
+  static constexpr int kRowBytes = Q8 ? W : 2 * W;
   static constexpr int kPool = kTile * kRowBytes;               // K or V of a tile
   static constexpr int kScales = Q8 ? kTile * kBlocks * 4 : 0;  // its scales
   static constexpr int kStage = 2 * (kPool + kScales);
-  static constexpr int kWarps = !Q8 && DP == 256 ? 4 : 8;
+  static constexpr int kWarps = R == 1 && (Q8 || W == 64) ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kFixed = (kThreads + 2) * 8 + kWarps * 64 + 64;
+  static constexpr int kWorkers = kWarps / H;    // runs of tiles in a CTA
+  static constexpr int kFixed = (kThreads + 2) * 8 + kWarps * 8 + kWorkers * 64 + 64;
   static constexpr int kRoom = (kSmemLimit - kFixed - kWarps * kPart * 4) / (kWarps * kStage);
   static constexpr int kStages = kRoom > 6 ? 6 : kRoom;
-  static constexpr size_t kSmem = (size_t)kFixed + kWarps * kPart * 4 + (size_t)kWarps * kStages * kStage;
+  static constexpr int kRing = kStages * kStage;
+  static constexpr size_t kSmem = (size_t)kFixed + kWarps * (kPart * 4 + kRing);
   static_assert(kStages >= 2 && kSmem <= kSmemLimit, "the ring does not fit");
-  static_assert(kStages * kStage >= kPart * 4, "a part must fit the warp's ring");
+  static_assert(kRing >= kPart * 4, "a part must fit the warp's ring");
+  static_assert(kPool >= 32 * 16 * R, "s is traded through the tile of K");
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool use) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(use ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool use) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(use ? 4 : 0) : "memory");
+template <int BYTES>
+__device__ __forceinline__ void cp_small(uint32_t dst, const void* src, bool use) {
+  if constexpr (BYTES == 16)
+    cp16(dst, src, use);
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(use ? BYTES : 0)
+                 : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 __device__ __forceinline__ void lds128(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
@@ -99,10 +113,32 @@ __device__ __forceinline__ uint32_t lds32(uint32_t at) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(at));
   return r;
 }
+template <int N>  // N = 2 or 4 floats
+__device__ __forceinline__ void lds_floats(float (&f)[N], uint32_t at) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]) : "r"(at));
+  else
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f[0]), "=f"(f[1]) : "r"(at));
+}
+__device__ __forceinline__ void sts128(uint32_t at, const float (&f)[4]) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]) : "memory");
+}
 __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(at));
+}
+
+// Four floats of a part in the workspace, past this SM's L1 (other SMs write it), or zeros: a load without a
+// branch, so that several are on their way at once.
+__device__ __forceinline__ float4 load_part4(const float* p, bool use) {
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  asm volatile(
+      "{\n.reg .pred use;\nsetp.ne.b32 use, %5, 0;\n@use ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];\n}\n"
+      : "+f"(x.x), "+f"(x.y), "+f"(x.z), "+f"(x.w)
+      : "l"(p), "r"((int)use)
+      : "memory");
+  return x;
 }
 
 template <bool F16>
@@ -177,7 +213,7 @@ __device__ __forceinline__ void advance(Walk& w, const KvAttendPlan& P, int rows
   while (w.q.tiles == 0 && w.s + 1 < P.a.n_seq);
 }
 
-// What a warp leaves for the CTA: part 0, the end (or all) of a row begun before its run, and
+// What a worker leaves for the CTA: part 0, the end (or all) of a row begun before its run, and
 // part 1, the beginning of a row that goes on behind it.
 struct Left {
   int has0, end0, s0, vh0;
@@ -187,28 +223,41 @@ struct Left {
 };
 static_assert(sizeof(Left) <= 64, "see Config::kFixed");
 
-template <bool Q8, int DP, int R>
-__global__ void __launch_bounds__(Config<Q8, DP, R>::kThreads, 1) kv_attend_kernel(const KvAttendPlan P) {
-  using C = Config<Q8, DP, R>;
-  constexpr int NB = C::kBlocks, NT = C::kThreads, NW = C::kWarps, S = C::kStages, ROWS = C::kRows;
+template <bool Q8, int W, int R, int H>
+__global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_kernel(const KvAttendPlan P) {
+  using C = Config<Q8, W, R, H>;
+  constexpr int NB = C::kBlocks, NT = C::kThreads, NW = C::kWarps, NK = C::kWorkers, S = C::kStages, ROWS = C::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* const ring_mem = smem;
-  float* const part_mem = reinterpret_cast<float*>(smem + (size_t)NW * S * C::kStage);
+  float* const part_mem = reinterpret_cast<float*>(smem + (size_t)NW * C::kRing);
   long long* const s_before = reinterpret_cast<long long*>(reinterpret_cast<uint8_t*>(part_mem) + NW * C::kPart * 4);
-  Left* const s_left = reinterpret_cast<Left*>(s_before + NT + 2);
-  long long* const s_warp = reinterpret_cast<long long*>(part_mem);  // of the scan: done before a part is written
-  int* const s_flag = reinterpret_cast<int*>(s_left + NW);
+  long long* const s_warp = s_before + NT + 2;
+  Left* const s_left = reinterpret_cast<Left*>(s_warp + NW);
+  int* const s_flag = reinterpret_cast<int*>(s_left + NK);  // of the two rows that may cross CTAs: parts to join, first CTA
+  unsigned* const s_mask = reinterpret_cast<unsigned*>(s_flag + 4);  // workers with a part 0, whose row ends in it, with a part 1
 
   const KvAttendArgs& a = P.a;
   const KvView& kv = a.kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
+  const int worker = warp / H, col0 = H == 1 ? 0 : (warp % H) * W;  // first column of this warp
   const int rows_per_seq = kv.n_heads * P.blocks, D = kv.head_dim;
   grid_dep_launch();
+  {
+    // the table and q into L2 while the launch before this one drains (both are read soon after the wait;
+    // whatever that launch still writes to them goes to the same L2 lines)
+    const int64_t at = ((int64_t)blockIdx.x * NT + tid) * 32, step = (int64_t)gridDim.x * NT * 32;
+    const int64_t tn = (int64_t)(a.n_seq - 1) * a.table_stride + a.table_width;
+    if (at < tn) prefetch_l2(a.table + at);
+    const int64_t qn = (int64_t)(a.n_seq - 1) * a.q_stride + (int64_t)a.n_q_heads * D;
+#pragma unroll 1
+    for (int64_t i = at; i < min(qn, 4 * step); i += step) prefetch_l2(a.q + i);
+  }
   grid_dep_wait();
 
   // ---- tiles before each run of sequences; sequences without tokens get their zeros
   const int run = (a.n_seq + NT - 1) / NT;
   long long mine = 0;
+#pragma unroll 1
   for (int k = 0; k < run; ++k) {
     const int s = tid * run + k;
     const bool in = s < a.n_seq;
@@ -219,9 +268,11 @@ __global__ void __launch_bounds__(Config<Q8, DP, R>::kThreads, 1) kv_attend_kern
       const int src = __ffs(none) - 1;
       none &= none - 1;
       const int64_t z = __shfl_sync(~0u, s, src);
+#pragma unroll 1
       for (int i = lane; i < a.n_q_heads * D / 4; i += 32)
         reinterpret_cast<float4*>(a.out + z * a.out_stride)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (a.lse != nullptr)
+#pragma unroll 1
         for (int i = lane; i < a.n_q_heads; i += 32) a.lse[z * a.n_q_heads + i] = -INFINITY;
     }
   }
@@ -232,6 +283,7 @@ __global__ void __launch_bounds__(Config<Q8, DP, R>::kThreads, 1) kv_attend_kern
     if (lane >= by) incl += o;
   }
   if (lane == 31) s_warp[warp] = incl;
+  if (tid < 3) s_mask[tid] = 0;
   __syncthreads();
   long long total = 0, before = 0;
 #pragma unroll
@@ -241,18 +293,17 @@ __global__ void __launch_bounds__(Config<Q8, DP, R>::kThreads, 1) kv_attend_kern
     total += t;
   }
   s_before[tid] = before + incl - mine;
-  if (tid == 0) s_before[NT] = total;
   __syncthreads();
 
-  // ---- this warp's run of the list: equal shares, the first `more` one tile longer
+  // ---- this worker's run of the list: equal shares, the first `more` one tile longer
   const long long units = total * rows_per_seq;
-  const int ctas = (int)min((long long)gridDim.x, (units + NW - 1) / NW);
+  const int ctas = (int)min((long long)gridDim.x, (units + NK - 1) / NK);
   if ((int)blockIdx.x >= ctas) return;
-  const int warps = ctas * NW;
-  const long long share = units < (1ll << 32) ? (long long)((uint32_t)units / (uint32_t)warps) : units / warps;
-  const int more = (int)(units - share * warps);
+  const int workers = ctas * NK;
+  const long long share = (long long)((unsigned long long)units / (unsigned)workers);
+  const int more = (int)(units - share * workers);
   auto begin_of = [&](int w) { return w * share + min(w, more); };
-  const int my = blockIdx.x * NW + warp;
+  const int my = blockIdx.x * NK + worker;
   const long long u0 = begin_of(my);
   const int n = (int)(begin_of(my + 1) - u0);  // a share of 2^31 tiles would be 10^5 GB of cache
 
@@ -263,8 +314,8 @@ __global__ void __launch_bounds__(Config<Q8, DP, R>::kThreads, 1) kv_attend_kern
     {
       int lo = 0;
 #pragma unroll
-      for (int step = NT / 2; step > 0; step /= 2)
-        if (s_before[lo + step] * rows_per_seq <= u0) lo += step;
+      for (int step = 256; step > 0; step /= 2)
+        if (lo + step < NT && s_before[lo + step] * rows_per_seq <= u0) lo += step;
       long long at = u0 - s_before[lo] * rows_per_seq;
       in.s = lo * run;
       in.q = seq_of(P, in.s);
@@ -272,90 +323,102 @@ __global__ void __launch_bounds__(Config<Q8, DP, R>::kThreads, 1) kv_attend_kern
         at -= (long long)in.q.tiles * rows_per_seq;
         in.q = seq_of(P, ++in.s);
       }
-      in.vh = (int)(at < (1ll << 32) ? (uint32_t)at / in.q.tiles : at / in.q.tiles);
+      in.vh = (int)((unsigned long long)at / in.q.tiles);
       in.tile = (uint32_t)(at - (long long)in.vh * in.q.tiles);
     }
     Walk at = in;  // tile being used
-    const uint32_t ring = smem_u32(ring_mem) + warp * S * C::kStage;
+    const uint32_t ring = smem_u32(ring_mem) + warp * C::kRing;
+
+    // 16-byte chunks of a row, rows of one copy instruction, this lane's chunk
+    constexpr int ES = Q8 ? 1 : 2, CPR = C::kRowBytes / 16, PER = 32 / CPR;
+    const int chunk = lane % CPR, sub = lane / CPR;
+    const bool in_row = col0 + chunk * (16 / ES) < D;
+    const int64_t lane_off = (sub * kv.token + col0) * ES + chunk * 16, row_step = PER * kv.token * ES;
+    // scales: the widest copy of a token's scales; a lane copies K's (lanes 0-15) or V's
+    constexpr int SB = NB * 4 > 16 ? 16 : NB * 4;
 
     auto token_of = [&](const Walk& w) { return (w.q.first + w.tile) * kTile + (lane & 15); };
     auto column_of = [&](uint32_t t) { return (__umulhi(P.div_m, t) + t) >> P.div_s; };
     auto page_of = [&](const Walk& w) {  // page of this lane's token of the tile (lanes 16-31 repeat 0-15)
       const uint32_t t = token_of(w);
-      int page = -1;
-      if (t >= w.q.begin && t < w.q.len) {
-        page = a.table[w.s * a.table_stride + column_of(t)];
-      }
-      return page;
+      return t >= w.q.begin && t < w.q.len ? a.table[w.s * a.table_stride + column_of(t)] : -1;
+    };
+    // Positions of the chunks of a row in shared memory, without bank conflicts in the reads below.
+    auto k_at = [&](int row) {
+      return row * C::kRowBytes +
+             ((Q8 ? chunk ^ ((W == 64 ? (row >> 1) & 1 : row & 3) << 1) : chunk ^ ((row & 1) << 2)) << 4);
+    };
+    auto v_at = [&](int row) {
+      if (!Q8) return row * C::kRowBytes + ((chunk ^ (row & 7)) << 4);
+      if (W == 64) row = (row >> 1) | ((row & 1) << 3);
+      return row * C::kRowBytes + ((chunk ^ (((row >> 1) & (W == 64 ? 1 : 3)) << 1)) << 4);
     };
     // Copies the tile at `w`; gives the mask of its tokens that exist.
-    auto fetch = [&](const Walk& w, int page, int stage) {
+    auto fetch = [&](const Walk& w, int page, int stage) -> uint32_t {
       const uint32_t t = token_of(w);
       const bool want = t >= w.q.begin && t < w.q.len;
       const bool ok = want && page >= 0 && page < kv.n_pages;
+      const uint32_t mask = __ballot_sync(~0u, ok) & 0xffffu;
       if (want && !ok) atomicOr(a.status, kStatusBadSlot);
-      const uint32_t in_page = t - column_of(t) * (uint32_t)kv.page_size;
       const int hk = w.vh / P.blocks;
-      long long off = -1, soff = 0;
-      if (ok) off = page * kv.page + in_page * kv.token + hk * kv.head;
-      if (Q8 && ok) soff = page * kv.spage + in_page * kv.stoken + hk * kv.shead;
-      constexpr int CPR = C::kRowBytes / 16, PER = 32 / CPR;  // 16-byte chunks of a row, rows of a copy
-      const int chunk = lane % CPR;
-      const bool in_row = chunk * (Q8 ? 16 : 8) < D;
       const uint32_t to = ring + stage * C::kStage;
+      if (P.simple && mask == 0xffffu) {
+        const uint32_t t0 = t - (lane & 15), in_page = t0 - column_of(t0) * (uint32_t)kv.page_size;
+        const int64_t off = (page * kv.page + in_page * kv.token + hk * kv.head) * ES + lane_off;
+        const uint8_t *kp = kv.k + off, *vp = kv.v + off;
 #pragma unroll
-      for (int i = 0; i < kTile / PER; ++i) {
-        const int row = i * PER + lane / CPR;
-        const long long o = __shfl_sync(~0u, off, row);
-        const bool use = o >= 0 && in_row;
-        const long long src = use ? (Q8 ? o + chunk * 16 : 2 * o + chunk * 16) : 0;
-        int kc, vc, vrow = row;  // chunk positions: see the reads below
+        for (int i = 0; i < kTile / PER; ++i) {
+          cp16(to + k_at(i * PER + sub), kp, in_row);
+          cp16(to + C::kPool + v_at(i * PER + sub), vp, in_row);
+          kp += row_step;
+          vp += row_step;
+        }
         if constexpr (Q8) {
-          kc = chunk ^ ((DP == 64 ? (row >> 1) & 1 : row & 3) << 1);
-          if (DP == 64) vrow = (row >> 1) | ((row & 1) << 3);
-          vc = chunk ^ ((DP == 64 ? (vrow >> 1) & 1 : (row >> 1) & 3) << 1);
-        } else {
-          kc = chunk ^ ((row & 1) << 2);
-          vc = chunk ^ (row & 7);
-        }
-        cp16(to + row * C::kRowBytes + kc * 16, kv.k + src, use);
-        cp16(to + C::kPool + vrow * C::kRowBytes + vc * 16, kv.v + src, use);
-      }
-      if constexpr (Q8) {
-        const uint32_t st = to + 2 * C::kPool;
+          const float* sc = (lane < 16 ? kv.k_scale : kv.v_scale) + page * kv.spage +
+                            (in_page + (lane & 15)) * kv.stoken + hk * kv.shead + col0 / 32;
+          const uint32_t st = to + 2 * C::kPool + lane * NB * 4;
 #pragma unroll
-        for (int i = 0; i < kTile * NB / 32; ++i) {
-          const int row = (i * 32 + lane) / NB, b = (i * 32 + lane) % NB;
-          const long long so = __shfl_sync(~0u, soff, row);
-          const bool use = __shfl_sync(~0u, ok, row) && b * 32 < D;
-          const long long src = use ? so + b : 0;
-          cp4(st + (i * 32 + lane) * 4, kv.k_scale + src, use);
-          cp4(st + C::kScales + (i * 32 + lane) * 4, kv.v_scale + src, use);
+          for (int i = 0; i < NB * 4 / SB; ++i) cp_small<SB>(st + i * SB, sc + i * (SB / 4), true);
+        }
+      } else {
+        const uint32_t in_page = t - column_of(t) * (uint32_t)kv.page_size;
+        long long off = 0, soff = 0;
+        if (ok) off = page * kv.page + in_page * kv.token + hk * kv.head + col0;
+        if (Q8 && ok) soff = page * kv.spage + in_page * kv.stoken + hk * kv.shead + col0 / 32;
+#pragma unroll 1
+        for (int i = 0; i < kTile / PER; ++i) {
+          const int row = i * PER + sub;
+          const long long o = __shfl_sync(~0u, off, row);
+          const bool use = ((mask >> row) & 1) && in_row;
+          const long long src = use ? o * ES + chunk * 16 : 0;
+          cp16(to + k_at(row), kv.k + src, use);
+          cp16(to + C::kPool + v_at(row), kv.v + src, use);
+        }
+        if constexpr (Q8) {
+          const uint32_t st = to + 2 * C::kPool;
+#pragma unroll 1
+          for (int i = 0; i < kTile * NB / 32; ++i) {
+            const int row = (i * 32 + lane) / NB, b = (i * 32 + lane) % NB;
+            const long long so = __shfl_sync(~0u, soff, row);
+            const bool use = ((mask >> row) & 1) && col0 + b * 32 < D;
+            const long long src = use ? so + b : 0;
+            cp_small<4>(st + (i * 32 + lane) * 4, kv.k_scale + src, use);
+            cp_small<4>(st + C::kScales + (i * 32 + lane) * 4, kv.v_scale + src, use);
+          }
         }
       }
-      return __ballot_sync(~0u, ok) & 0xffffu;
+      return mask;
     };
 
-    uint32_t mask[S];  // of the tiles in the ring
     int page = page_of(in);
-#pragma unroll
-    for (int i = 0; i < S - 1; ++i) {
-      if (i < n) {
-        mask[i] = fetch(in, page, i);
-        if (i + 1 < n) {
-          advance(in, P, rows_per_seq);
-          page = page_of(in);
-        }
-      }
-      cp_commit();
-    }
+    uint32_t masks[S];  // of the tiles in the ring, the tile being used first
 
     // ---- the row being worked on
     constexpr int QR = Q8 ? 4 * R : 6 * R;  // registers of q for 16 elements
     uint32_t qf[2 * NB][QR];
     float q_back[R];  // Q8: the power of two that q was divided by
     constexpr int OC = 2 * R;
-    float o[DP / 8][OC], m[R], l[R];
+    float o[W / 8][OC], m[R], l[R];
     int v_exp = 14;  // Q8: biased exponent of the largest V scale so far (of the sums' unit)
 
     auto load_q = [&]() {
@@ -364,14 +427,14 @@ __global__ void __launch_bounds__(Config<Q8, DP, R>::kThreads, 1) kv_attend_kern
       for (int r = 0; r < R; ++r) {
         const int in_group = block * ROWS + r * 8 + g;
         const bool use = in_group < P.group;
-        const float* src = a.q + at.s * a.q_stride + (int64_t)(hk * P.group + in_group) * D + 8 * q4;
+        const float* src = a.q + at.s * a.q_stride + (int64_t)(hk * P.group + in_group) * D + col0 + 8 * q4;
         float x[NB][8];
         float top = 0.f;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const bool in_row = use && 32 * b + 8 * q4 < D;
-          const float4 u = in_row ? *reinterpret_cast<const float4*>(src + 32 * b) : make_float4(0.f, 0.f, 0.f, 0.f);
-          const float4 v = in_row ? *reinterpret_cast<const float4*>(src + 32 * b + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+          const bool here = use && col0 + 32 * b + 8 * q4 < D;
+          const float4 u = here ? *reinterpret_cast<const float4*>(src + 32 * b) : make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 v = here ? *reinterpret_cast<const float4*>(src + 32 * b + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
           x[b][0] = u.x, x[b][1] = u.y, x[b][2] = u.z, x[b][3] = u.w;
           x[b][4] = v.x, x[b][5] = v.y, x[b][6] = v.z, x[b][7] = v.w;
 #pragma unroll
@@ -411,402 +474,530 @@ __global__ void __launch_bounds__(Config<Q8, DP, R>::kThreads, 1) kv_attend_kern
         l[r] = 0.f;
       }
 #pragma unroll
-      for (int j = 0; j < DP / 8; ++j)
+      for (int j = 0; j < W / 8; ++j)
 #pragma unroll
         for (int c = 0; c < OC; ++c) o[j][c] = 0.f;
       v_exp = 14;
     };
 
-    bool begun_here = at.tile == 0;
-    load_q();
-    for (int i0 = 0; i0 < n; i0 += S) {
+    // Tile i is used while tile i + S - 1 is on its way; the loop starts S - 1 tiles early, so that its
+    // body exists once (the code of a launch is read from L2, past the cache stream, and has to be short).
+    bool begun_here = at.tile == 0, fresh = true;
+    int stage = 0, ahead = 0;  // of tile i and of tile i + S - 1
+#pragma unroll 1
+    for (int i = 1 - S; i < n; ++i) {
+      // the stage used by the tile before this one takes the tile S - 1 ahead
+      auto fetch_ahead = [&]() {
 #pragma unroll
-      for (int st = 0; st < S; ++st) {
-        const int i = i0 + st;
-        if (i < n) {
-          cp_wait<S - 2>();
-          __syncwarp();
-          // the stage used by the tile before this one takes the tile S - 1 ahead
-          if (i + S - 1 < n) {
-            mask[(st + S - 1) % S] = fetch(in, page, (st + S - 1) % S);
-            if (i + S < n) {
-              advance(in, P, rows_per_seq);
-              page = page_of(in);
-            }
+        for (int k = 0; k + 1 < S; ++k) masks[k] = masks[k + 1];
+        if (i + S - 1 < n) {
+          masks[S - 1] = fetch(in, page, ahead);
+          if (i + S < n) {
+            advance(in, P, rows_per_seq);
+            page = page_of(in);
           }
-          cp_commit();
-          const uint32_t from = ring + st * C::kStage;
+        }
+        cp_commit();
+        ahead = ahead + 1 == S ? 0 : ahead + 1;
+      };
+      if (i >= 0) {
+        if (fresh) {
+          fresh = false;
+          load_q();
+        }
+        cp_wait<S - 2>();
+        __syncwarp();
+      }
+      if (H == 1) {
+        fetch_ahead();
+        if (i < 0) continue;
+      }
+      const uint32_t from = ring + stage * C::kStage;
 
-          // ---- s = q K^T: s[r][2 nt + c] of head row g + 8 r, token 8 nt + 2 q4 + c
-          float s[R][4];
+      // ---- s = q K^T: s[r][2 nt + c] of head row g + 8 r, token 8 nt + 2 q4 + c
+      float s[R][4];
+      if (H == 1 || i >= 0) {
+        if constexpr (Q8) {
+          const uint32_t sc = from + 2 * C::kPool + 2 * q4 * NB * 4;
+          float d[4][NB];  // K's scales of tokens 2 q4, 2 q4 + 1, and 8 more
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            const int row = 8 * nt + g;
-            if constexpr (Q8) {
-              const uint32_t sc = from + 2 * C::kPool + (8 * nt + 2 * q4) * NB * 4;
+          for (int t = 0; t < 4; ++t) lds_floats(d[t], sc + ((t & 1) + 8 * (t >> 1)) * NB * 4);
 #pragma unroll
-              for (int r = 0; r < R; ++r) s[r][2 * nt] = s[r][2 * nt + 1] = 0.f;
+          for (int r = 0; r < R; ++r)
 #pragma unroll
-              for (int b = 0; b < NB; ++b) {
-                // element order inside a block: lane q4 holds 8 q4 .. 8 q4 + 7, as q does
-                const int seg = b ^ (DP == 64 ? (row >> 1) & 1 : row & 3);
-                uint32_t w0, w1, b0, b1, b2, b3;
-                lds64(w0, w1, from + row * C::kRowBytes + seg * 32 + q4 * 8);
-                q8_word_to_f16x2(w0 ^ 0x80808080u, b0, b1);
-                q8_word_to_f16x2(w1 ^ 0x80808080u, b2, b3);
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
-                const uint32_t(&x)[QR] = qf[2 * b];
-                const uint32_t(&y)[QR] = qf[2 * b + 1];
-                const float d0 = __uint_as_float(lds32(sc + b * 4)), d1 = __uint_as_float(lds32(sc + (NB + b) * 4));
-                if constexpr (R == 1) {
-                  mma<true>(c, x[0], x[1], x[2], x[3], b0, b1);
-                  mma<true>(c, y[0], y[1], y[2], y[3], b2, b3);
-                  s[0][2 * nt] = fmaf(c[0] + c[2], d0, s[0][2 * nt]);
-                  s[0][2 * nt + 1] = fmaf(c[1] + c[3], d1, s[0][2 * nt + 1]);
-                } else {
-                  mma<true>(c, x[0], x[1], x[4], x[5], b0, b1);
-                  mma<true>(c, y[0], y[1], y[4], y[5], b2, b3);
-                  mma<true>(c, x[2], x[3], x[6], x[7], b0, b1);
-                  mma<true>(c, y[2], y[3], y[6], y[7], b2, b3);
-                  s[0][2 * nt] = fmaf(c[0], d0, s[0][2 * nt]);
-                  s[0][2 * nt + 1] = fmaf(c[1], d1, s[0][2 * nt + 1]);
-                  s[R - 1][2 * nt] = fmaf(c[2], d0, s[R - 1][2 * nt]);
-                  s[R - 1][2 * nt + 1] = fmaf(c[3], d1, s[R - 1][2 * nt + 1]);
-                }
-              }
+            for (int c = 0; c < 4; ++c) s[r][c] = 0.f;
 #pragma unroll
-              for (int r = 0; r < R; ++r) s[r][2 * nt] *= q_back[r], s[r][2 * nt + 1] *= q_back[r];
-            } else {
-              float c[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int b = 0; b < NB; ++b)
 #pragma unroll
-              for (int b = 0; b < NB; ++b) {
-                uint32_t w[4];
-                lds128(w, from + row * C::kRowBytes + (((4 * b + q4) ^ ((row & 1) << 2)) << 4));
-                const uint32_t(&x)[QR] = qf[2 * b];
-                const uint32_t(&y)[QR] = qf[2 * b + 1];
-                if constexpr (R == 1) {
-                  mma<false>(c, x[0], x[1], x[3], x[4], w[0], w[1]);
-                  mma<false>(e, x[2], 0u, x[5], 0u, w[0], w[1]);
-                  mma<false>(c, y[0], y[1], y[3], y[4], w[2], w[3]);
-                  mma<false>(e, y[2], 0u, y[5], 0u, w[2], w[3]);
-                } else {
-                  mma<false>(c, x[0], x[1], x[6], x[7], w[0], w[1]);
-                  mma<false>(e, x[2], x[3], x[8], x[9], w[0], w[1]);
-                  mma<false>(e, x[4], x[5], x[10], x[11], w[0], w[1]);
-                  mma<false>(c, y[0], y[1], y[6], y[7], w[2], w[3]);
-                  mma<false>(e, y[2], y[3], y[8], y[9], w[2], w[3]);
-                  mma<false>(e, y[4], y[5], y[10], y[11], w[2], w[3]);
-                }
-              }
+            for (int nt = 0; nt < 2; ++nt) {
+              const int row = 8 * nt + g;
+              // element order inside a block: lane q4 holds 8 q4 .. 8 q4 + 7, as q does
+              const int seg = b ^ (W == 64 ? (row >> 1) & 1 : row & 3);
+              uint32_t w0, w1, b0, b1, b2, b3;
+              lds64(w0, w1, from + row * C::kRowBytes + seg * 32 + q4 * 8);
+              q8_word_to_f16x2(w0 ^ 0x80808080u, b0, b1);
+              q8_word_to_f16x2(w1 ^ 0x80808080u, b2, b3);
+              float c[4] = {0.f, 0.f, 0.f, 0.f};
+              const uint32_t(&x)[QR] = qf[2 * b];
+              const uint32_t(&y)[QR] = qf[2 * b + 1];
+              const float d0 = d[2 * nt][b], d1 = d[2 * nt + 1][b];
               if constexpr (R == 1) {
-                s[0][2 * nt] = c[0] + (c[2] + e[0]);
-                s[0][2 * nt + 1] = c[1] + (c[3] + e[1]);
+                mma<true>(c, x[0], x[1], x[2], x[3], b0, b1);
+                mma<true>(c, y[0], y[1], y[2], y[3], b2, b3);
+                s[0][2 * nt] = fmaf(c[0] + c[2], d0, s[0][2 * nt]);
+                s[0][2 * nt + 1] = fmaf(c[1] + c[3], d1, s[0][2 * nt + 1]);
               } else {
-                s[0][2 * nt] = c[0] + e[0];
-                s[0][2 * nt + 1] = c[1] + e[1];
-                s[R - 1][2 * nt] = c[2] + e[2];
-                s[R - 1][2 * nt + 1] = c[3] + e[3];
+                mma<true>(c, x[0], x[1], x[4], x[5], b0, b1);
+                mma<true>(c, y[0], y[1], y[4], y[5], b2, b3);
+                mma<true>(c, x[2], x[3], x[6], x[7], b0, b1);
+                mma<true>(c, y[2], y[3], y[6], y[7], b2, b3);
+                s[0][2 * nt] = fmaf(c[0], d0, s[0][2 * nt]);
+                s[0][2 * nt + 1] = fmaf(c[1], d1, s[0][2 * nt + 1]);
+                s[R - 1][2 * nt] = fmaf(c[2], d0, s[R - 1][2 * nt]);
+                s[R - 1][2 * nt + 1] = fmaf(c[3], d1, s[R - 1][2 * nt + 1]);
               }
             }
-          }
-
-          // ---- softmax: the tile's maximum, p, and the factor of what came before
-          const uint32_t mk = mask[st];
-          if (mk != 0xffffu) {
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[r][c] *= q_back[r];
+        } else {
+          float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}}, e[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            uint32_t w[2][4];
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
+              lds128(w[nt], from + (8 * nt + g) * C::kRowBytes + (((4 * b + q4) ^ ((g & 1) << 2)) << 4));
 #pragma unroll
-              for (int c = 0; c < 2; ++c)
-                if (!((mk >> (8 * nt + 2 * q4 + c)) & 1))
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t(&x)[QR] = qf[2 * b + h];
 #pragma unroll
-                  for (int r = 0; r < R; ++r) s[r][2 * nt + c] = -INFINITY;
-          }
-          float keep[R];
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            float top = fmaxf(fmaxf(s[r][0], s[r][1]), fmaxf(s[r][2], s[r][3]));
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-            const float now = fmaxf(m[r], top), base = now == -INFINITY ? 0.f : now;
-            keep[r] = exp2_fast(m[r] - base);
-            m[r] = now;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) s[r][c] = exp2_fast(s[r][c] - base);
-            l[r] = fmaf(l[r], keep[r], (s[r][0] + s[r][1]) + (s[r][2] + s[r][3]));
-          }
-
-          // ---- o = o * keep + p V
-          const uint32_t fv = from + C::kPool;
-          if constexpr (Q8) {
-            const uint32_t sv = from + 2 * C::kPool + C::kScales;
-            float d[4][NB];  // scales of tokens 2 q4, 2 q4 + 1, and 8 more
-            uint32_t top = 0;
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-              for (int b = 0; b < NB; ++b) {
-                const uint32_t u = lds32(sv + ((2 * q4 + (t & 1) + 8 * (t >> 1)) * NB + b) * 4);
-                d[t][b] = __uint_as_float(u);
-                top = max(top, u & 0x7fffffffu);
-              }
-            top = max(top, __shfl_xor_sync(~0u, top, 1));
-            top = max(top, __shfl_xor_sync(~0u, top, 2));
-            const int e = max(v_exp, (int)(top >> 23));
-            const float up = pow2_biased(267 - e);  // the largest scale becomes 2^13 .. 2^14
-            const float shift = e - v_exp > 126 ? 0.f : pow2_biased(127 + v_exp - e);
-            v_exp = e;
-#pragma unroll
-            for (int r = 0; r < R; ++r) keep[r] *= shift;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              uint32_t p[4 * R];  // hi of tokens 2 q4 .. (of every row), lo, then of the tokens 8 further
-#pragma unroll
-              for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  split2(s[r][2 * h] * (d[2 * h][b] * up), s[r][2 * h + 1] * (d[2 * h + 1][b] * up), p[2 * R * h + r],
-                         p[2 * R * h + R + r]);
-              uint32_t f[2][4];  // V of tokens (2 q4, 2 q4 + 1) and 8 further, elements 32 b + 4 g + 0..3
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                auto word = [&](int t) {
-                  const int vrow = DP == 64 ? (t >> 1) | ((t & 1) << 3) : t;
-                  const int seg = b ^ (DP == 64 ? (vrow >> 1) & 1 : (t >> 1) & 3);
-                  return lds32(fv + vrow * C::kRowBytes + seg * 32 + g * 4) ^ 0x80808080u;
-                };
-                const uint32_t x = word(8 * h + 2 * q4), y = word(8 * h + 2 * q4 + 1);
-                q8_word_to_f16x2(__byte_perm(x, y, 0x5140), f[h][0], f[h][1]);
-                q8_word_to_f16x2(__byte_perm(x, y, 0x7362), f[h][2], f[h][3]);
-              }
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
-                float(&acc)[OC] = o[4 * b + j];
+              for (int nt = 0; nt < 2; ++nt) {
                 if constexpr (R == 1) {
-                  mma<true>(c, p[0], p[1], p[2], p[3], f[0][j], f[1][j]);
-                  acc[0] = fmaf(acc[0], keep[0], c[0] + c[2]);
-                  acc[1] = fmaf(acc[1], keep[0], c[1] + c[3]);
+                  mma<false>(c[nt], x[0], x[1], x[3], x[4], w[nt][2 * h], w[nt][2 * h + 1]);
+                  mma<false>(e[nt], x[2], 0u, x[5], 0u, w[nt][2 * h], w[nt][2 * h + 1]);
                 } else {
-                  mma<true>(c, p[0], p[1], p[4], p[5], f[0][j], f[1][j]);
-                  mma<true>(c, p[2], p[3], p[6], p[7], f[0][j], f[1][j]);
-#pragma unroll
-                  for (int x = 0; x < 4; ++x) acc[x % OC] = fmaf(acc[x % OC], keep[(x / 2) % R], c[x]);
-                }
-              }
-            }
-          } else {
-            uint32_t hi[2 * R], mid[2 * R], lo[2 * R];  // of tokens 2 q4 .. and 8 further, by row
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                split3(s[r][2 * h], s[r][2 * h + 1], hi[R * h + r], mid[R * h + r], lo[R * h + r]);
-#pragma unroll
-            for (int j = 0; j < DP / 8; j += 2) {
-              uint32_t w[4];
-              const int t = lane & 15;
-              ldmatrix4_trans(w, fv + t * C::kRowBytes + (((j + (lane >> 4)) ^ (t & 7)) << 4));
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
-                float(&acc)[OC] = o[j + h];
-                if constexpr (R == 1) {
-                  mma<false>(c, hi[0], mid[0], hi[1], mid[1], w[2 * h], w[2 * h + 1]);
-                  mma<false>(c, lo[0], 0u, lo[1], 0u, w[2 * h], w[2 * h + 1]);
-                  acc[0] = fmaf(acc[0], keep[0], c[0] + c[2]);
-                  acc[1] = fmaf(acc[1], keep[0], c[1] + c[3]);
-                } else {
-                  mma<false>(c, hi[0], hi[1], hi[2 % (2 * R)], hi[3 % (2 * R)], w[2 * h], w[2 * h + 1]);
-                  mma<false>(c, mid[0], mid[1], mid[2 % (2 * R)], mid[3 % (2 * R)], w[2 * h], w[2 * h + 1]);
-                  mma<false>(c, lo[0], lo[1], lo[2 % (2 * R)], lo[3 % (2 * R)], w[2 * h], w[2 * h + 1]);
-#pragma unroll
-                  for (int x = 0; x < 4; ++x) acc[x % OC] = fmaf(acc[x % OC], keep[(x / 2) % R], c[x]);
+                  mma<false>(c[nt], x[0], x[1], x[6], x[7], w[nt][2 * h], w[nt][2 * h + 1]);
+                  mma<false>(e[nt], x[2], x[3], x[8], x[9], w[nt][2 * h], w[nt][2 * h + 1]);
+                  mma<false>(e[nt], x[4], x[5], x[10], x[11], w[nt][2 * h], w[nt][2 * h + 1]);
                 }
               }
             }
           }
-
-          // ---- the row's or the run's end
-          const bool row_ends = at.tile + 1 == at.q.tiles;
-          if (row_ends || i + 1 == n) {
-            const float unit = Q8 ? pow2_biased(v_exp - 13) : 1.f;
-            const bool alone = begun_here && row_ends;
-            float* part = nullptr;
-            if (!alone) {
-              const long long row = u0 + i - at.tile;
-              if (!begun_here) {
-                left.has0 = 1, left.end0 = row_ends, left.s0 = at.s, left.vh0 = at.vh;
-                left.tiles0 = at.q.tiles, left.row0 = row;
-                part = part_mem + warp * C::kPart;
-              } else {  // the run's last tile: nothing is in flight into the ring any more
-                left.has1 = 1, left.s1 = at.s, left.vh1 = at.vh;
-                left.tiles1 = at.q.tiles, left.row1 = row;
-                part = reinterpret_cast<float*>(ring_mem + (size_t)warp * S * C::kStage);
-                cp_wait<0>();
-                __syncwarp();
-              }
-            }
-            const int hk = at.vh / P.blocks, block = at.vh - hk * P.blocks;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-              float sum = l[r];
-              sum += __shfl_xor_sync(~0u, sum, 1);
-              sum += __shfl_xor_sync(~0u, sum, 2);
-              const int in_group = block * ROWS + 8 * r + g;
-              const int64_t head = (int64_t)hk * P.group + in_group;
-              const float f = alone ? (sum == 0.f ? 0.f : unit / sum) : unit;
-              float* to = alone ? a.out + at.s * a.out_stride + head * D : part + (8 * r + g) * DP;
-              if (in_group < P.group) {
-                if constexpr (Q8) {
-#pragma unroll
-                  for (int b = 0; b < NB; ++b)
-                    if (32 * b < D) {
-#pragma unroll
-                      for (int c = 0; c < 2; ++c)
-                        *reinterpret_cast<float4*>(to + 32 * b + 8 * q4 + 4 * c) =
-                            make_float4(o[4 * b][2 * r + c] * f, o[4 * b + 1][2 * r + c] * f, o[4 * b + 2][2 * r + c] * f,
-                                        o[4 * b + 3][2 * r + c] * f);
-                    }
-                } else {
-#pragma unroll
-                  for (int j = 0; j < DP / 8; ++j)
-                    if (8 * j < D)
-                      *reinterpret_cast<float2*>(to + 8 * j + 2 * q4) = make_float2(o[j][2 * r] * f, o[j][2 * r + 1] * f);
-                }
-                if (q4 == 0) {
-                  if (alone) {
-                    if (a.lse != nullptr)
-                      a.lse[(int64_t)at.s * a.n_q_heads + head] =
-                          sum == 0.f ? -INFINITY : (m[r] + log2f(sum)) * 0.6931471805599453f;
-                  } else {
-                    part[ROWS * DP + 8 * r + g] = m[r];
-                    part[ROWS * DP + ROWS + 8 * r + g] = sum;
-                  }
-                }
-              }
-            }
-          }
-          if (i + 1 < n) {
-            advance(at, P, rows_per_seq);
-            if (at.tile == 0) {
-              begun_here = true;
-              load_q();
+          for (int nt = 0; nt < 2; ++nt) {
+            if constexpr (R == 1) {
+              s[0][2 * nt] = c[nt][0] + (c[nt][2] + e[nt][0]);
+              s[0][2 * nt + 1] = c[nt][1] + (c[nt][3] + e[nt][1]);
+            } else {
+              s[0][2 * nt] = c[nt][0] + e[nt][0];
+              s[0][2 * nt + 1] = c[nt][1] + e[nt][1];
+              s[R - 1][2 * nt] = c[nt][2] + e[nt][2];
+              s[R - 1][2 * nt + 1] = c[nt][3] + e[nt][3];
             }
           }
         }
+        if constexpr (H == 2) {
+          // the pair's halves of s: each puts its own where its tile of K was, both add the two.  The next
+          // copy into this stage starts behind the next tile's barrier, when both have read.
+          __syncwarp();
+#pragma unroll
+          for (int r = 0; r < R; ++r) sts128(from + (r * 32 + lane) * 16, s[r]);
+          asm volatile("bar.sync %0, 64;" ::"r"(worker + 1) : "memory");
+          const uint32_t other = from + (warp % 2 == 0 ? C::kRing : -C::kRing);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            float x[4];
+            lds_floats(x, other + (r * 32 + lane) * 16);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[r][c] += x[c];
+          }
+        }
+      }
+      if (H == 2) {
+        fetch_ahead();
+        if (i < 0) continue;
+      }
+
+      // ---- softmax: the tile's maximum, p, and the factor of what came before
+      const uint32_t mk = masks[0];
+      if (mk != 0xffffu) {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            if (!((mk >> (8 * nt + 2 * q4 + c)) & 1))
+#pragma unroll
+              for (int r = 0; r < R; ++r) s[r][2 * nt + c] = -INFINITY;
+      }
+      float keep[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float top = fmaxf(fmaxf(s[r][0], s[r][1]), fmaxf(s[r][2], s[r][3]));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        const float now = fmaxf(m[r], top), base = now == -INFINITY ? 0.f : now;
+        keep[r] = exp2_fast(m[r] - base);
+        m[r] = now;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[r][c] = exp2_fast(s[r][c] - base);
+        l[r] = fmaf(l[r], keep[r], (s[r][0] + s[r][1]) + (s[r][2] + s[r][3]));
+      }
+
+      // ---- o = o * keep + p V
+      const uint32_t fv = from + C::kPool;
+      if constexpr (Q8) {
+        const uint32_t sv = from + 2 * C::kPool + C::kScales + 2 * q4 * NB * 4;
+        float d[4][NB];  // scales of tokens 2 q4, 2 q4 + 1, and 8 more
+        float top = 0.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          lds_floats(d[t], sv + ((t & 1) + 8 * (t >> 1)) * NB * 4);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) top = fmaxf(top, fabsf(d[t][b]));
+        }
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        const int e = max(v_exp, (int)(__float_as_uint(top) >> 23));
+        const float up = pow2_biased(267 - e);  // the largest scale becomes 2^13 .. 2^14
+        const float shift = e - v_exp > 126 ? 0.f : pow2_biased(127 + v_exp - e);
+        v_exp = e;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          keep[r] *= shift;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[r][c] *= up;
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          uint32_t p[4 * R];  // hi of tokens 2 q4 .. (of every row), lo, then of the tokens 8 further
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              split2(s[r][2 * h] * d[2 * h][b], s[r][2 * h + 1] * d[2 * h + 1][b], p[2 * R * h + r],
+                     p[2 * R * h + R + r]);
+          uint32_t f[2][4];  // V of tokens (2 q4, 2 q4 + 1) and 8 further, elements 32 b + 4 g + 0..3
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            auto word = [&](int t) {
+              const int vrow = W == 64 ? (t >> 1) | ((t & 1) << 3) : t;
+              const int seg = b ^ ((vrow >> 1) & (W == 64 ? 1 : 3));
+              return lds32(fv + vrow * C::kRowBytes + seg * 32 + g * 4) ^ 0x80808080u;
+            };
+            const uint32_t x = word(8 * h + 2 * q4), y = word(8 * h + 2 * q4 + 1);
+            q8_word_to_f16x2(__byte_perm(x, y, 0x5140), f[h][0], f[h][1]);
+            q8_word_to_f16x2(__byte_perm(x, y, 0x7362), f[h][2], f[h][3]);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            float(&acc)[OC] = o[4 * b + j];
+            if constexpr (R == 1) {
+              mma<true>(c, p[0], p[1], p[2], p[3], f[0][j], f[1][j]);
+              acc[0] = fmaf(acc[0], keep[0], c[0] + c[2]);
+              acc[1] = fmaf(acc[1], keep[0], c[1] + c[3]);
+            } else {
+              mma<true>(c, p[0], p[1], p[4], p[5], f[0][j], f[1][j]);
+              mma<true>(c, p[2], p[3], p[6], p[7], f[0][j], f[1][j]);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) acc[x % OC] = fmaf(acc[x % OC], keep[(x / 2) % R], c[x]);
+            }
+          }
+        }
+      } else {
+        uint32_t hi[2 * R], mid[2 * R], lo[2 * R];  // of tokens 2 q4 .. and 8 further, by row
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            split3(s[r][2 * h], s[r][2 * h + 1], hi[R * h + r], mid[R * h + r], lo[R * h + r]);
+#pragma unroll
+        for (int j = 0; j < W / 8; j += 2) {
+          uint32_t w[4];
+          const int t = lane & 15;
+          ldmatrix4_trans(w, fv + t * C::kRowBytes + (((j + (lane >> 4)) ^ (t & 7)) << 4));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            float(&acc)[OC] = o[j + h];
+            if constexpr (R == 1) {
+              mma<false>(c, hi[0], mid[0], hi[1], mid[1], w[2 * h], w[2 * h + 1]);
+              mma<false>(c, lo[0], 0u, lo[1], 0u, w[2 * h], w[2 * h + 1]);
+              acc[0] = fmaf(acc[0], keep[0], c[0] + c[2]);
+              acc[1] = fmaf(acc[1], keep[0], c[1] + c[3]);
+            } else {
+              mma<false>(c, hi[0], hi[1], hi[2 % (2 * R)], hi[3 % (2 * R)], w[2 * h], w[2 * h + 1]);
+              mma<false>(c, mid[0], mid[1], mid[2 % (2 * R)], mid[3 % (2 * R)], w[2 * h], w[2 * h + 1]);
+              mma<false>(c, lo[0], lo[1], lo[2 % (2 * R)], lo[3 % (2 * R)], w[2 * h], w[2 * h + 1]);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) acc[x % OC] = fmaf(acc[x % OC], keep[(x / 2) % R], c[x]);
+            }
+          }
+        }
+      }
+
+      // ---- the row's or the run's end
+      const bool row_ends = at.tile + 1 == at.q.tiles;
+      if (row_ends || i + 1 == n) {
+        const float unit = Q8 ? pow2_biased(v_exp - 13) : 1.f;
+        const bool alone = begun_here && row_ends;
+        float* part = nullptr;
+        if (!alone) {
+          const long long row = u0 + i - at.tile;
+          if (!begun_here) {
+            left.has0 = 1, left.end0 = row_ends, left.s0 = at.s, left.vh0 = at.vh;
+            left.tiles0 = at.q.tiles, left.row0 = row;
+            part = part_mem + warp * C::kPart;
+          } else {  // the run's last tile: nothing is in flight into the ring any more
+            left.has1 = 1, left.s1 = at.s, left.vh1 = at.vh;
+            left.tiles1 = at.q.tiles, left.row1 = row;
+            part = reinterpret_cast<float*>(ring_mem + (size_t)warp * C::kRing);
+            cp_wait<0>();
+            __syncwarp();
+            // and the other warp of a pair has read this warp's half of s
+            if (H == 2) asm volatile("bar.sync %0, 64;" ::"r"(worker + 1) : "memory");
+          }
+        }
+        const int hk = at.vh / P.blocks, block = at.vh - hk * P.blocks;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float sum = l[r];
+          sum += __shfl_xor_sync(~0u, sum, 1);
+          sum += __shfl_xor_sync(~0u, sum, 2);
+          const int in_group = block * ROWS + 8 * r + g;
+          const int64_t head = (int64_t)hk * P.group + in_group;
+          const float f = alone ? (sum == 0.f ? 0.f : __fdividef(unit, sum)) : unit;
+          float* to = alone ? a.out + at.s * a.out_stride + head * D + col0 : part + (8 * r + g) * W;
+          if (in_group < P.group) {
+            if constexpr (Q8) {
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+                if (col0 + 32 * b < D) {
+#pragma unroll
+                  for (int c = 0; c < 2; ++c)
+                    *reinterpret_cast<float4*>(to + 32 * b + 8 * q4 + 4 * c) =
+                        make_float4(o[4 * b][2 * r + c] * f, o[4 * b + 1][2 * r + c] * f, o[4 * b + 2][2 * r + c] * f,
+                                    o[4 * b + 3][2 * r + c] * f);
+                }
+            } else {
+#pragma unroll
+              for (int j = 0; j < W / 8; ++j)
+                if (col0 + 8 * j < D)
+                  *reinterpret_cast<float2*>(to + 8 * j + 2 * q4) = make_float2(o[j][2 * r] * f, o[j][2 * r + 1] * f);
+            }
+            if (q4 == 0) {
+              if (alone) {
+                if (a.lse != nullptr && col0 == 0)
+                  a.lse[(int64_t)at.s * a.n_q_heads + head] =
+                      sum == 0.f ? -INFINITY : (m[r] + __log2f(sum)) * 0.6931471805599453f;
+              } else {
+                part[ROWS * W + 8 * r + g] = m[r];
+                part[ROWS * W + ROWS + 8 * r + g] = sum;
+              }
+            }
+          }
+        }
+      }
+      stage = stage + 1 == S ? 0 : stage + 1;
+      if (i + 1 < n) {
+        advance(at, P, rows_per_seq);
+        if (at.tile == 0) begun_here = fresh = true;
       }
     }
     cp_wait<0>();
   }
-  if (lane == 0) s_left[warp] = left;
+  if (lane == 0 && col0 == 0) {
+    s_left[worker] = left;
+    if (left.has0) atomicOr(s_mask, 1u << worker);
+    if (left.has0 && left.end0) atomicOr(s_mask + 1, 1u << worker);
+    if (left.has1) atomicOr(s_mask + 2, 1u << worker);
+  }
   __syncthreads();
 
-  // ---- parts of rows: sums of the CTA's, to the output or to the workspace
-  // Adds up parts in order; `of(i)` is the i-th, in shared memory or (past this SM's L1) in the workspace.
-  // Thread e takes four elements of a row.
-  auto join = [&](auto in_workspace, int count, int s, int vh, auto of, float* to_part) {
-    constexpr bool kL2 = decltype(in_workspace)::value;
-    auto load = [](const auto* x) {
-      if constexpr (kL2)
-        return __ldcg(x);
-      else
-        return *x;
-    };
-    const int hk = vh / P.blocks, block = vh - hk * P.blocks;
-    const int rows = min(ROWS, P.group - block * ROWS);
-    for (int e = tid; e < rows * (DP / 4); e += NT) {
-      const int row = e / (DP / 4), c = 4 * (e % (DP / 4));
-      if (c >= D) continue;
-      float M = -INFINITY, L = 0.f;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  // ---- parts of rows: added up with weights 2^(m_i - max m), to the output where the row is complete, else to a
+  // part in the workspace.  A chain is the parts of one row in this CTA: part 1 of the worker that left the
+  // row open (w; -1: the row came into the CTA) and parts 0 of the workers behind it; the warps of a
+  // chain's workers share its float4s.
+  auto global_part = [&](int cta, int which) { return P.parts + ((int64_t)cta * 2 + which) * (H * C::kPart); };
+  auto finish = [&](int s, int64_t head, int c, const float4& x, float M, float L) {
+    const float f = L == 0.f ? 0.f : __fdividef(1.f, L);
+    *reinterpret_cast<float4*>(a.out + s * a.out_stride + head * D + c) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+    if (c == 0 && a.lse != nullptr)
+      a.lse[(int64_t)s * a.n_q_heads + head] = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.6931471805599453f;
+  };
+  auto add = [](float4& x, const float4& y, float f) {
+    x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
+  };
+  const unsigned has0 = s_mask[0], end0 = s_mask[1], has1 = s_mask[2];
+  // End of the chain of w (exclusive), and whether its row ends there.
+  auto end_of = [&](int w, bool& ends) {
+    const unsigned stop = end0 >> (w + 1);
+    ends = stop != 0;
+    return w + 1 + (ends ? __ffs(stop) : __ffs(~(has0 >> (w + 1))) - 1);
+  };
+#pragma unroll 1
+  for (int own = 0; own < 2; ++own) {  // the chain that this worker's part 0 is in, then the one that it began
+    if ((((own ? has1 : has0) >> worker) & 1) == 0) continue;
+    const int w = own ? worker : 31 - __clz(has1 & ((1u << worker) - 1));
+    bool ends;
+    const int first = max(w, 0), count = end_of(w, ends) - first;
+    const Left& by = s_left[first];
+    const int s = w < 0 ? by.s0 : by.s1, vh = w < 0 ? by.vh0 : by.vh1;
+    const int hk = vh / P.blocks, block = vh - hk * P.blocks, rows = min(ROWS, P.group - block * ROWS);
+    constexpr int kNext = H * C::kPart;
+    const int wp = first * H + warp % H;  // the first worker's warp of this warp's columns
+    const float* const rest = part_mem + wp * C::kPart;
+    const float* const head = w < 0 ? rest : reinterpret_cast<const float*>(ring_mem + (size_t)wp * C::kRing);
+    float* const to = global_part(blockIdx.x, w < 0 ? 0 : 1) + (warp % H) * C::kPart;
+#pragma unroll 1
+    for (int e = (worker - first) * 32 + lane; e < rows * (W / 4); e += count * 32) {
+      const int row = e / (W / 4), c = 4 * (e % (W / 4));
+      const float* const hm = head + ROWS * W + row;
+      const float* const rm = rest + ROWS * W + row;
+      float M = *hm, L;
 #pragma unroll 4
-      for (int i = 0; i < count; ++i) {
-        const float* p = of(i);
-        const float pm = load(p + ROWS * DP + row), pl = load(p + ROWS * DP + ROWS + row);
-        const float4 y = load(reinterpret_cast<const float4*>(p + row * DP + c));
-        const float now = fmaxf(M, pm), base = now == -INFINITY ? 0.f : now;
-        const float f = exp2_fast(M - base), h = exp2_fast(pm - base);
-        M = now;
-        L = fmaf(L, f, pl * h);
-        x.x = fmaf(x.x, f, y.x * h);
-        x.y = fmaf(x.y, f, y.y * h);
-        x.z = fmaf(x.z, f, y.z * h);
-        x.w = fmaf(x.w, f, y.w * h);
+      for (int i = 1; i < count; ++i) M = fmaxf(M, rm[i * kNext]);
+      const float base = M == -INFINITY ? 0.f : M;
+      const float f0 = exp2_fast(*hm - base);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      add(x, *reinterpret_cast<const float4*>(head + row * W + c), f0);
+      L = hm[ROWS] * f0;
+#pragma unroll 4
+      for (int i = 1; i < count; ++i) {
+        const float f = exp2_fast(rm[i * kNext] - base);
+        add(x, *reinterpret_cast<const float4*>(rest + i * kNext + row * W + c), f);
+        L = fmaf(rm[i * kNext + ROWS], f, L);
       }
-      if (to_part != nullptr) {
-        *reinterpret_cast<float4*>(to_part + row * DP + c) = x;
-        if (c == 0) {
-          to_part[ROWS * DP + row] = M;
-          to_part[ROWS * DP + ROWS + row] = L;
-        }
+      if (w >= 0 && ends) {
+        if (col0 + c < D) finish(s, (int64_t)hk * P.group + block * ROWS + row, col0 + c, x, M, L);
       } else {
-        const int64_t head = (int64_t)hk * P.group + block * ROWS + row;
-        const float f = L == 0.f ? 0.f : 1.f / L;
-        *reinterpret_cast<float4*>(a.out + s * a.out_stride + head * D + c) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
-        if (c == 0 && a.lse != nullptr)
-          a.lse[(int64_t)s * a.n_q_heads + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+        *reinterpret_cast<float4*>(to + row * W + c) = x;
+        if (c == 0) to[ROWS * W + row] = M, to[ROWS * W + ROWS + row] = L;
       }
     }
-  };
-  auto global_part = [&](int cta, int which) { return P.parts + ((int64_t)cta * 2 + which) * C::kPart; };
+  }
 
-  bool crosses[2] = {false, false};
-  for (int w = -1; w < NW; ++w) {  // the row that came into the CTA, then those that warp w left open
-    if (w < 0 ? !s_left[0].has0 : !s_left[w].has1) continue;
-    int end = w + 1;
-    bool ends = false;
-    while (end < NW && s_left[end].has0 && !ends) ends = s_left[end++].end0 != 0;
-    const int s = w < 0 ? s_left[0].s0 : s_left[w].s1, vh = w < 0 ? s_left[0].vh0 : s_left[w].vh1;
-    const bool whole = w >= 0 && ends;
-    if (!whole) crosses[w < 0 ? 0 : 1] = true;
-    const int count = end - max(w, 0);
-    auto of = [&](int i) -> const float* {
-      const int at = max(w, 0) + i;
-      return at == w ? reinterpret_cast<const float*>(ring_mem + (size_t)at * S * C::kStage) : part_mem + at * C::kPart;
-    };
-    join(std::false_type(), count, s, vh, of, whole ? nullptr : global_part(blockIdx.x, w < 0 ? 0 : 1));
+  // ---- rows that cross CTAs: the last CTA to arrive adds them up in CTA order.  Of a CTA's rows only the one that
+  // came in (0) and the last one left open (1) can cross.
+  const int open = 31 - __clz(has1);
+  bool crosses[2] = {(has0 & 1) != 0, false};
+  if (open >= 0) {
+    end_of(open, crosses[1]);
+    crosses[1] = !crosses[1];
   }
   if (!crosses[0] && !crosses[1]) return;
-
-  // ---- rows that cross CTAs: the last to arrive sums them in CTA order
-  auto owner = [&](long long u) {  // CTA of tile u of the list
-    const long long split = more * (share + 1);
-    const long long w = u < split ? u / (share + 1) : more + (u - split) / share;
-    return (int)(w / NW);
-  };
-  __threadfence();
   __syncthreads();
-  for (int which = 0; which < 2; ++which) {
-    if (!crosses[which]) continue;
-    int w = 0;  // the warp that knows the row
-    if (which == 1) {
-      w = NW - 1;
-      while (!s_left[w].has1) --w;
-    }
-    const Left& r = s_left[w];
-    const long long row = which == 0 ? r.row0 : r.row1;
-    const int c0 = owner(row), c1 = owner(row + (which == 0 ? r.tiles0 : r.tiles1) - 1);
-    const int count = c1 - c0 + 1;
-    if (tid == 0) {
-      const unsigned seen = atomicAdd(P.arrived + c0, 1u);
-      *s_flag = seen == (unsigned)count - 1;
-      if (*s_flag) P.arrived[c0] = 0;
-    }
-    __syncthreads();
-    if (*s_flag) {
+  if (tid < 2) {
+    int joined = 0, c0 = 0;
+    if (tid == 0 ? crosses[0] : crosses[1]) {
+      const Left& r = s_left[tid == 0 ? 0 : open];
+      const long long row0 = tid == 0 ? r.row0 : r.row1, row1 = row0 + (tid == 0 ? r.tiles0 : r.tiles1) - 1;
+      const float per_tile = (float)ctas / (float)units;
+      auto owner = [&](long long u) {  // CTA of tile u of the list: an estimate, set right
+        int c = min((int)((float)u * per_tile), ctas - 1);
+        while (begin_of(c * NK) > u) --c;
+        while (c + 1 < ctas && begin_of((c + 1) * NK) <= u) ++c;
+        return c;
+      };
+      c0 = owner(row0);
+      const int count = owner(row1) - c0 + 1;
       __threadfence();
-      join(std::true_type(), count, which == 0 ? r.s0 : r.s1, which == 0 ? r.vh0 : r.vh1,
-           [&](int i) -> const float* { return global_part(c0 + i, i == 0 ? 1 : 0); }, nullptr);
+      const unsigned seen = atomicAdd(P.arrived + c0, 1u);
+      __threadfence();
+      if (seen == (unsigned)count - 1) {
+        joined = count;
+        P.arrived[c0] = 0;
+      }
+    }
+    s_flag[tid] = joined;
+    s_flag[2 + tid] = c0;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const int count = s_flag[which];
+    if (count == 0) continue;
+    const int c0 = s_flag[2 + which];
+    const Left& by = s_left[which == 0 ? 0 : open];
+    const int s = which == 0 ? by.s0 : by.s1, vh = which == 0 ? by.vh0 : by.vh1;
+    const int hk = vh / P.blocks, block = vh - hk * P.blocks, rows = min(ROWS, P.group - block * ROWS);
+    constexpr int kNext = 2 * H * C::kPart, WIDE = H * W / 4;
+    const float* const rest = global_part(c0, 0);  // part i: of the row that came into CTA c0 + i
+    const float* const head = global_part(c0, 1);  // part 0: of the row that CTA c0 left open
+    // the row's float4s over groups of threads; a group takes every groups-th part, 12 loads at a time
+    const int wide = rows * WIDE, groups = wide <= NT / 2 ? NT / wide : 1, grp = groups == 1 ? 0 : tid / wide;
+    float* const weight = reinterpret_cast<float*>(ring_mem);  // [rows][count]; nothing else uses the ring any more
+    float* const stat = weight + rows * count;                 // [rows][2]: max, sum
+    float4* const sums = reinterpret_cast<float4*>(weight + ((rows * (count + 2) + 3) & ~3));
+    bool weighed = false;
+#pragma unroll 1
+    for (int e = tid - grp * wide; e - tid + grp * wide < wide; e += NT) {
+      const bool mine = e < wide && grp < groups;
+      const int row = mine ? e / WIDE : 0, c = 4 * (e % WIDE);
+      const int at = (c / W) * C::kPart + row * W + c % W;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int i0 = grp; i0 - grp < count; i0 += 12 * groups) {
+        float4 y[12];
+#pragma unroll
+        for (int k = 0; k < 12; ++k) {
+          const int i = i0 + k * groups;
+          y[k] = load_part4((i == 0 ? head : rest + (int64_t)i * kNext) + at, mine && i < count);
+        }
+        if (!weighed) {
+          // while those are on their way: the weights, a warp a head row
+          weighed = true;
+#pragma unroll 1
+          for (int r = warp; r < rows; r += NW) {
+            float M = -INFINITY, L = 0.f;
+#pragma unroll 1
+            for (int i = lane; i < count; i += 32) {
+              const float* const p = (i == 0 ? head : rest + (int64_t)i * kNext) + ROWS * W + r;
+              const float m1 = __ldcg(p), l1 = __ldcg(p + ROWS);
+              weight[r * count + i] = m1;
+              const float now = fmaxf(M, m1), b = now == -INFINITY ? 0.f : now;
+              L = fmaf(L, exp2_fast(M - b), l1 * exp2_fast(m1 - b));
+              M = now;
+            }
+            float top = M;
+#pragma unroll
+            for (int by = 16; by > 0; by /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, by));
+            const float b = top == -INFINITY ? 0.f : top;
+            L *= exp2_fast(M - b);
+#pragma unroll
+            for (int by = 16; by > 0; by /= 2) L += __shfl_xor_sync(~0u, L, by);
+#pragma unroll 1
+            for (int i = lane; i < count; i += 32) weight[r * count + i] = exp2_fast(weight[r * count + i] - b);
+            if (lane == 0) stat[2 * r] = top, stat[2 * r + 1] = L;
+          }
+          __syncthreads();
+        }
+#pragma unroll
+        for (int k = 0; k < 12; ++k) {
+          const int i = min(i0 + k * groups, count - 1);  // past the last, y is 0
+          add(x, y[k], weight[row * count + i]);
+        }
+      }
+      if (groups > 1) {  // the groups' sums in order
+        if (mine) sums[tid] = x;
+        __syncthreads();
+#pragma unroll 1
+        for (int k = 1; k < groups && grp == 0; ++k) add(x, sums[tid + k * wide], 1.f);
+      }
+      if (mine && grp == 0 && c < D)
+        finish(s, (int64_t)hk * P.group + block * ROWS + row, c, x, stat[2 * row], stat[2 * row + 1]);
     }
     __syncthreads();
   }
 }
 
-template <bool Q8, int DP, int R>
+template <bool Q8, int W, int R, int H>
 cudaError_t prepare_variant(const KvAttendPlan& p, int ctas, Launch* out) {
-  using C = Config<Q8, DP, R>;
+  using C = Config<Q8, W, R, H>;
   static std::atomic<unsigned long long> attr_set{0};  // one bit per device (setting it twice is harmless)
-  const void* fn = reinterpret_cast<const void*>(kv_attend_kernel<Q8, DP, R>);
+  const void* fn = reinterpret_cast<const void*>(kv_attend_kernel<Q8, W, R, H>);
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 64 || !(attr_set.load() & (1ull << dev))) {
@@ -823,13 +1014,13 @@ cudaError_t prepare_variant(const KvAttendPlan& p, int ctas, Launch* out) {
   return cudaSuccess;
 }
 
-// The variant of a cache: head_dim rounded up to 64, 128 or 256, and blocks of 8 query heads, or of
-// 16 where the group has more than 8 and the registers hold them (head_dim <= 128).
+// The variant of a cache: heads of up to 64, 128 or (a pair of warps) 256 elements, in blocks of 8
+// query heads, or of 16 where a K/V head has more than 8.
 template <bool Q8>
 cudaError_t prepare_format(const KvAttendPlan& p, int dim, bool wide, int ctas, Launch* out) {
-  if (dim == 256) return prepare_variant<Q8, 256, 1>(p, ctas, out);
-  if (dim == 128) return wide ? prepare_variant<Q8, 128, 2>(p, ctas, out) : prepare_variant<Q8, 128, 1>(p, ctas, out);
-  return wide ? prepare_variant<Q8, 64, 2>(p, ctas, out) : prepare_variant<Q8, 64, 1>(p, ctas, out);
+  if (dim == 256) return wide ? prepare_variant<Q8, 128, 2, 2>(p, ctas, out) : prepare_variant<Q8, 128, 1, 2>(p, ctas, out);
+  if (dim == 128) return wide ? prepare_variant<Q8, 128, 2, 1>(p, ctas, out) : prepare_variant<Q8, 128, 1, 1>(p, ctas, out);
+  return wide ? prepare_variant<Q8, 64, 2, 1>(p, ctas, out) : prepare_variant<Q8, 64, 1, 1>(p, ctas, out);
 }
 
 }  // namespace attend

@@ -12,14 +12,15 @@ namespace {
 
 int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
-bool wide_block(const KvAttendArgs& a) { return a.n_q_heads / a.kv.n_heads > 8 && a.kv.head_dim <= 128; }
+bool wide_block(const KvAttendArgs& a) { return a.n_q_heads / a.kv.n_heads > 8; }
 
 }  // namespace
 
-// A counter and two parts for each CTA of the grid, one CTA per SM.
+// A counter and two parts (four half parts where a head takes two warps) for each CTA of the
+// grid, one CTA per SM.
 size_t kv_attend_workspace_bytes(const KvAttendArgs& a, int num_sms) {
-  const int rows = wide_block(a) ? 16 : 8;
-  return kSplitCounterBytes + (size_t)num_sms * 2 * rows * (padded_dim(a.kv.head_dim) + 2) * sizeof(float);
+  const int rows = wide_block(a) ? 16 : 8, dim = padded_dim(a.kv.head_dim);
+  return kSplitCounterBytes + (size_t)num_sms * 2 * rows * (dim + (dim == 256 ? 4 : 2)) * sizeof(float);
 }
 
 cudaError_t prepare_kv_attend(const KvAttendArgs& a, int num_sms, void* ws, size_t ws_bytes, Launch* out) {
@@ -38,9 +39,16 @@ cudaError_t prepare_kv_attend(const KvAttendArgs& a, int num_sms, void* ws, size
   p.group = a.n_q_heads / a.kv.n_heads;
   p.blocks = (p.group + (wide ? 15 : 7)) / (wide ? 16 : 8);
   p.q_scale = a.scale * 1.4426950408889634f;
+  // Pages of whole tiles; a token's scales copied as 16 bytes (8 for heads of 64) where they are aligned
+  // and all of a padded row exists
+  const int dim = padded_dim(a.kv.head_dim), unit = dim == 64 ? 2 : 4;
+  const auto fits = [&](int64_t stride) { return stride % unit == 0; };
+  const uintptr_t bases = reinterpret_cast<uintptr_t>(a.kv.k_scale) | reinterpret_cast<uintptr_t>(a.kv.v_scale);
+  p.simple = a.kv.page_size % attend::kTile == 0 &&
+             (a.kv.format != IL_Q8 || (a.kv.head_dim == dim && bases % (4 * unit) == 0 && fits(a.kv.spage) &&
+                                       fits(a.kv.stoken) && fits(a.kv.shead)));
   p.arrived = static_cast<unsigned*>(ws);
   p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kSplitCounterBytes);
-  const int dim = padded_dim(a.kv.head_dim);
   return a.kv.format == IL_Q8 ? prepare_kv_attend_q8(p, dim, wide, num_sms, out)
                               : prepare_kv_attend_bf16(p, dim, wide, num_sms, out);
 }
