@@ -141,19 +141,34 @@ __device__ __forceinline__ float4 load_part4(const float* p, bool use) {
   return x;
 }
 
+// c = A B, or c += A B.  The first has its zeros in the instruction, not in registers set to 0.
+#define IL_MMA(TYPE, C0, C1, C2, C3) \
+  "mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {" C0 "," C1 "," C2 "," C3 "};"
+template <bool F16>
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(IL_MMA("f16", "%10", "%10", "%10", "%10")
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm volatile(IL_MMA("bf16", "%10", "%10", "%10", "%10")
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 template <bool F16>
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
   if constexpr (F16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm volatile(IL_MMA("f16", "%0", "%1", "%2", "%3")
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm volatile(IL_MMA("bf16", "%0", "%1", "%2", "%3")
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+#undef IL_MMA
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -189,7 +204,7 @@ struct Seq {
 };
 struct Walk {
   int s;          // sequence
-  int vh;         // K/V head * blocks + block of query heads
+  int hk, block;  // K/V head, block of its query heads
   uint32_t tile;  // of the row
   Seq q;
 };
@@ -204,11 +219,13 @@ __device__ __forceinline__ Seq seq_of(const KvAttendPlan& P, int s) {
   return q;
 }
 
-__device__ __forceinline__ void advance(Walk& w, const KvAttendPlan& P, int rows_per_seq) {
+__device__ __forceinline__ void advance(Walk& w, const KvAttendPlan& P) {
   if (++w.tile < w.q.tiles) return;
   w.tile = 0;
-  if (++w.vh < rows_per_seq) return;
-  w.vh = 0;
+  if (++w.block < P.blocks) return;
+  w.block = 0;
+  if (++w.hk < P.a.kv.n_heads) return;
+  w.hk = 0;
   do w.q = seq_of(P, ++w.s);
   while (w.q.tiles == 0 && w.s + 1 < P.a.n_seq);
 }
@@ -216,8 +233,8 @@ __device__ __forceinline__ void advance(Walk& w, const KvAttendPlan& P, int rows
 // What a worker leaves for the CTA: part 0, the end (or all) of a row begun before its run, and
 // part 1, the beginning of a row that goes on behind it.
 struct Left {
-  int has0, end0, s0, vh0;
-  int has1, s1, vh1;
+  int has0, end0, s0, hk0, block0;
+  int has1, s1, hk1, block1;
   uint32_t tiles0, tiles1;
   long long row0, row1;  // first tiles of the rows in the list
 };
@@ -323,8 +340,10 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
         at -= (long long)in.q.tiles * rows_per_seq;
         in.q = seq_of(P, ++in.s);
       }
-      in.vh = (int)((unsigned long long)at / in.q.tiles);
-      in.tile = (uint32_t)(at - (long long)in.vh * in.q.tiles);
+      const int row = (int)((unsigned long long)at / in.q.tiles);
+      in.tile = (uint32_t)(at - (long long)row * in.q.tiles);
+      in.hk = row / P.blocks;
+      in.block = row - in.hk * P.blocks;
     }
     Walk at = in;  // tile being used
     const uint32_t ring = smem_u32(ring_mem) + warp * C::kRing;
@@ -360,11 +379,10 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
       const bool ok = want && page >= 0 && page < kv.n_pages;
       const uint32_t mask = __ballot_sync(~0u, ok) & 0xffffu;
       if (want && !ok) atomicOr(a.status, kStatusBadSlot);
-      const int hk = w.vh / P.blocks;
       const uint32_t to = ring + stage * C::kStage;
       if (P.simple && mask == 0xffffu) {
         const uint32_t t0 = t - (lane & 15), in_page = t0 - column_of(t0) * (uint32_t)kv.page_size;
-        const int64_t off = (page * kv.page + in_page * kv.token + hk * kv.head) * ES + lane_off;
+        const int64_t off = (page * kv.page + in_page * kv.token + w.hk * kv.head) * ES + lane_off;
         const uint8_t *kp = kv.k + off, *vp = kv.v + off;
 #pragma unroll
         for (int i = 0; i < kTile / PER; ++i) {
@@ -375,7 +393,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
         }
         if constexpr (Q8) {
           const float* sc = (lane < 16 ? kv.k_scale : kv.v_scale) + page * kv.spage +
-                            (in_page + (lane & 15)) * kv.stoken + hk * kv.shead + col0 / 32;
+                            (in_page + (lane & 15)) * kv.stoken + w.hk * kv.shead + col0 / 32;
           const uint32_t st = to + 2 * C::kPool + lane * NB * 4;
 #pragma unroll
           for (int i = 0; i < NB * 4 / SB; ++i) cp_small<SB>(st + i * SB, sc + i * (SB / 4), true);
@@ -383,8 +401,8 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
       } else {
         const uint32_t in_page = t - column_of(t) * (uint32_t)kv.page_size;
         long long off = 0, soff = 0;
-        if (ok) off = page * kv.page + in_page * kv.token + hk * kv.head + col0;
-        if (Q8 && ok) soff = page * kv.spage + in_page * kv.stoken + hk * kv.shead + col0 / 32;
+        if (ok) off = page * kv.page + in_page * kv.token + w.hk * kv.head + col0;
+        if (Q8 && ok) soff = page * kv.spage + in_page * kv.stoken + w.hk * kv.shead + col0 / 32;
 #pragma unroll 1
         for (int i = 0; i < kTile / PER; ++i) {
           const int row = i * PER + sub;
@@ -422,12 +440,11 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
     int v_exp = 14;  // Q8: biased exponent of the largest V scale so far (of the sums' unit)
 
     auto load_q = [&]() {
-      const int hk = at.vh / P.blocks, block = at.vh - hk * P.blocks;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int in_group = block * ROWS + r * 8 + g;
+        const int in_group = at.block * ROWS + r * 8 + g;
         const bool use = in_group < P.group;
-        const float* src = a.q + at.s * a.q_stride + (int64_t)(hk * P.group + in_group) * D + col0 + 8 * q4;
+        const float* src = a.q + at.s * a.q_stride + (int64_t)(at.hk * P.group + in_group) * D + col0 + 8 * q4;
         float x[NB][8];
         float top = 0.f;
 #pragma unroll
@@ -493,7 +510,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
         if (i + S - 1 < n) {
           masks[S - 1] = fetch(in, page, ahead);
           if (i + S < n) {
-            advance(in, P, rows_per_seq);
+            advance(in, P);
             page = page_of(in);
           }
         }
@@ -537,17 +554,17 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
               lds64(w0, w1, from + row * C::kRowBytes + seg * 32 + q4 * 8);
               q8_word_to_f16x2(w0 ^ 0x80808080u, b0, b1);
               q8_word_to_f16x2(w1 ^ 0x80808080u, b2, b3);
-              float c[4] = {0.f, 0.f, 0.f, 0.f};
+              float c[4];
               const uint32_t(&x)[QR] = qf[2 * b];
               const uint32_t(&y)[QR] = qf[2 * b + 1];
               const float d0 = d[2 * nt][b], d1 = d[2 * nt + 1][b];
               if constexpr (R == 1) {
-                mma<true>(c, x[0], x[1], x[2], x[3], b0, b1);
+                mma_first<true>(c, x[0], x[1], x[2], x[3], b0, b1);
                 mma<true>(c, y[0], y[1], y[2], y[3], b2, b3);
                 s[0][2 * nt] = fmaf(c[0] + c[2], d0, s[0][2 * nt]);
                 s[0][2 * nt + 1] = fmaf(c[1] + c[3], d1, s[0][2 * nt + 1]);
               } else {
-                mma<true>(c, x[0], x[1], x[4], x[5], b0, b1);
+                mma_first<true>(c, x[0], x[1], x[4], x[5], b0, b1);
                 mma<true>(c, y[0], y[1], y[4], y[5], b2, b3);
                 mma<true>(c, x[2], x[3], x[6], x[7], b0, b1);
                 mma<true>(c, y[2], y[3], y[6], y[7], b2, b3);
@@ -562,7 +579,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
 #pragma unroll
             for (int c = 0; c < 4; ++c) s[r][c] *= q_back[r];
         } else {
-          float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}}, e[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+          float c[2][4], e[2][4];
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             uint32_t w[2][4];
@@ -575,11 +592,21 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
 #pragma unroll
               for (int nt = 0; nt < 2; ++nt) {
                 if constexpr (R == 1) {
-                  mma<false>(c[nt], x[0], x[1], x[3], x[4], w[nt][2 * h], w[nt][2 * h + 1]);
-                  mma<false>(e[nt], x[2], 0u, x[5], 0u, w[nt][2 * h], w[nt][2 * h + 1]);
+                  if (b + h == 0) {
+                    mma_first<false>(c[nt], x[0], x[1], x[3], x[4], w[nt][0], w[nt][1]);
+                    mma_first<false>(e[nt], x[2], 0u, x[5], 0u, w[nt][0], w[nt][1]);
+                  } else {
+                    mma<false>(c[nt], x[0], x[1], x[3], x[4], w[nt][2 * h], w[nt][2 * h + 1]);
+                    mma<false>(e[nt], x[2], 0u, x[5], 0u, w[nt][2 * h], w[nt][2 * h + 1]);
+                  }
                 } else {
-                  mma<false>(c[nt], x[0], x[1], x[6], x[7], w[nt][2 * h], w[nt][2 * h + 1]);
-                  mma<false>(e[nt], x[2], x[3], x[8], x[9], w[nt][2 * h], w[nt][2 * h + 1]);
+                  if (b + h == 0) {
+                    mma_first<false>(c[nt], x[0], x[1], x[6], x[7], w[nt][0], w[nt][1]);
+                    mma_first<false>(e[nt], x[2], x[3], x[8], x[9], w[nt][0], w[nt][1]);
+                  } else {
+                    mma<false>(c[nt], x[0], x[1], x[6], x[7], w[nt][2 * h], w[nt][2 * h + 1]);
+                    mma<false>(e[nt], x[2], x[3], x[8], x[9], w[nt][2 * h], w[nt][2 * h + 1]);
+                  }
                   mma<false>(e[nt], x[4], x[5], x[10], x[11], w[nt][2 * h], w[nt][2 * h + 1]);
                 }
               }
@@ -692,14 +719,14 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            float c[4];
             float(&acc)[OC] = o[4 * b + j];
             if constexpr (R == 1) {
-              mma<true>(c, p[0], p[1], p[2], p[3], f[0][j], f[1][j]);
+              mma_first<true>(c, p[0], p[1], p[2], p[3], f[0][j], f[1][j]);
               acc[0] = fmaf(acc[0], keep[0], c[0] + c[2]);
               acc[1] = fmaf(acc[1], keep[0], c[1] + c[3]);
             } else {
-              mma<true>(c, p[0], p[1], p[4], p[5], f[0][j], f[1][j]);
+              mma_first<true>(c, p[0], p[1], p[4], p[5], f[0][j], f[1][j]);
               mma<true>(c, p[2], p[3], p[6], p[7], f[0][j], f[1][j]);
 #pragma unroll
               for (int x = 0; x < 4; ++x) acc[x % OC] = fmaf(acc[x % OC], keep[(x / 2) % R], c[x]);
@@ -720,15 +747,15 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
           ldmatrix4_trans(w, fv + t * C::kRowBytes + (((j + (lane >> 4)) ^ (t & 7)) << 4));
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            float c[4];
             float(&acc)[OC] = o[j + h];
             if constexpr (R == 1) {
-              mma<false>(c, hi[0], mid[0], hi[1], mid[1], w[2 * h], w[2 * h + 1]);
+              mma_first<false>(c, hi[0], mid[0], hi[1], mid[1], w[2 * h], w[2 * h + 1]);
               mma<false>(c, lo[0], 0u, lo[1], 0u, w[2 * h], w[2 * h + 1]);
               acc[0] = fmaf(acc[0], keep[0], c[0] + c[2]);
               acc[1] = fmaf(acc[1], keep[0], c[1] + c[3]);
             } else {
-              mma<false>(c, hi[0], hi[1], hi[2 % (2 * R)], hi[3 % (2 * R)], w[2 * h], w[2 * h + 1]);
+              mma_first<false>(c, hi[0], hi[1], hi[2 % (2 * R)], hi[3 % (2 * R)], w[2 * h], w[2 * h + 1]);
               mma<false>(c, mid[0], mid[1], mid[2 % (2 * R)], mid[3 % (2 * R)], w[2 * h], w[2 * h + 1]);
               mma<false>(c, lo[0], lo[1], lo[2 % (2 * R)], lo[3 % (2 * R)], w[2 * h], w[2 * h + 1]);
 #pragma unroll
@@ -747,11 +774,11 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
         if (!alone) {
           const long long row = u0 + i - at.tile;
           if (!begun_here) {
-            left.has0 = 1, left.end0 = row_ends, left.s0 = at.s, left.vh0 = at.vh;
+            left.has0 = 1, left.end0 = row_ends, left.s0 = at.s, left.hk0 = at.hk, left.block0 = at.block;
             left.tiles0 = at.q.tiles, left.row0 = row;
             part = part_mem + warp * C::kPart;
           } else {  // the run's last tile: nothing is in flight into the ring any more
-            left.has1 = 1, left.s1 = at.s, left.vh1 = at.vh;
+            left.has1 = 1, left.s1 = at.s, left.hk1 = at.hk, left.block1 = at.block;
             left.tiles1 = at.q.tiles, left.row1 = row;
             part = reinterpret_cast<float*>(ring_mem + (size_t)warp * C::kRing);
             cp_wait<0>();
@@ -760,14 +787,13 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
             if (H == 2) asm volatile("bar.sync %0, 64;" ::"r"(worker + 1) : "memory");
           }
         }
-        const int hk = at.vh / P.blocks, block = at.vh - hk * P.blocks;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           float sum = l[r];
           sum += __shfl_xor_sync(~0u, sum, 1);
           sum += __shfl_xor_sync(~0u, sum, 2);
-          const int in_group = block * ROWS + 8 * r + g;
-          const int64_t head = (int64_t)hk * P.group + in_group;
+          const int in_group = at.block * ROWS + 8 * r + g;
+          const int64_t head = (int64_t)at.hk * P.group + in_group;
           const float f = alone ? (sum == 0.f ? 0.f : __fdividef(unit, sum)) : unit;
           float* to = alone ? a.out + at.s * a.out_stride + head * D + col0 : part + (8 * r + g) * W;
           if (in_group < P.group) {
@@ -802,7 +828,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
       }
       stage = stage + 1 == S ? 0 : stage + 1;
       if (i + 1 < n) {
-        advance(at, P, rows_per_seq);
+        advance(at, P);
         if (at.tile == 0) begun_here = fresh = true;
       }
     }
@@ -844,8 +870,8 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
     bool ends;
     const int first = max(w, 0), count = end_of(w, ends) - first;
     const Left& by = s_left[first];
-    const int s = w < 0 ? by.s0 : by.s1, vh = w < 0 ? by.vh0 : by.vh1;
-    const int hk = vh / P.blocks, block = vh - hk * P.blocks, rows = min(ROWS, P.group - block * ROWS);
+    const int s = w < 0 ? by.s0 : by.s1, hk = w < 0 ? by.hk0 : by.hk1, block = w < 0 ? by.block0 : by.block1;
+    const int rows = min(ROWS, P.group - block * ROWS);
     constexpr int kNext = H * C::kPart;
     const int wp = first * H + warp % H;  // the first worker's warp of this warp's columns
     const float* const rest = part_mem + wp * C::kPart;
@@ -921,8 +947,8 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
     if (count == 0) continue;
     const int c0 = s_flag[2 + which];
     const Left& by = s_left[which == 0 ? 0 : open];
-    const int s = which == 0 ? by.s0 : by.s1, vh = which == 0 ? by.vh0 : by.vh1;
-    const int hk = vh / P.blocks, block = vh - hk * P.blocks, rows = min(ROWS, P.group - block * ROWS);
+    const int s = which == 0 ? by.s0 : by.s1, hk = which == 0 ? by.hk0 : by.hk1;
+    const int block = which == 0 ? by.block0 : by.block1, rows = min(ROWS, P.group - block * ROWS);
     constexpr int kNext = 2 * H * C::kPart, WIDE = H * W / 4;
     const float* const rest = global_part(c0, 0);  // part i: of the row that came into CTA c0 + i
     const float* const head = global_part(c0, 1);  // part 0: of the row that CTA c0 left open
