@@ -51,7 +51,9 @@ struct KvAttendPlan {
   int group;              // query heads of a K/V head
   int blocks;             // blocks of 8 R query heads of a K/V head
   float q_scale;          // scale * log2(e)
-  int simple;             // pages hold whole tiles and (Q8) scales allow the widest copies
+  int simple;             // pages hold whole tiles, the strides below fit, (Q8) scales allow the widest copies
+  uint32_t page_bytes, token_bytes, head_bytes;     // strides of k and v
+  uint32_t spage_bytes, stoken_bytes, shead_bytes;  // of the scales
   unsigned* arrived;      // one counter a CTA, zero before and after
   float* parts;           // two parts a CTA
 };
@@ -156,6 +158,13 @@ __device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a
                  : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
+// d = c + A B (fp16)
+__device__ __forceinline__ void mma_from(float (&d)[4], float c0, float c1, float c2, float c3, uint32_t a0, uint32_t a1,
+                                         uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(IL_MMA("f16", "%10", "%11", "%12", "%13")
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
 template <bool F16>
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -177,6 +186,15 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 
 __device__ __forceinline__ float pow2_biased(int e) { return __int_as_float(e << 23); }  // 2^(e - 127), 0 < e < 255
+
+// K's bytes u = q + 128 (0 .. 255) as fp16: the bit pattern 00uu is u 2^-24, a subnormal, exactly.  The products
+// with the 128 are taken off by where the sums start.  (V's become exact q: a sum over tokens may
+// meet nothing but small q, which 128 times the sum of p would drown.)
+__device__ __forceinline__ void bytes_to_f16x2(uint32_t w, uint32_t& p01, uint32_t& p23) {
+  const uint32_t u = w ^ 0x80808080u;
+  p01 = __byte_perm(u, 0u, 0x4140);
+  p23 = __byte_perm(u, 0u, 0x4342);
+}
 
 // x, y as packed pairs of parts whose sum is them: three bf16 or two fp16.
 __device__ __forceinline__ void split3(float x, float y, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
@@ -352,7 +370,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
     constexpr int ES = Q8 ? 1 : 2, CPR = C::kRowBytes / 16, PER = 32 / CPR;
     const int chunk = lane % CPR, sub = lane / CPR;
     const bool in_row = col0 + chunk * (16 / ES) < D;
-    const int64_t lane_off = (sub * kv.token + col0) * ES + chunk * 16, row_step = PER * kv.token * ES;
+    const uint32_t lane_off = sub * P.token_bytes + col0 * ES + chunk * 16, row_step = PER * P.token_bytes;
     // scales: the widest copy of a token's scales; a lane copies K's (lanes 0-15) or V's
     constexpr int SB = NB * 4 > 16 ? 16 : NB * 4;
 
@@ -374,15 +392,13 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
     };
     // Copies the tile at `w`; gives the mask of its tokens that exist.
     auto fetch = [&](const Walk& w, int page, int stage) -> uint32_t {
-      const uint32_t t = token_of(w);
-      const bool want = t >= w.q.begin && t < w.q.len;
-      const bool ok = want && page >= 0 && page < kv.n_pages;
-      const uint32_t mask = __ballot_sync(~0u, ok) & 0xffffu;
-      if (want && !ok) atomicOr(a.status, kStatusBadSlot);
+      const uint32_t t = token_of(w), t0 = t - (lane & 15);
       const uint32_t to = ring + stage * C::kStage;
-      if (P.simple && mask == 0xffffu) {
-        const uint32_t t0 = t - (lane & 15), in_page = t0 - column_of(t0) * (uint32_t)kv.page_size;
-        const int64_t off = (page * kv.page + in_page * kv.token + w.hk * kv.head) * ES + lane_off;
+      uint32_t mask = 0xffffu;
+      if (P.simple && t0 >= w.q.begin && t0 + kTile <= w.q.len && (uint32_t)page < (uint32_t)kv.n_pages) {
+        const uint32_t in_page = t0 - column_of(t0) * (uint32_t)kv.page_size;
+        const uint64_t off = (uint64_t)(uint32_t)page * P.page_bytes +
+                             (in_page * P.token_bytes + w.hk * P.head_bytes + lane_off);
         const uint8_t *kp = kv.k + off, *vp = kv.v + off;
 #pragma unroll
         for (int i = 0; i < kTile / PER; ++i) {
@@ -392,13 +408,18 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
           vp += row_step;
         }
         if constexpr (Q8) {
-          const float* sc = (lane < 16 ? kv.k_scale : kv.v_scale) + page * kv.spage +
-                            (in_page + (lane & 15)) * kv.stoken + w.hk * kv.shead + col0 / 32;
+          const uint8_t* const sc = reinterpret_cast<const uint8_t*>(lane < 16 ? kv.k_scale : kv.v_scale) +
+                                    ((uint64_t)(uint32_t)page * P.spage_bytes + ((in_page + (lane & 15)) * P.stoken_bytes +
+                                                                                 w.hk * P.shead_bytes + col0 / 8));
           const uint32_t st = to + 2 * C::kPool + lane * NB * 4;
 #pragma unroll
-          for (int i = 0; i < NB * 4 / SB; ++i) cp_small<SB>(st + i * SB, sc + i * (SB / 4), true);
+          for (int i = 0; i < NB * 4 / SB; ++i) cp_small<SB>(st + i * SB, sc + i * SB, true);
         }
       } else {
+        const bool want = t >= w.q.begin && t < w.q.len;
+        const bool ok = want && page >= 0 && page < kv.n_pages;
+        mask = __ballot_sync(~0u, ok) & 0xffffu;
+        if (want && !ok) atomicOr(a.status, kStatusBadSlot);
         const uint32_t in_page = t - column_of(t) * (uint32_t)kv.page_size;
         long long off = 0, soff = 0;
         if (ok) off = page * kv.page + in_page * kv.token + w.hk * kv.head + col0;
@@ -434,7 +455,8 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
     // ---- the row being worked on
     constexpr int QR = Q8 ? 4 * R : 6 * R;  // registers of q for 16 elements
     uint32_t qf[2 * NB][QR];
-    float q_back[R];  // Q8: the power of two that q was divided by
+    float q_back[R];      // Q8: what s is to be multiplied by for the scaling of q and the bytes' unit
+    float q_start[R][NB];  // Q8: -128 units times the sum of q over a block
     constexpr int OC = 2 * R;
     float o[W / 8][OC], m[R], l[R];
     int v_exp = 14;  // Q8: biased exponent of the largest V scale so far (of the sums' unit)
@@ -465,7 +487,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
           top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
           const int e = max((int)(__float_as_uint(top) >> 23), 14);
           const float up = pow2_biased(267 - e);  // the row's largest |q| becomes 2^13 .. 2^14
-          q_back[r] = pow2_biased(e - 13);
+          q_back[r] = pow2_biased(min(e + 11, 254));
 #pragma unroll
           for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -489,6 +511,27 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
         }
         m[r] = -INFINITY;
         l[r] = 0.f;
+      }
+      if constexpr (Q8) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {  // products with 0x8080, -2^-17 = -128 units
+          const uint32_t(&x)[QR] = qf[2 * b];
+          const uint32_t(&y)[QR] = qf[2 * b + 1];
+          constexpr uint32_t k = 0x80808080u;
+          float c[4];
+          if constexpr (R == 1) {
+            mma_first<true>(c, x[0], x[1], x[2], x[3], k, k);
+            mma<true>(c, y[0], y[1], y[2], y[3], k, k);
+            q_start[0][b] = c[0] + c[2];
+          } else {
+            mma_first<true>(c, x[0], x[1], x[4], x[5], k, k);
+            mma<true>(c, y[0], y[1], y[4], y[5], k, k);
+            mma<true>(c, x[2], x[3], x[6], x[7], k, k);
+            mma<true>(c, y[2], y[3], y[6], y[7], k, k);
+            q_start[0][b] = c[0];
+            q_start[R - 1][b] = c[2];
+          }
+        }
       }
 #pragma unroll
       for (int j = 0; j < W / 8; ++j)
@@ -552,19 +595,19 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
               const int seg = b ^ (W == 64 ? (row >> 1) & 1 : row & 3);
               uint32_t w0, w1, b0, b1, b2, b3;
               lds64(w0, w1, from + row * C::kRowBytes + seg * 32 + q4 * 8);
-              q8_word_to_f16x2(w0 ^ 0x80808080u, b0, b1);
-              q8_word_to_f16x2(w1 ^ 0x80808080u, b2, b3);
+              bytes_to_f16x2(w0, b0, b1);
+              bytes_to_f16x2(w1, b2, b3);
               float c[4];
               const uint32_t(&x)[QR] = qf[2 * b];
               const uint32_t(&y)[QR] = qf[2 * b + 1];
               const float d0 = d[2 * nt][b], d1 = d[2 * nt + 1][b];
               if constexpr (R == 1) {
-                mma_first<true>(c, x[0], x[1], x[2], x[3], b0, b1);
+                mma_from(c, q_start[0][b], q_start[0][b], 0.f, 0.f, x[0], x[1], x[2], x[3], b0, b1);
                 mma<true>(c, y[0], y[1], y[2], y[3], b2, b3);
                 s[0][2 * nt] = fmaf(c[0] + c[2], d0, s[0][2 * nt]);
                 s[0][2 * nt + 1] = fmaf(c[1] + c[3], d1, s[0][2 * nt + 1]);
               } else {
-                mma_first<true>(c, x[0], x[1], x[4], x[5], b0, b1);
+                mma_from(c, q_start[0][b], q_start[0][b], q_start[R - 1][b], q_start[R - 1][b], x[0], x[1], x[4], x[5], b0, b1);
                 mma<true>(c, y[0], y[1], y[4], y[5], b2, b3);
                 mma<true>(c, x[2], x[3], x[6], x[7], b0, b1);
                 mma<true>(c, y[2], y[3], y[6], y[7], b2, b3);

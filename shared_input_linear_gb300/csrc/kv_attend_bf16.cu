@@ -39,14 +39,24 @@ cudaError_t prepare_kv_attend(const KvAttendArgs& a, int num_sms, void* ws, size
   p.group = a.n_q_heads / a.kv.n_heads;
   p.blocks = (p.group + (wide ? 15 : 7)) / (wide ? 16 : 8);
   p.q_scale = a.scale * 1.4426950408889634f;
-  // Pages of whole tiles; a token's scales copied as 16 bytes (8 for heads of 64) where they are aligned
-  // and all of a padded row exists
-  const int dim = padded_dim(a.kv.head_dim), unit = dim == 64 ? 2 : 4;
-  const auto fits = [&](int64_t stride) { return stride % unit == 0; };
-  const uintptr_t bases = reinterpret_cast<uintptr_t>(a.kv.k_scale) | reinterpret_cast<uintptr_t>(a.kv.v_scale);
-  p.simple = a.kv.page_size % attend::kTile == 0 &&
-             (a.kv.format != IL_Q8 || (a.kv.head_dim == dim && bases % (4 * unit) == 0 && fits(a.kv.spage) &&
-                                       fits(a.kv.stoken) && fits(a.kv.shead)));
+  // Simple copies: pages of whole tiles; strides of 32 bits; a token's scales copied as 16 bytes (8 for heads of
+  // 64) where they are aligned and all of a padded row exists
+  const KvView& kv = a.kv;
+  const bool q8 = kv.format == IL_Q8;
+  const int dim = padded_dim(kv.head_dim), unit = dim == 64 ? 2 : 4;
+  const int64_t es = q8 ? 1 : 2;
+  const auto fits = [&](int64_t page, int64_t token, int64_t head) {
+    return page <= UINT32_MAX && token * kv.page_size + head * kv.n_heads <= INT32_MAX;
+  };
+  const auto even = [&](int64_t stride) { return stride % unit == 0; };
+  const uintptr_t bases = reinterpret_cast<uintptr_t>(kv.k_scale) | reinterpret_cast<uintptr_t>(kv.v_scale);
+  p.simple = kv.page_size % attend::kTile == 0 && fits(kv.page * es, kv.token * es, kv.head * es);
+  if (q8 && p.simple)
+    p.simple = kv.head_dim == dim && fits(kv.spage * 4, kv.stoken * 4, kv.shead * 4) && bases % (4 * unit) == 0 &&
+               even(kv.spage) && even(kv.stoken) && even(kv.shead);
+  p.page_bytes = (uint32_t)(kv.page * es), p.token_bytes = (uint32_t)(kv.token * es), p.head_bytes = (uint32_t)(kv.head * es);
+  p.spage_bytes = (uint32_t)(kv.spage * 4), p.stoken_bytes = (uint32_t)(kv.stoken * 4);
+  p.shead_bytes = (uint32_t)(kv.shead * 4);
   p.arrived = static_cast<unsigned*>(ws);
   p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kSplitCounterBytes);
   return a.kv.format == IL_Q8 ? prepare_kv_attend_q8(p, dim, wide, num_sms, out)
