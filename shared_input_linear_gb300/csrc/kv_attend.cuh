@@ -6,7 +6,7 @@
 // Each K and V byte is used G times, so the kernel is bound by HBM: it has to keep copies in
 // flight on every SM for the whole launch, whatever the lengths, and do the arithmetic beside them.
 //
-// Work.  The tokens of a (sequence, K/V head) pair -- a row -- are cut into tiles of 16.  All tiles of all
+// Work.  The tokens of a (sequence, K/V head) pair -- a row -- are cut into tiles of 16 or 32.  All tiles of all
 // rows form one list, and every warp of the launch (one CTA per SM) takes an equal contiguous
 // run of it, found from the prefix sums of the lengths that each CTA computes itself: ragged batches, long
 // sequences and idle slots balance to one tile a warp without any host knowledge of the lengths.
@@ -27,9 +27,10 @@
 // exactly enough to keep fp32's accuracy: against bf16 K and V into three bf16 parts (hi + mid + lo,
 // 24 bits); against int8 into two fp16 parts (22 bits), with K's and V's integers decoded to exact
 // fp16, K's block scales applied to each block's fp32 sum and V's to p, under a running power of two.
-// With up to 8 heads (R = 1) hi fills rows 0-7 of an MMA and mid (int8: lo) rows 8-15, so the
+// With up to 8 heads (R = 1) q's hi fills rows 0-7 of an MMA and mid (int8: lo) rows 8-15, so the
 // split costs one more MMA at bf16 and none at int8; with 9 to 16 heads (R = 2) every part is an MMA
-// of its own.  Each tile's product starts from zero accumulators and joins the running sum in fp32
+// of its own.  p V is computed transposed: the quad layout of s is that of a B operand, so p goes in as it is.
+// Each tile's product starts from zero accumulators and joins the running sum in fp32
 // FMAs (with the factor of the running maximum), which round to nearest.
 #pragma once
 
@@ -60,7 +61,7 @@ struct KvAttendPlan {
 
 namespace attend {
 
-constexpr int kTile = 16;
+constexpr int kGroup = 16;          // tokens of a product's step; pages of whole groups are copied the simple way
 constexpr int kSmemLimit = 232448;  // 227 KB
 
 // W columns of a head in a warp, H warps a head (H * W >= head_dim), R blocks of 8 query heads.
@@ -69,11 +70,13 @@ struct Config {
   static constexpr int kRows = 8 * R;            // query heads of a block
   static constexpr int kBlocks = W / 32;         // 32-element blocks of a warp's columns
   static constexpr int kPart = kRows * (W + 2);  // floats of a part: sums, maxima, sums of p
+  // Tokens of a tile: 32 where a row is short in bytes, so that what a tile costs beside its bytes counts half
+  static constexpr int kTile = R == 1 && (Q8 || W == 64) ? 32 : 16;
   static constexpr int kRowBytes = Q8 ? W : 2 * W;
   static constexpr int kPool = kTile * kRowBytes;               // K or V of a tile
   static constexpr int kScales = Q8 ? kTile * kBlocks * 4 : 0;  // its scales
   static constexpr int kStage = 2 * (kPool + kScales);
-  static constexpr int kWarps = R == 1 && (Q8 || W == 64) ? 12 : 8;
+  static constexpr int kWarps = Q8 && R == 1 && W == 64 ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kWorkers = kWarps / H;    // runs of tiles in a CTA
   static constexpr int kFixed = (kThreads + 2) * 8 + kWarps * 8 + kWorkers * 64 + 64;
@@ -83,7 +86,7 @@ struct Config {
   static constexpr size_t kSmem = (size_t)kFixed + kWarps * (kPart * 4 + kRing);
   static_assert(kStages >= 2 && kSmem <= kSmemLimit, "the ring does not fit");
   static_assert(kRing >= kPart * 4, "a part must fit the warp's ring");
-  static_assert(kPool >= 32 * 16 * R, "s is traded through the tile of K");
+  static_assert(kPool >= 32 * kTile * R, "s is traded through the tile of K");
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool use) {
@@ -227,16 +230,18 @@ struct Walk {
   Seq q;
 };
 
+template <int T>
 __device__ __forceinline__ Seq seq_of(const KvAttendPlan& P, int s) {
   Seq q;
   const int len = min(max(P.a.lens[s], 0), P.cap);
   q.len = (uint32_t)len;
   q.begin = P.window > 0 ? (uint32_t)max(len - P.window, 0) : 0u;
-  q.first = q.begin / kTile;
-  q.tiles = len == 0 ? 0u : (q.len + kTile - 1) / kTile - q.first;
+  q.first = q.begin / T;
+  q.tiles = len == 0 ? 0u : (q.len + T - 1) / T - q.first;
   return q;
 }
 
+template <int T>
 __device__ __forceinline__ void advance(Walk& w, const KvAttendPlan& P) {
   if (++w.tile < w.q.tiles) return;
   w.tile = 0;
@@ -244,7 +249,7 @@ __device__ __forceinline__ void advance(Walk& w, const KvAttendPlan& P) {
   w.block = 0;
   if (++w.hk < P.a.kv.n_heads) return;
   w.hk = 0;
-  do w.q = seq_of(P, ++w.s);
+  do w.q = seq_of<T>(P, ++w.s);
   while (w.q.tiles == 0 && w.s + 1 < P.a.n_seq);
 }
 
@@ -261,6 +266,7 @@ static_assert(sizeof(Left) <= 64, "see Config::kFixed");
 template <bool Q8, int W, int R, int H>
 __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_kernel(const KvAttendPlan P) {
   using C = Config<Q8, W, R, H>;
+  constexpr int T = C::kTile, NN = T / 8, GR = T / kGroup;  // tokens of a tile, in eights, in groups
   constexpr int NB = C::kBlocks, NT = C::kThreads, NW = C::kWarps, NK = C::kWorkers, S = C::kStages, ROWS = C::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* const ring_mem = smem;
@@ -296,7 +302,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
   for (int k = 0; k < run; ++k) {
     const int s = tid * run + k;
     const bool in = s < a.n_seq;
-    const Seq q = in ? seq_of(P, s) : Seq{0, 0, 0, 0};
+    const Seq q = in ? seq_of<T>(P, s) : Seq{0, 0, 0, 0};
     mine += q.tiles;
     unsigned none = __ballot_sync(~0u, in && q.tiles == 0 && s % gridDim.x == blockIdx.x);
     while (none != 0) {
@@ -353,10 +359,10 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
         if (lo + step < NT && s_before[lo + step] * rows_per_seq <= u0) lo += step;
       long long at = u0 - s_before[lo] * rows_per_seq;
       in.s = lo * run;
-      in.q = seq_of(P, in.s);
+      in.q = seq_of<T>(P, in.s);
       while (at >= (long long)in.q.tiles * rows_per_seq && in.s + 1 < a.n_seq) {
         at -= (long long)in.q.tiles * rows_per_seq;
-        in.q = seq_of(P, ++in.s);
+        in.q = seq_of<T>(P, ++in.s);
       }
       const int row = (int)((unsigned long long)at / in.q.tiles);
       in.tile = (uint32_t)(at - (long long)row * in.q.tiles);
@@ -374,9 +380,9 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
     // scales: the widest copy of a token's scales; a lane copies K's (lanes 0-15) or V's
     constexpr int SB = NB * 4 > 16 ? 16 : NB * 4;
 
-    auto token_of = [&](const Walk& w) { return (w.q.first + w.tile) * kTile + (lane & 15); };
+    auto token_of = [&](const Walk& w) { return (w.q.first + w.tile) * T + (lane & (T - 1)); };
     auto column_of = [&](uint32_t t) { return (__umulhi(P.div_m, t) + t) >> P.div_s; };
-    auto page_of = [&](const Walk& w) {  // page of this lane's token of the tile (lanes 16-31 repeat 0-15)
+    auto page_of = [&](const Walk& w) {  // page of this lane's token of the tile (of 16 tokens, lanes 16-31 repeat 0-15)
       const uint32_t t = token_of(w);
       return t >= w.q.begin && t < w.q.len ? a.table[w.s * a.table_stride + column_of(t)] : -1;
     };
@@ -387,45 +393,47 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
     };
     auto v_at = [&](int row) {
       if (!Q8) return row * C::kRowBytes + ((chunk ^ (row & 7)) << 4);
-      if (W == 64) row = (row >> 1) | ((row & 1) << 3);
+      if (W == 64) row = (row & ~15) | ((row >> 1) & 7) | ((row & 1) << 3);
       return row * C::kRowBytes + ((chunk ^ (((row >> 1) & (W == 64 ? 1 : 3)) << 1)) << 4);
     };
     // Copies the tile at `w`; gives the mask of its tokens that exist.
     auto fetch = [&](const Walk& w, int page, int stage) -> uint32_t {
-      const uint32_t t = token_of(w), t0 = t - (lane & 15);
+      const uint32_t t = token_of(w), t0 = t - (lane & (T - 1));
       const uint32_t to = ring + stage * C::kStage;
-      uint32_t mask = 0xffffu;
-      if (P.simple && t0 >= w.q.begin && t0 + kTile <= w.q.len && (uint32_t)page < (uint32_t)kv.n_pages) {
-        const uint32_t in_page = t0 - column_of(t0) * (uint32_t)kv.page_size;
-        const uint64_t off = (uint64_t)(uint32_t)page * P.page_bytes +
-                             (in_page * P.token_bytes + w.hk * P.head_bytes + lane_off);
-        const uint8_t *kp = kv.k + off, *vp = kv.v + off;
+      const bool want = t >= w.q.begin && t < w.q.len, ok = want && (uint32_t)page < (uint32_t)kv.n_pages;
+      const uint32_t mask = __ballot_sync(~0u, ok) & (uint32_t)((1ull << T) - 1);
+      if (P.simple && mask == (uint32_t)((1ull << T) - 1)) {
 #pragma unroll
-        for (int i = 0; i < kTile / PER; ++i) {
-          cp16(to + k_at(i * PER + sub), kp, in_row);
-          cp16(to + C::kPool + v_at(i * PER + sub), vp, in_row);
-          kp += row_step;
-          vp += row_step;
-        }
-        if constexpr (Q8) {
-          const uint8_t* const sc = reinterpret_cast<const uint8_t*>(lane < 16 ? kv.k_scale : kv.v_scale) +
-                                    ((uint64_t)(uint32_t)page * P.spage_bytes + ((in_page + (lane & 15)) * P.stoken_bytes +
-                                                                                 w.hk * P.shead_bytes + col0 / 8));
-          const uint32_t st = to + 2 * C::kPool + lane * NB * 4;
+        for (int k = 0; k < GR; ++k) {
+          const uint32_t first = t0 + k * kGroup, pg = GR == 1 ? (uint32_t)page : (uint32_t)__shfl_sync(~0u, page, k * kGroup);
+          const uint32_t in_page = first - column_of(first) * (uint32_t)kv.page_size;
+          const uint64_t off = (uint64_t)pg * P.page_bytes + (in_page * P.token_bytes + w.hk * P.head_bytes + lane_off);
+          const uint8_t *kp = kv.k + off, *vp = kv.v + off;
 #pragma unroll
-          for (int i = 0; i < NB * 4 / SB; ++i) cp_small<SB>(st + i * SB, sc + i * SB, true);
+          for (int i = 0; i < kGroup / PER; ++i) {
+            const int row = k * kGroup + i * PER + sub;
+            cp16(to + k_at(row), kp, in_row);
+            cp16(to + C::kPool + v_at(row), vp, in_row);
+            kp += row_step;
+            vp += row_step;
+          }
+          if constexpr (Q8) {
+            const uint8_t* const sc = reinterpret_cast<const uint8_t*>(lane < 16 ? kv.k_scale : kv.v_scale) +
+                                      ((uint64_t)pg * P.spage_bytes + ((in_page + (lane & 15)) * P.stoken_bytes +
+                                                                       w.hk * P.shead_bytes + col0 / 8));
+            const uint32_t st = to + 2 * C::kPool + (lane < 16 ? 0 : C::kScales) + (k * kGroup + (lane & 15)) * NB * 4;
+#pragma unroll
+            for (int i = 0; i < NB * 4 / SB; ++i) cp_small<SB>(st + i * SB, sc + i * SB, true);
+          }
         }
       } else {
-        const bool want = t >= w.q.begin && t < w.q.len;
-        const bool ok = want && page >= 0 && page < kv.n_pages;
-        mask = __ballot_sync(~0u, ok) & 0xffffu;
         if (want && !ok) atomicOr(a.status, kStatusBadSlot);
         const uint32_t in_page = t - column_of(t) * (uint32_t)kv.page_size;
         long long off = 0, soff = 0;
         if (ok) off = page * kv.page + in_page * kv.token + w.hk * kv.head + col0;
         if (Q8 && ok) soff = page * kv.spage + in_page * kv.stoken + w.hk * kv.shead + col0 / 32;
 #pragma unroll 1
-        for (int i = 0; i < kTile / PER; ++i) {
+        for (int i = 0; i < T / PER; ++i) {
           const int row = i * PER + sub;
           const long long o = __shfl_sync(~0u, off, row);
           const bool use = ((mask >> row) & 1) && in_row;
@@ -436,7 +444,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
         if constexpr (Q8) {
           const uint32_t st = to + 2 * C::kPool;
 #pragma unroll 1
-          for (int i = 0; i < kTile * NB / 32; ++i) {
+          for (int i = 0; i < T * NB / 32; ++i) {
             const int row = (i * 32 + lane) / NB, b = (i * 32 + lane) % NB;
             const long long so = __shfl_sync(~0u, soff, row);
             const bool use = ((mask >> row) & 1) && col0 + b * 32 < D;
@@ -457,9 +465,13 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
     uint32_t qf[2 * NB][QR];
     float q_back[R];      // Q8: what s is to be multiplied by for the scaling of q and the bytes' unit
     float q_start[R][NB];  // Q8: -128 units times the sum of q over a block
-    constexpr int OC = 2 * R;
-    float o[W / 8][OC], m[R], l[R];
-    int v_exp = 14;  // Q8: biased exponent of the largest V scale so far (of the sums' unit)
+    // sums of p V, transposed: o[i][4 r + x] of MMA rows (columns of the head) g (x = 0, 1) or g + 8 (2, 3) of step i
+    // and of query heads 8 r + 2 q4 + (x & 1)
+    float o[W / 16][4 * R], m[R], l[R];
+    // Q8: the largest s so far (m may lie below it), the biased exponent of the largest V scale so far, and that of
+    // the sums' unit
+    float highest[R];
+    int v_exp = 14, o_exp = 14;
 
     auto load_q = [&]() {
 #pragma unroll
@@ -509,7 +521,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
               qf[2 * b + i / 2][(i & 1) * 3 * R + 2 * R + r] = lo;
             }
         }
-        m[r] = -INFINITY;
+        m[r] = highest[r] = -INFINITY;
         l[r] = 0.f;
       }
       if constexpr (Q8) {
@@ -534,10 +546,10 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
         }
       }
 #pragma unroll
-      for (int j = 0; j < W / 8; ++j)
+      for (int i = 0; i < W / 16; ++i)
 #pragma unroll
-        for (int c = 0; c < OC; ++c) o[j][c] = 0.f;
-      v_exp = 14;
+        for (int x = 0; x < 4 * R; ++x) o[i][x] = 0.f;
+      v_exp = o_exp = 14;
     };
 
     // Tile i is used while tile i + S - 1 is on its way; the loop starts S - 1 tiles early, so that its
@@ -553,7 +565,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
         if (i + S - 1 < n) {
           masks[S - 1] = fetch(in, page, ahead);
           if (i + S < n) {
-            advance(in, P);
+            advance<T>(in, P);
             page = page_of(in);
           }
         }
@@ -575,21 +587,19 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
       const uint32_t from = ring + stage * C::kStage;
 
       // ---- s = q K^T: s[r][2 nt + c] of head row g + 8 r, token 8 nt + 2 q4 + c
-      float s[R][4];
+      float s[R][2 * NN];
       if (H == 1 || i >= 0) {
         if constexpr (Q8) {
-          const uint32_t sc = from + 2 * C::kPool + 2 * q4 * NB * 4;
-          float d[4][NB];  // K's scales of tokens 2 q4, 2 q4 + 1, and 8 more
 #pragma unroll
-          for (int t = 0; t < 4; ++t) lds_floats(d[t], sc + ((t & 1) + 8 * (t >> 1)) * NB * 4);
+          for (int nt = 0; nt < NN; ++nt) {
+            float d0[NB], d1[NB];  // K's scales of tokens 8 nt + 2 q4, and the next
+            const uint32_t sc = from + 2 * C::kPool + (8 * nt + 2 * q4) * NB * 4;
+            lds_floats(d0, sc);
+            lds_floats(d1, sc + NB * 4);
 #pragma unroll
-          for (int r = 0; r < R; ++r)
+            for (int r = 0; r < R; ++r) s[r][2 * nt] = s[r][2 * nt + 1] = 0.f;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) s[r][c] = 0.f;
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
+            for (int b = 0; b < NB; ++b) {
               const int row = 8 * nt + g;
               // element order inside a block: lane q4 holds 8 q4 .. 8 q4 + 7, as q does
               const int seg = b ^ (W == 64 ? (row >> 1) & 1 : row & 3);
@@ -600,71 +610,75 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
               float c[4];
               const uint32_t(&x)[QR] = qf[2 * b];
               const uint32_t(&y)[QR] = qf[2 * b + 1];
-              const float d0 = d[2 * nt][b], d1 = d[2 * nt + 1][b];
               if constexpr (R == 1) {
                 mma_from(c, q_start[0][b], q_start[0][b], 0.f, 0.f, x[0], x[1], x[2], x[3], b0, b1);
                 mma<true>(c, y[0], y[1], y[2], y[3], b2, b3);
-                s[0][2 * nt] = fmaf(c[0] + c[2], d0, s[0][2 * nt]);
-                s[0][2 * nt + 1] = fmaf(c[1] + c[3], d1, s[0][2 * nt + 1]);
+                s[0][2 * nt] = fmaf(c[0] + c[2], d0[b], s[0][2 * nt]);
+                s[0][2 * nt + 1] = fmaf(c[1] + c[3], d1[b], s[0][2 * nt + 1]);
               } else {
                 mma_from(c, q_start[0][b], q_start[0][b], q_start[R - 1][b], q_start[R - 1][b], x[0], x[1], x[4], x[5], b0, b1);
                 mma<true>(c, y[0], y[1], y[4], y[5], b2, b3);
                 mma<true>(c, x[2], x[3], x[6], x[7], b0, b1);
                 mma<true>(c, y[2], y[3], y[6], y[7], b2, b3);
-                s[0][2 * nt] = fmaf(c[0], d0, s[0][2 * nt]);
-                s[0][2 * nt + 1] = fmaf(c[1], d1, s[0][2 * nt + 1]);
-                s[R - 1][2 * nt] = fmaf(c[2], d0, s[R - 1][2 * nt]);
-                s[R - 1][2 * nt + 1] = fmaf(c[3], d1, s[R - 1][2 * nt + 1]);
-              }
-            }
-#pragma unroll
-          for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) s[r][c] *= q_back[r];
-        } else {
-          float c[2][4], e[2][4];
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            uint32_t w[2][4];
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-              lds128(w[nt], from + (8 * nt + g) * C::kRowBytes + (((4 * b + q4) ^ ((g & 1) << 2)) << 4));
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t(&x)[QR] = qf[2 * b + h];
-#pragma unroll
-              for (int nt = 0; nt < 2; ++nt) {
-                if constexpr (R == 1) {
-                  if (b + h == 0) {
-                    mma_first<false>(c[nt], x[0], x[1], x[3], x[4], w[nt][0], w[nt][1]);
-                    mma_first<false>(e[nt], x[2], 0u, x[5], 0u, w[nt][0], w[nt][1]);
-                  } else {
-                    mma<false>(c[nt], x[0], x[1], x[3], x[4], w[nt][2 * h], w[nt][2 * h + 1]);
-                    mma<false>(e[nt], x[2], 0u, x[5], 0u, w[nt][2 * h], w[nt][2 * h + 1]);
-                  }
-                } else {
-                  if (b + h == 0) {
-                    mma_first<false>(c[nt], x[0], x[1], x[6], x[7], w[nt][0], w[nt][1]);
-                    mma_first<false>(e[nt], x[2], x[3], x[8], x[9], w[nt][0], w[nt][1]);
-                  } else {
-                    mma<false>(c[nt], x[0], x[1], x[6], x[7], w[nt][2 * h], w[nt][2 * h + 1]);
-                    mma<false>(e[nt], x[2], x[3], x[8], x[9], w[nt][2 * h], w[nt][2 * h + 1]);
-                  }
-                  mma<false>(e[nt], x[4], x[5], x[10], x[11], w[nt][2 * h], w[nt][2 * h + 1]);
-                }
+                s[0][2 * nt] = fmaf(c[0], d0[b], s[0][2 * nt]);
+                s[0][2 * nt + 1] = fmaf(c[1], d1[b], s[0][2 * nt + 1]);
+                s[R - 1][2 * nt] = fmaf(c[2], d0[b], s[R - 1][2 * nt]);
+                s[R - 1][2 * nt + 1] = fmaf(c[3], d1[b], s[R - 1][2 * nt + 1]);
               }
             }
           }
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            if constexpr (R == 1) {
-              s[0][2 * nt] = c[nt][0] + (c[nt][2] + e[nt][0]);
-              s[0][2 * nt + 1] = c[nt][1] + (c[nt][3] + e[nt][1]);
-            } else {
-              s[0][2 * nt] = c[nt][0] + e[nt][0];
-              s[0][2 * nt + 1] = c[nt][1] + e[nt][1];
-              s[R - 1][2 * nt] = c[nt][2] + e[nt][2];
-              s[R - 1][2 * nt + 1] = c[nt][3] + e[nt][3];
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int c = 0; c < 2 * NN; ++c) s[r][c] *= q_back[r];
+        } else {
+#pragma unroll
+          for (int k = 0; k < GR; ++k) {
+            float c[2][4], e[2][4];  // of q's first two parts, and of the others
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              uint32_t w[2][4];
+#pragma unroll
+              for (int nt = 0; nt < 2; ++nt)
+                lds128(w[nt], from + (16 * k + 8 * nt + g) * C::kRowBytes + (((4 * b + q4) ^ ((g & 1) << 2)) << 4));
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t(&x)[QR] = qf[2 * b + h];
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                  if constexpr (R == 1) {
+                    if (b + h == 0) {
+                      mma_first<false>(c[nt], x[0], x[1], x[3], x[4], w[nt][0], w[nt][1]);
+                      mma_first<false>(e[nt], x[2], 0u, x[5], 0u, w[nt][0], w[nt][1]);
+                    } else {
+                      mma<false>(c[nt], x[0], x[1], x[3], x[4], w[nt][2 * h], w[nt][2 * h + 1]);
+                      mma<false>(e[nt], x[2], 0u, x[5], 0u, w[nt][2 * h], w[nt][2 * h + 1]);
+                    }
+                  } else {
+                    if (b + h == 0) {
+                      mma_first<false>(c[nt], x[0], x[1], x[6], x[7], w[nt][0], w[nt][1]);
+                      mma_first<false>(e[nt], x[2], x[3], x[8], x[9], w[nt][0], w[nt][1]);
+                    } else {
+                      mma<false>(c[nt], x[0], x[1], x[6], x[7], w[nt][2 * h], w[nt][2 * h + 1]);
+                      mma<false>(e[nt], x[2], x[3], x[8], x[9], w[nt][2 * h], w[nt][2 * h + 1]);
+                    }
+                    mma<false>(e[nt], x[4], x[5], x[10], x[11], w[nt][2 * h], w[nt][2 * h + 1]);
+                  }
+                }
+              }
+            }
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              const int at0 = 4 * k + 2 * nt;
+              if constexpr (R == 1) {
+                s[0][at0] = c[nt][0] + (c[nt][2] + e[nt][0]);
+                s[0][at0 + 1] = c[nt][1] + (c[nt][3] + e[nt][1]);
+              } else {
+                s[0][at0] = c[nt][0] + e[nt][0];
+                s[0][at0 + 1] = c[nt][1] + e[nt][1];
+                s[R - 1][at0] = c[nt][2] + e[nt][2];
+                s[R - 1][at0 + 1] = c[nt][3] + e[nt][3];
+              }
             }
           }
         }
@@ -673,15 +687,19 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
           // copy into this stage starts behind the next tile's barrier, when both have read.
           __syncwarp();
 #pragma unroll
-          for (int r = 0; r < R; ++r) sts128(from + (r * 32 + lane) * 16, s[r]);
+          for (int x = 0; x < R * GR; ++x) {
+            const float(&v)[2 * NN] = s[x / GR];
+            const float part[4] = {v[4 * (x % GR)], v[4 * (x % GR) + 1], v[4 * (x % GR) + 2], v[4 * (x % GR) + 3]};
+            sts128(from + (x * 32 + lane) * 16, part);
+          }
           asm volatile("bar.sync %0, 64;" ::"r"(worker + 1) : "memory");
           const uint32_t other = from + (warp % 2 == 0 ? C::kRing : -C::kRing);
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            float x[4];
-            lds_floats(x, other + (r * 32 + lane) * 16);
+          for (int x = 0; x < R * GR; ++x) {
+            float part[4];
+            lds_floats(part, other + (x * 32 + lane) * 16);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) s[r][c] += x[c];
+            for (int c = 0; c < 4; ++c) s[x / GR][4 * (x % GR) + c] += part[c];
           }
         }
       }
@@ -690,128 +708,207 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
         if (i < 0) continue;
       }
 
-      // ---- softmax: the tile's maximum, p, and the factor of what came before
+      // ---- softmax: p = 2^(s - m) and the factor of what came before
       const uint32_t mk = masks[0];
-      if (mk != 0xffffu) {
+      float low[R];
+      if constexpr (Q8) {
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int r = 0; r < R; ++r) {
+          low[r] = s[r][0];
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-            if (!((mk >> (8 * nt + 2 * q4 + c)) & 1))
-#pragma unroll
-              for (int r = 0; r < R; ++r) s[r][2 * nt + c] = -INFINITY;
+          for (int c = 1; c < 2 * NN; ++c) low[r] = fminf(low[r], s[r][c]);
+        }
       }
+      if (mk != (uint32_t)((1ull << T) - 1)) {
+#pragma unroll
+        for (int c = 0; c < 2 * NN; ++c)
+          if (!((mk >> (8 * (c / 2) + 2 * q4 + c % 2)) & 1))
+#pragma unroll
+            for (int r = 0; r < R; ++r) s[r][c] = -INFINITY;
+      }
+      float top[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        top[r] = s[r][0];
+#pragma unroll
+        for (int c = 1; c < 2 * NN; ++c) top[r] = fmaxf(top[r], s[r][c]);
+        top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
+        top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
+      }
+      // bf16 parts of p have fp32's range: m is the maximum so far.  fp16 parts keep 12 bits or more of p only
+      // above 2^-26, so that m follows the tile's own maximum, down to 2^-24 of the largest p; a tile with
+      // smaller p all the same (`wide`) takes its products in classes of 2^-26 (below).
+      bool wide = false;
+      float next[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if constexpr (Q8) {
+          highest[r] = fmaxf(highest[r], top[r]);
+          next[r] = fmaxf(top[r], highest[r] - 24.f);
+          wide |= next[r] - low[r] > 26.f;
+        } else {
+          next[r] = fmaxf(m[r], top[r]);
+        }
+      }
+      if (Q8) wide = __any_sync(~0u, wide);
       float keep[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        float top = fmaxf(fmaxf(s[r][0], s[r][1]), fmaxf(s[r][2], s[r][3]));
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-        const float now = fmaxf(m[r], top), base = now == -INFINITY ? 0.f : now;
+        if (Q8 && wide) next[r] = highest[r];
+        const float base = next[r] == -INFINITY ? 0.f : next[r];
         keep[r] = exp2_fast(m[r] - base);
-        m[r] = now;
+        m[r] = next[r];
+        float sum = 0.f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[r][c] = exp2_fast(s[r][c] - base);
-        l[r] = fmaf(l[r], keep[r], (s[r][0] + s[r][1]) + (s[r][2] + s[r][3]));
+        for (int c = 0; c < 2 * NN; c += 2) {
+          s[r][c] = exp2_fast(s[r][c] - base);
+          s[r][c + 1] = exp2_fast(s[r][c + 1] - base);
+          sum += s[r][c] + s[r][c + 1];
+        }
+        l[r] = fmaf(l[r], keep[r], sum);
       }
 
-      // ---- o = o * keep + p V
+      // ---- o^T = o^T keep + V^T p^T: p is the B operand as it stands, its parts add up in the accumulators
       const uint32_t fv = from + C::kPool;
+      float kept[2 * R];  // keep of the heads that this lane's sums are of
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        kept[2 * r] = __shfl_sync(~0u, keep[r], 8 * q4);
+        kept[2 * r + 1] = __shfl_sync(~0u, keep[r], 8 * q4 + 4);
+      }
+      auto join = [&](float (&acc)[4 * R], const float (&c)[R][4]) {
+#pragma unroll
+        for (int x = 0; x < 4 * R; ++x) acc[x] = fmaf(acc[x], kept[2 * (x / 4) + x % 2], c[x / 4][x % 4]);
+      };
       if constexpr (Q8) {
+        float d[2 * NN][NB];  // V's scales of the lane's tokens
         const uint32_t sv = from + 2 * C::kPool + C::kScales + 2 * q4 * NB * 4;
-        float d[4][NB];  // scales of tokens 2 q4, 2 q4 + 1, and 8 more
-        float top = 0.f;
+        float most = 0.f;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          lds_floats(d[t], sv + ((t & 1) + 8 * (t >> 1)) * NB * 4);
+        for (int c = 0; c < 2 * NN; ++c) {
+          lds_floats(d[c], sv + (8 * (c / 2) + c % 2) * NB * 4);
 #pragma unroll
-          for (int b = 0; b < NB; ++b) top = fmaxf(top, fabsf(d[t][b]));
+          for (int b = 0; b < NB; ++b) most = fmaxf(most, fabsf(d[c][b]));
         }
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-        const int e = max(v_exp, (int)(__float_as_uint(top) >> 23));
-        const float up = pow2_biased(267 - e);  // the largest scale becomes 2^13 .. 2^14
-        const float shift = e - v_exp > 126 ? 0.f : pow2_biased(127 + v_exp - e);
-        v_exp = e;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          keep[r] *= shift;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) s[r][c] *= up;
-        }
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          uint32_t p[4 * R];  // hi of tokens 2 q4 .. (of every row), lo, then of the tokens 8 further
+        most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
+        v_exp = max(v_exp, (int)(__float_as_uint(most) >> 23));
+        const float up = pow2_biased(267 - v_exp);  // the largest scale becomes 2^13 .. 2^14
+        // Classes of p to be taken, class k being 2^(-26 (k + 1)) <= p < 2^(-26 k) (p = 1 in class 0): all of p as class 0
+        // unless it is wide; p below 2^-104 is 0.  Class k is multiplied by 2^(26 k), and the sums' unit goes down as far.
+        constexpr float kClass = 67108864.f;  // 2^26
+        uint32_t classes = 1;
+        if (wide) {
+          classes = 0;
 #pragma unroll
           for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              split2(s[r][2 * h] * d[2 * h][b], s[r][2 * h + 1] * d[2 * h + 1][b], p[2 * R * h + r],
-                     p[2 * R * h + R + r]);
-          uint32_t f[2][4];  // V of tokens (2 q4, 2 q4 + 1) and 8 further, elements 32 b + 4 g + 0..3
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            auto word = [&](int t) {
-              const int vrow = W == 64 ? (t >> 1) | ((t & 1) << 3) : t;
-              const int seg = b ^ ((vrow >> 1) & (W == 64 ? 1 : 3));
-              return lds32(fv + vrow * C::kRowBytes + seg * 32 + g * 4) ^ 0x80808080u;
-            };
-            const uint32_t x = word(8 * h + 2 * q4), y = word(8 * h + 2 * q4 + 1);
-            q8_word_to_f16x2(__byte_perm(x, y, 0x5140), f[h][0], f[h][1]);
-            q8_word_to_f16x2(__byte_perm(x, y, 0x7362), f[h][2], f[h][3]);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float c[4];
-            float(&acc)[OC] = o[4 * b + j];
-            if constexpr (R == 1) {
-              mma_first<true>(c, p[0], p[1], p[2], p[3], f[0][j], f[1][j]);
-              acc[0] = fmaf(acc[0], keep[0], c[0] + c[2]);
-              acc[1] = fmaf(acc[1], keep[0], c[1] + c[3]);
-            } else {
-              mma_first<true>(c, p[0], p[1], p[4], p[5], f[0][j], f[1][j]);
-              mma<true>(c, p[2], p[3], p[6], p[7], f[0][j], f[1][j]);
-#pragma unroll
-              for (int x = 0; x < 4; ++x) acc[x % OC] = fmaf(acc[x % OC], keep[(x / 2) % R], c[x]);
+            for (int c = 0; c < 2 * NN; ++c) {
+              const int k = (126 - (int)(__float_as_uint(s[r][c]) >> 23)) / 26;
+              if (s[r][c] > 0.f && k < 4) classes |= 1u << k;
             }
+          classes = max(__reduce_or_sync(~0u, classes), 1u);  // one at least: what came before takes its factor there
+        }
+#pragma unroll 1
+        while (classes != 0) {
+          const int k = 31 - __clz(classes);
+          classes ^= 1u << k;
+          float w[R][2 * NN];
+          if (!wide) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+              for (int c = 0; c < 2 * NN; ++c) w[r][c] = s[r][c] * up;
+          } else {
+            float factor = 1.f;
+            for (int i26 = 0; i26 < k; ++i26) factor *= kClass;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+              for (int c = 0; c < 2 * NN; ++c) {
+                const float x = s[r][c] * factor;  // of a higher class: 2^26 or more above 1; of a lower: under 2^-26
+                w[r][c] = x >= 1.f / kClass && (x < 1.f || k == 0) ? x * up : 0.f;
+              }
           }
+          const int unit = v_exp - 26 * k, change = o_exp - unit;
+          const float shift = change < -126 ? 0.f : pow2_biased(127 + change);
+          o_exp = unit;
+#pragma unroll
+          for (int x = 0; x < 2 * R; ++x) kept[x] *= shift;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            float c[2][R][4];  // MMA rows g, g + 8 of step j: elements 32 b + 4 g + 2 j, and the next
+#pragma unroll
+            for (int k = 0; k < GR; ++k) {
+              uint32_t f[2][4];  // V of tokens (2 q4, 2 q4 + 1) and 8 further, elements 32 b + 4 g + 0..3
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                auto word = [&](int t) {
+                  const int vrow = W == 64 ? (t & ~15) | ((t >> 1) & 7) | ((t & 1) << 3) : t;
+                  const int seg = b ^ ((vrow >> 1) & (W == 64 ? 1 : 3));
+                  return lds32(fv + vrow * C::kRowBytes + seg * 32 + g * 4) ^ 0x80808080u;
+                };
+                const uint32_t x = word(16 * k + 8 * h + 2 * q4), y = word(16 * k + 8 * h + 2 * q4 + 1);
+                q8_word_to_f16x2(__byte_perm(x, y, 0x5140), f[h][0], f[h][1]);
+                q8_word_to_f16x2(__byte_perm(x, y, 0x7362), f[h][2], f[h][3]);
+              }
+#pragma unroll
+              for (int r = 0; r < R; ++r) {
+                uint32_t hi[2], lo[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const int t = 4 * k + 2 * h;
+                  split2(w[r][t] * d[t][b], w[r][t + 1] * d[t + 1][b], hi[h], lo[h]);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  if (k == 0)
+                    mma_first<true>(c[j][r], f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1], hi[0], hi[1]);
+                  else
+                    mma<true>(c[j][r], f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1], hi[0], hi[1]);
+                  mma<true>(c[j][r], f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1], lo[0], lo[1]);
+                }
+              }
+            }
+            join(o[2 * b], c[0]);
+            join(o[2 * b + 1], c[1]);
+          }
+#pragma unroll
+          for (int x = 0; x < 2 * R; ++x) kept[x] = 1.f;  // of a class still to come
         }
       } else {
-        uint32_t hi[2 * R], mid[2 * R], lo[2 * R];  // of tokens 2 q4 .. and 8 further, by row
+        uint32_t hi[R][NN], mid[R][NN], lo[R][NN];  // of tokens 8 nt + 2 q4, and the next
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            split3(s[r][2 * h], s[r][2 * h + 1], hi[R * h + r], mid[R * h + r], lo[R * h + r]);
+          for (int nt = 0; nt < NN; ++nt)
+            split3(s[r][2 * nt], s[r][2 * nt + 1], hi[r][nt], mid[r][nt], lo[r][nt]);
 #pragma unroll
-        for (int j = 0; j < W / 8; j += 2) {
-          uint32_t w[4];
-          const int t = lane & 15;
-          ldmatrix4_trans(w, fv + t * C::kRowBytes + (((j + (lane >> 4)) ^ (t & 7)) << 4));
+        for (int i16 = 0; i16 < W / 16; ++i16) {  // MMA rows g, g + 8: elements 16 i16 + g, and 8 further
+          float c[R][4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float c[4];
-            float(&acc)[OC] = o[j + h];
-            if constexpr (R == 1) {
-              mma_first<false>(c, hi[0], mid[0], hi[1], mid[1], w[2 * h], w[2 * h + 1]);
-              mma<false>(c, lo[0], 0u, lo[1], 0u, w[2 * h], w[2 * h + 1]);
-              acc[0] = fmaf(acc[0], keep[0], c[0] + c[2]);
-              acc[1] = fmaf(acc[1], keep[0], c[1] + c[3]);
-            } else {
-              mma_first<false>(c, hi[0], hi[1], hi[2 % (2 * R)], hi[3 % (2 * R)], w[2 * h], w[2 * h + 1]);
-              mma<false>(c, mid[0], mid[1], mid[2 % (2 * R)], mid[3 % (2 * R)], w[2 * h], w[2 * h + 1]);
-              mma<false>(c, lo[0], lo[1], lo[2 % (2 * R)], lo[3 % (2 * R)], w[2 * h], w[2 * h + 1]);
+          for (int k = 0; k < GR; ++k) {
+            uint32_t w[4];
+            const int t = 16 * k + (lane & 15);
+            ldmatrix4_trans(w, fv + t * C::kRowBytes + (((2 * i16 + (lane >> 4)) ^ (t & 7)) << 4));
 #pragma unroll
-              for (int x = 0; x < 4; ++x) acc[x % OC] = fmaf(acc[x % OC], keep[(x / 2) % R], c[x]);
+            for (int r = 0; r < R; ++r) {
+              if (k == 0)
+                mma_first<false>(c[r], w[0], w[2], w[1], w[3], hi[r][0], hi[r][1]);
+              else
+                mma<false>(c[r], w[0], w[2], w[1], w[3], hi[r][2 * k], hi[r][2 * k + 1]);
+              mma<false>(c[r], w[0], w[2], w[1], w[3], mid[r][2 * k], mid[r][2 * k + 1]);
+              mma<false>(c[r], w[0], w[2], w[1], w[3], lo[r][2 * k], lo[r][2 * k + 1]);
             }
           }
+          join(o[i16], c);
         }
       }
 
       // ---- the row's or the run's end
       const bool row_ends = at.tile + 1 == at.q.tiles;
       if (row_ends || i + 1 == n) {
-        const float unit = Q8 ? pow2_biased(v_exp - 13) : 1.f;
+        const float unit = Q8 ? (o_exp > 13 ? pow2_biased(o_exp - 13) : 0.f) : 1.f;
         const bool alone = begun_here && row_ends;
         float* part = nullptr;
         if (!alone) {
@@ -835,43 +932,41 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
           float sum = l[r];
           sum += __shfl_xor_sync(~0u, sum, 1);
           sum += __shfl_xor_sync(~0u, sum, 2);
-          const int in_group = at.block * ROWS + 8 * r + g;
-          const int64_t head = (int64_t)at.hk * P.group + in_group;
+          const int in_group = at.block * ROWS + 8 * r + g;  // of the softmax row
+          if (q4 == 0 && in_group < P.group) {
+            if (!alone) {
+              part[ROWS * W + 8 * r + g] = m[r];
+              part[ROWS * W + ROWS + 8 * r + g] = sum;
+            } else if (a.lse != nullptr && col0 == 0) {
+              a.lse[(int64_t)at.s * a.n_q_heads + (int64_t)at.hk * P.group + in_group] =
+                  sum == 0.f ? -INFINITY : (m[r] + __log2f(sum)) * 0.6931471805599453f;
+            }
+          }
           const float f = alone ? (sum == 0.f ? 0.f : __fdividef(unit, sum)) : unit;
-          float* to = alone ? a.out + at.s * a.out_stride + head * D + col0 : part + (8 * r + g) * W;
-          if (in_group < P.group) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {  // the heads of this lane's sums
+            const float fx = __shfl_sync(~0u, f, 8 * q4 + 4 * x);
+            const int row = 8 * r + 2 * q4 + x, of_group = at.block * ROWS + row;
+            float* to = alone ? a.out + at.s * a.out_stride + ((int64_t)at.hk * P.group + of_group) * D + col0 : part + row * W;
+            if (of_group >= P.group) continue;
             if constexpr (Q8) {
 #pragma unroll
               for (int b = 0; b < NB; ++b)
-                if (col0 + 32 * b < D) {
-#pragma unroll
-                  for (int c = 0; c < 2; ++c)
-                    *reinterpret_cast<float4*>(to + 32 * b + 8 * q4 + 4 * c) =
-                        make_float4(o[4 * b][2 * r + c] * f, o[4 * b + 1][2 * r + c] * f, o[4 * b + 2][2 * r + c] * f,
-                                    o[4 * b + 3][2 * r + c] * f);
-                }
+                if (col0 + 32 * b < D)
+                  *reinterpret_cast<float4*>(to + 32 * b + 4 * g) =
+                      make_float4(o[2 * b][4 * r + x] * fx, o[2 * b][4 * r + x + 2] * fx, o[2 * b + 1][4 * r + x] * fx,
+                                  o[2 * b + 1][4 * r + x + 2] * fx);
             } else {
 #pragma unroll
-              for (int j = 0; j < W / 8; ++j)
-                if (col0 + 8 * j < D)
-                  *reinterpret_cast<float2*>(to + 8 * j + 2 * q4) = make_float2(o[j][2 * r] * f, o[j][2 * r + 1] * f);
-            }
-            if (q4 == 0) {
-              if (alone) {
-                if (a.lse != nullptr && col0 == 0)
-                  a.lse[(int64_t)at.s * a.n_q_heads + head] =
-                      sum == 0.f ? -INFINITY : (m[r] + __log2f(sum)) * 0.6931471805599453f;
-              } else {
-                part[ROWS * W + 8 * r + g] = m[r];
-                part[ROWS * W + ROWS + 8 * r + g] = sum;
-              }
+              for (int c8 = 0; c8 < W / 8; ++c8)
+                if (col0 + 8 * c8 < D) to[8 * c8 + g] = o[c8 / 2][4 * r + x + 2 * (c8 % 2)] * fx;
             }
           }
         }
       }
       stage = stage + 1 == S ? 0 : stage + 1;
       if (i + 1 < n) {
-        advance(at, P);
+        advance<T>(at, P);
         if (at.tile == 0) begun_here = fresh = true;
       }
     }

@@ -39,7 +39,7 @@ cudaError_t prepare_kv_attend(const KvAttendArgs& a, int num_sms, void* ws, size
   p.group = a.n_q_heads / a.kv.n_heads;
   p.blocks = (p.group + (wide ? 15 : 7)) / (wide ? 16 : 8);
   p.q_scale = a.scale * 1.4426950408889634f;
-  // Simple copies: pages of whole tiles; strides of 32 bits; a token's scales copied as 16 bytes (8 for heads of
+  // Simple copies: pages of whole groups of 16 tokens; strides of 32 bits; a token's scales copied as 16 bytes (8 for heads of
   // 64) where they are aligned and all of a padded row exists
   const KvView& kv = a.kv;
   const bool q8 = kv.format == IL_Q8;
@@ -50,7 +50,7 @@ cudaError_t prepare_kv_attend(const KvAttendArgs& a, int num_sms, void* ws, size
   };
   const auto even = [&](int64_t stride) { return stride % unit == 0; };
   const uintptr_t bases = reinterpret_cast<uintptr_t>(kv.k_scale) | reinterpret_cast<uintptr_t>(kv.v_scale);
-  p.simple = kv.page_size % attend::kTile == 0 && fits(kv.page * es, kv.token * es, kv.head * es);
+  p.simple = kv.page_size % attend::kGroup == 0 && fits(kv.page * es, kv.token * es, kv.head * es);
   if (q8 && p.simple)
     p.simple = kv.head_dim == dim && fits(kv.spage * 4, kv.stoken * 4, kv.shead * 4) && bases % (4 * unit) == 0 &&
                even(kv.spage) && even(kv.stoken) && even(kv.shead);
