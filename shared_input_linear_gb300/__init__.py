@@ -225,7 +225,9 @@ def weight_bytes(w: Weight) -> int:
 def _stream_ptr(stream) -> int:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle of torch.cuda.current_stream() without the object (3 us on the host)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return torch.cuda.current_stream().cuda_stream if raw is None else raw(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -393,34 +395,35 @@ def kv_cache(fmt, n_pages: int, page_size: int, n_heads: int, head_dim: int, dev
     return KVCache(*kv, *([pool(head_dim // 32, torch.float32) for _ in range(2)] if q8 else []))
 
 
-def _ptr(t, dtype, numel=None, what="an argument"):
-    """Address of a contiguous CUDA tensor of ``dtype`` (0 for None)."""
+def _ptr(t, dtype, numel, what: str):
+    """Address of a contiguous CUDA tensor of ``dtype`` and ``numel`` elements (0 for None)."""
     if t is None:
         return 0
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or (numel is not None and t.numel() != numel):
-        raise ILError(-1, f"{what} must be a contiguous CUDA {dtype} tensor" + (f" of {numel}" if numel is not None else ""))
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != numel:
+        raise ILError(-1, f"{what} must be a contiguous CUDA {dtype} tensor of {numel} elements")
     return t.data_ptr()
 
 
-def _rows(t, heads: int, dim: int, what: str):
+def _rows(t, n: int, heads: int, dim: int, f32, what: str):
     """(address, row stride) of fp32 ``[n][heads][dim]`` (or ``[n][heads*dim]``) whose rows are contiguous."""
-    import torch
     shape, st = t.shape, t.stride()
-    if len(shape) == 3:
-        ok = shape[1] == heads and shape[2] == dim and st[2] == 1 and (heads == 1 or st[1] == dim)
+    if shape == (n, heads, dim):
+        ok = st[2] == 1 and (st[1] == dim or heads == 1)
     else:
-        ok = len(shape) == 2 and shape[1] == heads * dim and st[1] == 1
-    if not ok or t.dtype is not torch.float32 or not t.is_cuda:
-        raise ILError(-1, f"{what} must be CUDA float32 [n][{heads}][{dim}] with contiguous rows")
+        ok = shape == (n, heads * dim) and st[1] == 1
+    if not ok or t.dtype is not f32 or not t.is_cuda:
+        if shape[1:] in ((heads, dim), (heads * dim,)) and shape[0] != n:
+            raise ILError(-2, f"{what} has {shape[0]} rows, not {n}")
+        raise ILError(-1, f"{what} must be CUDA float32 [{n}][{heads}][{dim}] with contiguous rows")
     return t.data_ptr(), st[0]
 
 
-def _table(t, n_seq: int):
+def _table(t, n_seq: int, i32):
     """(address, row stride, width) of an int32 block table."""
-    import torch
-    if t.dim() != 2 or t.dtype is not torch.int32 or not t.is_cuda or t.shape[0] != n_seq or t.stride(1) != 1:
+    shape, st = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != n_seq or st[1] != 1 or t.dtype is not i32 or not t.is_cuda:
         raise ILError(-1, f"table must be CUDA int32 [{n_seq}][width] with contiguous rows")
-    return t.data_ptr(), t.stride(0), t.shape[1]
+    return t.data_ptr(), st[0], shape[1]
 
 
 def kv_extend(lens, add, table, ring, cursor, page_size: int, slots, lens_out=None, cursor_out=None, positions=None,
@@ -435,39 +438,43 @@ def kv_extend(lens, add, table, ring, cursor, page_size: int, slots, lens_out=No
     """
     import torch
     i32, i64 = torch.int32, torch.int64
-    n = lens.numel()
-    tp, ts, tw = _table(table, n)
-    most = slots.numel()
-    lp, cp = _ptr(lens, i32, None, "lens"), _ptr(cursor, i64, 2, "cursor")
-    _check(load().il_kv_extend(
-        n, page_size, lp, _ptr(add, i32, n, "add"), tp, ts, tw, _ptr(ring, i32, None, "ring"), ring.numel(), cp,
+    n, most = lens.numel(), slots.numel()
+    tp, ts, tw = _table(table, n, i32)
+    size = ring.numel()
+    lp, cp = _ptr(lens, i32, n, "lens"), _ptr(cursor, i64, 2, "cursor")
+    rc = (_lib or load()).il_kv_extend(
+        n, page_size, lp, _ptr(add, i32, n, "add"), tp, ts, tw, _ptr(ring, i32, size, "ring"), size, cp,
         lp if lens_out is None else _ptr(lens_out, i32, n, "lens_out"),
         cp if cursor_out is None else _ptr(cursor_out, i64, 2, "cursor_out"),
-        _ptr(slots, i32, None, "slots"), most, _ptr(positions, i32, most, "positions"), _ptr(first, i32, n + 1, "first"),
-        _ptr(info, i64, 4, "info"), _stream_ptr(stream)))
+        _ptr(slots, i32, most, "slots"), most, _ptr(positions, i32, most, "positions"), _ptr(first, i32, n + 1, "first"),
+        _ptr(info, i64, 4, "info"), _stream_ptr(stream))
+    if rc:
+        _check(rc)
 
 
 def kv_append(cache: KVCache, k, v, slots, stream=None) -> None:
     """``il_kv_append``: fp32 rows ``k``, ``v`` ``[n][n_heads][head_dim]`` into the cache's ``slots``
     (int32 ``[n]``; a negative one is skipped).  The rows may be columns of a wider tensor."""
     import torch
-    n = slots.numel()
-    kp, ks = _rows(k, cache.n_heads, cache.head_dim, "k")
-    vp, vs = _rows(v, cache.n_heads, cache.head_dim, "v")
-    if k.shape[0] != n or v.shape[0] != n:
-        raise ILError(-2, "k, v and slots must have the same number of tokens")
-    _check(load().il_kv_append(cache._ref, kp, ks, vp, vs, _ptr(slots, torch.int32, n, "slots"), n, _stream_ptr(stream)))
+    n, heads, dim, f32 = slots.numel(), cache.n_heads, cache.head_dim, torch.float32
+    kp, ks = _rows(k, n, heads, dim, f32, "k")
+    vp, vs = _rows(v, n, heads, dim, f32, "v")
+    rc = (_lib or load()).il_kv_append(cache._ref, kp, ks, vp, vs, _ptr(slots, torch.int32, n, "slots"), n,
+                                       _stream_ptr(stream))
+    if rc:
+        _check(rc)
 
 
 def kv_read(cache: KVCache, slots, k, v, stream=None) -> None:
     """``il_kv_read``: the cached values of ``slots`` as fp32 into ``k`` and ``v`` (as for :func:`kv_append`)."""
     import torch
-    n = slots.numel()
-    kp, ks = _rows(k, cache.n_heads, cache.head_dim, "k")
-    vp, vs = _rows(v, cache.n_heads, cache.head_dim, "v")
-    if k.shape[0] != n or v.shape[0] != n:
-        raise ILError(-2, "k, v and slots must have the same number of tokens")
-    _check(load().il_kv_read(cache._ref, _ptr(slots, torch.int32, n, "slots"), n, kp, ks, vp, vs, _stream_ptr(stream)))
+    n, heads, dim, f32 = slots.numel(), cache.n_heads, cache.head_dim, torch.float32
+    kp, ks = _rows(k, n, heads, dim, f32, "k")
+    vp, vs = _rows(v, n, heads, dim, f32, "v")
+    rc = (_lib or load()).il_kv_read(cache._ref, _ptr(slots, torch.int32, n, "slots"), n, kp, ks, vp, vs,
+                                     _stream_ptr(stream))
+    if rc:
+        _check(rc)
 
 
 def kv_attend(cache: KVCache, q, table, lens, out, lse=None, scale=None, window: int = 0, stream=None) -> None:
@@ -479,16 +486,16 @@ def kv_attend(cache: KVCache, q, table, lens, out, lse=None, scale=None, window:
     import torch
     if q.dim() != 3:
         raise ILError(-1, "q must be [n_seq][n_q_heads][head_dim]")
-    n, heads = q.shape[0], q.shape[1]
-    dim = cache.head_dim
-    qp, qs = _rows(q, heads, dim, "q")
-    op, os_ = _rows(out, heads, dim, "out")
-    if out.shape[0] != n:
-        raise ILError(-2, "q and out must have the same number of sequences")
-    tp, ts, tw = _table(table, n)
-    _check(load().il_kv_attend(cache._ref, qp, qs, tp, ts, tw, _ptr(lens, torch.int32, n, "lens"), n, heads,
-                               dim ** -0.5 if scale is None else scale, window, op, os_,
-                               _ptr(lse, torch.float32, n * heads, "lse"), _stream_ptr(stream)))
+    n, heads, _ = q.shape
+    dim, f32, i32 = cache.head_dim, torch.float32, torch.int32
+    qp, qs = _rows(q, n, heads, dim, f32, "q")
+    op, os_ = _rows(out, n, heads, dim, f32, "out")
+    tp, ts, tw = _table(table, n, i32)
+    rc = (_lib or load()).il_kv_attend(cache._ref, qp, qs, tp, ts, tw, _ptr(lens, i32, n, "lens"), n, heads,
+                                       dim ** -0.5 if scale is None else scale, window, op, os_,
+                                       _ptr(lse, f32, n * heads, "lse"), _stream_ptr(stream))
+    if rc:
+        _check(rc)
 
 
 def check_device_status(stream=None) -> None:
