@@ -345,6 +345,22 @@ cudaError_t prepare_lmhead(const float* x, int h, const float* cl, int n_cent, i
 // ---------------------------------------------------------------------------
 constexpr unsigned kStatusBadSlot = 0x200;  // status word: a page or slot outside the cache was skipped
 constexpr int kMaxKvSeqs = 65536;
+
+// Division of t < 2^31 by a number of the launch, 1 <= d <= 2^31: with l = ceil(log2 d), floor(t / d) is
+// the high word of t * (2^32 + m) shifted by l, m = floor(2^32 (2^l - d) / d) + 1 (Granlund and
+// Montgomery, "Division by invariant integers using multiplication").
+struct FastDiv {
+  uint32_t m = 1, s = 0, d = 1;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t by) : d(by) {
+    while ((1ull << s) < by) ++s;
+    m = (uint32_t)((((1ull << s) - by) << 32) / by + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ uint32_t of(uint32_t t) const { return (__umulhi(m, t) + t) >> s; }
+#endif
+};
+
 constexpr int kMaxKvDim = 256;
 
 // The cache as the kernels see it: il_kv checked, the strides of dimensions of extent 1 set to 0.

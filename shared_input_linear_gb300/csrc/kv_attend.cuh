@@ -48,7 +48,7 @@ struct KvAttendPlan {
   KvAttendArgs a;
   int cap;                // longest length: table_width * page_size, at most 2^31 - 1
   int window;             // 0: all
-  uint32_t div_m, div_s;  // t / page_size = (mulhi(div_m, t) + t) >> div_s
+  FastDiv by_page;        // t / page_size
   int group;              // query heads of a K/V head
   int blocks;             // blocks of 8 R query heads of a K/V head
   float q_scale;          // scale * log2(e)
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
     constexpr int SB = NB * 4 > 16 ? 16 : NB * 4;
 
     auto token_of = [&](const Walk& w) { return (w.q.first + w.tile) * T + (lane & (T - 1)); };
-    auto column_of = [&](uint32_t t) { return (__umulhi(P.div_m, t) + t) >> P.div_s; };
+    auto column_of = [&](uint32_t t) { return P.by_page.of(t); };
     auto page_of = [&](const Walk& w) {  // page of this lane's token of the tile (of 16 tokens, lanes 16-31 repeat 0-15)
       const uint32_t t = token_of(w);
       return t >= w.q.begin && t < w.q.len ? a.table[w.s * a.table_stride + column_of(t)] : -1;

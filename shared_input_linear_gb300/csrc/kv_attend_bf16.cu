@@ -26,16 +26,11 @@ size_t kv_attend_workspace_bytes(const KvAttendArgs& a, int num_sms) {
 cudaError_t prepare_kv_attend(const KvAttendArgs& a, int num_sms, void* ws, size_t ws_bytes, Launch* out) {
   if (num_sms > kSplitCounters || ws_bytes < kv_attend_workspace_bytes(a, num_sms)) return cudaErrorInvalidValue;
   const bool wide = wide_block(a);
-  KvAttendPlan p;
-  memset(&p, 0, sizeof p);
+  KvAttendPlan p{};
   p.a = a;
   p.cap = (int)std::min<int64_t>(a.table_width * a.kv.page_size, INT32_MAX);
   p.window = (int)std::min<int64_t>(a.window, INT32_MAX);
-  // exact division of t < 2^31 by page_size: with l = ceil(log2 d), floor(t / d) is the high
-  // word of t * (2^32 + m) shifted by l, m = floor(2^32 (2^l - d) / d) + 1 (Granlund and Montgomery)
-  const uint64_t d = (uint64_t)a.kv.page_size;
-  while ((1ull << p.div_s) < d) ++p.div_s;
-  p.div_m = (uint32_t)((((1ull << p.div_s) - d) << 32) / d + 1);
+  p.by_page = FastDiv((uint32_t)a.kv.page_size);
   p.group = a.n_q_heads / a.kv.n_heads;
   p.blocks = (p.group + (wide ? 15 : 7)) / (wide ? 16 : 8);
   p.q_scale = a.scale * 1.4426950408889634f;

@@ -221,20 +221,58 @@ __global__ void __launch_bounds__(kExtendThreads) kv_extend_kernel(const KvExten
 // ---------------------------------------------------------------------------
 // il_kv_append / il_kv_read
 // ---------------------------------------------------------------------------
-// One thread moves 8 elements of K and the same 8 of V (32 bytes of fp32 and 16 or 8 of the cache
-// each).  Q8: the four lanes of a 32-element block share its largest |w| with two shuffles;
-// d = amax / 127 and w / d are IEEE divisions, so that q is the definition's in every tie.
-// Bound by HBM.
+// One thread moves units of 8 elements of K and the same 8 of V (32 bytes of fp32 and 16 or 8 of the cache each).
+// Bound by HBM; at Q8 the arithmetic comes near it, so that:
+// - q = round(w / d) is taken from w times an approximate 1 / d, which is off by at most 127 * (2^-23 + 2^-23) =
+//   3.1e-5, and by the definition's division only where the product lies within 5e-5 of half way between integers;
+// - a float's integer is read from its low byte after adding 1.5 * 2^23, and made from a byte by the reverse;
+// - the four lanes of a 32-element block share its largest |w| with two shuffles; d = amax / 127 is the IEEE
+//   division, so that d and q are the definition's bit for bit.
 constexpr int kRowThreads = 256;
+// Units of a thread at a time: two, all loads first, but for Q8's quantiser, where more warps hide its chains
+// better (4097 tokens of 8 x 128: 13.0 us with two, 11.0 us with one; bf16 append 9.6 and 9.2, Q8 read of
+// 16384 28.8 and 31.1).
+constexpr int row_units(bool write, bool q8) { return write && q8 ? 1 : 2; }
 
 struct RowArgs {
   KvView kv;
   float *k, *v;
   int64_t k_stride, v_stride;
   const int32_t* slots;
-  int64_t n;
+  int64_t n, run;                        // tokens, tokens whose units 31 bits count
+  FastDiv per_token, per_head, by_page;  // units of a token and of a head
+  int whole;                             // a unit's 32 bytes of fp32 are aligned: one access
   unsigned* status;
 };
+
+struct Eight {
+  float4 lo, hi;
+};
+
+// 32 bytes of fp32: one access where they are aligned (two 16-byte stores each cover half of every sector).
+__device__ __forceinline__ Eight load8(const float* p, bool whole) {
+  Eight e;
+  if (whole) {
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(e.lo.x), "=f"(e.lo.y), "=f"(e.lo.z), "=f"(e.lo.w), "=f"(e.hi.x), "=f"(e.hi.y), "=f"(e.hi.z), "=f"(e.hi.w)
+                 : "l"(p)
+                 : "memory");
+  } else {
+    e.lo = reinterpret_cast<const float4*>(p)[0];
+    e.hi = reinterpret_cast<const float4*>(p)[1];
+  }
+  return e;
+}
+__device__ __forceinline__ void store8(float* p, const Eight& e, bool whole) {
+  if (whole) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(e.lo.x), "f"(e.lo.y), "f"(e.lo.z),
+                 "f"(e.lo.w), "f"(e.hi.x), "f"(e.hi.y), "f"(e.hi.z), "f"(e.hi.w)
+                 : "memory");
+  } else {
+    reinterpret_cast<float4*>(p)[0] = e.lo;
+    reinterpret_cast<float4*>(p)[1] = e.hi;
+  }
+}
 
 // max that gives NaN where an operand is NaN
 __device__ __forceinline__ float max_nan(float x, float y) {
@@ -248,13 +286,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-__device__ __forceinline__ void write8(const float4& x, const float4& y, __nv_bfloat16* to) {
+__device__ __forceinline__ void write8(const Eight& e, __nv_bfloat16* to) {
+  const float4 &x = e.lo, &y = e.hi;
   *reinterpret_cast<uint4*>(to) =
       make_uint4(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w), pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
 }
 
-__device__ __forceinline__ void write8(const float4& x, const float4& y, int8_t* to, float* scale, unsigned quad,
-                                       bool first_of_block) {
+constexpr float kToInt = 12582912.f;  // 1.5 * 2^23
+
+__device__ __forceinline__ void write8(const Eight& e, int8_t* to, float* scale, unsigned quad, bool first_of_block) {
+  const float4 &x = e.lo, &y = e.hi;
   const float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
   float m = 0.f;
 #pragma unroll
@@ -262,80 +303,118 @@ __device__ __forceinline__ void write8(const float4& x, const float4& y, int8_t*
   m = max_nan(m, __shfl_xor_sync(quad, m, 1));
   m = max_nan(m, __shfl_xor_sync(quad, m, 2));
   const float d = __fdiv_rn(m, 127.0f);
-  const bool normal = d > 0.f && d < __int_as_float(0x7f800000);  // otherwise q = 0 (and d = 0, NaN or infinity)
-  uint32_t b[2] = {0, 0};
-  if (normal) {
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(d));
+  uint32_t f[8];
+  uint32_t unsure = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int q = (int)fminf(fmaxf(rintf(__fdiv_rn(w[i], d)), -127.f), 127.f);
-      b[i / 4] |= (uint32_t)(q & 0xff) << (8 * (i % 4));
-    }
+  for (int i = 0; i < 8; ++i) {
+    const float t = w[i] * inv, r = t + kToInt;
+    f[i] = __float_as_uint(r);
+    if (!(fabsf(t - (r - kToInt)) < 0.49995f)) unsure |= 1u << i;  // NaN too
   }
-  *reinterpret_cast<uint2*>(to) = make_uint2(b[0], b[1]);
+  const bool normal = d > 0.f && d < __int_as_float(0x7f800000);  // otherwise q = 0 (and d = 0, NaN or infinity)
+#pragma unroll 1
+  while (unsure != 0) {
+    const int i = __ffs(unsure) - 1;
+    unsure &= unsure - 1;
+    float v = w[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) v = j == i ? w[j] : v;
+    const uint32_t q = normal ? (uint32_t)(int)fminf(fmaxf(rintf(__fdiv_rn(v, d)), -127.f), 127.f) : 0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = j == i ? q : f[j];
+  }
+  auto word = [&](int i) {
+    return __byte_perm(__byte_perm(f[i], f[i + 1], 0x0040), __byte_perm(f[i + 2], f[i + 3], 0x0040), 0x5410);
+  };
+  *reinterpret_cast<uint2*>(to) = make_uint2(word(0), word(4));
   if (first_of_block) *scale = d;
 }
 
-__device__ __forceinline__ void read8(const __nv_bfloat16* from, float* to) {
-  const uint4 u = *reinterpret_cast<const uint4*>(from);
-  *reinterpret_cast<float4*>(to) = make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
-  *reinterpret_cast<float4*>(to + 4) = make_float4(bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w));
+__device__ __forceinline__ Eight read8(const uint4& u, float) {
+  return {make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y)),
+          make_float4(bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w))};
 }
 
-__device__ __forceinline__ void read8(const int8_t* from, float d, float* to) {
-  const uint2 u = *reinterpret_cast<const uint2*>(from);
-  auto val = [&](uint32_t word, int i) { return d * (float)(int8_t)(word >> (8 * i)); };
-  *reinterpret_cast<float4*>(to) = make_float4(val(u.x, 0), val(u.x, 1), val(u.x, 2), val(u.x, 3));
-  *reinterpret_cast<float4*>(to + 4) = make_float4(val(u.y, 0), val(u.y, 1), val(u.y, 2), val(u.y, 3));
+__device__ __forceinline__ Eight read8(const uint2& u, float d) {
+  auto four = [&](uint32_t word) {
+    const uint32_t b = word ^ 0x80808080u;  // q + 128
+    auto one = [&](uint32_t sel) { return d * (__uint_as_float(__byte_perm(b, 0x4b000000u, sel)) - 8388736.f); };
+    return make_float4(one(0x7440), one(0x7441), one(0x7442), one(0x7443));
+  };
+  return {four(u.x), four(u.y)};
 }
 
 template <bool WRITE, bool Q8>
-__global__ void __launch_bounds__(kRowThreads) kv_rows_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(kRowThreads, WRITE && Q8 ? 5 : 4) kv_rows_kernel(const RowArgs a) {
   using T = typename std::conditional<Q8, int8_t, __nv_bfloat16>::type;
+  constexpr int kRowUnits = row_units(WRITE, Q8);
+  using Cached = typename std::conditional<Q8, uint2, uint4>::type;  // 8 elements
   grid_dep_launch();
   grid_dep_wait();
   const KvView& kv = a.kv;
-  const uint32_t per_head = (uint32_t)kv.head_dim / 8, per_token = per_head * kv.n_heads;
   const unsigned quad = 0xfu << (threadIdx.x & 28);
-  // tokens in runs whose 8-element units 31 bits count
-  const int64_t run = max((int64_t)1, (int64_t)(0x7fffffffu / per_token) - 1);
-  for (int64_t t0 = 0; t0 < a.n; t0 += run) {
-    const uint32_t units = (uint32_t)min(run, a.n - t0) * per_token;
-    for (uint32_t u = blockIdx.x * kRowThreads + threadIdx.x; u < units; u += gridDim.x * kRowThreads) {
-      const uint32_t t = u / per_token, in_token = u - t * per_token;
-      const uint32_t head = in_token / per_head, i = 8 * (in_token - head * per_head);
-      const int32_t slot = a.slots[t0 + t];
-      float* k = a.k + (t0 + t) * a.k_stride + (int64_t)head * kv.head_dim + i;
-      float* v = a.v + (t0 + t) * a.v_stride + (int64_t)head * kv.head_dim + i;
-      if (slot < 0 || slot >= kv.n_slots) {
-        if (slot >= 0) atomicOr(a.status, kStatusBadSlot);
-        if (!WRITE) {
-          const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-          reinterpret_cast<float4*>(k)[0] = reinterpret_cast<float4*>(k)[1] = z;
-          reinterpret_cast<float4*>(v)[0] = reinterpret_cast<float4*>(v)[1] = z;
+  const uint32_t step = gridDim.x * kRowThreads;
+  for (int64_t t0 = 0; t0 < a.n; t0 += a.run) {
+    const uint32_t units = (uint32_t)min(a.run, a.n - t0) * a.per_token.d;
+    for (uint32_t first = blockIdx.x * kRowThreads + threadIdx.x; first < units; first += kRowUnits * step) {
+      float *k[kRowUnits], *v[kRowUnits];
+      int64_t off[kRowUnits], soff[kRowUnits];
+      bool live[kRowUnits], block_start[kRowUnits];
+      Eight x[WRITE ? kRowUnits : 1][2];
+      Cached c[WRITE ? 1 : kRowUnits][2];
+      float d[kRowUnits][2];
+#pragma unroll
+      for (int j = 0; j < kRowUnits; ++j) {
+        const bool in = first + j * step < units;
+        const uint32_t u = in ? first + j * step : first;
+        const uint32_t t = a.per_token.of(u), in_token = u - t * a.per_token.d;
+        const uint32_t head = a.per_head.of(in_token), i = 8 * (in_token - head * a.per_head.d);
+        const int32_t slot = in ? a.slots[t0 + t] : -1;
+        live[j] = slot >= 0 && slot < kv.n_slots;
+        if (slot >= kv.n_slots) atomicOr(a.status, kStatusBadSlot);
+        k[j] = in ? a.k + (t0 + t) * a.k_stride + (int64_t)head * kv.head_dim + i : nullptr;
+        v[j] = a.v + (t0 + t) * a.v_stride + (int64_t)head * kv.head_dim + i;
+        const uint32_t page = a.by_page.of((uint32_t)max(slot, 0)), at = (uint32_t)slot - page * a.by_page.d;
+        off[j] = page * kv.page + at * kv.token + (int64_t)head * kv.head + i;
+        soff[j] = Q8 ? page * kv.spage + at * kv.stoken + (int64_t)head * kv.shead + i / 32 : 0;
+        block_start[j] = i % 32 == 0;
+        if (live[j]) {
+          if constexpr (WRITE) {
+            x[j][0] = load8(k[j], a.whole);
+            x[j][1] = load8(v[j], a.whole);
+          } else {
+            c[j][0] = *reinterpret_cast<const Cached*>(reinterpret_cast<const T*>(kv.k) + off[j]);
+            c[j][1] = *reinterpret_cast<const Cached*>(reinterpret_cast<const T*>(kv.v) + off[j]);
+            if constexpr (Q8) d[j][0] = kv.k_scale[soff[j]], d[j][1] = kv.v_scale[soff[j]];
+          }
         }
-        continue;
       }
-      const int64_t page = (uint32_t)slot / (uint32_t)kv.page_size, at = slot - page * kv.page_size;
-      const int64_t off = page * kv.page + at * kv.token + (int64_t)head * kv.head + i;
-      T* ck = reinterpret_cast<T*>(kv.k) + off;
-      T* cv = reinterpret_cast<T*>(kv.v) + off;
-      const int64_t soff = Q8 ? page * kv.spage + at * kv.stoken + (int64_t)head * kv.shead + i / 32 : 0;
-      if constexpr (WRITE) {
-        const float4 k0 = reinterpret_cast<const float4*>(k)[0], k1 = reinterpret_cast<const float4*>(k)[1];
-        const float4 v0 = reinterpret_cast<const float4*>(v)[0], v1 = reinterpret_cast<const float4*>(v)[1];
-        if constexpr (Q8) {
-          write8(k0, k1, ck, kv.k_scale + soff, quad, i % 32 == 0);
-          write8(v0, v1, cv, kv.v_scale + soff, quad, i % 32 == 0);
-        } else {
-          write8(k0, k1, ck);
-          write8(v0, v1, cv);
+#pragma unroll
+      for (int j = 0; j < kRowUnits; ++j) {
+        if (!live[j]) {
+          if (!WRITE && k[j] != nullptr) {
+            const Eight z = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+            store8(k[j], z, a.whole);
+            store8(v[j], z, a.whole);
+          }
+          continue;
         }
-      } else if constexpr (Q8) {
-        read8(ck, kv.k_scale[soff], k);
-        read8(cv, kv.v_scale[soff], v);
-      } else {
-        read8(ck, k);
-        read8(cv, v);
+        if constexpr (WRITE) {
+          T* const ck = reinterpret_cast<T*>(kv.k) + off[j];
+          T* const cv = reinterpret_cast<T*>(kv.v) + off[j];
+          if constexpr (Q8) {
+            write8(x[j][0], ck, kv.k_scale + soff[j], quad, block_start[j]);
+            write8(x[j][1], cv, kv.v_scale + soff[j], quad, block_start[j]);
+          } else {
+            write8(x[j][0], ck);
+            write8(x[j][1], cv);
+          }
+        } else {
+          store8(k[j], read8(c[j][0], d[j][0]), a.whole);
+          store8(v[j], read8(c[j][1], d[j][1]), a.whole);
+        }
       }
     }
   }
@@ -357,12 +436,19 @@ cudaError_t prepare_kv_extend(const KvExtendArgs& a, int num_sms, Launch* out) {
 cudaError_t prepare_kv_rows(bool write, const KvView& kv, float* k, int64_t k_stride, float* v, int64_t v_stride,
                             const int32_t* slots, int64_t n, unsigned* status, int num_sms, Launch* out) {
   const bool q8 = kv.format == IL_Q8;
-  const RowArgs a = {kv, k, v, k_stride, v_stride, slots, n, status};
+  const uint32_t per_head = (uint32_t)kv.head_dim / 8, per_token = per_head * kv.n_heads;
+  // runs of tokens whose units (and a grid's step beyond them) 31 bits count
+  const int64_t run = std::max<int64_t>(1, (int64_t)((0x7fffffffu - (1u << 24)) / per_token));
+  const RowArgs a = {kv, k, v, k_stride, v_stride, slots, n, run, FastDiv(per_token), FastDiv(per_head),
+                     FastDiv((uint32_t)kv.page_size),
+                     (reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % 32 == 0 &&
+                         (n == 1 || (k_stride % 8 == 0 && v_stride % 8 == 0)),
+                     status};
   out->fn = write ? (q8 ? reinterpret_cast<const void*>(kv_rows_kernel<true, true>)
                         : reinterpret_cast<const void*>(kv_rows_kernel<true, false>))
                   : (q8 ? reinterpret_cast<const void*>(kv_rows_kernel<false, true>)
                         : reinterpret_cast<const void*>(kv_rows_kernel<false, false>));
-  const int64_t units = n * kv.n_heads * (kv.head_dim / 8);
+  const int64_t units = n * per_token;  // one a thread while that fills the GPU's threads less than once
   out->grid = dim3((unsigned)std::min<int64_t>((units + kRowThreads - 1) / kRowThreads, (int64_t)num_sms * 8));
   out->block = dim3(kRowThreads);
   if (!out->set_args(a)) return cudaErrorMemoryAllocation;
