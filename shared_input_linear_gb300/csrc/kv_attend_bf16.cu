@@ -33,6 +33,7 @@ cudaError_t prepare_kv_attend(const KvAttendArgs& a, int num_sms, void* ws, size
   p.by_page = FastDiv((uint32_t)a.kv.page_size);
   p.group = a.n_q_heads / a.kv.n_heads;
   p.blocks = (p.group + (wide ? 15 : 7)) / (wide ? 16 : 8);
+  p.by_blocks = FastDiv((uint32_t)p.blocks);
   p.q_scale = a.scale * 1.4426950408889634f;
   // Simple copies: pages of whole groups of 16 tokens; strides of 32 bits; a token's scales copied as 16 bytes (8 for heads of
   // 64) where they are aligned and all of a padded row exists
