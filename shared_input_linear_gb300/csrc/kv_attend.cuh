@@ -155,18 +155,18 @@ template <bool F16>
 __device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
   if constexpr (F16)
-    asm volatile(IL_MMA("f16", "%10", "%10", "%10", "%10")
+    asm(IL_MMA("f16", "%10", "%10", "%10", "%10")
                  : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
   else
-    asm volatile(IL_MMA("bf16", "%10", "%10", "%10", "%10")
+    asm(IL_MMA("bf16", "%10", "%10", "%10", "%10")
                  : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // d = c + A B (fp16)
 __device__ __forceinline__ void mma_from(float (&d)[4], float c0, float c1, float c2, float c3, uint32_t a0, uint32_t a1,
                                          uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(IL_MMA("f16", "%10", "%11", "%12", "%13")
+  asm(IL_MMA("f16", "%10", "%11", "%12", "%13")
                : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
@@ -174,11 +174,11 @@ template <bool F16>
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
   if constexpr (F16)
-    asm volatile(IL_MMA("f16", "%0", "%1", "%2", "%3")
+    asm(IL_MMA("f16", "%0", "%1", "%2", "%3")
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile(IL_MMA("bf16", "%0", "%1", "%2", "%3")
+    asm(IL_MMA("bf16", "%0", "%1", "%2", "%3")
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -824,43 +824,9 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
         most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
         v_exp = max(v_exp, (int)(__float_as_uint(most) >> 23));
         const float up = pow2_biased(267 - v_exp);  // the largest scale becomes 2^13 .. 2^14
-        // Classes of p to be taken, class k being 2^(-26 (k + 1)) <= p < 2^(-26 k) (p = 1 in class 0): all of p as class 0
-        // unless it is wide; p below 2^-104 is 0.  Class k is multiplied by 2^(26 k), and the sums' unit goes down as far.
-        constexpr float kClass = 67108864.f;  // 2^26
-        uint32_t classes = 1;
-        if (wide) {
-          classes = 0;
-#pragma unroll
-          for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int c = 0; c < 2 * NN; ++c) {
-              const int k = (126 - (int)(__float_as_uint(s[r][c]) >> 23)) / 26;
-              if (s[r][c] > 0.f && k < 4) classes |= 1u << k;
-            }
-          classes = max(__reduce_or_sync(~0u, classes), 1u);  // one at least: what came before takes its factor there
-        }
-#pragma unroll 1
-        while (classes != 0) {
-          const int k = 31 - __clz(classes);
-          classes ^= 1u << k;
-          float w[R][2 * NN];
-          if (!wide) {
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-              for (int c = 0; c < 2 * NN; ++c) w[r][c] = s[r][c] * up;
-          } else {
-            float factor = 1.f;
-            for (int i26 = 0; i26 < k; ++i26) factor *= kClass;
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-              for (int c = 0; c < 2 * NN; ++c) {
-                const float x = s[r][c] * factor;  // of a higher class: 2^26 or more above 1; of a lower: under 2^-26
-                w[r][c] = x >= 1.f / kClass && (x < 1.f || k == 0) ? x * up : 0.f;
-              }
-          }
-          const int unit = v_exp - 26 * k, change = o_exp - unit;
+        // Products of weights w, with the sums' unit moved to the biased exponent `unit`.
+        auto products = [&](const float (&w)[R][2 * NN], int unit) {
+          const int change = o_exp - unit;
           const float shift = change < -126 ? 0.f : pow2_biased(127 + change);
           o_exp = unit;
 #pragma unroll
@@ -903,8 +869,44 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
             join(o[2 * b], c[0]);
             join(o[2 * b + 1], c[1]);
           }
+        };
+        float w[R][2 * NN];
+        if (!wide) {
 #pragma unroll
-          for (int x = 0; x < 2 * R; ++x) kept[x] = 1.f;  // of a class still to come
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int c = 0; c < 2 * NN; ++c) w[r][c] = s[r][c] * up;
+          products(w, v_exp);
+        } else {
+          // Classes of p, class k being 2^(-26 (k + 1)) <= p < 2^(-26 k) (p = 1 in class 0); p below 2^-104 is 0.  Class k is
+          // multiplied by 2^(26 k), and the sums' unit goes down as far.
+          constexpr float kClass = 67108864.f;  // 2^26
+          uint32_t classes = 0;
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int c = 0; c < 2 * NN; ++c) {
+              const int k = (126 - (int)(__float_as_uint(s[r][c]) >> 23)) / 26;
+              if (s[r][c] > 0.f && k < 4) classes |= 1u << k;
+            }
+          classes = max(__reduce_or_sync(~0u, classes), 1u);  // one at least: what came before takes its factor there
+#pragma unroll 1
+          while (classes != 0) {
+            const int k = 31 - __clz(classes);
+            classes ^= 1u << k;
+            float factor = 1.f;
+            for (int i26 = 0; i26 < k; ++i26) factor *= kClass;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+              for (int c = 0; c < 2 * NN; ++c) {
+                const float x = s[r][c] * factor;  // of a higher class: 2^26 or more above 1; of a lower: under 2^-26
+                w[r][c] = x >= 1.f / kClass && (x < 1.f || k == 0) ? x * up : 0.f;
+              }
+            products(w, v_exp - 26 * k);
+#pragma unroll
+            for (int x = 0; x < 2 * R; ++x) kept[x] = 1.f;  // of a class still to come
+          }
         }
       } else {
         uint32_t hi[R][NN], mid[R][NN], lo[R][NN];  // of tokens 8 nt + 2 q4, and the next
