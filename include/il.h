@@ -371,8 +371,11 @@ int il_kv_read(const il_kv* kv, const int32_t* slots, int64_t n, float* k, int64
  * sums and softmax statistics are fp32.  q, K and V that are attended must be finite:
  * where one is not, that sequence's heads that read it give NaN or infinity.  Work is split
  * over the length and joined in an order that depends on the lengths only, so that equal
- * calls give equal bits.  The library's split workspace for `stream` holds the parts (see
- * il_matmul_batch for its growth and stream capture).
+ * calls give equal bits.  In a Q8 cache a weight p keeps 22 bits; one below 2^-104 of the largest so far
+ * counts as 0.
+ * Workspace: il_kv_extend and il_kv_attend share one of about 5 MB per (device, stream), owned by the library,
+ * allocated (stream-ordered) by the first of these calls on the stream and never moved: run one before
+ * capturing the stream (IL_ERR_UNSUPPORTED otherwise).  il_release_scratch frees it.
  */
 int il_kv_attend(const il_kv* kv, const float* q, int64_t q_stride, const int32_t* table, int64_t table_stride,
                  int64_t table_width, const int32_t* lens, int64_t n_seq, int64_t n_q_heads, float scale,
@@ -418,7 +421,7 @@ int il_check_device_status(void* stream);
 
 /* Frees the scratch the library keeps for `stream` on the current device (the
  * bf16 copy of x, the split-K workspace, the LM-head scratch, the device copies
- * of x and y of il_matmul_batch_host), in stream order:
+ * of x and y of il_matmul_batch_host, the K/V workspace), in stream order:
  * call it before destroying a stream the library has run on.  A later call on
  * the stream allocates afresh.  Returns IL_OK or IL_ERR_CUDA. */
 int il_release_scratch(void* stream);

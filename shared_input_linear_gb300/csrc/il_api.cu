@@ -360,6 +360,38 @@ int get_host_staging(int dev, cudaStream_t stream, size_t bytes, uint8_t** out) 
   return IL_OK;
 }
 
+// Workspace of the il_kv_* calls, one per (device, stream): arrival counters (zero between launches) and the
+// parts of rows that cross CTAs.  Of one size for every call, so that it never moves under a captured graph.
+struct KvScratch {
+  void* ptr = nullptr;
+  size_t bytes = 0;
+};
+std::map<std::pair<int, cudaStream_t>, KvScratch> g_kv_scratch;
+
+int get_kv_workspace(int dev, cudaStream_t stream, size_t bytes, void** out) {
+  std::lock_guard<std::mutex> lk(g_scratch_mu);
+  KvScratch& s = g_kv_scratch[{dev, stream}];
+  if (s.ptr == nullptr) {
+    const int rc = check_not_capturing(stream, "the K/V workspace");
+    if (rc != IL_OK) return rc;
+    void* np = nullptr;
+    cudaError_t e = il_malloc_async(&np, bytes, stream);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return fail(IL_ERR_OOM, "allocating %zu bytes of K/V workspace failed", bytes);
+    }
+    e = cudaMemsetAsync(np, 0, bytes, stream);
+    if (e != cudaSuccess) {
+      cudaFreeAsync(np, stream);
+      return cuda_fail(e, "cudaMemsetAsync(K/V workspace)");
+    }
+    s.ptr = np;
+    s.bytes = bytes;
+  }
+  *out = s.ptr;
+  return IL_OK;
+}
+
 // A buffer of il_matmul_batch_host must be host memory (page-locked or pageable)
 // or managed memory; device memory is il_matmul_batch's.  *mapped: the device
 // address of page-locked host memory that kernels can access in place (NULL for
@@ -696,6 +728,11 @@ int il_release_scratch(void* stream_) {
     if (e == cudaSuccess && is->second.ptr != nullptr) e = cudaFreeAsync(is->second.ptr, stream);
     g_host_staging.erase(is);
   }
+  auto ik = g_kv_scratch.find({dev, stream});
+  if (ik != g_kv_scratch.end()) {
+    if (e == cudaSuccess && ik->second.ptr != nullptr) e = cudaFreeAsync(ik->second.ptr, stream);
+    g_kv_scratch.erase(ik);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "il_release_scratch");
   return IL_OK;
 }
@@ -1023,8 +1060,8 @@ int api_device(int* num_sms, unsigned** status) {
   return dev;
 }
 
-int api_workspace(int dev, cudaStream_t stream, size_t bytes, void** ws, size_t* got) {
-  return get_workspace(dev, stream, bytes, ws, got);
+int api_kv_workspace(int dev, cudaStream_t stream, int num_sms, void** ws) {
+  return get_kv_workspace(dev, stream, kv_workspace_bytes(num_sms), ws);
 }
 
 int api_fail(int code, const char* msg) { return fail(code, "%s", msg); }

@@ -411,13 +411,14 @@ cudaError_t prepare_kv_extend(const KvExtendArgs& a, int num_sms, Launch* out);
 // write: fp32 rows into the cache; otherwise the cached values into the rows.
 cudaError_t prepare_kv_rows(bool write, const KvView& kv, float* k, int64_t k_stride, float* v, int64_t v_stride,
                             const int32_t* slots, int64_t n, unsigned* status, int num_sms, Launch* out);
-// Split workspace that il_kv_attend wants (0: none).
-size_t kv_attend_workspace_bytes(const KvAttendArgs& a, int num_sms);
-cudaError_t prepare_kv_attend(const KvAttendArgs& a, int num_sms, void* ws, size_t ws_bytes, Launch* out);
+// Workspace of the il_kv_* calls: arrival counters, zero before and after each launch, then il_kv_attend's parts.
+constexpr size_t kKvCounterBytes = 4096;
+size_t kv_workspace_bytes(int num_sms);
+cudaError_t prepare_kv_attend(const KvAttendArgs& a, int num_sms, void* ws, Launch* out);
 
 // Helpers of entry points defined in other translation units: the calling thread's device
-// (negative: an il_status, error set) and the split workspace of a stream.
+// (negative: an il_status, error set) and the K/V workspace of a stream.
 int api_device(int* num_sms, unsigned** status);
-int api_workspace(int dev, cudaStream_t stream, size_t bytes, void** ws, size_t* got);
+int api_kv_workspace(int dev, cudaStream_t stream, int num_sms, void** ws);
 
 }  // namespace il

@@ -198,8 +198,7 @@ int il_kv_extend(int64_t n_seq, int64_t page_size, const int32_t* lens, const in
   const int dev = api_device(&num_sms, &status);
   if (dev < 0) return dev;
   void* ws = nullptr;
-  size_t got = 0;
-  int rc = api_workspace(dev, static_cast<cudaStream_t>(stream), kSplitCounterBytes, &ws, &got);
+  const int rc = api_kv_workspace(dev, static_cast<cudaStream_t>(stream), num_sms, &ws);
   if (rc != IL_OK) return rc;
   KvExtendArgs a;
   memset(&a, 0, sizeof a);
@@ -295,14 +294,10 @@ int il_kv_attend(const il_kv* kv, const float* q, int64_t q_stride, const int32_
   a.out_stride = os;
   a.lse = lse;
   void* ws = nullptr;
-  size_t got = 0;
-  const size_t want = kv_attend_workspace_bytes(a, num_sms);
-  if (want > 0) {
-    rc = api_workspace(dev, static_cast<cudaStream_t>(stream), want, &ws, &got);
-    if (rc != IL_OK) return rc;
-  }
+  rc = api_kv_workspace(dev, static_cast<cudaStream_t>(stream), num_sms, &ws);
+  if (rc != IL_OK) return rc;
   Launch L;
-  const cudaError_t e = prepare_kv_attend(a, num_sms, ws, got, &L);
+  const cudaError_t e = prepare_kv_attend(a, num_sms, ws, &L);
   if (e != cudaSuccess) return api_cuda_fail(e, fn);
   return enqueue(fn, L, stream);
 }

@@ -16,15 +16,12 @@ bool wide_block(const KvAttendArgs& a) { return a.n_q_heads / a.kv.n_heads > 8; 
 
 }  // namespace
 
-// A counter and two parts (four half parts where a head takes two warps) for each CTA of the
-// grid, one CTA per SM.
-size_t kv_attend_workspace_bytes(const KvAttendArgs& a, int num_sms) {
-  const int rows = wide_block(a) ? 16 : 8, dim = padded_dim(a.kv.head_dim);
-  return kSplitCounterBytes + (size_t)num_sms * 2 * rows * (dim + (dim == 256 ? 4 : 2)) * sizeof(float);
-}
+// The counters, and two parts for each CTA of the grid, one CTA per SM: the largest part is 16 rows of 256 columns
+// in two halves, each with the rows' maxima and sums.
+size_t kv_workspace_bytes(int num_sms) { return kKvCounterBytes + (size_t)num_sms * 2 * 16 * (256 + 4) * sizeof(float); }
 
-cudaError_t prepare_kv_attend(const KvAttendArgs& a, int num_sms, void* ws, size_t ws_bytes, Launch* out) {
-  if (num_sms > kSplitCounters || ws_bytes < kv_attend_workspace_bytes(a, num_sms)) return cudaErrorInvalidValue;
+cudaError_t prepare_kv_attend(const KvAttendArgs& a, int num_sms, void* ws, Launch* out) {
+  if (num_sms * sizeof(unsigned) > kKvCounterBytes) return cudaErrorInvalidValue;
   const bool wide = wide_block(a);
   KvAttendPlan p{};
   p.a = a;
@@ -54,7 +51,7 @@ cudaError_t prepare_kv_attend(const KvAttendArgs& a, int num_sms, void* ws, size
   p.spage_bytes = (uint32_t)(kv.spage * 4), p.stoken_bytes = (uint32_t)(kv.stoken * 4);
   p.shead_bytes = (uint32_t)(kv.shead * 4);
   p.arrived = static_cast<unsigned*>(ws);
-  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kSplitCounterBytes);
+  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kKvCounterBytes);
   return a.kv.format == IL_Q8 ? prepare_kv_attend_q8(p, dim, wide, num_sms, out)
                               : prepare_kv_attend_bf16(p, dim, wide, num_sms, out);
 }

@@ -342,3 +342,57 @@ def test_refusals(sil):
     no(-2, cache=sil.KVCache(odd, odd))                               # rows not 16-byte aligned
     assert bool((out == 9.0).all())
     sil.check_device_status()
+
+
+def test_the_most_sequences(sil):
+    import torch
+    n = 65536
+    lens = torch.zeros(n, dtype=torch.int32)
+    live = [0, 1, 255, 256, 30000, 65000, n - 1]
+    lens[live] = torch.tensor([1, 40, 16, 17, 33, 2, 20], dtype=torch.int32)
+    kv = torch.randn((9, 16, 1, 32), device="cuda").bfloat16()
+    cache = sil.KVCache(kv, kv)
+    q = torch.randn((n, 2, 32), device="cuda")
+    table = torch.full((n, 3), -1, dtype=torch.int32, device="cuda")
+    table[live] = torch.tensor([[1, 5, 8]], dtype=torch.int32, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full((n, 2), 7.0, device="cuda")
+    sil.kv_attend(cache, q, table, lens.cuda(), out, lse=lse)
+    torch.cuda.synchronize()
+    tok = kv[[1, 5, 8]].reshape(48, 1, 32).float().cpu().numpy()
+    for r in live:
+        o, l, ot, lt = kv_util.attend(q[r].cpu().numpy(), tok[:int(lens[r])], tok[:int(lens[r])], 32 ** -0.5, 0)
+        assert np.all(np.abs(out[r].cpu().numpy() - o) <= ot) and np.all(np.abs(lse[r].cpu().numpy() - l) <= lt)
+    rest = torch.ones(n, dtype=torch.bool)
+    rest[live] = False
+    assert bool((out[rest] == 0).all()) and bool(torch.isneginf(lse[rest]).all())
+    e = torch.empty((n + 1, 2, 32), device="cuda")
+    with pytest.raises(sil.ILError):
+        sil.kv_attend(cache, e, torch.empty((n + 1, 1), dtype=torch.int32, device="cuda"),
+                      torch.empty(n + 1, dtype=torch.int32, device="cuda"), e.clone())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "q8"])
+def test_logits_that_rise_and_fall_along_a_sequence(sil, fmt):
+    # a token far above the others first, then in the middle, and slopes of a few units a token: what came before is
+    # scaled up and down, and tiles span more than fp16 does
+    import torch
+    for shape in ("first", "middle", "rise", "fall"):
+        n, dim = 400, 64
+        c = Case(sil, fmt, 8, 2, dim, 16, [n], seed=21)
+        t = np.arange(n)
+        level = {"first": np.where(t == 0, 60.0, 0.0), "middle": np.where(t == 200, 45.0, 0.0), "rise": t * 1.5 - 300,
+                 "fall": 300 - t * 1.5}[shape]
+        # K's first block becomes level / sqrt(dim) * sign(q0): adds `level` to every head whose q starts with that sign
+        c.q[:, :, 0] = 8.0
+        kd = c.keys[0].copy()
+        kd[:, :, 0] = level[:, None]
+        rows = torch.from_numpy(c.table[0, t // 16].astype(np.int64)).cuda(), torch.from_numpy(t % 16).cuda()
+        if fmt == "bf16":
+            c.cache.k[rows] = torch.from_numpy(kd).float().cuda().bfloat16()
+            c.keys[0] = c.cache.k[rows].double().cpu().numpy()
+        else:
+            kq, ks = kv_util.quantise(kd.astype(np.float32))
+            c.cache.k[rows] = torch.from_numpy(kq).cuda()
+            c.cache.k_scale[rows] = torch.from_numpy(ks).cuda()
+            c.keys[0] = kq * np.repeat(ks, 32, -1).astype(np.float64)
+        c.check(*c.run())
