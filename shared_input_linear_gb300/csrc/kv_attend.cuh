@@ -81,13 +81,15 @@ struct Config {
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kWorkers = kWarps / H;    // runs of tiles in a CTA
   static constexpr uint32_t kWhole = 2 * kWorkers;  // tiles of a row that is not cut over CTAs
-  static constexpr int kFixed = (kThreads + 2) * 8 + kWarps * 8 + kWorkers * 64 + 64;
-  static constexpr int kRoom = (kSmemLimit - kFixed - kWarps * kPart * 4) / (kWarps * kStage);
-  static constexpr int kStages = kRoom > 6 ? 6 : kRoom;
+  static constexpr int kFixed = kThreads * 8 + kWorkers * 48 + 32;
+  // Two stages, one on its way while the other is used, are 70 KB in flight an SM.  More cost DRAM efficiency: with
+  // three, 128 x 4096 tokens bf16 took 332 us instead of 317, heads of 64 92.3 instead of 89.5 (Q8 70.7, 69.1).
+  static constexpr int kStages = 2;
   static constexpr int kRing = kStages * kStage;
   static constexpr size_t kSmem = (size_t)kFixed + kWarps * (kPart * 4 + kRing);
   static_assert(kStages >= 2 && kSmem <= kSmemLimit, "the ring does not fit");
   static_assert(kRing >= kPart * 4, "a part must fit the warp's ring");
+  static_assert(kWorkers * 48 >= kWarps * 8, "the sums over sequences are kept where the workers' parts are described");
   static_assert(kPool >= 32 * kTile * R, "s is traded through the tile of K");
 };
 
@@ -264,12 +266,12 @@ __device__ __forceinline__ void advance(Walk& w, const KvAttendPlan& P) {
 // What a worker leaves for the CTA: part 0, the end (or all) of a row begun before its run, and
 // part 1, the beginning of a row that goes on behind it.
 struct Left {
-  int has0, end0, s0, hk0, block0;
-  int has1, s1, hk1, block1;
+  int s0, hk0, block0;
+  int s1, hk1, block1;
   uint32_t tiles0, tiles1;
   long long row0, row1;  // first tiles of the rows in the list
 };
-static_assert(sizeof(Left) <= 64, "see Config::kFixed");
+static_assert(sizeof(Left) == 48, "see Config::kFixed");
 
 template <bool Q8, int W, int R, int H>
 __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_kernel(const KvAttendPlan P) {
@@ -280,8 +282,8 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
   uint8_t* const ring_mem = smem;
   float* const part_mem = reinterpret_cast<float*>(smem + (size_t)NW * C::kRing);
   long long* const s_before = reinterpret_cast<long long*>(reinterpret_cast<uint8_t*>(part_mem) + NW * C::kPart * 4);
-  long long* const s_warp = s_before + NT + 2;
-  Left* const s_left = reinterpret_cast<Left*>(s_warp + NW);
+  Left* const s_left = reinterpret_cast<Left*>(s_before + NT);
+  long long* const s_warp = reinterpret_cast<long long*>(s_left);  // at the start, of the sums over sequences
   int* const s_flag = reinterpret_cast<int*>(s_left + NK);  // of the two rows that may cross CTAs: parts to join, first CTA
   unsigned* const s_mask = reinterpret_cast<unsigned*>(s_flag + 4);  // workers with a part 0, whose row ends in it, with a part 1
 
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
   }
 
   Left left;
-  left.has0 = left.has1 = 0;
+  bool has0 = false, end0 = false, has1 = false;  // part 0, its row's end in it, part 1
   if (n > 0) {
     Walk at = in;  // tile being used
     const uint32_t ring = smem_u32(ring_mem) + warp * C::kRing;
@@ -946,11 +948,11 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
         if (!alone) {
           const long long row = u0 + i - at.tile;
           if (!begun_here) {
-            left.has0 = 1, left.end0 = row_ends, left.s0 = at.s, left.hk0 = at.hk, left.block0 = at.block;
+            has0 = true, end0 = row_ends, left.s0 = at.s, left.hk0 = at.hk, left.block0 = at.block;
             left.tiles0 = at.q.tiles, left.row0 = row;
             part = part_mem + warp * C::kPart;
           } else {  // the run's last tile: nothing is in flight into the ring any more
-            left.has1 = 1, left.s1 = at.s, left.hk1 = at.hk, left.block1 = at.block;
+            has1 = true, left.s1 = at.s, left.hk1 = at.hk, left.block1 = at.block;
             left.tiles1 = at.q.tiles, left.row1 = row;
             part = reinterpret_cast<float*>(ring_mem + (size_t)warp * C::kRing);
             cp_wait<0>();
@@ -1006,9 +1008,9 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
   }
   if (lane == 0 && col0 == 0) {
     s_left[worker] = left;
-    if (left.has0) atomicOr(s_mask, 1u << worker);
-    if (left.has0 && left.end0) atomicOr(s_mask + 1, 1u << worker);
-    if (left.has1) atomicOr(s_mask + 2, 1u << worker);
+    if (has0) atomicOr(s_mask, 1u << worker);
+    if (has0 && end0) atomicOr(s_mask + 1, 1u << worker);
+    if (has1) atomicOr(s_mask + 2, 1u << worker);
   }
   __syncthreads();
 
@@ -1026,17 +1028,17 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
   auto add = [](float4& x, const float4& y, float f) {
     x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
   };
-  const unsigned has0 = s_mask[0], end0 = s_mask[1], has1 = s_mask[2];
+  const unsigned parts0 = s_mask[0], ends0 = s_mask[1], parts1 = s_mask[2];
   // End of the chain of w (exclusive), and whether its row ends there.
   auto end_of = [&](int w, bool& ends) {
-    const unsigned stop = end0 >> (w + 1);
+    const unsigned stop = ends0 >> (w + 1);
     ends = stop != 0;
-    return w + 1 + (ends ? __ffs(stop) : __ffs(~(has0 >> (w + 1))) - 1);
+    return w + 1 + (ends ? __ffs(stop) : __ffs(~(parts0 >> (w + 1))) - 1);
   };
 #pragma unroll 1
   for (int own = 0; own < 2; ++own) {  // the chain that this worker's part 0 is in, then the one that it began
-    if ((((own ? has1 : has0) >> worker) & 1) == 0) continue;
-    const int w = own ? worker : 31 - __clz(has1 & ((1u << worker) - 1));
+    if ((((own ? parts1 : parts0) >> worker) & 1) == 0) continue;
+    const int w = own ? worker : 31 - __clz(parts1 & ((1u << worker) - 1));
     bool ends;
     const int first = max(w, 0), count = end_of(w, ends) - first;
     const Left& by = s_left[first];
@@ -1077,8 +1079,8 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
 
   // ---- rows that cross CTAs: the last CTA to arrive adds them up in CTA order.  Of a CTA's rows only the one that
   // came in (0) and the last one left open (1) can cross.
-  const int open = 31 - __clz(has1);
-  bool crosses[2] = {(has0 & 1) != 0, false};
+  const int open = 31 - __clz(parts1);
+  bool crosses[2] = {(parts0 & 1) != 0, false};
   if (open >= 0) {
     end_of(open, crosses[1]);
     crosses[1] = !crosses[1];
