@@ -93,13 +93,15 @@ struct Config {
   static_assert(kPool >= 32 * kTile * R, "s is traded through the tile of K");
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool use) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(use ? 16 : 0) : "memory");
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool use, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(use ? 16 : 0),
+               "l"(policy)
+               : "memory");
 }
 template <int BYTES>
-__device__ __forceinline__ void cp_small(uint32_t dst, const void* src, bool use) {
+__device__ __forceinline__ void cp_small(uint32_t dst, const void* src, bool use, uint64_t policy) {
   if constexpr (BYTES == 16)
-    cp16(dst, src, use);
+    cp16(dst, src, use, policy);
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(use ? BYTES : 0)
                  : "memory");
@@ -403,6 +405,10 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
   if (n > 0) {
     Walk at = in;  // tile being used
     const uint32_t ring = smem_u32(ring_mem) + warp * C::kRing;
+    // K and V pass once, so that they need not push the rest (code, table, parts) out of L2: about 1 % of a long call.
+    // Where several blocks of query heads read them they are ordinary lines.
+    uint64_t policy = policy_evict_first();
+    if (P.blocks > 1) asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
 
     // 16-byte chunks of a row, rows of one copy instruction, this lane's chunk
     constexpr int ES = Q8 ? 1 : 2, CPR = C::kRowBytes / 16, PER = 32 / CPR;
@@ -444,8 +450,8 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
 #pragma unroll
           for (int i = 0; i < kGroup / PER; ++i) {
             const int row = k * kGroup + i * PER + sub;
-            cp16(to + k_at(row), kp, in_row);
-            cp16(to + C::kPool + v_at(row), vp, in_row);
+            cp16(to + k_at(row), kp, in_row, policy);
+            cp16(to + C::kPool + v_at(row), vp, in_row, policy);
             kp += row_step;
             vp += row_step;
           }
@@ -455,7 +461,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
                                                                        w.hk * P.shead_bytes + col0 / 8));
             const uint32_t st = to + 2 * C::kPool + (lane < 16 ? 0 : C::kScales) + (k * kGroup + (lane & 15)) * NB * 4;
 #pragma unroll
-            for (int i = 0; i < NB * 4 / SB; ++i) cp_small<SB>(st + i * SB, sc + i * SB, true);
+            for (int i = 0; i < NB * 4 / SB; ++i) cp_small<SB>(st + i * SB, sc + i * SB, true, policy);
           }
         }
       } else {
@@ -470,8 +476,8 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
           const long long o = __shfl_sync(~0u, off, row);
           const bool use = ((mask >> row) & 1) && in_row;
           const long long src = use ? o * ES + chunk * 16 : 0;
-          cp16(to + k_at(row), kv.k + src, use);
-          cp16(to + C::kPool + v_at(row), kv.v + src, use);
+          cp16(to + k_at(row), kv.k + src, use, policy);
+          cp16(to + C::kPool + v_at(row), kv.v + src, use, policy);
         }
         if constexpr (Q8) {
           const uint32_t st = to + 2 * C::kPool;
@@ -481,8 +487,8 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
             const long long so = __shfl_sync(~0u, soff, row);
             const bool use = ((mask >> row) & 1) && col0 + b * 32 < D;
             const long long src = use ? so + b : 0;
-            cp_small<4>(st + (i * 32 + lane) * 4, kv.k_scale + src, use);
-            cp_small<4>(st + C::kScales + (i * 32 + lane) * 4, kv.v_scale + src, use);
+            cp_small<4>(st + (i * 32 + lane) * 4, kv.k_scale + src, use, policy);
+            cp_small<4>(st + C::kScales + (i * 32 + lane) * 4, kv.v_scale + src, use, policy);
           }
         }
       }
