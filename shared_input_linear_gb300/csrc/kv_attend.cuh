@@ -64,6 +64,7 @@ namespace attend {
 
 constexpr int kGroup = 16;          // tokens of a product's step; pages of whole groups are copied the simple way
 constexpr int kSmemLimit = 232448;  // 227 KB
+constexpr int kMaxCtas = 256;       // of a grid, one an SM
 
 // W columns of a head in a warp, H warps a head (H * W >= head_dim), R blocks of 8 query heads.
 template <bool Q8, int W, int R, int H>
@@ -1119,31 +1120,37 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
     s_flag[2 + tid] = c0;
   }
   __syncthreads();
-#pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    const int count = s_flag[which];
-    if (count == 0) continue;
-    const int c0 = s_flag[2 + which];
+  // The CTA that ends last is often the last of both its rows: then half of the warps take each.
+  {
+    const bool both = s_flag[0] != 0 && s_flag[1] != 0;
+    const int team = both ? NT / 2 : NT, which = both ? tid / (NT / 2) : s_flag[0] != 0 ? 0 : 1, tt = both ? tid % (NT / 2) : tid;
+    const int team_warp = tt / 32, team_warps = team / 32;
+    auto sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(both ? 14 + which : 0), "r"(team) : "memory"); };
+    const int count = s_flag[which], c0 = s_flag[2 + which];
+    if (count == 0) return;
     const Left& by = s_left[which == 0 ? 0 : open];
     const int s = which == 0 ? by.s0 : by.s1, hk = which == 0 ? by.hk0 : by.hk1;
     const int block = which == 0 ? by.block0 : by.block1, rows = min(ROWS, P.group - block * ROWS);
     constexpr int kNext = 2 * H * C::kPart, WIDE = H * W / 4;
+    constexpr int kJoin = 32768;  // bytes of a row's join: weights of up to kMaxCtas parts, and the groups' sums
+    static_assert(ROWS * (kMaxCtas + 2) * 4 + 16 + NT * 16 <= kJoin && 2 * kJoin <= NW * (C::kRing + C::kPart * 4),
+                  "two joins must fit what the ring and the parts took");
     const float* const rest = global_part(c0, 0);  // part i: of the row that came into CTA c0 + i
     const float* const head = global_part(c0, 1);  // part 0: of the row that CTA c0 left open
     // the row's float4s over groups of threads; a group takes every groups-th part, 12 loads at a time
-    const int wide = rows * WIDE, groups = wide <= NT / 2 ? NT / wide : 1, grp = groups == 1 ? 0 : tid / wide;
-    float* const weight = reinterpret_cast<float*>(ring_mem);  // [rows][count]; nothing else uses the ring any more
+    const int wide = rows * WIDE, groups = wide <= team / 2 ? team / wide : 1, grp = groups == 1 ? 0 : tt / wide;
+    float* const weight = reinterpret_cast<float*>(ring_mem + which * kJoin);  // [rows][count]
     float* const stat = weight + rows * count;                 // [rows][2]: max, sum
     float4* const sums = reinterpret_cast<float4*>(weight + ((rows * (count + 2) + 3) & ~3));
     auto part_of = [&](int i) { return i == 0 ? head : rest + (int64_t)i * kNext; };
     bool weighed = false;
     float m1 = -INFINITY, l1 = 0.f;  // of the first part whose weight this lane computes
-    if (warp < rows && lane < count) {
-      m1 = __ldcg(part_of(lane) + ROWS * W + warp);
-      l1 = __ldcg(part_of(lane) + ROWS * W + ROWS + warp);
+    if (team_warp < rows && lane < count) {
+      m1 = __ldcg(part_of(lane) + ROWS * W + team_warp);
+      l1 = __ldcg(part_of(lane) + ROWS * W + ROWS + team_warp);
     }
 #pragma unroll 1
-    for (int e = tid - grp * wide; e - tid + grp * wide < wide; e += NT) {
+    for (int e = tt - grp * wide; e - tt + grp * wide < wide; e += team) {
       const bool mine = e < wide && grp < groups;
       const int row = mine ? e / WIDE : 0, c = 4 * (e % WIDE);
       const int at = (c / W) * C::kPart + row * W + c % W;
@@ -1160,11 +1167,11 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
           // while those are on their way: the weights, a warp a head row
           weighed = true;
 #pragma unroll 1
-          for (int r = warp; r < rows; r += NW) {
+          for (int r = team_warp; r < rows; r += team_warps) {
             float M = -INFINITY, L = 0.f;
 #pragma unroll 1
             for (int i = lane; i < count; i += 32) {
-              if (r != warp || i != lane) {
+              if (r != team_warp || i != lane) {
                 m1 = __ldcg(part_of(i) + ROWS * W + r);
                 l1 = __ldcg(part_of(i) + ROWS * W + ROWS + r);
               }
@@ -1184,7 +1191,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
             for (int i = lane; i < count; i += 32) weight[r * count + i] = exp2_fast(weight[r * count + i] - b);
             if (lane == 0) stat[2 * r] = top, stat[2 * r + 1] = L;
           }
-          __syncthreads();
+          sync();
         }
 #pragma unroll
         for (int k = 0; k < 12; ++k) {
@@ -1193,15 +1200,14 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
         }
       }
       if (groups > 1) {  // the groups' sums in order
-        if (mine) sums[tid] = x;
-        __syncthreads();
+        if (mine) sums[tt] = x;
+        sync();
 #pragma unroll 1
-        for (int k = 1; k < groups && grp == 0; ++k) add(x, sums[tid + k * wide], 1.f);
+        for (int k = 1; k < groups && grp == 0; ++k) add(x, sums[tt + k * wide], 1.f);
       }
       if (mine && grp == 0 && c < D)
         finish(s, (int64_t)hk * P.group + block * ROWS + row, c, x, stat[2 * row], stat[2 * row + 1]);
     }
-    __syncthreads();
   }
 }
 

@@ -21,7 +21,8 @@ bool wide_block(const KvAttendArgs& a) { return a.n_q_heads / a.kv.n_heads > 8; 
 size_t kv_workspace_bytes(int num_sms) { return kKvCounterBytes + (size_t)num_sms * 2 * 16 * (256 + 4) * sizeof(float); }
 
 cudaError_t prepare_kv_attend(const KvAttendArgs& a, int num_sms, void* ws, Launch* out) {
-  if (num_sms * sizeof(unsigned) > kKvCounterBytes) return cudaErrorInvalidValue;
+  static_assert(attend::kMaxCtas * sizeof(unsigned) <= kKvCounterBytes, "a counter for each CTA");
+  num_sms = std::min(num_sms, attend::kMaxCtas);
   const bool wide = wide_block(a);
   KvAttendPlan p{};
   p.a = a;
