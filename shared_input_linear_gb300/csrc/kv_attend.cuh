@@ -12,12 +12,12 @@
 // sequences and idle slots balance to one tile a warp without any host knowledge of the lengths.
 // A row inside a warp's run is finished by the warp alone.  The ends of runs are parts of rows;
 // they are joined in shared memory by the CTA (one barrier, after its stream), and rows that cross CTAs
-// through the split workspace by the last CTA of the row to arrive, in CTA order: the result does
+// through the workspace by the last CTA of the row to arrive, in CTA order: the result does
 // not depend on the order of arrival.
 //
 // Stream.  Every warp owns a ring of stages, one tile of K and V each, filled with 16-byte
 // cp.async (any strides, any page size: a lane looks up its token's page one tile ahead) and zeros for
-// tokens outside the attended range.  Where pages hold whole tiles the addresses of a tile are one base and
+// tokens outside the attended range.  Where pages hold whole groups of 16 tokens their addresses are one base and
 // constants of the lane.  No barrier other than the warp's own sits in the stream.  A head of more than 128
 // elements takes a pair of warps, half of its columns each: they trade their halves of s
 // through shared memory, with a barrier of the two.
@@ -32,6 +32,12 @@
 // of its own.  p V is computed transposed: the quad layout of s is that of a B operand, so p goes in as it is.
 // Each tile's product starts from zero accumulators and joins the running sum in fp32
 // FMAs (with the factor of the running maximum), which round to nearest.
+//
+// Measured (GB300, 32 query heads on 8 K/V heads of 128, device time): bf16, 128 sequences of 4096 tokens 315 us, 6.8 TB/s
+// (the rate of a plain copy); 32 of 0 to 8192 86 us, 6.0 TB/s; one of 512 8.3 us.  Q8, 64 of 1 to 8192 106 us, 5.5 TB/s,
+// one of 131071 59 us, 5.2 TB/s.  What bounds it: HBM at bf16 (64 sequences of 8192: 317 us, 263 us with pages that stay in
+// L2); at Q8 the arithmetic (208 us either way: about 520 instructions per 16 tokens and warp, 200 of them on the ALU
+// pipe, two warps a scheduler); of a short call the latencies before the first tile and in the joins.
 #pragma once
 
 #include <algorithm>
@@ -53,7 +59,7 @@ struct KvAttendPlan {
   int group;              // query heads of a K/V head
   int blocks;             // blocks of 8 R query heads of a K/V head
   float q_scale;          // scale * log2(e)
-  int simple;             // pages hold whole tiles, the strides below fit, (Q8) scales allow the widest copies
+  int simple;             // pages hold whole groups, the strides below fit, (Q8) scales allow the widest copies
   uint32_t page_bytes, token_bytes, head_bytes;     // strides of k and v
   uint32_t spage_bytes, stoken_bytes, shead_bytes;  // of the scales
   unsigned* arrived;      // one counter a CTA, zero before and after
