@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
     // and of query heads 8 r + 2 q4 + (x & 1)
     float o[W / 16][4 * R], m[R], l[R];
     // Q8: the largest s so far (m may lie below it), the biased exponent of the largest V scale so far, and that of
-    // the sums' unit
+    // the sums' unit: the same but inside a tile
     float highest[R];
     int v_exp = 14, o_exp = 14;
 
@@ -894,7 +894,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
           products(w, v_exp);
         } else {
           // Classes of p, class k being 2^(-26 (k + 1)) <= p < 2^(-26 k) (p = 1 in class 0); p below 2^-104 is 0.  Class k is
-          // multiplied by 2^(26 k), and the sums' unit goes down as far.
+          // multiplied by 2^(26 k), and the sums' unit goes down as far, until the last class is in.
           constexpr float kClass = 67108864.f;  // 2^26
           uint32_t classes = 0;
 #pragma unroll
@@ -922,6 +922,12 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
 #pragma unroll
             for (int x = 0; x < 2 * R; ++x) kept[x] = 1.f;  // of a class still to come
           }
+          const float up_again = pow2_biased(127 + o_exp - v_exp);  // from the last class's unit
+          o_exp = v_exp;
+#pragma unroll
+          for (int k = 0; k < W / 16; ++k)
+#pragma unroll
+            for (int x = 0; x < 4 * R; ++x) o[k][x] *= up_again;
         }
       } else {
         uint32_t hi[R][NN], mid[R][NN], lo[R][NN];  // of tokens 8 nt + 2 q4, and the next
@@ -955,7 +961,14 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
       // ---- the row's or the run's end
       const bool row_ends = at.tile + 1 == at.q.tiles;
       if (row_ends || i + 1 == n) {
-        const float unit = Q8 ? (o_exp > 13 ? pow2_biased(o_exp - 13) : 0.f) : 1.f;
+        float unit = Q8 ? pow2_biased(o_exp - 13) : 1.f;
+        if (Q8 && o_exp < 80) {  // unit / sum may be below 2^-126: two factors
+#pragma unroll
+          for (int k = 0; k < W / 16; ++k)
+#pragma unroll
+            for (int x = 0; x < 4 * R; ++x) o[k][x] *= unit;
+          unit = 1.f;
+        }
         const bool alone = begun_here && row_ends;
         float* part = nullptr;
         if (!alone) {
