@@ -367,12 +367,17 @@ int il_kv_read(const il_kv* kv, const int32_t* slots, int64_t n, float* k, int64
  *   n_q_heads : a multiple of the cache's n_heads, at most 32768.    n_seq: 0 .. 65536.
  *   window : tokens seen, counted from the end; 0: all.
  * A sequence of length 0 gives out = 0 and lse = -inf.  Cached values outside the
- * attended range are never used, NaN or not.  q is kept to 21 or more of its 24 bits,
- * sums and softmax statistics are fp32.  q, K and V that are attended must be finite:
+ * attended range are never used, NaN or not.  q, K and V that are attended must be finite:
  * where one is not, that sequence's heads that read it give NaN or infinity.  Work is split
  * over the length and joined in an order that depends on the lengths only, so that equal
- * calls give equal bits.  In a Q8 cache a weight p keeps 22 bits; one below 2^-104 of the largest so far
- * counts as 0.
+ * calls give equal bits.
+ * Rounding: sums and softmax statistics are fp32.  Over a bf16 cache q and the weights p keep
+ * 21 or more of their 24 bits.  Over a Q8 cache an element of q keeps 22 bits, or 2^-38 of its
+ * head's largest where that is coarser.  A weight p there multiplies V's scale d, in tiles of 16
+ * or 32 tokens; p below is relative to the tile's largest, or to 2^-24 of the sequence's largest so
+ * far where that is more.  p d keeps 22 bits, or 2^-28 d where that is coarser.  In a tile with p below
+ * 2^-26 or d below 2^-10 of the sequence's largest so far, the second bound is 2^-12 of p times the
+ * tile's largest d of the same 32 columns instead, and p below 2^-104 counts as 0.
  * Workspace: il_kv_extend and il_kv_attend share one of about 5 MB per (device, stream), owned by the library,
  * allocated (stream-ordered) by the first of these calls on the stream and never moved: run one before
  * capturing the stream (IL_ERR_UNSUPPORTED otherwise).  il_release_scratch frees it.

@@ -828,19 +828,23 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
       if constexpr (Q8) {
         float d[2 * NN][NB];  // V's scales of the lane's tokens
         const uint32_t sv = from + 2 * C::kPool + C::kScales + 2 * q4 * NB * 4;
-        float most = 0.f;
+        float vs[NB], most = 0.f;  // of one token
+        lds_floats(vs, from + 2 * C::kPool + C::kScales + (lane & (T - 1)) * NB * 4);
 #pragma unroll
-        for (int c = 0; c < 2 * NN; ++c) {
-          lds_floats(d[c], sv + (8 * (c / 2) + c % 2) * NB * 4);
+        for (int b = 0; b < NB; ++b) most = fmaxf(most, fabsf(vs[b]));
+        v_exp = max(v_exp, (int)(__reduce_max_sync(~0u, __float_as_uint(most)) >> 23));
+        // fp16 parts of p d keep 2^-38 of the largest scale: 2^-28 of one that lies 2^10 below it.  A tile with smaller
+        // ones takes its products in classes too, with each block's scales up to the largest.
+        const float little = pow2_biased(v_exp - 10);
 #pragma unroll
-          for (int b = 0; b < NB; ++b) most = fmaxf(most, fabsf(d[c][b]));
-        }
-        most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
-        most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
-        v_exp = max(v_exp, (int)(__float_as_uint(most) >> 23));
+        for (int b = 0; b < NB; ++b) wide |= fabsf(vs[b]) < little && vs[b] != 0.f;
+        wide = __any_sync(~0u, wide);
+#pragma unroll
+        for (int c = 0; c < 2 * NN; ++c) lds_floats(d[c], sv + (8 * (c / 2) + c % 2) * NB * 4);
         const float up = pow2_biased(267 - v_exp);  // the largest scale becomes 2^13 .. 2^14
-        // Products of weights w, with the sums' unit moved to the biased exponent `unit`.
-        auto products = [&](const float (&w)[R][2 * NN], int unit) {
+        // Products of weights w, with the sums' unit moved to the biased exponent `unit`; back(b) undoes what d[.][b] was
+        // multiplied by.
+        auto products = [&](const float (&w)[R][2 * NN], int unit, auto back) {
           const int change = o_exp - unit;
           const float shift = change < -126 ? 0.f : pow2_biased(127 + change);
           o_exp = unit;
@@ -881,6 +885,8 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
                 }
               }
             }
+#pragma unroll
+            for (int x = 0; x < 8 * R; ++x) c[x / (4 * R)][x / 4 % R][x % 4] *= back(b);
             join(o[2 * b], c[0]);
             join(o[2 * b + 1], c[1]);
           }
@@ -891,11 +897,20 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
           for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int c = 0; c < 2 * NN; ++c) w[r][c] = s[r][c] * up;
-          products(w, v_exp);
+          products(w, v_exp, [](int) { return 1.f; });
         } else {
           // Classes of p, class k being 2^(-26 (k + 1)) <= p < 2^(-26 k) (p = 1 in class 0); p below 2^-104 is 0.  Class k is
           // multiplied by 2^(26 k), and the sums' unit goes down as far, until the last class is in.
           constexpr float kClass = 67108864.f;  // 2^26
+          float back[NB];
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const int e = (int)(__reduce_max_sync(~0u, __float_as_uint(fabsf(vs[b]))) >> 23);
+            const int gap = min(max(v_exp - e, 0), 120);  // (a NaN's e is 255)
+            back[b] = pow2_biased(127 - gap);
+#pragma unroll
+            for (int c = 0; c < 2 * NN; ++c) d[c][b] *= pow2_biased(127 + gap);
+          }
           uint32_t classes = 0;
 #pragma unroll
           for (int r = 0; r < R; ++r)
@@ -918,7 +933,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
                 const float x = s[r][c] * factor;  // of a higher class: 2^26 or more above 1; of a lower: under 2^-26
                 w[r][c] = x >= 1.f / kClass && (x < 1.f || k == 0) ? x * up : 0.f;
               }
-            products(w, v_exp - 26 * k);
+            products(w, v_exp - 26 * k, [&](int b) { return back[b]; });
 #pragma unroll
             for (int x = 0; x < 2 * R; ++x) kept[x] = 1.f;  // of a class still to come
           }

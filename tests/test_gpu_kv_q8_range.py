@@ -16,11 +16,45 @@ def sil():
     return lib()
 
 
+def _bound(c, r, scale):
+    """out, lse and their bounds (kv_util.attend) without its floor of 1e-30, for values of any size."""
+    o, l, ot, lt = kv_util.attend(c.q[r], c.keys[r], c.values[r], scale, c.window)
+    return o, l, ot - 1e-30, lt
+
+
 def _scale_values(c, factor):
     """V's scales times `factor` [dim / 32], on the device and in the plain values."""
     import torch
     c.cache.v_scale.mul_(torch.from_numpy(np.asarray(factor, np.float32)).cuda())
     c.values = [v * np.repeat(np.asarray(factor, np.float64), 32) for v in c.values]
+
+
+@pytest.mark.parametrize("heads,kv,dim", [(8, 2, 128), (8, 2, 64), (16, 1, 128), (16, 1, 64), (4, 1, 256), (9, 1, 256), (4, 1, 96)])
+@pytest.mark.parametrize("apart", [20, 27, 40, 70])
+def test_blocks_of_columns_do_not_share_their_bits(sil, heads, kv, dim, apart):
+    # each block of 32 columns is 2^-apart of one beside it: as accurate as the other
+    c = Case(sil, "q8", heads, kv, dim, 16, [1, 40, 333, 1500], seed=apart)
+    _scale_values(c, 2.0 ** (-apart * (np.arange(dim // 32) % 2)))
+    out, lse = c.run()
+    got = out.double().cpu().numpy()
+    for r in range(len(c.lens)):
+        o, _, ot, _ = _bound(c, r, dim ** -0.5)
+        assert np.all(np.abs(got[r] - o) <= ot), f"sequence {r}"
+    c.check(out, lse)
+
+
+def test_blocks_may_grow_along_a_sequence(sil):
+    # scales that rise by 2^40 from token to token and back, in another order in each block: what came before keeps its size
+    c = Case(sil, "q8", 8, 2, 128, 16, [700], seed=5)
+    t, b = np.arange(700)[:, None], np.arange(4)
+    f = np.exp2(np.rint(np.minimum(t * (b + 1) / 40.0, 40.0)))
+    import torch
+    rows = torch.from_numpy(c.table[0, np.arange(700) // 16].astype(np.int64)).cuda(), torch.arange(700).cuda() % 16
+    c.cache.v_scale[rows] *= torch.from_numpy(f.astype(np.float32)).cuda()[:, None]
+    c.values[0] = c.values[0] * np.repeat(f, 32, -1)[:, None]
+    out, _ = c.run()
+    o, _, ot, _ = _bound(c, 0, 128 ** -0.5)
+    assert np.all(np.abs(out[0].double().cpu().numpy() - o) <= ot)
 
 
 def _levels(c, level):
