@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
     // ---- the row being worked on
     constexpr int QR = Q8 ? 4 * R : 6 * R;  // registers of q for 16 elements
     uint32_t qf[2 * NB][QR];
-    float q_back[R];      // Q8: what s is to be multiplied by for the scaling of q and the bytes' unit
+    float q_back[R];      // Q8: what s is to be multiplied by for the scaling of q and the bytes' unit; -2^-64 times it if above 2^127
     float q_start[R][NB];  // Q8: -128 units times the sum of q over a block
     // sums of p V, transposed: o[i][4 r + x] of MMA rows (columns of the head) g (x = 0, 1) or g + 8 (2, 3) of step i
     // and of query heads 8 r + 2 q4 + (x & 1)
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
           top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
           const int e = max((int)(__float_as_uint(top) >> 23), 14);
           const float up = pow2_biased(267 - e);  // the row's largest |q| becomes 2^13 .. 2^14
-          q_back[r] = pow2_biased(min(e + 11, 254));
+          q_back[r] = e + 11 < 255 ? pow2_biased(e + 11) : -pow2_biased(e + 11 - 64);
 #pragma unroll
           for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -676,6 +676,11 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
           for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int c = 0; c < 2 * NN; ++c) s[r][c] *= q_back[r];
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+            if (q_back[r] < 0.f)  // |q| of 2^117 and more
+#pragma unroll
+              for (int c = 0; c < 2 * NN; ++c) s[r][c] *= -18446744073709551616.f;
         } else {
 #pragma unroll
           for (int k = 0; k < GR; ++k) {

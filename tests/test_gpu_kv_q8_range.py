@@ -90,3 +90,12 @@ def test_small_values_behind_a_peak(sil, heads, dim, n, shape):
         assert bool(((off == 0) | ((out.abs() < 2.0 ** -30) & (off <= 2.0 ** (k - 140)))).all()), k
         assert torch.equal(same, lse)
         _scale_values(c, [2.0 ** k] * (dim // 32))
+
+
+@pytest.mark.parametrize("heads,kv,dim", [(8, 2, 64), (16, 1, 128), (4, 1, 256)])
+def test_large_queries_on_small_keys(sil, heads, kv, dim):
+    # |scale * q| of 2^117 and more, logits of ordinary size
+    c = Case(sil, "q8", heads, kv, dim, 16, [5, 130, 700], seed=13, spread=2.0 ** -119)
+    c.q *= np.float32(2.0 ** 62)
+    scale = 2.0 ** 57 * dim ** -0.5
+    c.check(*c.run(scale=scale), scale=scale)
