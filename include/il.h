@@ -322,6 +322,9 @@ typedef struct {
  *   first            : int32 [n_seq + 1] or NULL: index in slots of each sequence's first new
  *                      token, and their number.
  *   info             : int64 [4] or NULL: {code, new tokens, pages taken, pages given}.
+ * Pages in the ring and the table are not accessed here and move as they are.  A new token in
+ * one that no cache has (negative, or with the token's slot at 2^31 - 1 or more) gets the
+ * slot 2^31 - 1, which il_kv_append and il_kv_read skip and flag.
  * All or nothing: where there are too few free pages (code bit 0), a sequence
  * would need more pages than table_width (bit 1), the new tokens are more than
  * max_slots (bit 2) or the ring's state is impossible (bit 3), nothing changes: table and ring stay,

@@ -172,7 +172,8 @@ __global__ void __launch_bounds__(kExtendThreads) kv_extend_kernel(const KvExten
         page = a.ring[ring_at(head_at, taken + (col - c.had))];
         if (in_page == 0) *entry = page;
       }
-      slot = (int32_t)((uint32_t)page * P + in_page);
+      // a page that no cache has (negative, or with slots past 31 bits) gives a slot that none has
+      slot = (int32_t)min((unsigned long long)(uint32_t)page * P + in_page, 0x7fffffffull);
       pos = (int32_t)p;
     }
     a.slots[i] = slot;
