@@ -21,7 +21,9 @@
  *            f32 d[n_out][n_in/32] starting at byte n_out*n_in/2.
  *
  * Threading: every entry point is thread-safe.  The library works on the
- * CUDA device that is current on the calling thread.
+ * CUDA device that is current on the calling thread.  What it keeps per
+ * stream it keeps per thread too for cudaStreamPerThread, one handle for a
+ * stream of each thread.
  */
 #ifndef IL_H_
 #define IL_H_
@@ -430,7 +432,8 @@ int il_check_device_status(void* stream);
 /* Frees the scratch the library keeps for `stream` on the current device (the
  * bf16 copy of x, the split-K workspace, the LM-head scratch, the device copies
  * of x and y of il_matmul_batch_host, the K/V workspace), in stream order:
- * call it before destroying a stream the library has run on.  A later call on
+ * call it before destroying a stream the library has run on (for
+ * cudaStreamPerThread on the thread itself, before it ends).  A later call on
  * the stream allocates afresh.  Returns IL_OK or IL_ERR_CUDA. */
 int il_release_scratch(void* stream);
 

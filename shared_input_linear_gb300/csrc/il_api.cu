@@ -15,6 +15,7 @@
 #include <mutex>
 #include <new>
 #include <string>
+#include <tuple>
 #include <unordered_set>
 #include <utility>
 #include <vector>
@@ -133,6 +134,19 @@ struct DeviceState {
 std::mutex g_dev_mu;
 std::map<int, DeviceState> g_devices;
 
+// What per-stream scratch is kept under.  cudaStreamPerThread is one handle for a stream
+// of each thread, so that the thread is part of the key there.
+using StreamKey = std::tuple<int, cudaStream_t, uint64_t>;
+StreamKey stream_key(int dev, cudaStream_t stream) {
+  static std::atomic<uint64_t> threads{0};
+  uint64_t thread = 0;
+  if (stream == cudaStreamPerThread) {
+    thread_local const uint64_t mine = threads.fetch_add(1) + 1;
+    thread = mine;
+  }
+  return {dev, stream, thread};
+}
+
 // Scratch of the tensor-core path, one set per (device, stream): the bf16 copy
 // of x and the split-K workspace.  Grown with the stream-ordered allocator, so
 // growing never waits for the stream: the old buffer is released in stream
@@ -145,7 +159,7 @@ struct Scratch {
 };
 
 std::mutex g_scratch_mu;
-std::map<std::pair<int, cudaStream_t>, Scratch> g_scratch;
+std::map<StreamKey, Scratch> g_scratch;
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -247,7 +261,7 @@ int check_not_capturing(cudaStream_t stream, const char* what) {
 
 int get_scratch(int dev, cudaStream_t stream, size_t bytes, void** out) {
   std::lock_guard<std::mutex> lk(g_scratch_mu);
-  Scratch& s = g_scratch[{dev, stream}];
+  Scratch& s = g_scratch[stream_key(dev, stream)];
   if (s.bytes < bytes) {
     const int rc = check_not_capturing(stream, "the bf16 copy of x");
     if (rc != IL_OK) return rc;
@@ -268,7 +282,7 @@ int get_scratch(int dev, cudaStream_t stream, size_t bytes, void** out) {
 
 int get_workspace(int dev, cudaStream_t stream, size_t bytes, void** out, size_t* got) {
   std::lock_guard<std::mutex> lk(g_scratch_mu);
-  Scratch& s = g_scratch[{dev, stream}];
+  Scratch& s = g_scratch[stream_key(dev, stream)];
   if (s.ws_bytes < bytes) {
     const int rc = check_not_capturing(stream, "the split-K workspace");
     if (rc != IL_OK) return rc;
@@ -299,13 +313,13 @@ struct HeadScratch {
   void* ptr = nullptr;
   int64_t n_cent = 0, k = 0;
 };
-std::map<std::pair<int, cudaStream_t>, HeadScratch> g_head_scratch;
+std::map<StreamKey, HeadScratch> g_head_scratch;
 
 constexpr size_t kHeadStateBytes = 256;  // best key (8 bytes) and counter, at the start
 
 int get_head_scratch(int dev, cudaStream_t stream, int64_t n_cent, int64_t k, uint8_t** out) {
   std::lock_guard<std::mutex> lk(g_scratch_mu);
-  HeadScratch& s = g_head_scratch[{dev, stream}];
+  HeadScratch& s = g_head_scratch[stream_key(dev, stream)];
   if (s.n_cent < n_cent || s.k < k) {
     const int rc = check_not_capturing(stream, "the LM-head scratch");
     if (rc != IL_OK) return rc;
@@ -337,11 +351,11 @@ struct HostStaging {
   void* ptr = nullptr;
   size_t bytes = 0;
 };
-std::map<std::pair<int, cudaStream_t>, HostStaging> g_host_staging;
+std::map<StreamKey, HostStaging> g_host_staging;
 
 int get_host_staging(int dev, cudaStream_t stream, size_t bytes, uint8_t** out) {
   std::lock_guard<std::mutex> lk(g_scratch_mu);
-  HostStaging& s = g_host_staging[{dev, stream}];
+  HostStaging& s = g_host_staging[stream_key(dev, stream)];
   if (s.bytes < bytes) {
     const int rc = check_not_capturing(stream, "the device copies of x and y");
     if (rc != IL_OK) return rc;
@@ -366,11 +380,11 @@ struct KvScratch {
   void* ptr = nullptr;
   size_t bytes = 0;
 };
-std::map<std::pair<int, cudaStream_t>, KvScratch> g_kv_scratch;
+std::map<StreamKey, KvScratch> g_kv_scratch;
 
 int get_kv_workspace(int dev, cudaStream_t stream, size_t bytes, void** out) {
   std::lock_guard<std::mutex> lk(g_scratch_mu);
-  KvScratch& s = g_kv_scratch[{dev, stream}];
+  KvScratch& s = g_kv_scratch[stream_key(dev, stream)];
   if (s.ptr == nullptr) {
     const int rc = check_not_capturing(stream, "the K/V workspace");
     if (rc != IL_OK) return rc;
@@ -692,7 +706,7 @@ int il_check_device_status(void* stream) {
     {
       std::lock_guard<std::mutex> lk(g_scratch_mu);
       for (auto& kv : g_scratch)
-        if (kv.first.first == dev && kv.second.ws != nullptr && e == cudaSuccess)
+        if (std::get<0>(kv.first) == dev && kv.second.ws != nullptr && e == cudaSuccess)
           e = cudaMemset(kv.second.ws, 0, kv.second.ws_bytes);
     }
     size_t nb = 0;
@@ -712,23 +726,23 @@ int il_release_scratch(void* stream_) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   std::lock_guard<std::mutex> lk(g_scratch_mu);
-  auto it = g_scratch.find({dev, stream});
+  auto it = g_scratch.find(stream_key(dev, stream));
   if (it != g_scratch.end()) {
     if (it->second.ptr != nullptr) e = cudaFreeAsync(it->second.ptr, stream);
     if (e == cudaSuccess && it->second.ws != nullptr) e = cudaFreeAsync(it->second.ws, stream);
     g_scratch.erase(it);
   }
-  auto ih = g_head_scratch.find({dev, stream});
+  auto ih = g_head_scratch.find(stream_key(dev, stream));
   if (ih != g_head_scratch.end()) {
     if (e == cudaSuccess && ih->second.ptr != nullptr) e = cudaFreeAsync(ih->second.ptr, stream);
     g_head_scratch.erase(ih);
   }
-  auto is = g_host_staging.find({dev, stream});
+  auto is = g_host_staging.find(stream_key(dev, stream));
   if (is != g_host_staging.end()) {
     if (e == cudaSuccess && is->second.ptr != nullptr) e = cudaFreeAsync(is->second.ptr, stream);
     g_host_staging.erase(is);
   }
-  auto ik = g_kv_scratch.find({dev, stream});
+  auto ik = g_kv_scratch.find(stream_key(dev, stream));
   if (ik != g_kv_scratch.end()) {
     if (e == cudaSuccess && ik->second.ptr != nullptr) e = cudaFreeAsync(ik->second.ptr, stream);
     g_kv_scratch.erase(ik);
