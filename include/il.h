@@ -127,6 +127,12 @@ il_weight* il_upload_weight(int format, const void* host_ptr, int64_t n_out, int
  * waits for the stream; they cannot grow while `stream` is being captured
  * (IL_ERR_UNSUPPORTED): run one call of the largest size on the stream before
  * capturing it.  il_release_scratch frees them.
+ * Graphs: a captured call of any entry point uses the scratch of the stream it was captured
+ * on, wherever its graph is replayed.  Replays of graphs captured on one stream, and calls
+ * on that stream, must therefore not overlap (nothing detects it, and the results would be
+ * wrong); capture graphs that are to run side by side on streams of their own.  Scratch that
+ * grows after the capture (a larger call on the stream) and il_release_scratch leave the graph
+ * without its memory: capture it again before the next replay.
  */
 int il_matmul_batch(const float* x, int64_t t, int64_t n_in, const il_job* jobs, int n_jobs,
                     void* stream);
@@ -385,7 +391,8 @@ int il_kv_read(const il_kv* kv, const int32_t* slots, int64_t n, float* k, int64
  * tile's largest d of the same 32 columns instead, and p below 2^-104 counts as 0.
  * Workspace: il_kv_extend and il_kv_attend share one of about 5 MB per (device, stream), owned by the library,
  * allocated (stream-ordered) by the first of these calls on the stream and never moved: run one before
- * capturing the stream (IL_ERR_UNSUPPORTED otherwise).  il_release_scratch frees it.
+ * capturing the stream (IL_ERR_UNSUPPORTED otherwise).  il_release_scratch frees it.  A graph keeps using
+ * the workspace of the stream it was captured on: see "Graphs" at il_matmul_batch.
  */
 int il_kv_attend(const il_kv* kv, const float* q, int64_t q_stride, const int32_t* table, int64_t table_stride,
                  int64_t table_width, const int32_t* lens, int64_t n_seq, int64_t n_q_heads, float scale,
@@ -433,7 +440,8 @@ int il_check_device_status(void* stream);
  * bf16 copy of x, the split-K workspace, the LM-head scratch, the device copies
  * of x and y of il_matmul_batch_host, the K/V workspace), in stream order:
  * call it before destroying a stream the library has run on (for
- * cudaStreamPerThread on the thread itself, before it ends).  A later call on
+ * cudaStreamPerThread on the thread itself, before it ends).  Graphs captured on the
+ * stream must not be replayed any more.  A later call on
  * the stream allocates afresh.  Returns IL_OK or IL_ERR_CUDA. */
 int il_release_scratch(void* stream);
 

@@ -482,7 +482,10 @@ def kv_attend(cache: KVCache, q, table, lens, out, lse=None, scale=None, window:
 
     ``q``, ``out``: fp32 ``[n_seq][n_q_heads][head_dim]`` (sequences may be apart); ``table``, ``lens`` as
     :func:`kv_extend` leaves them; ``lse``: fp32 ``[n_seq][n_q_heads]`` or None; ``scale`` defaults
-    to ``head_dim ** -0.5``; ``window``: tokens seen, counted from the end (0: all)."""
+    to ``head_dim ** -0.5``; ``window``: tokens seen, counted from the end (0: all).
+
+    A captured call uses the workspace of the stream it was captured on: graphs of one capture stream, and calls
+    on that stream, must not run side by side."""
     import torch
     if q.dim() != 3:
         raise ILError(-1, "q must be [n_seq][n_q_heads][head_dim]")
@@ -503,7 +506,8 @@ def check_device_status(stream=None) -> None:
 
 
 def release_scratch(stream=None) -> None:
-    """``il_release_scratch``: frees the library's scratch for ``stream`` (stream-ordered)."""
+    """``il_release_scratch``: frees the library's scratch for ``stream`` (stream-ordered); graphs captured on
+    the stream must not be replayed any more."""
     _check(load().il_release_scratch(_stream_ptr(stream)))
 
 

@@ -109,3 +109,58 @@ def test_threads_at_once_on_their_streams(sil):
         sil.release_scratch(PER_THREAD)
         return same
     assert _on_threads(4, work) == [True] * 4
+
+
+def _graph(call, out, stream):
+    import torch
+    with torch.cuda.stream(stream):
+        call(out, stream)  # the workspace exists before the capture
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            for _ in range(10):
+                call(out, stream)
+    return graph
+
+
+def test_graphs_of_streams_of_their_own_side_by_side(sil):
+    # a graph uses the workspace of its capture stream, wherever it is replayed
+    import torch
+    cases = [_attend_case(sil, seed) for seed in (5, 6)]
+    outs = [torch.empty_like(want) for _, want in cases]
+    captured_on = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    graphs = [_graph(call, out, s) for (call, _), out, s in zip(cases, outs, captured_on)]
+    for o in outs:
+        o.fill_(7.0)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g in graphs:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                g.replay()
+        torch.cuda.synchronize()
+        for (_, want), o in zip(cases, outs):
+            assert torch.equal(o, want)
+            o.fill_(7.0)
+        torch.cuda.synchronize()
+
+
+def test_graphs_of_one_stream_one_after_the_other(sil):
+    import torch
+    cases = [_attend_case(sil, seed) for seed in (7, 8)]
+    outs = [torch.empty_like(want) for _, want in cases]
+    stream, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graphs = [_graph(call, out, stream) for (call, _), out in zip(cases, outs)]
+    for _ in range(5):
+        for o in outs:
+            o.fill_(7.0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            graphs[0].replay()
+        other.wait_stream(stream)
+        with torch.cuda.stream(other):
+            graphs[1].replay()
+        torch.cuda.synchronize()
+        for (_, want), o in zip(cases, outs):
+            assert torch.equal(o, want)
