@@ -83,6 +83,7 @@ class AttentionBlock:
     def capture(self):
         """A graph of :meth:`step`.  One step runs first, so that the library's workspaces exist, and is taken back."""
         stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())  # for the prompts' last kv_append, and x
         with torch.cuda.stream(stream):
             self.step()
             sil.kv_extend(self.lens, -self.one, self.table, self.ring, self.cursor, self.page, self.slots)
