@@ -371,7 +371,8 @@ int il_kv_read(const il_kv* kv, const int32_t* slots, int64_t n, float* k, int64
  * over t in [max(0, len - window), len), query head h reading K/V head
  * h / (n_q_heads / n_heads).  The new token itself is one of the len (append it first).
  *   q      : fp32 [n_seq][n_q_heads][head_dim], sequences q_stride apart; 16-byte aligned,
- *            q_stride a multiple of 4.         out: likewise with out_stride, overwritten.
+ *            q_stride a multiple of 4.         out: likewise with out_stride, overwritten; apart
+ *            from q, or columns of the same buffer beside it.
  *   lse    : fp32 [n_seq][n_q_heads] or NULL.
  *   table, table_stride, table_width, lens : as il_kv_extend leaves them.  A length is cut to
  *            0 .. table_width * page_size.

@@ -3,6 +3,7 @@
 // prepared before it is enqueued, as in the matmul entry points.
 #include <algorithm>
 #include <cstdio>
+#include <cstdlib>
 #include <cstring>
 #include <vector>
 
@@ -38,6 +39,13 @@ bool clash(const Range& a, const Range& b) {
   if (a.p == nullptr || b.p == nullptr || a.bytes <= 0 || b.bytes <= 0 || !(a.written || b.written)) return false;
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
   return a0 < b0 + (uintptr_t)b.bytes && b0 < a0 + (uintptr_t)a.bytes;
+}
+
+// Whether n rows of `row` floats at a and at b lie side by side, as columns of one buffer.
+bool side_by_side(const float* a, int64_t a_stride, const float* b, int64_t b_stride, int64_t n, int64_t row) {
+  if (n <= 1 || a_stride != b_stride || a_stride <= 0) return false;
+  const int64_t apart = std::abs((int64_t)(reinterpret_cast<intptr_t>(a) - reinterpret_cast<intptr_t>(b))) / 4 % a_stride;
+  return apart >= row && a_stride - apart >= row;
 }
 
 // Strides of one pool: positive multiples of `unit`, at least a row where the dimension has
@@ -131,12 +139,8 @@ int rows_call(const char* fn, bool write, const il_kv* kv, float* k, int64_t k_s
     for (const Range& r : {kr, vr, sr})
       if (clash(c, r)) return bad(IL_ERR_ARG, fn, "k, v and slots must not overlap the cache");
   if (clash(kr, sr) || clash(vr, sr)) return bad(IL_ERR_ARG, fn, "k and v must not overlap slots");
-  if (!write && clash(kr, vr)) {
-    const int64_t apart = std::abs((int64_t)(reinterpret_cast<intptr_t>(k) - reinterpret_cast<intptr_t>(v))) / 4;
-    const int64_t in_row = k_stride > 0 ? apart % k_stride : 0;
-    if (n == 1 || k_stride != v_stride || in_row < row || k_stride - in_row < row)
-      return bad(IL_ERR_ARG, fn, "k and v must not overlap");
-  }
+  if (!write && clash(kr, vr) && !side_by_side(k, k_stride, v, v_stride, n, row))
+    return bad(IL_ERR_ARG, fn, "k and v must not overlap");
   int num_sms = 0;
   unsigned* status = nullptr;
   const int dev = api_device(&num_sms, &status);
@@ -275,7 +279,7 @@ int il_kv_attend(const il_kv* kv, const float* q, int64_t q_stride, const int32_
                        {a.kv.v_scale, extent_bytes(a.kv, true), false}};
   for (const Range& o : outs)
     for (const Range& i : ins)
-      if (clash(o, i)) return bad(IL_ERR_ARG, fn, "out and lse must not overlap q, table, lens or the cache");
+      if (clash(o, i) && !(&o == outs && &i == ins && side_by_side(out, os, q, qs, n_seq, row))) return bad(IL_ERR_ARG, fn, "out and lse must not overlap q, table, lens or the cache");
   if (clash(outs[0], outs[1])) return bad(IL_ERR_ARG, fn, "out and lse must not overlap");
   int num_sms = 0;
   const int dev = api_device(&num_sms, &a.status);
