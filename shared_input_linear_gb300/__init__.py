@@ -337,6 +337,11 @@ def dequantize_weight(w: Weight, out, stream=None) -> None:
 # ---------------------------------------------------------------------------
 # Paged K/V cache
 # ---------------------------------------------------------------------------
+def _steps(t):
+    """Strides of ``t``; 0 for a dimension of one entry, whose stride means nothing."""
+    return [st if n > 1 else 0 for n, st in zip(t.shape, t.stride())]
+
+
 class KVCache:
     """A paged K/V cache in the caller's tensors (``il_kv``); holds references to them.
 
@@ -348,7 +353,7 @@ class KVCache:
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         import torch
-        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+        if k.dim() != 4 or k.shape != v.shape or _steps(k) != _steps(v) or k.dtype != v.dtype:
             raise ILError(-1, "k and v must be [n_pages][page_size][n_heads][head_dim] of one shape, stride and dtype")
         if k.dtype not in (torch.bfloat16, torch.int8):
             raise ILError(-3, "the cache must be bfloat16 or int8")
@@ -369,7 +374,7 @@ class KVCache:
                 if (tuple(t.shape) != shape or t.dtype != torch.float32 or not t.is_cuda
                         or (shape[3] > 1 and t.stride(3) != 1)):
                     raise ILError(-1, f"scales must be CUDA float32 {list(shape)}, the last dimension contiguous")
-            if k_scale.stride()[:3] != v_scale.stride()[:3]:
+            if _steps(k_scale)[:3] != _steps(v_scale)[:3]:
                 raise ILError(-1, "k_scale and v_scale must have the same strides")
             c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
             c.scale_page_stride, c.scale_token_stride, c.scale_head_stride = k_scale.stride()[:3]
@@ -421,7 +426,7 @@ def _rows(t, n: int, heads: int, dim: int, f32, what: str):
 def _table(t, n_seq: int, i32):
     """(address, row stride, width) of an int32 block table."""
     shape, st = t.shape, t.stride()
-    if len(shape) != 2 or shape[0] != n_seq or st[1] != 1 or t.dtype is not i32 or not t.is_cuda:
+    if len(shape) != 2 or shape[0] != n_seq or (st[1] != 1 and shape[1] > 1) or t.dtype is not i32 or not t.is_cuda:
         raise ILError(-1, f"table must be CUDA int32 [{n_seq}][width] with contiguous rows")
     return t.data_ptr(), st[0], shape[1]
 
