@@ -1176,13 +1176,9 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
                   "two joins must fit what the ring and the parts took");
     const float* const rest = global_part(c0, 0);  // part i: of the row that came into CTA c0 + i
     const float* const head = global_part(c0, 1);  // part 0: of the row that CTA c0 left open
-    // A row's float4s over groups of threads, 12 loads at a time.  The parts are added up in 2 * half sums (of every
-    // 2 * half-th part), the sums in order: twice as many as half a CTA has groups, whoever joins the row -- the whole CTA,
-    // a group a sum, or half of it, a group two sums -- so that the bits do not depend on who arrives last.
-    const int wide = rows * WIDE;
-    const int half = wide > NT / 2 ? 0 : (unsigned)(NT / 2 / WIDE) / (unsigned)rows;  // 0: one sum, a thread a float4 or more
-    const bool two = both && half > 0;
-    const int groups = half == 0 ? 1 : both ? half : 2 * half, grp = groups == 1 ? 0 : tt / wide;
+    // The row's float4s over groups of threads; a group takes every groups-th part, 12 loads at a time.  As many groups as
+    // half a CTA has, also for a whole one: the order of the sums, and with it the bits, must not depend on who arrives last.
+    const int wide = rows * WIDE, groups = wide <= NT / 4 ? NT / 2 / wide : 1, grp = groups == 1 ? 0 : tt / wide;
     float* const weight = reinterpret_cast<float*>(ring_mem + which * kJoin);  // [rows][count]
     float* const stat = weight + rows * count;                 // [rows][2]: max, sum
     float4* const sums = reinterpret_cast<float4*>(weight + ((rows * (count + 2) + 3) & ~3));
@@ -1198,7 +1194,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
       const bool mine = e < wide && grp < groups;
       const int row = mine ? e / WIDE : 0, c = 4 * (e % WIDE);
       const int at = (c / W) * C::kPart + row * W + c % W;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), x2 = x;  // x2: the second of two sums, of every other part of the group
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
       for (int i0 = grp; i0 - grp < count; i0 += 12 * groups) {
         float4 y[12];
@@ -1240,17 +1236,14 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
 #pragma unroll
         for (int k = 0; k < 12; ++k) {
           const int i = min(i0 + k * groups, count - 1);  // past the last, y is 0
-          add(k % 2 != 0 && two ? x2 : x, y[k], weight[row * count + i]);
+          add(x, y[k], weight[row * count + i]);
         }
       }
-      if (two && half == 1) {
-        add(x, x2, 1.f);
-      } else if (half > 0) {  // the groups' sums in order
+      if (groups > 1) {  // the groups' sums in order
         if (mine) sums[tt] = x;
-        if (mine && two) sums[tt + half * wide] = x2;
         sync();
 #pragma unroll 1
-        for (int k = 1; k < 2 * half && grp == 0; ++k) add(x, sums[tt + k * wide], 1.f);
+        for (int k = 1; k < groups && grp == 0; ++k) add(x, sums[tt + k * wide], 1.f);
       }
       if (mine && grp == 0 && c < D)
         finish(s, (int64_t)hk * P.group + block * ROWS + row, c, x, stat[2 * row], stat[2 * row + 1]);
