@@ -387,8 +387,8 @@ int il_kv_read(const il_kv* kv, const int32_t* slots, int64_t n, float* k, int64
  * 21 or more of their 24 bits.  Over a Q8 cache an element of q keeps 22 bits, or 2^-38 of its
  * head's largest where that is coarser.  A weight p there multiplies V's scale d, in tiles of 16
  * or 32 tokens; p below is relative to the tile's largest, or to 2^-24 of the sequence's largest so
- * far where that is more.  p d keeps 22 bits, or 2^-28 d where that is coarser.  In a tile with p below
- * 2^-26 or d below 2^-10 of the sequence's largest so far, the second bound is 2^-12 of p times the
+ * far where that is more.  p d keeps 22 bits, or 2^-26 d where that is coarser.  In a tile with p below
+ * 2^-26 or d below 2^-12 of the sequence's largest so far, the second bound is 2^-12 of p times the
  * tile's largest d of the same 32 columns instead, and p below 2^-104 counts as 0.
  * Workspace: il_kv_extend and il_kv_attend share one of about 5 MB per (device, stream), owned by the library,
  * allocated (stream-ordered) by the first of these calls on the stream and never moved: run one before
