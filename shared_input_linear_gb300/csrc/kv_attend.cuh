@@ -34,10 +34,11 @@
 // FMAs (with the factor of the running maximum), which round to nearest.
 //
 // Measured (GB300, 32 query heads on 8 K/V heads of 128, device time): bf16, 128 sequences of 4096 tokens 315 us, 6.8 TB/s
-// (the rate of a plain copy); 32 of 0 to 8192 86 us, 6.0 TB/s; one of 512 8.3 us.  Q8, 64 of 1 to 8192 106 us, 5.5 TB/s,
+// (the rate of a plain copy); 32 of 0 to 8192 86 us, 6.0 TB/s; one of 512 8.1 us.  Q8, 64 of 1 to 8192 106 us, 5.6 TB/s,
 // one of 131071 59 us, 5.2 TB/s.  What bounds it: HBM at bf16 (64 sequences of 8192: 317 us, 263 us with pages that stay in
-// L2); at Q8 the arithmetic (208 us either way: about 520 instructions per 16 tokens and warp, 200 of them on the ALU
-// pipe, two warps a scheduler); of a short call the latencies before the first tile and in the joins.
+// L2); at Q8 no unit (207 us either way; issue slots 50 % used, ALU 44 %, tensor pipe 27 %, DRAM 65 %) but the chain of a tile
+// in a warp -- q K^T, maximum, exp2, split, p V -- at two warps a scheduler, about 520 instructions per 16 tokens; of
+// a short call the latencies before the first tile and in the joins.
 #pragma once
 
 #include <algorithm>
@@ -840,7 +841,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
         v_exp = max(v_exp, (int)(__reduce_max_sync(~0u, __float_as_uint(most)) >> 23));
         // fp16 parts of p d keep 2^-38 of the largest scale: 2^-26 of one that lies 2^12 below it.  A tile with smaller
         // ones takes its products in classes too, with each block's scales brought up to the largest (64 x 8192 tokens whose
-        // blocks lie further apart: 268 us, else 207).
+        // blocks lie further apart: 267 us, else 207).
         const float little = pow2_biased(v_exp - 12);
 #pragma unroll
         for (int b = 0; b < NB; ++b) wide |= fabsf(vs[b]) < little && vs[b] != 0.f;

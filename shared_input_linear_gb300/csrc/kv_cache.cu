@@ -25,8 +25,8 @@ namespace {
 // lengths come from L2) and then does its share of the tokens, which finds its sequence by a
 // binary search over the runs' sums in shared memory and a walk inside the run.  The state is
 // written where no CTA reads it any more: table entries taken, the ring's tail and separate
-// outputs at once, lens and cursor in place by the last CTA to finish.  Bound by latency.  Measured, device time:
-// 32 sequences by one token 3.1 us, 1024 sequences of a mixed batch (0.55 MB in all) 5.4 us.
+// outputs at once, lens and cursor in place by the last CTA to finish.  Measured, device time: 32 sequences by one token
+// 3.1 us, 1024 sequences of a mixed batch (0.55 MB in all) 5.5 us.
 constexpr int kExtendThreads = 512;
 constexpr int kExtendWarps = kExtendThreads / 32;
 
@@ -224,19 +224,18 @@ __global__ void __launch_bounds__(kExtendThreads) kv_extend_kernel(const KvExten
 // il_kv_append / il_kv_read
 // ---------------------------------------------------------------------------
 // One thread moves units of 8 elements of K and the same 8 of V (32 bytes of fp32 and 16 or 8 of the cache each).
-// Bound by HBM; at Q8 the arithmetic comes near it, so that:
+// Bound by HBM where there are many tokens; at Q8 the arithmetic comes near it, so that:
 // - q = round(w / d) is taken from w times an approximate 1 / d, which is off by at most 127 * (2^-23 + 2^-23) =
 //   3.1e-5, and by the definition's division only where the product lies within 5e-5 of half way between integers;
 // - a float's integer is read from its low byte after adding 1.5 * 2^23, and made from a byte by the reverse;
 // - the four lanes of a 32-element block share its largest |w| with two shuffles; d = amax / 127 is the IEEE
 //   division, so that d and q are the definition's bit for bit.
-// Bound by HBM where there are many tokens.  Measured (8 heads of 128, device time): append of 16384 tokens bf16 30.4 us,
-// 6.6 TB/s, Q8 31.3 us, 5.5 TB/s; of 4097 Q8 10.1 us; read of 16384 bf16 32.9 us, 6.1 TB/s, Q8 28.8 us, 6.0 TB/s, of 4097
-// Q8 9.2 us; append of one token 1.4 us.
+// Measured (8 heads of 128, device time): append of 16384 tokens bf16 30.4 us, 6.6 TB/s, Q8 31.3 us, 5.5 TB/s; of 4097 Q8
+// 10.0 us; read of 16384 bf16 32.9 us, 6.1 TB/s, Q8 28.8 us, 6.0 TB/s, of 4097 Q8 9.2 us; append of one token 1.3 us.
 constexpr int kRowThreads = 256;
 // Units of a thread at a time: two, all loads first, but for Q8's quantiser, where more warps hide its chains
-// better (4097 tokens of 8 x 128: 13.0 us with two, 11.0 us with one; bf16 append 9.6 and 9.2, Q8 read of
-// 16384 28.8 and 31.1).
+// better (when it was chosen, 4097 tokens of 8 x 128: 13.0 us with two, 11.0 us with one; bf16 append 9.6 and 9.2,
+// Q8 read of 16384 28.8 and 31.1).
 constexpr int row_units(bool write, bool q8) { return write && q8 ? 1 : 2; }
 
 struct RowArgs {
