@@ -36,8 +36,9 @@ extern "C" {
 
 #define IL_VERSION 3
 
-/* Storage format of a weight (oxinfer src/gpu.rs, enum WeightRef). */
-typedef enum { IL_BF16 = 0, IL_Q8 = 1, IL_Q4 = 2 } il_format;
+/* Storage format of a weight (oxinfer src/gpu.rs, enum WeightRef: the first three) or of a
+ * K/V cache (IL_BF16, IL_Q8 and IL_A4, which il_kv describes). */
+typedef enum { IL_BF16 = 0, IL_Q8 = 1, IL_Q4 = 2, IL_A4 = 3 } il_format;
 
 /* Status codes.  IL_OK is 0; every error is negative.  An entry point that
  * returns an error has launched no work and written no output. */
@@ -269,7 +270,8 @@ int il_centroid_head(const float* x, int64_t h, const il_weight* centroids, cons
  * x of the next batch, on the same stream, without a copy or a host round trip:
  *     il_kv_extend  block tables and slot maps from the sequences' lengths
  *     il_kv_append  k and v rows into the cache (and il_kv_read back)
- *     il_kv_attend  one new token's attention over each sequence's cache
+ *     il_kv_attend  one new token's attention over each sequence's cache (il_kv_attend_scored:
+ *                   with capped or biased logits, or from a later token on)
  * The cache is the caller's memory, described by value: n_pages pages of
  * page_size tokens.  A token's slot is page * page_size + its index in the page;
  * a sequence's block table lists its pages, so that its position p is in page
@@ -284,18 +286,21 @@ int il_centroid_head(const float* x, int64_t h, const il_weight* centroids, cons
 
 /* A paged cache.
  *   format   : IL_BF16, or IL_Q8 as the weights have it: int8 q and one fp32 scale
- *              d per 32 elements of head_dim, value fp32(d*q).
+ *              d per 32 elements of head_dim, value fp32(d*q), or IL_A4: u of 0 .. 15, two per byte,
+ *              element 2k in bits 0-3 of byte k, and one pair of bf16 {d, m} per 32 elements, value
+ *              fp32(d*u + m).  (The weights' Q4 has no offset; the channels of K seldom lie about 0.)
  *   page_size: tokens per page, 1 .. 2^20.      n_pages: 1 .., n_pages * page_size < 2^31.
  *   n_heads  : K/V heads, 1 .. 1024.
- *   head_dim : 8 .. 256, a multiple of 8 (IL_BF16) or of 32 (IL_Q8).
- *   k, v     : bf16 or int8 elements; (page, token, head, i) is at
- *              page*page_stride + token*token_stride + head*head_stride + i.  Any order of
- *              the three strides (64-bit offsets); 16-byte aligned rows: base
- *              address and strides times the element size are multiples of 16.
+ *   head_dim : 8 .. 256, a multiple of 8 (IL_BF16) or of 32 (IL_Q8, IL_A4).
+ *   k, v     : bf16 or int8 elements, or bytes of two; (page, token, head, i) is at
+ *              page*page_stride + token*token_stride + head*head_stride + i (IL_A4: strides in
+ *              bytes, and i / 2).  Any order of the three strides (64-bit offsets); 16-byte aligned
+ *              rows: base address and strides times the element size are multiples of 16.
  *   k_scale, v_scale : IL_Q8: fp32 scales, (page, token, head, i / 32) likewise with
- *              the scale_ strides, in floats (4-byte alignment); NULL for IL_BF16.
- * Strides of a dimension of extent 1 are not used; the others are at least
- * head_dim (scales: head_dim / 32).  Elements must not overlap. */
+ *              the scale_ strides, in floats (4-byte alignment); IL_A4: the pairs, 4 bytes each with d in the
+ *              lower half, in their place; NULL for IL_BF16.
+ * Strides of a dimension of extent 1 are not used; the others are at least a
+ * row (head_dim, IL_A4 head_dim / 2; scales: head_dim / 32).  Elements must not overlap. */
 typedef struct {
   int32_t format;
   int32_t page_size;
@@ -354,13 +359,17 @@ int il_kv_extend(int64_t n_seq, int64_t page_size, const int32_t* lens, const in
  * bf16 rounds to nearest even.  Q8: d = max|w| / 127 over the 32 elements, q = w / d
  * rounded to nearest even (IEEE divisions, as the weights' test quantiser); a block of
  * zeros has d = 0, q = 0; a block with a NaN or an infinity reads back as NaN.
+ * IL_A4: m is the least of the 32 elements rounded down to bf16, d = (max - m) / 15 rounded up to bf16,
+ * u = (w - m) / d rounded to nearest even and cut to 0 .. 15 (IEEE single operations each); u = 0 where
+ * d = 0, and a block with a NaN, an infinity or a range beyond bf16 reads back as NaN.  A value is off by
+ * at most d / 2 and a rounding; d is at most (1 + 2^-7) ((max - min) + 2^-7 |min|) / 15.
  */
 int il_kv_append(const il_kv* kv, const float* k, int64_t k_stride, const float* v, int64_t v_stride,
                  const int32_t* slots, int64_t n, void* stream);
 
 /*
  * il_kv_read -- the inverse of il_kv_append: the cached values of n slots as fp32 (exact
- * for bf16, fp32(d*q) for Q8), rows of a negative slot as zeros.  k, v as above, written.
+ * for bf16, fp32(d*q) for Q8, fp32(d*u + m) for A4), rows of a negative slot as zeros.  k, v as above, written.
  */
 int il_kv_read(const il_kv* kv, const int32_t* slots, int64_t n, float* k, int64_t k_stride, float* v,
                int64_t v_stride, void* stream);
@@ -389,7 +398,9 @@ int il_kv_read(const il_kv* kv, const int32_t* slots, int64_t n, float* k, int64
  * or 32 tokens; p below is relative to the tile's largest, or to 2^-24 of the sequence's largest so
  * far where that is more.  p d keeps 22 bits, or 2^-26 d where that is coarser.  In a tile with p below
  * 2^-26 or d below 2^-12 of the sequence's largest so far, the second bound is 2^-12 of p times the
- * tile's largest d of the same 32 columns instead, and p below 2^-104 counts as 0.
+ * tile's largest d of the same 32 columns instead, and p below 2^-104 counts as 0.  Over an A4 cache an element of q
+ * keeps 22 bits, or 2^-49 of its head's largest where that is coarser, and p d keeps 22 bits, or 2^-49 of the sequence's
+ * largest so far; in a tile with p below 2^-26 or d below 2^-12 of those, 22 bits down to 2^-104 of it, where it counts as 0.
  * Workspace: il_kv_extend and il_kv_attend share one of about 5 MB per (device, stream), owned by the library,
  * allocated (stream-ordered) by the first of these calls on the stream and never moved: run one before
  * capturing the stream (IL_ERR_UNSUPPORTED otherwise).  il_release_scratch frees it.  A graph keeps using
@@ -398,6 +409,32 @@ int il_kv_read(const il_kv* kv, const int32_t* slots, int64_t n, float* k, int64
 int il_kv_attend(const il_kv* kv, const float* q, int64_t q_stride, const int32_t* table, int64_t table_stride,
                  int64_t table_width, const int32_t* lens, int64_t n_seq, int64_t n_q_heads, float scale,
                  int64_t window, float* out, int64_t out_stride, float* lse, void* stream);
+
+/* What il_kv_attend_scored does to a logit, scale q_h . k_t at first; all of it zero or NULL: nothing.
+ *   cap       : > 0: s = cap tanh(s / cap).
+ *   slopes    : fp32 [n_q_heads] or NULL: then s += slopes[h] (pos_t - pos_last), a bias that grows with the
+ *               distance from the sequence's last token.
+ *   starts    : int32 [n_seq] or NULL: tokens before starts[r] are not seen (the first token of the document that
+ *               the new token belongs to); negative: all are, len or more: none is.
+ *   positions : int32 [n_seq][positions_width], rows positions_stride apart, or NULL (a token's position is its index):
+ *               positions of the tokens where il_kv_evict has moved them.  A length is cut to positions_width.
+ * cap, scale / cap and slopes must be finite. */
+typedef struct {
+  float cap;
+  const float* slopes;
+  const int32_t* starts;
+  const int32_t* positions;
+  int64_t positions_stride, positions_width;
+} il_kv_score;
+
+/*
+ * il_kv_attend_scored -- il_kv_attend with capped and biased logits and sequences that begin later.  The window
+ * counts by index; with starts, a token is seen that both allow.  A sequence of which no token is seen gives out = 0 and
+ * lse = -inf.  The cap and the bias are fp32: a logit's error is that of tanhf times cap, and a rounding of the bias.
+ */
+int il_kv_attend_scored(const il_kv* kv, const float* q, int64_t q_stride, const int32_t* table, int64_t table_stride,
+                        int64_t table_width, const int32_t* lens, int64_t n_seq, int64_t n_q_heads, float scale,
+                        int64_t window, const il_kv_score* score, float* out, int64_t out_stride, float* lse, void* stream);
 
 /* 1 if the handle came from il_upload_gate_up, 0 if from il_upload_weight,
  * -1 for an invalid handle. */

@@ -17,13 +17,14 @@ import threading
 
 import numpy as np
 
-__all__ = ["ILError", "Weight", "FORMATS", "IL_BF16", "IL_Q8", "IL_Q4", "load", "build",
+__all__ = ["ILError", "Weight", "FORMATS", "KV_FORMATS", "IL_BF16", "IL_Q8", "IL_Q4", "IL_A4", "load", "build",
            "upload_weight", "matmul_batch", "matmul_batch_ptr", "matmul_batch_noalloc_ptr", "free_weight", "weight_bytes",
            "dequantize_weight", "check_device_status", "release_scratch", "get_stats", "reset_stats", "last_error",
            "version", "LIB_PATH", "STATUS", "KVCache", "kv_cache", "kv_extend", "kv_append", "kv_read", "kv_attend"]
 
-IL_BF16, IL_Q8, IL_Q4 = 0, 1, 2
+IL_BF16, IL_Q8, IL_Q4, IL_A4 = 0, 1, 2, 3
 FORMATS = {"bf16": IL_BF16, "q8": IL_Q8, "q4": IL_Q4}
+KV_FORMATS = {"bf16": IL_BF16, "q8": IL_Q8, "a4": IL_A4}
 STATUS = {0: "IL_OK", -1: "IL_ERR_ARG", -2: "IL_ERR_SHAPE", -3: "IL_ERR_FORMAT",
           -4: "IL_ERR_HANDLE", -5: "IL_ERR_OOM", -6: "IL_ERR_CUDA",
           -7: "IL_ERR_DEVICE_TIMEOUT", -8: "IL_ERR_UNSUPPORTED"}
@@ -56,6 +57,11 @@ class _KV(ctypes.Structure):
                 + [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
                 + [(n, ctypes.c_int64) for n in ("page_stride", "token_stride", "head_stride", "scale_page_stride",
                                                  "scale_token_stride", "scale_head_stride")])
+
+
+class _Score(ctypes.Structure):
+    _fields_ = ([("cap", ctypes.c_float)] + [(n, ctypes.c_void_p) for n in ("slopes", "starts", "positions")]
+                + [(n, ctypes.c_int64) for n in ("positions_stride", "positions_width")])
 
 
 _lib = None
@@ -99,6 +105,8 @@ def load() -> ctypes.CDLL:
         lib.il_kv_read.restype = ci
         lib.il_kv_attend.argtypes = [vp, vp, i64, vp, i64, i64, vp, i64, i64, ctypes.c_float, i64, vp, i64, vp, vp]
         lib.il_kv_attend.restype = ci
+        lib.il_kv_attend_scored.argtypes = [vp, vp, i64, vp, i64, i64, vp, i64, i64, ctypes.c_float, i64, vp, vp, i64, vp, vp]
+        lib.il_kv_attend_scored.restype = ci
         lib.il_weight_is_gate_up.argtypes = [vp]
         lib.il_weight_is_gate_up.restype = ci
         lib.il_free_weight.argtypes = [vp]
@@ -348,36 +356,43 @@ class KVCache:
     ``k``, ``v``: CUDA ``[n_pages][page_size][n_heads][head_dim]`` of one shape and one set of
     strides, the last dimension contiguous; pass ``pool.transpose(1, 2)`` of a pool stored
     head-major.  ``torch.bfloat16`` is IL_BF16; ``torch.int8`` is IL_Q8 with fp32 ``k_scale``,
-    ``v_scale`` ``[n_pages][page_size][n_heads][head_dim / 32]``.  :func:`kv_cache` allocates one.
+    ``v_scale`` ``[n_pages][page_size][n_heads][head_dim / 32]``; ``torch.uint8`` is IL_A4, two elements a byte
+    (a last dimension of ``head_dim / 2``), with bfloat16 ``k_scale``, ``v_scale``
+    ``[n_pages][page_size][n_heads][head_dim / 32][2]``, the pairs (d, m).  :func:`kv_cache` allocates one.
     """
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         import torch
         if k.dim() != 4 or k.shape != v.shape or _steps(k) != _steps(v) or k.dtype != v.dtype:
             raise ILError(-1, "k and v must be [n_pages][page_size][n_heads][head_dim] of one shape, stride and dtype")
-        if k.dtype not in (torch.bfloat16, torch.int8):
-            raise ILError(-3, "the cache must be bfloat16 or int8")
+        formats = {torch.bfloat16: IL_BF16, torch.int8: IL_Q8, torch.uint8: IL_A4}
+        if k.dtype not in formats:
+            raise ILError(-3, "the cache must be bfloat16, int8 or uint8")
         if k.stride(3) != 1:
             raise ILError(-1, "the last dimension of k and v must be contiguous")
         if not (k.is_cuda and v.is_cuda):
             raise ILError(-1, "k and v must be CUDA tensors")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.page_size, self.n_heads, self.head_dim = k.shape
-        self.format = IL_BF16 if k.dtype == torch.bfloat16 else IL_Q8
+        self.format = formats[k.dtype]
+        pairs = self.format == IL_A4
+        if pairs:
+            self.head_dim *= 2
         c = self._c = _KV(self.format, self.page_size, self.n_pages, self.n_heads, self.head_dim, k.data_ptr(),
                           v.data_ptr(), None, None, *k.stride()[:3], 0, 0, 0)
-        if (self.format == IL_Q8) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
-            raise ILError(-1, "an int8 cache needs k_scale and v_scale, a bfloat16 cache has none")
+        if (self.format != IL_BF16) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+            raise ILError(-1, "an int8 or uint8 cache needs k_scale and v_scale, a bfloat16 cache has none")
         if k_scale is not None:
-            shape = (*k.shape[:3], self.head_dim // 32)
+            shape = (*k.shape[:3], self.head_dim // 32) + ((2,) if pairs else ())
+            dtype = torch.bfloat16 if pairs else torch.float32
             for t in (k_scale, v_scale):
-                if (tuple(t.shape) != shape or t.dtype != torch.float32 or not t.is_cuda
-                        or (shape[3] > 1 and t.stride(3) != 1)):
-                    raise ILError(-1, f"scales must be CUDA float32 {list(shape)}, the last dimension contiguous")
+                if (tuple(t.shape) != shape or t.dtype != dtype or not t.is_cuda or (shape[3] > 1 and t.stride(3) != len(shape) - 3)
+                        or (pairs and (t.stride(4) != 1 or any(s % 2 for s in _steps(t)[:3])))):
+                    raise ILError(-1, f"scales must be CUDA {dtype} {list(shape)}, the last dimension{'s' * pairs} contiguous")
             if _steps(k_scale)[:3] != _steps(v_scale)[:3]:
                 raise ILError(-1, "k_scale and v_scale must have the same strides")
             c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
-            c.scale_page_stride, c.scale_token_stride, c.scale_head_stride = k_scale.stride()[:3]
+            c.scale_page_stride, c.scale_token_stride, c.scale_head_stride = (s >> pairs for s in k_scale.stride()[:3])
         self._ref = ctypes.addressof(c)
 
     @property
@@ -390,14 +405,15 @@ def kv_cache(fmt, n_pages: int, page_size: int, n_heads: int, head_dim: int, dev
     """A zeroed :class:`KVCache`, stored head-major within a page: a head's tokens of one page
     are one contiguous run."""
     import torch
-    q8 = _fmt(fmt) == IL_Q8
-    if not q8 and _fmt(fmt) != IL_BF16:
-        raise ILError(-3, "the cache must be bf16 or q8")
+    f = KV_FORMATS.get(fmt, fmt) if isinstance(fmt, str) else fmt
+    if f not in KV_FORMATS.values():
+        raise ILError(-3, "the cache must be bf16, q8 or a4")
 
-    def pool(last, dtype):
-        return torch.zeros((n_pages, n_heads, page_size, last), dtype=dtype, device=device).transpose(1, 2)
-    kv = [pool(head_dim, torch.int8 if q8 else torch.bfloat16) for _ in range(2)]
-    return KVCache(*kv, *([pool(head_dim // 32, torch.float32) for _ in range(2)] if q8 else []))
+    def pool(dtype, *last):
+        return torch.zeros((n_pages, n_heads, page_size, *last), dtype=dtype, device=device).transpose(1, 2)
+    row = {IL_BF16: (torch.bfloat16, head_dim), IL_Q8: (torch.int8, head_dim), IL_A4: (torch.uint8, head_dim // 2)}[f]
+    scales = {IL_BF16: None, IL_Q8: (torch.float32, head_dim // 32), IL_A4: (torch.bfloat16, head_dim // 32, 2)}[f]
+    return KVCache(*(pool(*row) for _ in range(2)), *(pool(*scales) for _ in range(2) if scales))
 
 
 def _ptr(t, dtype, numel, what: str):
@@ -423,11 +439,11 @@ def _rows(t, n: int, heads: int, dim: int, f32, what: str):
     return t.data_ptr(), st[0]
 
 
-def _table(t, n_seq: int, i32):
-    """(address, row stride, width) of an int32 block table."""
+def _table(t, n_seq: int, dtype, what: str = "table"):
+    """(address, row stride, width) of a row a sequence: a block table, positions, weights."""
     shape, st = t.shape, t.stride()
-    if len(shape) != 2 or shape[0] != n_seq or (st[1] != 1 and shape[1] > 1) or t.dtype is not i32 or not t.is_cuda:
-        raise ILError(-1, f"table must be CUDA int32 [{n_seq}][width] with contiguous rows")
+    if len(shape) != 2 or shape[0] != n_seq or (st[1] != 1 and shape[1] > 1) or t.dtype is not dtype or not t.is_cuda:
+        raise ILError(-1, f"{what} must be CUDA {dtype} [{n_seq}][width] with contiguous rows")
     return t.data_ptr(), st[0], shape[1]
 
 
@@ -482,12 +498,28 @@ def kv_read(cache: KVCache, slots, k, v, stream=None) -> None:
         _check(rc)
 
 
-def kv_attend(cache: KVCache, q, table, lens, out, lse=None, scale=None, window: int = 0, stream=None) -> None:
+def _score(n: int, heads: int, cap: float, slopes, starts, positions):
+    """An ``il_kv_score``, or None where nothing of it is set."""
+    if not cap and slopes is None and starts is None:
+        return None
+    import torch
+    c = _Score(cap, _ptr(slopes, torch.float32, heads, "slopes"), _ptr(starts, torch.int32, n, "starts"), 0, 0, 0)
+    if positions is not None:
+        c.positions, c.positions_stride, c.positions_width = _table(positions, n, torch.int32, "positions")
+    return c
+
+
+def kv_attend(cache: KVCache, q, table, lens, out, lse=None, scale=None, window: int = 0, stream=None, cap: float = 0.0,
+              slopes=None, starts=None, positions=None) -> None:
     """``il_kv_attend``: attention of one token per sequence over its cached tokens.
 
     ``q``, ``out``: fp32 ``[n_seq][n_q_heads][head_dim]`` (sequences may be apart); ``table``, ``lens`` as
     :func:`kv_extend` leaves them; ``lse``: fp32 ``[n_seq][n_q_heads]`` or None; ``scale`` defaults
     to ``head_dim ** -0.5``; ``window``: tokens seen, counted from the end (0: all).
+
+    ``il_kv_attend_scored`` with one of these: ``cap``: logits are ``cap * tanh(s / cap)``; ``slopes`` fp32
+    ``[n_q_heads]``: a bias of ``slopes[h]`` times the distance from the last token (a negative number), by index or by
+    ``positions`` int32 ``[n_seq][width]``; ``starts`` int32 ``[n_seq]``: the first token seen.
 
     A captured call uses the workspace of the stream it was captured on: graphs of one capture stream, and calls
     on that stream, must not run side by side."""
@@ -499,9 +531,14 @@ def kv_attend(cache: KVCache, q, table, lens, out, lse=None, scale=None, window:
     qp, qs = _rows(q, n, heads, dim, f32, "q")
     op, os_ = _rows(out, n, heads, dim, f32, "out")
     tp, ts, tw = _table(table, n, i32)
-    rc = (_lib or load()).il_kv_attend(cache._ref, qp, qs, tp, ts, tw, _ptr(lens, i32, n, "lens"), n, heads,
-                                       dim ** -0.5 if scale is None else scale, window, op, os_,
-                                       _ptr(lse, f32, n * heads, "lse"), _stream_ptr(stream))
+    lp, ep, stream = _ptr(lens, i32, n, "lens"), _ptr(lse, f32, n * heads, "lse"), _stream_ptr(stream)
+    scale = dim ** -0.5 if scale is None else scale
+    score = _score(n, heads, cap, slopes, starts, positions)
+    if score is None:
+        rc = (_lib or load()).il_kv_attend(cache._ref, qp, qs, tp, ts, tw, lp, n, heads, scale, window, op, os_, ep, stream)
+    else:
+        rc = (_lib or load()).il_kv_attend_scored(cache._ref, qp, qs, tp, ts, tw, lp, n, heads, scale, window,
+                                                  ctypes.addressof(score), op, os_, ep, stream)
     if rc:
         _check(rc)
 

@@ -370,8 +370,8 @@ struct KvView {
   int64_t n_pages;
   uint8_t *k, *v;
   float *k_scale, *v_scale;
-  int64_t page, token, head;     // strides in elements
-  int64_t spage, stoken, shead;  // strides of the scales in floats
+  int64_t page, token, head;     // strides in elements (A4: in bytes)
+  int64_t spage, stoken, shead;  // strides of the scales in floats (A4: in {d, m})
 };
 
 struct KvExtendArgs {
@@ -405,6 +405,12 @@ struct KvAttendArgs {
   int64_t out_stride;
   float* lse;
   unsigned* status;
+  // il_kv_score, where `scored`
+  int scored;
+  float cap;
+  const float* slopes;
+  const int32_t *starts, *positions;
+  int64_t positions_stride, positions_width;
 };
 
 cudaError_t prepare_kv_extend(const KvExtendArgs& a, int num_sms, Launch* out);

@@ -1,5 +1,5 @@
 // il_kv.cu -- entry points of the paged K/V cache (include/il.h: il_kv_extend, il_kv_append,
-// il_kv_read, il_kv_attend): every argument that the host can see is checked and the launch
+// il_kv_read, il_kv_attend, il_kv_attend_scored): every argument that the host can see is checked and the launch
 // prepared before it is enqueued, as in the matmul entry points.
 #include <algorithm>
 #include <cstdio>
@@ -56,21 +56,24 @@ bool stride_ok(int64_t s, int64_t extent, int64_t row, int64_t unit) {
 
 int check_cache(const char* fn, const il_kv* kv, KvView* out) {
   if (kv == nullptr) return bad(IL_ERR_ARG, fn, "kv is NULL");
-  if (kv->format != IL_BF16 && kv->format != IL_Q8) return bad(IL_ERR_FORMAT, fn, "the cache must be IL_BF16 or IL_Q8");
-  const bool q8 = kv->format == IL_Q8;
+  if (kv->format != IL_BF16 && kv->format != IL_Q8 && kv->format != IL_A4)
+    return bad(IL_ERR_FORMAT, fn, "the cache must be IL_BF16, IL_Q8 or IL_A4");
+  const bool blocks_of_32 = kv->format != IL_BF16;
   if (kv->page_size < 1 || kv->page_size > (1 << 20) || kv->n_pages < 1 || kv->n_pages > INT32_MAX / kv->page_size)
     return bad(IL_ERR_SHAPE, fn, "page_size or n_pages out of range");
   if (kv->n_heads < 1 || kv->n_heads > 1024) return bad(IL_ERR_SHAPE, fn, "n_heads out of range");
-  if (kv->head_dim < 8 || kv->head_dim > kMaxKvDim || kv->head_dim % (q8 ? 32 : 8) != 0)
-    return bad(IL_ERR_SHAPE, fn, "head_dim must be at most 256 and a multiple of 8 (bf16) or of 32 (Q8)");
+  if (kv->head_dim < 8 || kv->head_dim > kMaxKvDim || kv->head_dim % (blocks_of_32 ? 32 : 8) != 0)
+    return bad(IL_ERR_SHAPE, fn, "head_dim must be at most 256 and a multiple of 8 (bf16) or of 32 (Q8, A4)");
   if (kv->k == nullptr || kv->v == nullptr) return bad(IL_ERR_ARG, fn, "the cache's k or v is NULL");
   if (!aligned(kv->k, 16) || !aligned(kv->v, 16)) return bad(IL_ERR_ARG, fn, "the cache's k or v is not 16-byte aligned");
-  const int64_t unit = q8 ? 16 : 8, dim = kv->head_dim, blocks = dim / 32;
-  if (!stride_ok(kv->page_stride, kv->n_pages, dim, unit) || !stride_ok(kv->token_stride, kv->page_size, dim, unit) ||
-      !stride_ok(kv->head_stride, kv->n_heads, dim, unit))
+  const int64_t unit = blocks_of_32 ? 16 : 8, blocks = kv->head_dim / 32;
+  const int64_t row = kv->format == IL_A4 ? kv->head_dim / 2 : kv->head_dim;  // in what the strides count
+  if (!stride_ok(kv->page_stride, kv->n_pages, row, unit) || !stride_ok(kv->token_stride, kv->page_size, row, unit) ||
+      !stride_ok(kv->head_stride, kv->n_heads, row, unit))
     return bad(IL_ERR_SHAPE, fn, "a stride of the cache is smaller than a row or not a multiple of 16 bytes");
-  if (q8) {
-    if (kv->k_scale == nullptr || kv->v_scale == nullptr) return bad(IL_ERR_ARG, fn, "a Q8 cache needs k_scale and v_scale");
+  if (blocks_of_32) {
+    if (kv->k_scale == nullptr || kv->v_scale == nullptr)
+      return bad(IL_ERR_ARG, fn, "a Q8 or A4 cache needs k_scale and v_scale");
     if (!aligned(kv->k_scale, 4) || !aligned(kv->v_scale, 4))
       return bad(IL_ERR_ARG, fn, "the cache's scales are not 4-byte aligned");
     if (!stride_ok(kv->scale_page_stride, kv->n_pages, blocks, 1) ||
@@ -100,11 +103,12 @@ int check_cache(const char* fn, const il_kv* kv, KvView* out) {
   return IL_OK;
 }
 
-// Byte extent of a pool (elements of `size` bytes, rows of `row` elements).
+// Byte extent of a pool.
 int64_t extent_bytes(const KvView& w, bool scales) {
   const int64_t last = (w.n_pages - 1) * (scales ? w.spage : w.page) + (w.page_size - 1) * (scales ? w.stoken : w.token) +
                        (w.n_heads - 1) * (scales ? w.shead : w.head);
-  return scales ? 4 * (last + w.head_dim / 32) : (w.format == IL_BF16 ? 2 : 1) * (last + w.head_dim);
+  if (scales) return 4 * (last + w.head_dim / 32);
+  return w.format == IL_BF16 ? 2 * (last + w.head_dim) : last + (w.format == IL_A4 ? w.head_dim / 2 : w.head_dim);
 }
 
 int enqueue(const char* fn, const Launch& L, void* stream) {
@@ -147,6 +151,100 @@ int rows_call(const char* fn, bool write, const il_kv* kv, float* k, int64_t k_s
   if (dev < 0) return dev;
   Launch L;
   const cudaError_t e = prepare_kv_rows(write, w, k, k_stride, v, v_stride, slots, n, status, num_sms, &L);
+  if (e != cudaSuccess) return api_cuda_fail(e, fn);
+  return enqueue(fn, L, stream);
+}
+
+// The parts of a score into `a` (nothing where score is nullptr).
+int check_score(const char* fn, const il_kv_score* score, float scale, int64_t n_seq, KvAttendArgs* a) {
+  if (score == nullptr) return IL_OK;
+  const il_kv_score& c = *score;
+  if (!(c.cap >= 0.0f) || !(c.cap - c.cap == 0.0f)) return bad(IL_ERR_ARG, fn, "cap is negative or not finite");
+  if (c.cap > 0.0f && !(scale / c.cap - scale / c.cap == 0.0f)) return bad(IL_ERR_ARG, fn, "scale / cap is not finite");
+  if (!aligned(c.slopes, 4) || !aligned(c.starts, 4) || !aligned(c.positions, 4))
+    return bad(IL_ERR_ARG, fn, "slopes, starts or positions is not 4-byte aligned");
+  if (c.positions != nullptr &&
+      (c.positions_width < 1 || c.positions_width > INT32_MAX ||
+       (n_seq > 1 && (c.positions_stride < c.positions_width || c.positions_stride > INT32_MAX))))
+    return bad(IL_ERR_SHAPE, fn, "positions_width or positions_stride out of range");
+  a->scored = c.cap > 0.0f || c.slopes != nullptr || c.starts != nullptr;
+  a->cap = c.cap;
+  a->slopes = c.slopes;
+  a->starts = c.starts;
+  if (c.positions != nullptr) {
+    a->positions = c.positions;
+    a->positions_width = c.positions_width;
+    a->positions_stride = n_seq > 1 ? c.positions_stride : 0;
+  }
+  return IL_OK;
+}
+
+// score: nullptr, or what il_kv_attend_scored adds.
+int attend_call(const char* fn, const il_kv* kv, const float* q, int64_t q_stride, const int32_t* table, int64_t table_stride,
+                int64_t table_width, const int32_t* lens, int64_t n_seq, int64_t n_q_heads, float scale, int64_t window,
+                const il_kv_score* score, float* out, int64_t out_stride, float* lse, void* stream) {
+  NvtxRange range(fn);
+  api_clear_error();
+  KvAttendArgs a;
+  memset(&a, 0, sizeof a);
+  int rc = check_cache(fn, kv, &a.kv);
+  if (rc != IL_OK) return rc;
+  if (n_seq < 0 || n_seq > kMaxKvSeqs) return bad(IL_ERR_ARG, fn, "n_seq out of range");
+  if (n_q_heads < 1 || n_q_heads > 32768 || n_q_heads % a.kv.n_heads != 0)
+    return bad(IL_ERR_SHAPE, fn, "n_q_heads must be a multiple of the cache's n_heads, at most 32768");
+  if (window < 0) return bad(IL_ERR_ARG, fn, "window is negative");
+  if (!(scale - scale == 0.0f)) return bad(IL_ERR_ARG, fn, "scale is not finite");
+  rc = check_score(fn, score, scale, n_seq, &a);
+  if (rc != IL_OK || n_seq == 0) return rc;
+  if (q == nullptr || table == nullptr || lens == nullptr || out == nullptr)
+    return bad(IL_ERR_ARG, fn, "q, table, lens and out must not be NULL");
+  if (!aligned(q, 16) || !aligned(out, 16)) return bad(IL_ERR_ARG, fn, "q or out is not 16-byte aligned");
+  if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(lse, 4))
+    return bad(IL_ERR_ARG, fn, "table, lens or lse is not 4-byte aligned");
+  const int64_t row = n_q_heads * a.kv.head_dim;
+  if (n_seq > 1 && (q_stride < row || out_stride < row || q_stride % 4 != 0 || out_stride % 4 != 0 ||
+                    q_stride > INT64_MAX / 8 / n_seq || out_stride > INT64_MAX / 8 / n_seq))
+    return bad(IL_ERR_SHAPE, fn, "q_stride or out_stride is smaller than a row or not a multiple of 4");
+  if (table_width < 1 || table_width > INT32_MAX || (n_seq > 1 && (table_stride < table_width || table_stride > INT32_MAX)))
+    return bad(IL_ERR_SHAPE, fn, "table_width or table_stride out of range");
+  const int64_t qs = n_seq > 1 ? q_stride : 0, os = n_seq > 1 ? out_stride : 0, ts = n_seq > 1 ? table_stride : 0;
+  const Range outs[] = {{out, 4 * ((n_seq - 1) * os + row), true}, {lse, 4 * n_seq * n_q_heads, true}};
+  const Range ins[] = {{q, 4 * ((n_seq - 1) * qs + row), false},
+                       {table, 4 * ((n_seq - 1) * ts + table_width), false},
+                       {lens, 4 * n_seq, false},
+                       {a.kv.k, extent_bytes(a.kv, false), false},
+                       {a.kv.v, extent_bytes(a.kv, false), false},
+                       {a.kv.k_scale, extent_bytes(a.kv, true), false},
+                       {a.kv.v_scale, extent_bytes(a.kv, true), false},
+                       {a.slopes, 4 * n_q_heads, false},
+                       {a.starts, 4 * n_seq, false},
+                       {a.positions, 4 * ((n_seq - 1) * a.positions_stride + a.positions_width), false}};
+  for (const Range& o : outs)
+    for (const Range& i : ins)
+      if (clash(o, i) && !(&o == outs && &i == ins && side_by_side(out, os, q, qs, n_seq, row)))
+        return bad(IL_ERR_ARG, fn, "out and lse must not overlap q, table, lens, the score's arrays or the cache");
+  if (clash(outs[0], outs[1])) return bad(IL_ERR_ARG, fn, "out and lse must not overlap");
+  int num_sms = 0;
+  const int dev = api_device(&num_sms, &a.status);
+  if (dev < 0) return dev;
+  a.q = q;
+  a.q_stride = qs;
+  a.table = table;
+  a.table_stride = ts;
+  a.table_width = table_width;
+  a.lens = lens;
+  a.n_seq = (int)n_seq;
+  a.n_q_heads = (int)n_q_heads;
+  a.scale = scale;
+  a.window = window;
+  a.out = out;
+  a.out_stride = os;
+  a.lse = lse;
+  void* ws = nullptr;
+  rc = api_kv_workspace(dev, static_cast<cudaStream_t>(stream), num_sms, &ws);
+  if (rc != IL_OK) return rc;
+  Launch L;
+  const cudaError_t e = prepare_kv_attend(a, num_sms, ws, &L);
   if (e != cudaSuccess) return api_cuda_fail(e, fn);
   return enqueue(fn, L, stream);
 }
@@ -244,66 +342,15 @@ int il_kv_read(const il_kv* kv, const int32_t* slots, int64_t n, float* k, int64
 int il_kv_attend(const il_kv* kv, const float* q, int64_t q_stride, const int32_t* table, int64_t table_stride,
                  int64_t table_width, const int32_t* lens, int64_t n_seq, int64_t n_q_heads, float scale, int64_t window,
                  float* out, int64_t out_stride, float* lse, void* stream) {
-  const char* fn = "il_kv_attend";
-  NvtxRange range(fn);
-  api_clear_error();
-  KvAttendArgs a;
-  memset(&a, 0, sizeof a);
-  int rc = check_cache(fn, kv, &a.kv);
-  if (rc != IL_OK) return rc;
-  if (n_seq < 0 || n_seq > kMaxKvSeqs) return bad(IL_ERR_ARG, fn, "n_seq out of range");
-  if (n_q_heads < 1 || n_q_heads > 32768 || n_q_heads % a.kv.n_heads != 0)
-    return bad(IL_ERR_SHAPE, fn, "n_q_heads must be a multiple of the cache's n_heads, at most 32768");
-  if (window < 0) return bad(IL_ERR_ARG, fn, "window is negative");
-  if (!(scale - scale == 0.0f)) return bad(IL_ERR_ARG, fn, "scale is not finite");
-  if (n_seq == 0) return IL_OK;
-  if (q == nullptr || table == nullptr || lens == nullptr || out == nullptr)
-    return bad(IL_ERR_ARG, fn, "q, table, lens and out must not be NULL");
-  if (!aligned(q, 16) || !aligned(out, 16)) return bad(IL_ERR_ARG, fn, "q or out is not 16-byte aligned");
-  if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(lse, 4))
-    return bad(IL_ERR_ARG, fn, "table, lens or lse is not 4-byte aligned");
-  const int64_t row = n_q_heads * a.kv.head_dim;
-  if (n_seq > 1 && (q_stride < row || out_stride < row || q_stride % 4 != 0 || out_stride % 4 != 0 ||
-                    q_stride > INT64_MAX / 8 / n_seq || out_stride > INT64_MAX / 8 / n_seq))
-    return bad(IL_ERR_SHAPE, fn, "q_stride or out_stride is smaller than a row or not a multiple of 4");
-  if (table_width < 1 || table_width > INT32_MAX || (n_seq > 1 && (table_stride < table_width || table_stride > INT32_MAX)))
-    return bad(IL_ERR_SHAPE, fn, "table_width or table_stride out of range");
-  const int64_t qs = n_seq > 1 ? q_stride : 0, os = n_seq > 1 ? out_stride : 0, ts = n_seq > 1 ? table_stride : 0;
-  const Range outs[] = {{out, 4 * ((n_seq - 1) * os + row), true}, {lse, 4 * n_seq * n_q_heads, true}};
-  const Range ins[] = {{q, 4 * ((n_seq - 1) * qs + row), false},
-                       {table, 4 * ((n_seq - 1) * ts + table_width), false},
-                       {lens, 4 * n_seq, false},
-                       {a.kv.k, extent_bytes(a.kv, false), false},
-                       {a.kv.v, extent_bytes(a.kv, false), false},
-                       {a.kv.k_scale, extent_bytes(a.kv, true), false},
-                       {a.kv.v_scale, extent_bytes(a.kv, true), false}};
-  for (const Range& o : outs)
-    for (const Range& i : ins)
-      if (clash(o, i) && !(&o == outs && &i == ins && side_by_side(out, os, q, qs, n_seq, row))) return bad(IL_ERR_ARG, fn, "out and lse must not overlap q, table, lens or the cache");
-  if (clash(outs[0], outs[1])) return bad(IL_ERR_ARG, fn, "out and lse must not overlap");
-  int num_sms = 0;
-  const int dev = api_device(&num_sms, &a.status);
-  if (dev < 0) return dev;
-  a.q = q;
-  a.q_stride = qs;
-  a.table = table;
-  a.table_stride = ts;
-  a.table_width = table_width;
-  a.lens = lens;
-  a.n_seq = (int)n_seq;
-  a.n_q_heads = (int)n_q_heads;
-  a.scale = scale;
-  a.window = window;
-  a.out = out;
-  a.out_stride = os;
-  a.lse = lse;
-  void* ws = nullptr;
-  rc = api_kv_workspace(dev, static_cast<cudaStream_t>(stream), num_sms, &ws);
-  if (rc != IL_OK) return rc;
-  Launch L;
-  const cudaError_t e = prepare_kv_attend(a, num_sms, ws, &L);
-  if (e != cudaSuccess) return api_cuda_fail(e, fn);
-  return enqueue(fn, L, stream);
+  return attend_call("il_kv_attend", kv, q, q_stride, table, table_stride, table_width, lens, n_seq, n_q_heads, scale, window,
+                     nullptr, out, out_stride, lse, stream);
+}
+
+int il_kv_attend_scored(const il_kv* kv, const float* q, int64_t q_stride, const int32_t* table, int64_t table_stride,
+                        int64_t table_width, const int32_t* lens, int64_t n_seq, int64_t n_q_heads, float scale,
+                        int64_t window, const il_kv_score* score, float* out, int64_t out_stride, float* lse, void* stream) {
+  return attend_call("il_kv_attend_scored", kv, q, q_stride, table, table_stride, table_width, lens, n_seq, n_q_heads, scale,
+                     window, score, out, out_stride, lse, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,156 @@
+// kv_a4.cuh -- products with 4-bit rows of the cache (IL_A4: value d u + m, u of 0 .. 15) on m16n8k16 MMAs.
+//
+// Tokens (for q K^T) or elements of V (for p V) are the rows of an MMA, and each query head has two columns: the hi and the lo
+// part of its fp32 operand, x = hi + lo 2^-11 in fp16.  The parts have accumulators of their own, so that lo is kept 2^11
+// times as large: x keeps 22 bits down to 2^-27 of the largest and is cut at 2^-49 of it.  With four heads a K/V head nothing of an
+// MMA is idle, a lane's accumulators are of one head (that of column pair q4 = lane % 4), and a softmax value is in one lane.
+//
+// Decoding costs 5 instructions for 8 elements: nibbles at bits 0-3 and 4-7 of a 16-bit half are fp16 subnormals as they stand,
+// u 2^-24 and 16 u 2^-24, exactly; one shift brings the other two there.  The factor 16 is taken from q, or from the sums
+// over p V at the end.  d multiplies a block's fp32 sum (K) or p (V); m meets the sum of q over the block, and sum p m is a
+// sum of its own, 8 FMAs for 16 tokens.
+#pragma once
+
+#include "il_internal.cuh"
+
+namespace il {
+namespace a4 {
+
+constexpr float kLoUnit = 1.f / 2048.f;  // of the lo part
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at));
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at));
+}
+// Transpose of an 8 x 8 matrix of 16-bit elements, one row in the four lanes of a quad.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// Nibbles 0, 1, 2, 3 of both halves of w, as fp16 pairs of u 2^-24 (even) and 16 u 2^-24 (odd).
+__device__ __forceinline__ void nibbles(uint32_t w, uint32_t (&p)[4]) {
+  p[0] = w & 0x000f000fu;
+  p[1] = w & 0x00f000f0u;
+  w >>= 8;
+  p[2] = w & 0x000f000fu;
+  p[3] = w & 0x00f000f0u;
+}
+
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float step_of(uint32_t dm) { return __uint_as_float(dm << 16); }
+__device__ __forceinline__ float least_of(uint32_t dm) { return __uint_as_float(dm & 0xffff0000u); }
+
+// {hi, lo 2^11} of x.
+__device__ __forceinline__ uint32_t split(float x) {
+  const __half h = __float2half_rn(x);
+  const __half2 p = __halves2half2(h, __float2half_rn((x - __half2float(h)) * 2048.f));
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// The {d, m} of one token: NB of them in shared memory, 4 NB-byte aligned.
+template <int NB>
+__device__ __forceinline__ void load_steps(uint32_t (&dm)[NB], uint32_t at) {
+  static_assert(NB == 2 || NB == 4, "heads of 64 or 128 columns");
+  if constexpr (NB == 4)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(dm[0]), "=r"(dm[1]), "=r"(dm[2]), "=r"(dm[3]) : "r"(at));
+  else
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(dm[0]), "=r"(dm[1]) : "r"(at));
+}
+
+// Where chunk `b` (of one 32-element block, 16 bytes) of row `row` is in a tile: eight rows of one chunk cover the banks.
+template <int NB>
+__device__ __forceinline__ uint32_t chunk_at(int row, int b) {
+  return row * (16 * NB) + ((b ^ (NB == 4 ? (row >> 1) & 3 : (row >> 2) & 1)) << 4);
+}
+
+// Query heads of 4 R columns as B operands, scaled so that the largest of a head becomes 2^13 .. 2^14.
+template <int NB, int R>
+struct Query {
+  uint32_t f[R][4 * NB];  // of head 4 r + g / 2, its hi (g even) or lo part: elements 8 q4 .. 8 q4 + 7 of each block
+  float sum[R][NB];       // of head 4 r + q4: the sum over a block, in the products' unit
+  float back[R][2];       // of head 4 r + q4: the unit, as two factors
+
+  // Elements x[b][0 .. 7] = 8 q4 .. of block b, of head 4 r + g / 2; `top`: their largest magnitude over the whole head.
+  __device__ __forceinline__ void take(int r, const float (&x)[NB][8], float top, int lane) {
+    const int q4 = lane & 3, head_lane = q4 * 8;  // a lane with g / 2 = q4
+    const bool lo_part = (lane >> 2) & 1;
+    const int e = max((int)(__float_as_uint(top) >> 23), 14);
+    const float up = __int_as_float((267 - e) << 23);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      float total = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // nibble j of both halves of the lane's word: elements j, j + 4
+        const float y = x[b][j] * up, z = x[b][j + 4] * up, sixteenth = j % 2 == 0 ? 1.f : 0.0625f;
+        const uint32_t u = split(y * sixteenth), v = split(z * sixteenth);
+        f[r][4 * b + j] = lo_part ? __byte_perm(u, v, 0x7632) : __byte_perm(u, v, 0x5410);
+        total += y + z;
+      }
+      total += __shfl_xor_sync(~0u, total, 1);
+      total += __shfl_xor_sync(~0u, total, 2);
+      sum[r][b] = __shfl_sync(~0u, total, head_lane) * 5.9604644775390625e-08f;  // 2^-24
+    }
+    const int unit = __shfl_sync(~0u, e, head_lane) - 116, half = unit >> 1;  // 2^unit = 2^24 / up
+    back[r][0] = __int_as_float((half + 127) << 23);
+    back[r][1] = __int_as_float((unit - half + 127) << 23);
+  }
+
+  // s[r][h]: the product of head 4 r + q4 with token 8 h + g of the 16 from `first` on in the tile of K at `tile`.
+  __device__ __forceinline__ void dot(float (&s)[R][2], uint32_t tile, uint32_t steps, int first, int lane) const {
+    const int g = lane >> 2;
+    uint32_t d[2][NB];
+    load_steps<NB>(d[0], steps + (first + g) * (4 * NB));
+    load_steps<NB>(d[1], steps + (first + 8 + g) * (4 * NB));
+#pragma unroll
+    for (int r = 0; r < R; ++r) s[r][0] = s[r][1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NB / 2; ++i) {
+      uint32_t w[4];  // tokens g and g + 8 of blocks 2 i and 2 i + 1
+      ldmatrix4(w, tile + chunk_at<NB>(first + (lane & 15), 2 * i + (lane >> 4)));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int b = 2 * i + h;
+        uint32_t x[4], y[4];
+        nibbles(w[2 * h], x);
+        nibbles(w[2 * h + 1], y);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float c[4];
+          mma_first(c, x[0], y[0], x[1], y[1], f[r][4 * b], f[r][4 * b + 1]);
+          mma(c, x[2], y[2], x[3], y[3], f[r][4 * b + 2], f[r][4 * b + 3]);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            s[r][t] = fmaf(fmaf(c[2 * t + 1], kLoUnit, c[2 * t]), step_of(d[t][b]), s[r][t]);
+            s[r][t] = fmaf(sum[r][b], least_of(d[t][b]), s[r][t]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) s[r][t] = s[r][t] * back[r][0] * back[r][1];
+  }
+};
+
+}  // namespace a4
+}  // namespace il

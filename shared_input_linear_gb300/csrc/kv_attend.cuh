@@ -47,6 +47,7 @@
 
 #include "il_internal.cuh"
 #include "il_ptx.cuh"
+#include "kv_a4.cuh"
 
 namespace il {
 
@@ -59,7 +60,8 @@ struct KvAttendPlan {
   FastDiv by_blocks;      // row of a sequence / blocks
   int group;              // query heads of a K/V head
   int blocks;             // blocks of 8 R query heads of a K/V head
-  float q_scale;          // scale * log2(e)
+  float q_scale;          // scale * log2(e), or scale / cap
+  float cap_log2;         // cap * log2(e); 0: none
   int simple;             // pages hold whole groups, the strides below fit, (Q8) scales allow the widest copies
   uint32_t page_bytes, token_bytes, head_bytes;     // strides of k and v
   uint32_t spage_bytes, stoken_bytes, shead_bytes;  // of the scales
@@ -73,19 +75,23 @@ constexpr int kGroup = 16;          // tokens of a product's step; pages of whol
 constexpr int kSmemLimit = 232448;  // 227 KB
 constexpr int kMaxCtas = 256;       // of a grid, one an SM
 
-// W columns of a head in a warp, H warps a head (H * W >= head_dim), R blocks of 8 query heads.
-template <bool Q8, int W, int R, int H>
+// F: format of the cache.  W columns of a head in a warp, H warps a head (H * W >= head_dim), R blocks of 8 (A4: of 4) query
+// heads.
+template <int F, int W, int R, int H>
 struct Config {
-  static constexpr int kRows = 8 * R;            // query heads of a block
-  static constexpr int kBlocks = W / 32;         // 32-element blocks of a warp's columns
-  static constexpr int kPart = kRows * (W + 2);  // floats of a part: sums, maxima, sums of p
+  static constexpr bool kA4 = F == IL_A4, kQ8 = F == IL_Q8;
+  static constexpr int kRows = (kA4 ? 4 : 8) * R;  // query heads of a block
+  static constexpr int kBlocks = W / 32;           // 32-element blocks of a warp's columns
+  static constexpr int kPart = kRows * (W + 2);    // floats of a part: sums, maxima, sums of p
   // Tokens of a tile: 32 where a row is short in bytes, so that what a tile costs beside its bytes counts half
-  static constexpr int kTile = R == 1 && (Q8 || W == 64) ? 32 : 16;
-  static constexpr int kRowBytes = Q8 ? W : 2 * W;
-  static constexpr int kPool = kTile * kRowBytes;               // K or V of a tile
-  static constexpr int kScales = Q8 ? kTile * kBlocks * 4 : 0;  // its scales
+  static constexpr int kTile = kA4 || (R == 1 && (kQ8 || W == 64)) ? 32 : 16;
+  static constexpr int kValues = kTile / (kA4 ? 8 : 4);  // of s, of a softmax row in a lane
+  static constexpr int kRowBytes = kA4 ? W / 2 : kQ8 ? W : 2 * W;
+  static constexpr int kChunk = 16 * W / kRowBytes;                    // elements of 16 bytes
+  static constexpr int kPool = kTile * kRowBytes;                      // K or V of a tile
+  static constexpr int kScales = F != IL_BF16 ? kTile * kBlocks * 4 : 0;  // its scales
   static constexpr int kStage = 2 * (kPool + kScales);
-  static constexpr int kWarps = Q8 && R == 1 && W == 64 ? 12 : 8;
+  static constexpr int kWarps = kA4 ? (R == 1 ? 16 : R == 2 ? 12 : 8) : kQ8 && R == 1 && W == 64 ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kWorkers = kWarps / H;    // runs of tiles in a CTA
   static constexpr uint32_t kWhole = 2 * kWorkers;  // tiles of a row that is not cut over CTAs
@@ -98,7 +104,7 @@ struct Config {
   static_assert(kStages >= 2 && kSmem <= kSmemLimit, "the ring does not fit");
   static_assert(kRing >= kPart * 4, "a part must fit the warp's ring");
   static_assert(kWorkers * 48 >= kWarps * 8, "the sums over sequences are kept where the workers' parts are described");
-  static_assert(kPool >= 32 * kTile * R, "s is traded through the tile of K");
+  static_assert(H == 1 || kPool >= 128 * kValues * R, "s is traded through the tile of K");
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool use, uint64_t policy) {
@@ -250,18 +256,19 @@ __device__ __forceinline__ unsigned long long divide(unsigned long long a, uint3
   return a >> 32 == 0 ? (unsigned long long)((uint32_t)a / b) : divide_wide(a, b);
 }
 
-template <int T>
+template <int T, bool SCORED>
 __device__ __forceinline__ Seq seq_of(const KvAttendPlan& P, int s) {
   Seq q;
   const int len = min(max(P.a.lens[s], 0), P.cap);
   q.len = (uint32_t)len;
   q.begin = P.window > 0 ? (uint32_t)max(len - P.window, 0) : 0u;
+  if (SCORED && P.a.starts != nullptr) q.begin = max(q.begin, (uint32_t)min(max(P.a.starts[s], 0), len));
   q.first = q.begin / T;
-  q.tiles = len == 0 ? 0u : (q.len + T - 1) / T - q.first;
+  q.tiles = len == 0 || (SCORED && q.begin == q.len) ? 0u : (q.len + T - 1) / T - q.first;
   return q;
 }
 
-template <int T>
+template <int T, bool SCORED>
 __device__ __forceinline__ void advance(Walk& w, const KvAttendPlan& P) {
   if (++w.tile < w.q.tiles) return;
   w.tile = 0;
@@ -269,7 +276,7 @@ __device__ __forceinline__ void advance(Walk& w, const KvAttendPlan& P) {
   w.block = 0;
   if (++w.hk < P.a.kv.n_heads) return;
   w.hk = 0;
-  do w.q = seq_of<T>(P, ++w.s);
+  do w.q = seq_of<T, SCORED>(P, ++w.s);
   while (w.q.tiles == 0 && w.s + 1 < P.a.n_seq);
 }
 
@@ -283,9 +290,11 @@ struct Left {
 };
 static_assert(sizeof(Left) == 48, "see Config::kFixed");
 
-template <bool Q8, int W, int R, int H>
-__global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_kernel(const KvAttendPlan P) {
-  using C = Config<Q8, W, R, H>;
+template <int F, bool SCORED, int W, int R, int H>
+__global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_kernel(const KvAttendPlan P) {
+  using C = Config<F, W, R, H>;
+  constexpr bool Q8 = C::kQ8, A4 = C::kA4, BLOCKED = Q8 || A4;  // scales of 32 elements
+  constexpr int NV = C::kValues;
   constexpr int T = C::kTile, NN = T / 8, GR = T / kGroup;  // tokens of a tile, in eights, in groups
   constexpr int NB = C::kBlocks, NT = C::kThreads, NW = C::kWarps, NK = C::kWorkers, S = C::kStages, ROWS = C::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -323,7 +332,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
   for (int k = 0; k < run; ++k) {
     const int s = tid * run + k;
     const bool in = s < a.n_seq;
-    const Seq q = in ? seq_of<T>(P, s) : Seq{0, 0, 0, 0};
+    const Seq q = in ? seq_of<T, SCORED>(P, s) : Seq{0, 0, 0, 0};
     mine += q.tiles;
     short_rows |= q.tiles - 1 < C::kWhole;
     unsigned none = __ballot_sync(~0u, in && q.tiles == 0 && s % gridDim.x == blockIdx.x);
@@ -392,10 +401,10 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
     const int lo = runs - 1;
     long long off = target - s_before[lo] * rows_per_seq;
     in.s = lo * run;
-    in.q = seq_of<T>(P, in.s);
+    in.q = seq_of<T, SCORED>(P, in.s);
     while (off >= (long long)in.q.tiles * rows_per_seq && in.s + 1 < a.n_seq) {
       off -= (long long)in.q.tiles * rows_per_seq;
-      in.q = seq_of<T>(P, ++in.s);
+      in.q = seq_of<T, SCORED>(P, ++in.s);
     }
     const int row = (int)divide(off, in.q.tiles);
     in.tile = (uint32_t)(off - (long long)row * in.q.tiles);
@@ -419,10 +428,11 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
     if (P.blocks > 1) asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
 
     // 16-byte chunks of a row, rows of one copy instruction, this lane's chunk
-    constexpr int ES = Q8 ? 1 : 2, CPR = C::kRowBytes / 16, PER = 32 / CPR;
+    constexpr int ES = BLOCKED ? 1 : 2, CPR = C::kRowBytes / 16, PER = 32 / CPR;  // ES: bytes of what strides count
     const int chunk = lane % CPR, sub = lane / CPR;
-    const bool in_row = col0 + chunk * (16 / ES) < D;
-    const uint32_t lane_off = sub * P.token_bytes + col0 * ES + chunk * 16, row_step = PER * P.token_bytes;
+    const bool in_row = col0 + chunk * C::kChunk < D;
+    const int col_bytes = A4 ? col0 / 2 : col0 * ES;
+    const uint32_t lane_off = sub * P.token_bytes + col_bytes + chunk * 16, row_step = PER * P.token_bytes;
     // scales: the widest copy of a token's scales; a lane copies K's (lanes 0-15) or V's
     constexpr int SB = NB * 4 > 16 ? 16 : NB * 4;
 
@@ -434,10 +444,12 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
     };
     // Positions of the chunks of a row in shared memory, without bank conflicts in the reads below.
     auto k_at = [&](int row) {
+      if (A4) return (int)a4::chunk_at<NB>(row, chunk);
       return row * C::kRowBytes +
              ((Q8 ? chunk ^ ((W == 64 ? (row >> 1) & 1 : row & 3) << 1) : chunk ^ ((row & 1) << 2)) << 4);
     };
     auto v_at = [&](int row) {
+      if (A4) return (int)a4::chunk_at<NB>(row, chunk);
       if (!Q8) return row * C::kRowBytes + ((chunk ^ (row & 7)) << 4);
       if (W == 64) row = (row & ~15) | ((row >> 1) & 7) | ((row & 1) << 3);
       return row * C::kRowBytes + ((chunk ^ (((row >> 1) & (W == 64 ? 1 : 3)) << 1)) << 4);
@@ -463,7 +475,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
             kp += row_step;
             vp += row_step;
           }
-          if constexpr (Q8) {
+          if constexpr (BLOCKED) {
             const uint8_t* const sc = reinterpret_cast<const uint8_t*>(lane < 16 ? kv.k_scale : kv.v_scale) +
                                       ((uint64_t)pg * P.spage_bytes + ((in_page + (lane & 15)) * P.stoken_bytes +
                                                                        w.hk * P.shead_bytes + col0 / 8));
@@ -476,8 +488,8 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
         if (want && !ok) atomicOr(a.status, kStatusBadSlot);
         const uint32_t in_page = t - column_of(t) * (uint32_t)kv.page_size;
         long long off = 0, soff = 0;
-        if (ok) off = page * kv.page + in_page * kv.token + w.hk * kv.head + col0;
-        if (Q8 && ok) soff = page * kv.spage + in_page * kv.stoken + w.hk * kv.shead + col0 / 32;
+        if (ok) off = page * kv.page + in_page * kv.token + w.hk * kv.head + (A4 ? col_bytes : col0);
+        if (BLOCKED && ok) soff = page * kv.spage + in_page * kv.stoken + w.hk * kv.shead + col0 / 32;
 #pragma unroll 1
         for (int i = 0; i < T / PER; ++i) {
           const int row = i * PER + sub;
@@ -487,7 +499,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
           cp16(to + k_at(row), kv.k + src, use, policy);
           cp16(to + C::kPool + v_at(row), kv.v + src, use, policy);
         }
-        if constexpr (Q8) {
+        if constexpr (BLOCKED) {
           const uint32_t st = to + 2 * C::kPool;
 #pragma unroll 1
           for (int i = 0; i < T * NB / 32; ++i) {
@@ -503,26 +515,47 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
       return mask;
     };
 
+    // Position of this lane's token of the tile, for the bias by distance.
+    auto position_of = [&](const Walk& w) {
+      const uint32_t t = token_of(w);
+      if (a.positions == nullptr || !(t >= w.q.begin && t < w.q.len)) return (int)t;
+      return (int)a.positions[w.s * a.positions_stride + t];
+    };
+
     int page = page_of(in);
     uint32_t masks[S];  // of the tiles in the ring, the tile being used first
+    int place = SCORED ? position_of(in) : 0, places[SCORED ? S : 1];
 
     // ---- the row being worked on
-    constexpr int QR = Q8 ? 4 * R : 6 * R;  // registers of q for 16 elements
+    constexpr int QR = A4 ? 1 : Q8 ? 4 * R : 6 * R;  // registers of q for 16 elements
+    constexpr int OX = A4 ? 2 * R : 4 * R;
     uint32_t qf[2 * NB][QR];
     float q_back[R];      // Q8: what s is to be multiplied by for the scaling of q and the bytes' unit; -2^-64 times it if above 2^127
     float q_start[R][NB];  // Q8: -128 units times the sum of q over a block
     // sums of p V, transposed: o[i][4 r + x] of MMA rows (columns of the head) g (x = 0, 1) or g + 8 (2, 3) of step i
-    // and of query heads 8 r + 2 q4 + (x & 1)
-    float o[W / 16][4 * R], m[R], l[R];
+    // and of query heads 8 r + 2 q4 + (x & 1).  A4: o[2 b + j][2 r + x] of element 32 b + 4 g + 2 j + x, head 4 r + q4
+    float o[W / 16][OX], m[R], l[R];
+    a4::Query<A4 ? NB : 1, A4 ? R : 1> aq;
+    float om[A4 ? R : 1][A4 ? NB : 1];  // A4: this lane's tokens' part of sum p m, of block b
+    float slope[SCORED ? R : 1];        // of this lane's softmax rows, times log2(e)
+    int newest = 0;                     // position of the row's last token
     // Q8: the largest s so far (m may lie below it), the biased exponent of the largest V scale so far, and that of
     // the sums' unit: the same but inside a tile
     float highest[R];
     int v_exp = 14, o_exp = 14;
 
     auto load_q = [&]() {
+      if constexpr (SCORED) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int in_group = at.block * ROWS + (A4 ? 4 * r + q4 : 8 * r + g);
+          slope[r] = a.slopes != nullptr && in_group < P.group ? a.slopes[(int64_t)at.hk * P.group + in_group] * 1.4426950408889634f : 0.f;
+        }
+        newest = a.positions != nullptr ? a.positions[at.s * a.positions_stride + at.q.len - 1] : (int)at.q.len - 1;
+      }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int in_group = at.block * ROWS + r * 8 + g;
+        const int in_group = at.block * ROWS + (A4 ? r * 4 + g / 2 : r * 8 + g);
         const bool use = in_group < P.group;
         const float* src = a.q + at.s * a.q_stride + (int64_t)(at.hk * P.group + in_group) * D + col0 + 8 * q4;
         float x[NB][8];
@@ -537,12 +570,18 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             x[b][i] *= P.q_scale;
-            if (Q8) top = fmaxf(top, fabsf(x[b][i]));
+            if (BLOCKED) top = fmaxf(top, fabsf(x[b][i]));
           }
         }
-        if constexpr (Q8) {
+        if constexpr (BLOCKED) {
           top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
           top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        }
+        if constexpr (A4) {
+          aq.take(r, x, top, lane);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) om[r][b] = 0.f;
+        } else if constexpr (Q8) {
           const int e = max((int)(__float_as_uint(top) >> 23), 14);
           const float up = pow2_biased(267 - e);  // the row's largest |q| becomes 2^13 .. 2^14
           q_back[r] = e + 11 < 255 ? pow2_biased(e + 11) : -pow2_biased(e + 11 - 64);
@@ -594,7 +633,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
 #pragma unroll
       for (int i = 0; i < W / 16; ++i)
 #pragma unroll
-        for (int x = 0; x < 4 * R; ++x) o[i][x] = 0.f;
+        for (int x = 0; x < OX; ++x) o[i][x] = 0.f;
       v_exp = o_exp = 14;
     };
 
@@ -607,12 +646,17 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
       // the stage used by the tile before this one takes the tile S - 1 ahead
       auto fetch_ahead = [&]() {
 #pragma unroll
-        for (int k = 0; k + 1 < S; ++k) masks[k] = masks[k + 1];
+        for (int k = 0; k + 1 < S; ++k) {
+          masks[k] = masks[k + 1];
+          if (SCORED) places[k] = places[k + 1];
+        }
         if (i + S - 1 < n) {
           masks[S - 1] = fetch(in, page, ahead);
+          if (SCORED) places[S - 1] = place;
           if (i + S < n) {
-            advance<T>(in, P);
+            advance<T, SCORED>(in, P);
             page = page_of(in);
+            if (SCORED) place = position_of(in);
           }
         }
         cp_commit();
@@ -632,10 +676,19 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
       }
       const uint32_t from = ring + stage * C::kStage;
 
-      // ---- s = q K^T: s[r][2 nt + c] of head row g + 8 r, token 8 nt + 2 q4 + c
-      float s[R][2 * NN];
+      // ---- s = q K^T: s[r][2 nt + c] of head row g + 8 r, token 8 nt + 2 q4 + c (A4: s[r][c] of head 4 r + q4, token 8 c + g)
+      float s[R][NV];
+      auto token_at = [&](int c) { return A4 ? 8 * c + g : 8 * (c / 2) + 2 * q4 + c % 2; };
       if (H == 1 || i >= 0) {
-        if constexpr (Q8) {
+        if constexpr (A4) {
+#pragma unroll
+          for (int k = 0; k < GR; ++k) {
+            float c[R][2];
+            aq.dot(c, from, from + 2 * C::kPool, 16 * k, lane);
+#pragma unroll
+            for (int r = 0; r < R; ++r) s[r][2 * k] = c[r][0], s[r][2 * k + 1] = c[r][1];
+          }
+        } else if constexpr (Q8) {
 #pragma unroll
           for (int nt = 0; nt < NN; ++nt) {
             float d0[NB], d1[NB];  // K's scales of tokens 8 nt + 2 q4, and the next
@@ -737,26 +790,45 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
           // the pair's halves of s: each puts its own where its tile of K was, both add the two.  The next
           // copy into this stage starts behind the next tile's barrier, when both have read.
           __syncwarp();
+          constexpr int NX = NV / 4;
 #pragma unroll
-          for (int x = 0; x < R * GR; ++x) {
-            const float(&v)[2 * NN] = s[x / GR];
-            const float part[4] = {v[4 * (x % GR)], v[4 * (x % GR) + 1], v[4 * (x % GR) + 2], v[4 * (x % GR) + 3]};
+          for (int x = 0; x < R * NX; ++x) {
+            const float(&v)[NV] = s[x / NX];
+            const float part[4] = {v[4 * (x % NX)], v[4 * (x % NX) + 1], v[4 * (x % NX) + 2], v[4 * (x % NX) + 3]};
             sts128(from + (x * 32 + lane) * 16, part);
           }
           asm volatile("bar.sync %0, 64;" ::"r"(worker + 1) : "memory");
           const uint32_t other = from + (warp % 2 == 0 ? C::kRing : -C::kRing);
 #pragma unroll
-          for (int x = 0; x < R * GR; ++x) {
+          for (int x = 0; x < R * NX; ++x) {
             float part[4];
             lds_floats(part, other + (x * 32 + lane) * 16);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) s[x / GR][4 * (x % GR) + c] += part[c];
+            for (int c = 0; c < 4; ++c) s[x / NX][4 * (x % NX) + c] += part[c];
           }
         }
       }
       if (H == 2) {
         fetch_ahead();
         if (i < 0) continue;
+      }
+
+      // ---- capped and biased
+      if constexpr (SCORED) {
+        if (P.cap_log2 > 0.f) {
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int c = 0; c < NV; ++c) s[r][c] = P.cap_log2 * tanhf(s[r][c]);
+        }
+        if (a.slopes != nullptr) {
+#pragma unroll
+          for (int c = 0; c < NV; ++c) {
+            const float far = (float)(__shfl_sync(~0u, places[0], token_at(c)) - newest);
+#pragma unroll
+            for (int r = 0; r < R; ++r) s[r][c] = fmaf(slope[r], far, s[r][c]);
+          }
+        }
       }
 
       // ---- softmax: p = 2^(s - m) and the factor of what came before
@@ -767,13 +839,13 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
         for (int r = 0; r < R; ++r) {
           low[r] = s[r][0];
 #pragma unroll
-          for (int c = 1; c < 2 * NN; ++c) low[r] = fminf(low[r], s[r][c]);
+          for (int c = 1; c < NV; ++c) low[r] = fminf(low[r], s[r][c]);
         }
       }
       if (mk != (uint32_t)((1ull << T) - 1)) {
 #pragma unroll
-        for (int c = 0; c < 2 * NN; ++c)
-          if (!((mk >> (8 * (c / 2) + 2 * q4 + c % 2)) & 1))
+        for (int c = 0; c < NV; ++c)
+          if (!((mk >> token_at(c)) & 1))
 #pragma unroll
             for (int r = 0; r < R; ++r) s[r][c] = -INFINITY;
       }
@@ -782,9 +854,15 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
       for (int r = 0; r < R; ++r) {
         top[r] = s[r][0];
 #pragma unroll
-        for (int c = 1; c < 2 * NN; ++c) top[r] = fmaxf(top[r], s[r][c]);
-        top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
-        top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
+        for (int c = 1; c < NV; ++c) top[r] = fmaxf(top[r], s[r][c]);
+        if constexpr (A4) {
+          top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 4));
+          top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 8));
+          top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 16));
+        } else {
+          top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
+          top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
+        }
       }
       // bf16 parts of p have fp32's range: m is the maximum so far.  fp16 parts keep 12 bits or more of p only
       // above 2^-26, so that m follows the tile's own maximum, down to 2^-24 of the largest p; a tile with
@@ -797,6 +875,9 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
           highest[r] = fmaxf(highest[r], top[r]);
           next[r] = fmaxf(top[r], highest[r] - 24.f);
           wide |= next[r] - low[r] > 26.f;
+        } else if constexpr (A4) {
+          highest[r] = fmaxf(highest[r], top[r]);
+          next[r] = fmaxf(top[r], highest[r] - 24.f);
         } else {
           next[r] = fmaxf(m[r], top[r]);
         }
@@ -811,10 +892,11 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
         m[r] = next[r];
         float sum = 0.f;
 #pragma unroll
-        for (int c = 0; c < 2 * NN; c += 2) {
+        for (int c = 0; c < NV; c += 2) {
           s[r][c] = exp2_fast(s[r][c] - base);
           s[r][c + 1] = exp2_fast(s[r][c + 1] - base);
           sum += s[r][c] + s[r][c + 1];
+          if (A4) wide |= (s[r][c] < 1.f / 67108864.f && s[r][c] > 0.f) || (s[r][c + 1] < 1.f / 67108864.f && s[r][c + 1] > 0.f);
         }
         l[r] = fmaf(l[r], keep[r], sum);
       }
@@ -823,15 +905,125 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
       const uint32_t fv = from + C::kPool;
       float kept[2 * R];  // keep of the heads that this lane's sums are of
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
+      for (int r = 0; r < (A4 ? 0 : R); ++r) {
         kept[2 * r] = __shfl_sync(~0u, keep[r], 8 * q4);
         kept[2 * r + 1] = __shfl_sync(~0u, keep[r], 8 * q4 + 4);
       }
-      auto join = [&](float (&acc)[4 * R], const float (&c)[R][4]) {
+      auto join = [&](float (&acc)[OX], const float (&c)[R][4]) {
 #pragma unroll
         for (int x = 0; x < 4 * R; ++x) acc[x] = fmaf(acc[x], kept[2 * (x / 4) + x % 2], c[x / 4][x % 4]);
       };
-      if constexpr (Q8) {
+      if constexpr (A4) {
+        static_assert(!A4 || T == 32, "a lane looks at one token's steps");
+        const uint32_t sv = from + 2 * C::kPool + C::kScales;
+        uint32_t dm[NV][NB];  // {d, m} of the lane's tokens
+#pragma unroll
+        for (int c = 0; c < NV; ++c) a4::load_steps<NB>(dm[c], sv + (8 * c + g) * NB * 4);
+        uint32_t one[NB], most = 0;  // of one token
+        a4::load_steps<NB>(one, sv + lane * NB * 4);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) most = max(most, one[b] & 0x7fffu);
+        v_exp = max(v_exp, (int)(__reduce_max_sync(~0u, most) >> 7));
+        const uint32_t little = (uint32_t)(v_exp - 12) << 7;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) wide |= (one[b] & 0x7fffu) < little && (one[b] & 0x7fffu) != 0;
+        wide = __any_sync(~0u, wide);
+        const float up = pow2_biased(267 - v_exp);  // the largest d becomes 2^13 .. 2^14
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            float sum = s[r][0] * a4::least_of(dm[0][b]);
+#pragma unroll
+            for (int c = 1; c < NV; ++c) sum = fmaf(s[r][c], a4::least_of(dm[c][b]), sum);
+            om[r][b] = fmaf(om[r][b], keep[r], sum);
+          }
+#pragma unroll
+          for (int c = 0; c < NV; ++c) s[r][c] *= up;
+          kept[r] = keep[r];
+        }
+        // Weights w = p d up, at most 2^14, in classes of 2^26 where a tile has p below 2^-26 or a d below 2^-12 of the
+        // largest: class k, 2^(14 - 26 (k + 1)) <= w < 2^(14 - 26 k), is multiplied by 2^(26 k) and the sums' unit goes down as
+        // far until the last class is in; below 2^-90 w is 0.
+        uint32_t classes = 1;
+        if (wide) {
+          classes = 0;
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int c = 0; c < NV; ++c)
+#pragma unroll
+              for (int b = 0; b < NB; ++b) {
+                const float x = fabsf(s[r][c] * a4::step_of(dm[c][b]));
+                const int k = max(140 - (int)(__float_as_uint(x) >> 23), 0) / 26;
+                if (x > 0.f && k < 4) classes |= 1u << k;
+              }
+          classes = max(__reduce_or_sync(~0u, classes), 1u);  // one at least: what came before takes its factor there
+        }
+#pragma unroll 1
+        while (classes != 0) {
+          const int k26 = 26 * (31 - __clz(classes));
+          classes &= ~(1u << (k26 / 26));
+          const int change = o_exp - (v_exp - k26);
+          const float shift = change < -126 ? 0.f : pow2_biased(127 + change), class_up = pow2_biased(127 + k26);
+          o_exp = v_exp - k26;
+#pragma unroll
+          for (int r = 0; r < R; ++r) kept[r] *= shift;
+          uint32_t z[GR][4];
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            float c[2][R][4];  // MMA rows g, g + 8 of step j: elements 32 b + 4 g + 2 j, and (16 times) the next
+#pragma unroll
+            for (int k = 0; k < GR; ++k) {
+              // tokens 2 q4, 2 q4 + 1 and 8 further of 16, elements 4 g .. 4 g + 3 of blocks b and b + 1
+              if (b % 2 == 0) a4::ldmatrix4_trans(z[k], fv + a4::chunk_at<NB>(16 * k + (lane & 15), b + (lane >> 4)));
+              uint32_t x[4], y[4];
+              a4::nibbles(z[k][2 * (b % 2)], x);
+              a4::nibbles(z[k][2 * (b % 2) + 1], y);
+#pragma unroll
+              for (int r = 0; r < R; ++r) {
+                uint32_t w[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  float v = s[r][2 * k + h] * a4::step_of(dm[2 * k + h][b]);
+                  if (wide) {
+                    v *= class_up;
+                    const float size = fabsf(v);
+                    v = size >= 1.f / 4096.f && (size < 16384.f || k26 == 0) ? v : 0.f;
+                  }
+                  w[h] = a4::movmatrix(a4::split(v));
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  if (k == 0)
+                    a4::mma_first(c[j][r], x[2 * j], x[2 * j + 1], y[2 * j], y[2 * j + 1], w[0], w[1]);
+                  else
+                    a4::mma(c[j][r], x[2 * j], x[2 * j + 1], y[2 * j], y[2 * j + 1], w[0], w[1]);
+                }
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  const float sum = fmaf(c[j][r][2 * x + 1], a4::kLoUnit, c[j][r][2 * x]);
+                  o[2 * b + j][2 * r + x] = fmaf(o[2 * b + j][2 * r + x], kept[r], sum);
+                }
+          }
+#pragma unroll
+          for (int r = 0; r < R; ++r) kept[r] = 1.f;  // of a class still to come
+        }
+        if (o_exp != v_exp) {
+          const float back = pow2_biased(127 + o_exp - v_exp);  // from the last class's unit
+          o_exp = v_exp;
+#pragma unroll
+          for (int k = 0; k < W / 16; ++k)
+#pragma unroll
+            for (int x = 0; x < OX; ++x) o[k][x] *= back;
+        }
+      } else if constexpr (Q8) {
         float d[2 * NN][NB];  // V's scales of the lane's tokens
         const uint32_t sv = from + 2 * C::kPool + C::kScales + 2 * q4 * NB * 4;
         float vs[NB], most = 0.f;  // of one token
@@ -983,12 +1175,12 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
       // ---- the row's or the run's end
       const bool row_ends = at.tile + 1 == at.q.tiles;
       if (row_ends || i + 1 == n) {
-        float unit = Q8 ? pow2_biased(o_exp - 13) : 1.f;
+        float unit = Q8 ? pow2_biased(o_exp - 13) : 1.f;  // (A4: below)
         if (Q8 && o_exp < 80) {  // unit / sum may be below 2^-126: two factors
 #pragma unroll
           for (int k = 0; k < W / 16; ++k)
 #pragma unroll
-            for (int x = 0; x < 4 * R; ++x) o[k][x] *= unit;
+            for (int x = 0; x < OX; ++x) o[k][x] *= unit;
           unit = 1.f;
         }
         const bool alone = begun_here && row_ends;
@@ -1009,8 +1201,42 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
             if (H == 2) asm volatile("bar.sync %0, 64;" ::"r"(worker + 1) : "memory");
           }
         }
+        if constexpr (A4) {
+          const int exp = o_exp - 116, half = exp >> 1;  // the sums' unit is 2^exp, as two factors
+          const float ua = pow2_biased(127 + half), ub = pow2_biased(127 + exp - half);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
+          for (int r = 0; r < R; ++r) {
+            float sum = l[r];
+#pragma unroll
+            for (int by = 4; by < 32; by *= 2) {
+              sum += __shfl_xor_sync(~0u, sum, by);
+#pragma unroll
+              for (int b = 0; b < NB; ++b) om[r][b] += __shfl_xor_sync(~0u, om[r][b], by);
+            }
+            const int row = 4 * r + q4, of_group = at.block * ROWS + row;
+            if (of_group >= P.group) continue;
+            if (g == 0) {
+              if (!alone) {
+                part[ROWS * W + row] = m[r];
+                part[ROWS * W + ROWS + row] = sum;
+              } else if (a.lse != nullptr && col0 == 0) {
+                a.lse[(int64_t)at.s * a.n_q_heads + (int64_t)at.hk * P.group + of_group] =
+                    sum == 0.f ? -INFINITY : (m[r] + __log2f(sum)) * 0.6931471805599453f;
+              }
+            }
+            const float f = !alone ? 1.f : sum == 0.f ? 0.f : __fdividef(1.f, sum);
+            float* const to = alone ? a.out + at.s * a.out_stride + ((int64_t)at.hk * P.group + of_group) * D + col0 : part + row * W;
+            auto value = [&](int b, int e) {
+              return fmaf(o[2 * b + e / 2][2 * r + e % 2] * ua, e % 2 == 0 ? ub : ub * 0.0625f, om[r][b]) * f;
+            };
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+              if (col0 + 32 * b < D)
+                *reinterpret_cast<float4*>(to + 32 * b + 4 * g) = make_float4(value(b, 0), value(b, 1), value(b, 2), value(b, 3));
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < (A4 ? 0 : R); ++r) {
           float sum = l[r];
           sum += __shfl_xor_sync(~0u, sum, 1);
           sum += __shfl_xor_sync(~0u, sum, 2);
@@ -1048,7 +1274,7 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
       }
       stage = stage + 1 == S ? 0 : stage + 1;
       if (i + 1 < n) {
-        advance<T>(at, P);
+        advance<T, SCORED>(at, P);
         if (at.tile == 0) begun_here = fresh = true;
       }
     }
@@ -1253,11 +1479,11 @@ __global__ void __launch_bounds__(Config<Q8, W, R, H>::kThreads, 1) kv_attend_ke
   }
 }
 
-template <bool Q8, int W, int R, int H>
+template <int F, bool SCORED, int W, int R, int H>
 cudaError_t prepare_variant(const KvAttendPlan& p, int ctas, Launch* out) {
-  using C = Config<Q8, W, R, H>;
+  using C = Config<F, W, R, H>;
   static std::atomic<unsigned long long> attr_set{0};  // one bit per device (setting it twice is harmless)
-  const void* fn = reinterpret_cast<const void*>(kv_attend_kernel<Q8, W, R, H>);
+  const void* fn = reinterpret_cast<const void*>(kv_attend_kernel<F, SCORED, W, R, H>);
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 64 || !(attr_set.load() & (1ull << dev))) {
@@ -1274,18 +1500,30 @@ cudaError_t prepare_variant(const KvAttendPlan& p, int ctas, Launch* out) {
   return cudaSuccess;
 }
 
-// The variant of a cache: heads of up to 64, 128 or (a pair of warps) 256 elements, in blocks of 8
-// query heads, or of 16 where a K/V head has more than 8.
-template <bool Q8>
-cudaError_t prepare_format(const KvAttendPlan& p, int dim, bool wide, int ctas, Launch* out) {
-  if (dim == 256) return wide ? prepare_variant<Q8, 128, 2, 2>(p, ctas, out) : prepare_variant<Q8, 128, 1, 2>(p, ctas, out);
-  if (dim == 128) return wide ? prepare_variant<Q8, 128, 2, 1>(p, ctas, out) : prepare_variant<Q8, 128, 1, 1>(p, ctas, out);
-  return wide ? prepare_variant<Q8, 64, 2, 1>(p, ctas, out) : prepare_variant<Q8, 64, 1, 1>(p, ctas, out);
+// The variant of a cache: heads of up to 64, 128 or (a pair of warps) 256 elements, in blocks of kRows query heads (R blocks of 8
+// or, A4, of 4).
+template <int F, bool SCORED>
+cudaError_t prepare_format(const KvAttendPlan& p, int dim, int blocks, int ctas, Launch* out) {
+  auto of = [&](auto w, auto h) {
+    constexpr int W = decltype(w)::value, H = decltype(h)::value;
+    if constexpr (F == IL_A4)
+      if (blocks == 4) return prepare_variant<F, SCORED, W, 4, H>(p, ctas, out);
+    return blocks == 2 ? prepare_variant<F, SCORED, W, 2, H>(p, ctas, out) : prepare_variant<F, SCORED, W, 1, H>(p, ctas, out);
+  };
+  using std::integral_constant;
+  if (dim == 256) return of(integral_constant<int, 128>{}, integral_constant<int, 2>{});
+  if (dim == 128) return of(integral_constant<int, 128>{}, integral_constant<int, 1>{});
+  return of(integral_constant<int, 64>{}, integral_constant<int, 1>{});
 }
 
 }  // namespace attend
 
-cudaError_t prepare_kv_attend_bf16(const KvAttendPlan& p, int dim, bool wide, int ctas, Launch* out);
-cudaError_t prepare_kv_attend_q8(const KvAttendPlan& p, int dim, bool wide, int ctas, Launch* out);
+// One translation unit each.
+cudaError_t prepare_kv_attend_bf16(const KvAttendPlan& p, int dim, int blocks, int ctas, Launch* out);
+cudaError_t prepare_kv_attend_q8(const KvAttendPlan& p, int dim, int blocks, int ctas, Launch* out);
+cudaError_t prepare_kv_attend_a4(const KvAttendPlan& p, int dim, int blocks, int ctas, Launch* out);
+cudaError_t prepare_kv_attend_bf16_scored(const KvAttendPlan& p, int dim, int blocks, int ctas, Launch* out);
+cudaError_t prepare_kv_attend_q8_scored(const KvAttendPlan& p, int dim, int blocks, int ctas, Launch* out);
+cudaError_t prepare_kv_attend_a4_scored(const KvAttendPlan& p, int dim, int blocks, int ctas, Launch* out);
 
 }  // namespace il

@@ -1,0 +1,10 @@
+// kv_attend_bf16_scored.cu -- il_kv_attend_scored over a bf16 cache (see kv_attend.cuh).
+#include "kv_attend.cuh"
+
+namespace il {
+
+cudaError_t prepare_kv_attend_bf16_scored(const KvAttendPlan& p, int dim, int blocks, int ctas, Launch* out) {
+  return attend::prepare_format<IL_BF16, true>(p, dim, blocks, ctas, out);
+}
+
+}  // namespace il

@@ -3,8 +3,8 @@
 
 namespace il {
 
-cudaError_t prepare_kv_attend_q8(const KvAttendPlan& p, int dim, bool wide, int ctas, Launch* out) {
-  return attend::prepare_format<true>(p, dim, wide, ctas, out);
+cudaError_t prepare_kv_attend_q8(const KvAttendPlan& p, int dim, int blocks, int ctas, Launch* out) {
+  return attend::prepare_format<IL_Q8, false>(p, dim, blocks, ctas, out);
 }
 
 }  // namespace il

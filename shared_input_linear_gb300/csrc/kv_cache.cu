@@ -230,13 +230,14 @@ __global__ void __launch_bounds__(kExtendThreads) kv_extend_kernel(const KvExten
 // - a float's integer is read from its low byte after adding 1.5 * 2^23, and made from a byte by the reverse;
 // - the four lanes of a 32-element block share its largest |w| with two shuffles; d = amax / 127 is the IEEE
 //   division, so that d and q are the definition's bit for bit.
+// - A4 takes its u from (w - m) / d in the same way, with the least and the largest of the block by four shuffles.
 // Measured (8 heads of 128, device time): append of 16384 tokens bf16 30.4 us, 6.6 TB/s, Q8 31.3 us, 5.5 TB/s; of 4097 Q8
 // 10.0 us; read of 16384 bf16 32.9 us, 6.1 TB/s, Q8 28.8 us, 6.0 TB/s, of 4097 Q8 9.2 us; append of one token 1.3 us.
 constexpr int kRowThreads = 256;
 // Units of a thread at a time: two, all loads first, but for Q8's quantiser, where more warps hide its chains
 // better (when it was chosen, 4097 tokens of 8 x 128: 13.0 us with two, 11.0 us with one; bf16 append 9.6 and 9.2,
 // Q8 read of 16384 28.8 and 31.1).
-constexpr int row_units(bool write, bool q8) { return write && q8 ? 1 : 2; }
+constexpr int row_units(bool write, int fmt) { return write && fmt != IL_BF16 ? 1 : 2; }
 
 struct RowArgs {
   KvView kv;
@@ -298,6 +299,31 @@ __device__ __forceinline__ void write8(const Eight& e, __nv_bfloat16* to) {
 
 constexpr float kToInt = 12582912.f;  // 1.5 * 2^23
 
+// Integers of 8 quotients v / d, which lie between low and high but for a rounding, in the low bytes of f (see above).
+// `fine`: d is above 0 and finite; otherwise 0.
+__device__ __forceinline__ void quotients8(const float (&v)[8], float d, bool fine, float low, float high, uint32_t (&f)[8]) {
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(d));
+  uint32_t unsure = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float t = v[i] * inv, r = t + kToInt;
+    f[i] = __float_as_uint(r);
+    if (!(fabsf(t - (r - kToInt)) < 0.49995f)) unsure |= 1u << i;  // NaN too
+  }
+#pragma unroll 1
+  while (unsure != 0) {
+    const int i = __ffs(unsure) - 1;
+    unsure &= unsure - 1;
+    float x = v[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) x = j == i ? v[j] : x;
+    const uint32_t q = fine ? (uint32_t)(int)fminf(fmaxf(rintf(__fdiv_rn(x, d)), low), high) : 0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = j == i ? q : f[j];
+  }
+}
+
 __device__ __forceinline__ void write8(const Eight& e, int8_t* to, float* scale, unsigned quad, bool first_of_block) {
   const float4 &x = e.lo, &y = e.hi;
   const float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
@@ -307,33 +333,52 @@ __device__ __forceinline__ void write8(const Eight& e, int8_t* to, float* scale,
   m = max_nan(m, __shfl_xor_sync(quad, m, 1));
   m = max_nan(m, __shfl_xor_sync(quad, m, 2));
   const float d = __fdiv_rn(m, 127.0f);
-  float inv;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(d));
   uint32_t f[8];
-  uint32_t unsure = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = w[i] * inv, r = t + kToInt;
-    f[i] = __float_as_uint(r);
-    if (!(fabsf(t - (r - kToInt)) < 0.49995f)) unsure |= 1u << i;  // NaN too
-  }
-  const bool normal = d > 0.f && d < __int_as_float(0x7f800000);  // otherwise q = 0 (and d = 0, NaN or infinity)
-#pragma unroll 1
-  while (unsure != 0) {
-    const int i = __ffs(unsure) - 1;
-    unsure &= unsure - 1;
-    float v = w[0];
-#pragma unroll
-    for (int j = 1; j < 8; ++j) v = j == i ? w[j] : v;
-    const uint32_t q = normal ? (uint32_t)(int)fminf(fmaxf(rintf(__fdiv_rn(v, d)), -127.f), 127.f) : 0u;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = j == i ? q : f[j];
-  }
+  quotients8(w, d, d > 0.f && d < __int_as_float(0x7f800000), -127.f, 127.f, f);  // (d may be 0, NaN or infinity)
   auto word = [&](int i) {
     return __byte_perm(__byte_perm(f[i], f[i + 1], 0x0040), __byte_perm(f[i + 2], f[i + 3], 0x0040), 0x5410);
   };
   *reinterpret_cast<uint2*>(to) = make_uint2(word(0), word(4));
   if (first_of_block) *scale = d;
+}
+
+// The bf16 at or below (above) x, as the upper half of a float's bits; x is not NaN.
+__device__ __forceinline__ uint32_t bf16_toward(float x, bool up) {
+  const uint32_t bits = __float_as_uint(x), head = bits & 0xffff0000u;
+  return bits != head && ((int)bits < 0) != up ? head + 0x10000u : head;
+}
+
+__device__ __forceinline__ void write8(const Eight& e, uint8_t* to, float* scale, unsigned quad, bool first_of_block) {
+  const float4 &x = e.lo, &y = e.hi;
+  float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  float least = w[0], most = w[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) least = -max_nan(-least, -w[i]), most = max_nan(most, w[i]);
+#pragma unroll
+  for (int by = 1; by < 4; by *= 2) {
+    least = -max_nan(-least, -__shfl_xor_sync(quad, least, by));
+    most = max_nan(most, __shfl_xor_sync(quad, most, by));
+  }
+  const uint32_t m = bf16_toward(least, false);
+  const float from = __uint_as_float(m);
+  const uint32_t step = bf16_toward(__fdiv_rn(most - from, 15.0f), true);
+  const float d = __uint_as_float(step);
+  const bool good = d < __int_as_float(0x7f800000) && fabsf(least) < __int_as_float(0x7f800000);  // no NaN either
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] -= from;
+  uint32_t f[8];
+  quotients8(w, d, good && d > 0.f, 0.f, 15.f, f);
+  uint32_t word = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) word |= (good ? f[i] & 15u : 0u) << (4 * i);
+  *reinterpret_cast<uint32_t*>(to) = word;
+  if (first_of_block) *reinterpret_cast<uint32_t*>(scale) = good ? step >> 16 | m : 0x7fc00000u;
+}
+
+__device__ __forceinline__ Eight read8(uint32_t u, float dm) {
+  const float d = bf16_lo(__float_as_uint(dm)), m = bf16_hi(__float_as_uint(dm));
+  auto one = [&](int i) { return fmaf((float)(u >> (4 * i) & 15u), d, m); };
+  return {make_float4(one(0), one(1), one(2), one(3)), make_float4(one(4), one(5), one(6), one(7))};
 }
 
 __device__ __forceinline__ Eight read8(const uint4& u, float) {
@@ -350,11 +395,30 @@ __device__ __forceinline__ Eight read8(const uint2& u, float d) {
   return {four(u.x), four(u.y)};
 }
 
-template <bool WRITE, bool Q8>
-__global__ void __launch_bounds__(kRowThreads, WRITE && Q8 ? 5 : 4) kv_rows_kernel(const RowArgs a) {
-  using T = typename std::conditional<Q8, int8_t, __nv_bfloat16>::type;
-  constexpr int kRowUnits = row_units(WRITE, Q8);
-  using Cached = typename std::conditional<Q8, uint2, uint4>::type;  // 8 elements
+template <int FMT>
+struct Cache;  // 8 elements, and the type that the strides count
+template <>
+struct Cache<IL_BF16> {
+  using Eight = uint4;
+  using T = __nv_bfloat16;
+};
+template <>
+struct Cache<IL_Q8> {
+  using Eight = uint2;
+  using T = int8_t;
+};
+template <>
+struct Cache<IL_A4> {
+  using Eight = uint32_t;
+  using T = uint8_t;
+};
+
+template <bool WRITE, int FMT>
+__global__ void __launch_bounds__(kRowThreads, WRITE && FMT != IL_BF16 ? 5 : 4) kv_rows_kernel(const RowArgs a) {
+  constexpr bool kScaled = FMT != IL_BF16;
+  constexpr int kRowUnits = row_units(WRITE, FMT);
+  using T = typename Cache<FMT>::T;
+  using Cached = typename Cache<FMT>::Eight;
   grid_dep_launch();
   grid_dep_wait();
   const KvView& kv = a.kv;
@@ -381,8 +445,8 @@ __global__ void __launch_bounds__(kRowThreads, WRITE && Q8 ? 5 : 4) kv_rows_kern
         k[j] = in ? a.k + (t0 + t) * a.k_stride + (int64_t)head * kv.head_dim + i : nullptr;
         v[j] = a.v + (t0 + t) * a.v_stride + (int64_t)head * kv.head_dim + i;
         const uint32_t page = a.by_page.of((uint32_t)max(slot, 0)), at = (uint32_t)slot - page * a.by_page.d;
-        off[j] = page * kv.page + at * kv.token + (int64_t)head * kv.head + i;
-        soff[j] = Q8 ? page * kv.spage + at * kv.stoken + (int64_t)head * kv.shead + i / 32 : 0;
+        off[j] = page * kv.page + at * kv.token + (int64_t)head * kv.head + (FMT == IL_A4 ? i / 2 : i);
+        soff[j] = kScaled ? page * kv.spage + at * kv.stoken + (int64_t)head * kv.shead + i / 32 : 0;
         block_start[j] = i % 32 == 0;
         if (live[j]) {
           if constexpr (WRITE) {
@@ -391,7 +455,7 @@ __global__ void __launch_bounds__(kRowThreads, WRITE && Q8 ? 5 : 4) kv_rows_kern
           } else {
             c[j][0] = *reinterpret_cast<const Cached*>(reinterpret_cast<const T*>(kv.k) + off[j]);
             c[j][1] = *reinterpret_cast<const Cached*>(reinterpret_cast<const T*>(kv.v) + off[j]);
-            if constexpr (Q8) d[j][0] = kv.k_scale[soff[j]], d[j][1] = kv.v_scale[soff[j]];
+            if constexpr (kScaled) d[j][0] = kv.k_scale[soff[j]], d[j][1] = kv.v_scale[soff[j]];
           }
         }
       }
@@ -408,7 +472,7 @@ __global__ void __launch_bounds__(kRowThreads, WRITE && Q8 ? 5 : 4) kv_rows_kern
         if constexpr (WRITE) {
           T* const ck = reinterpret_cast<T*>(kv.k) + off[j];
           T* const cv = reinterpret_cast<T*>(kv.v) + off[j];
-          if constexpr (Q8) {
+          if constexpr (kScaled) {
             write8(x[j][0], ck, kv.k_scale + soff[j], quad, block_start[j]);
             write8(x[j][1], cv, kv.v_scale + soff[j], quad, block_start[j]);
           } else {
@@ -439,7 +503,6 @@ cudaError_t prepare_kv_extend(const KvExtendArgs& a, int num_sms, Launch* out) {
 
 cudaError_t prepare_kv_rows(bool write, const KvView& kv, float* k, int64_t k_stride, float* v, int64_t v_stride,
                             const int32_t* slots, int64_t n, unsigned* status, int num_sms, Launch* out) {
-  const bool q8 = kv.format == IL_Q8;
   const uint32_t per_head = (uint32_t)kv.head_dim / 8, per_token = per_head * kv.n_heads;
   // runs of tokens whose units (and a grid's step beyond them) 31 bits count
   const int64_t run = std::max<int64_t>(1, (int64_t)((0x7fffffffu - (1u << 24)) / per_token));
@@ -448,10 +511,13 @@ cudaError_t prepare_kv_rows(bool write, const KvView& kv, float* k, int64_t k_st
                      (reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % 32 == 0 &&
                          (n == 1 || (k_stride % 8 == 0 && v_stride % 8 == 0)),
                      status};
-  out->fn = write ? (q8 ? reinterpret_cast<const void*>(kv_rows_kernel<true, true>)
-                        : reinterpret_cast<const void*>(kv_rows_kernel<true, false>))
-                  : (q8 ? reinterpret_cast<const void*>(kv_rows_kernel<false, true>)
-                        : reinterpret_cast<const void*>(kv_rows_kernel<false, false>));
+  const void* const fns[2][3] = {{reinterpret_cast<const void*>(kv_rows_kernel<false, IL_BF16>),
+                                  reinterpret_cast<const void*>(kv_rows_kernel<false, IL_Q8>),
+                                  reinterpret_cast<const void*>(kv_rows_kernel<false, IL_A4>)},
+                                 {reinterpret_cast<const void*>(kv_rows_kernel<true, IL_BF16>),
+                                  reinterpret_cast<const void*>(kv_rows_kernel<true, IL_Q8>),
+                                  reinterpret_cast<const void*>(kv_rows_kernel<true, IL_A4>)}};
+  out->fn = fns[write][kv.format == IL_BF16 ? 0 : kv.format == IL_Q8 ? 1 : 2];
   const int64_t units = n * per_token;  // one a thread while that fills the GPU's threads less than once
   out->grid = dim3((unsigned)std::min<int64_t>((units + kRowThreads - 1) / kRowThreads, (int64_t)num_sms * 8));
   out->block = dim3(kRowThreads);

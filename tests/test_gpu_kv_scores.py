@@ -1,0 +1,137 @@
+"""il_kv_attend_scored: capped logits, a bias by distance, sequences that begin later, against 64 bits."""
+import math
+
+import numpy as np
+import pytest
+
+import kv_long_util as kl
+from gpu_util import lib
+
+pytestmark = pytest.mark.gpu
+FORMATS = ["bf16", "q8", "a4"]
+
+
+@pytest.fixture(scope="module")
+def sil():
+    import torch
+    torch.cuda.set_device(0)
+    return lib()
+
+
+def _slopes(heads):
+    return np.exp2(-8 * np.arange(1, heads + 1) / heads).astype(np.float32)
+
+
+def _check(sil, *args, **kw):
+    c = kl.Case(sil, *args, **kw)
+    out, lse = c.run()
+    c.check(out, lse)
+    sil.check_device_status()
+    return c, out, lse
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("heads,kv,dim", [(32, 8, 128), (4, 4, 64), (8, 1, 256), (16, 8, 256), (18, 2, 64), (16, 1, 128), (40, 1, 96), (34, 2, 256)])
+@pytest.mark.parametrize("what", ["cap", "slopes", "starts", "all"])
+def test_forms_and_layouts(sil, fmt, heads, kv, dim, what):
+    lens = [1, 0, 37, 300, 16, 129, 64]
+    kw = {}
+    if what in ("cap", "all"):
+        kw["cap"] = 5.0 if what == "cap" else 30.0
+    if what in ("slopes", "all"):
+        kw["slopes"] = _slopes(heads)
+    if what in ("starts", "all"):
+        kw["starts"] = [0, 0, 36, 5, 16, 64, -3]
+    if what == "all":
+        kw.update(window=100, positions=True)
+    _check(sil, fmt, heads, kv, dim, 16, lens, seed=heads + dim, spread=4.0, **kw)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("cap", [1e-3, 1.0, 50.0, 1e4, 1e30])
+def test_caps(sil, fmt, cap):
+    """From logits that all lie at the cap to a cap that does nothing."""
+    _check(sil, fmt, 8, 2, 128, 16, [5, 77, 600], cap=cap, spread=6.0, seed=3)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("slopes", [[0.0] * 8, [1.0, 0.5, 0.0, -0.001, 3.0, 1e-6, 20.0, 1e3], [-0.01] * 8])
+def test_slopes(sil, fmt, slopes):
+    """Of any size and sign; steep ones leave little but the newest tokens."""
+    _check(sil, fmt, 8, 2, 128, 16, [5, 77, 1200, 0, 1], slopes=np.float32(slopes), seed=4)
+    _check(sil, fmt, 8, 2, 128, 24, [5, 77, 1200, 0, 1], slopes=np.float32(slopes), positions=True, seed=5)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("window", [0, 20])
+def test_starts(sil, fmt, window):
+    """Inside and at the ends of tiles and pages, behind the last token, below 0 and beyond 31 bits of the length."""
+    lens = [64] * 10 + [0, 1, 1]
+    starts = [0, 1, 15, 16, 17, 31, 32, 33, 63, 64, 5, 1, -2**31]
+    c, out, lse = _check(sil, fmt, 8, 2, 64, 16, lens, starts=starts, window=window, seed=window)
+    assert bool((out[9] == 0).all()) and bool(lse[9].isneginf().all()) and bool((out[11] == 0).all())
+    c.starts = [2**31 - 1] * 13
+    out, lse = c.run()
+    assert bool((out == 0).all()) and bool(lse.isneginf().all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_long_sequences_split_and_join(sil, fmt):
+    c, out, lse = _check(sil, fmt, 16, 4, 128, 64, [20011, 9, 4096], cap=20.0, slopes=_slopes(16), starts=[777, 0, 4000], seed=1)
+    again = c.run()
+    assert bool((again[0] == out).all()) and bool((again[1] == lse).all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_nothing_set_is_the_plain_call(sil, fmt):
+    c = kl.Case(sil, fmt, 8, 2, 128, 16, [70, 3, 0, 128], seed=2)
+    plain = c.run()
+    c.starts = [0] * 4
+    zeros = c.run()
+    assert bool((plain[0] == zeros[0]).all()) and bool((plain[1] == zeros[1]).all())
+
+
+def test_a_length_is_cut_to_the_positions(sil):
+    import torch
+    c = kl.Case(sil, "bf16", 4, 1, 64, 16, [40, 40], slopes=_slopes(4), positions=True, seed=2)
+    q, table, lens = c.device()
+    out = torch.empty_like(q)
+    more = c.score()
+    more["positions"] = more["positions"][:, :25]  # rows stay apart
+    sil.kv_attend(c.cache, q, table, lens, out, **more)
+    c.lens = [25, 25]
+    c.rows = [tuple(x[:25] for x in r) for r in c.rows]
+    o, _ = c.run()
+    assert torch.equal(out, o)
+
+
+def test_refusals(sil):
+    import torch
+    c = kl.Case(sil, "bf16", 8, 2, 64, 16, [70, 3], seed=2)
+    q, table, lens = c.device()
+    out = torch.full_like(q, 9.0)
+    f32, i32 = (lambda *s: torch.zeros(s, device="cuda")), (lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda"))
+
+    def no(code, **kw):
+        with pytest.raises(sil.ILError) as e:
+            sil.kv_attend(c.cache, q, table, lens, kw.pop("out", out), **kw)
+        assert e.value.code == code
+
+    no(-1, cap=-1.0)
+    no(-1, cap=math.inf)
+    no(-1, cap=math.nan)
+    no(-1, cap=1e-30, scale=1e30)
+    no(-1, slopes=f32(7))
+    no(-1, slopes=f32(8).double())
+    no(-1, starts=i32(3))
+    no(-1, starts=f32(2))
+    no(-1, starts=i32(2), positions=i32(3, 80))
+    no(-1, starts=i32(2), positions=i32(80))
+    no(-2, starts=i32(2), positions=i32(2, 80).as_strided((2, 80), (40, 1)))
+    no(-1, starts=i32(2).cpu())
+    flat = torch.zeros(2 * 8 * 64, device="cuda")
+    no(-1, slopes=flat[:8], out=flat.view(2, 8, 64))
+    no(-1, starts=flat[8:10].view(torch.int32), out=flat.view(2, 8, 64))
+    no(-1, starts=i32(2), positions=flat[:160].view(torch.int32).view(2, 80), out=flat.view(2, 8, 64))
+    torch.cuda.synchronize()
+    assert bool((out == 9.0).all()) and bool((flat == 0).all())
