@@ -272,11 +272,13 @@ int il_centroid_head(const float* x, int64_t h, const il_weight* centroids, cons
  *     il_kv_append  k and v rows into the cache (and il_kv_read back)
  *     il_kv_attend  one new token's attention over each sequence's cache (il_kv_attend_scored:
  *                   with capped or biased logits, or from a later token on)
+ *     il_kv_weigh   the attention that each cached token collects
+ *     il_kv_evict   sequences cut to the tokens that collected most
  * The cache is the caller's memory, described by value: n_pages pages of
  * page_size tokens.  A token's slot is page * page_size + its index in the page;
  * a sequence's block table lists its pages, so that its position p is in page
  * table[p / page_size].  All pointers are DEVICE pointers; every call is one
- * kernel launch (none for an empty call), asynchronous on `stream`, and can be
+ * kernel launch (il_kv_evict two; none for an empty call), asynchronous on `stream`, and can be
  * captured in a CUDA graph.  Lengths, tables and slots live on the device and may
  * change between the replays of a graph.  Arguments that only the device can
  * see are checked there: a page or slot outside the cache is never accessed;
@@ -435,6 +437,49 @@ typedef struct {
 int il_kv_attend_scored(const il_kv* kv, const float* q, int64_t q_stride, const int32_t* table, int64_t table_stride,
                         int64_t table_width, const int32_t* lens, int64_t n_seq, int64_t n_q_heads, float scale,
                         int64_t window, const il_kv_score* score, float* out, int64_t out_stride, float* lse, void* stream);
+
+/*
+ * il_kv_weigh -- what each cached token collects of one new token's attention, over all query heads:
+ *     weights_out[r][t] = (t is new ? 0 : weights[r][t]) + sum_h exp(s_t - lse_h)
+ * for t < lens[r], with s as il_kv_attend (or, with score, il_kv_attend_scored) has it; tokens that are not seen add
+ * nothing.  Call it with the same arguments, and that call's lse.  K is read, V is not.
+ *   q .. score : as for il_kv_attend_scored; score may be NULL.
+ *   lse       : fp32 [n_seq][n_q_heads].
+ *   add       : int32 [n_seq] or NULL: the last add[r] tokens are new, whatever weights holds there (il_kv_extend's
+ *               add; all of them for a new sequence; negative: none).
+ *   weights, weights_out : fp32 [n_seq][weights_width], rows weights_stride apart; may be the same.  A length is cut to
+ *               weights_width (at most 2^30).  Entries from the length on are left as they are.
+ * Sums are fp32, in an order that depends on the lengths only: equal calls give equal bits.  K, q and lse that are read must
+ * be finite.  Needs no workspace.
+ */
+int il_kv_weigh(const il_kv* kv, const float* q, int64_t q_stride, const int32_t* table, int64_t table_stride,
+                int64_t table_width, const int32_t* lens, int64_t n_seq, int64_t n_q_heads, float scale, int64_t window,
+                const il_kv_score* score, const float* lse, const int32_t* add, const float* weights, float* weights_out,
+                int64_t weights_stride, int64_t weights_width, void* stream);
+
+/*
+ * il_kv_evict -- cuts sequences longer than `keep` to that many tokens: those at the first positions, the most recent
+ * ones and, of the others, those of the largest weight (of equal ones those of the lower index; NaN counts as the least).
+ * Kept tokens of index keep and more move to the places of tokens before it that go, the i-th to the i-th; the others stay
+ * where they are, so that a token's index no longer tells its position (hence `positions`).
+ * Sequences of up to `keep` tokens stay as they are.  lens, table and the free pages stay too: drop holds the
+ * changes of length for il_kv_extend's add, which gives the pages back -- once, where the caches of several
+ * layers share a table and each has been cut by a call of its own.
+ *   keep      : 1 to 2^30.     first, recent : tokens of position below first, or above that of the last token less
+ *               recent, stay whatever their weight; first + recent <= keep.
+ *   weights, weights_out : as for il_kv_weigh; the weights move with their tokens.
+ *   positions, positions_out : int32 likewise [n_seq][positions_width], distinct in a sequence and the last token's the
+ *               newest; both NULL: a token's position is its index.  A length is cut to their width.
+ *   kept      : int32 [n_seq][keep], rows kept_stride apart: the index that a token now at i had, -1 from the new length on.
+ *   drop      : int32 [n_seq]: the new length less the length.
+ * The pages of a sequence that is cut must be its own.  Outputs must not overlap each other or an input, except
+ * weights_out == weights and positions_out == positions.  Two launches; needs no workspace.
+ */
+int il_kv_evict(const il_kv* kv, const int32_t* table, int64_t table_stride, int64_t table_width, const int32_t* lens,
+                int64_t n_seq, int64_t keep, int64_t first, int64_t recent, const float* weights, float* weights_out,
+                int64_t weights_stride, int64_t weights_width, const int32_t* positions, int32_t* positions_out,
+                int64_t positions_stride, int64_t positions_width, int32_t* kept, int64_t kept_stride, int32_t* drop,
+                void* stream);
 
 /* 1 if the handle came from il_upload_gate_up, 0 if from il_upload_weight,
  * -1 for an invalid handle. */

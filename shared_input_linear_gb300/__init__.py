@@ -20,7 +20,8 @@ import numpy as np
 __all__ = ["ILError", "Weight", "FORMATS", "KV_FORMATS", "IL_BF16", "IL_Q8", "IL_Q4", "IL_A4", "load", "build",
            "upload_weight", "matmul_batch", "matmul_batch_ptr", "matmul_batch_noalloc_ptr", "free_weight", "weight_bytes",
            "dequantize_weight", "check_device_status", "release_scratch", "get_stats", "reset_stats", "last_error",
-           "version", "LIB_PATH", "STATUS", "KVCache", "kv_cache", "kv_extend", "kv_append", "kv_read", "kv_attend"]
+           "version", "LIB_PATH", "STATUS", "KVCache", "kv_cache", "kv_extend", "kv_append", "kv_read", "kv_attend", "kv_weigh",
+           "kv_evict"]
 
 IL_BF16, IL_Q8, IL_Q4, IL_A4 = 0, 1, 2, 3
 FORMATS = {"bf16": IL_BF16, "q8": IL_Q8, "q4": IL_Q4}
@@ -107,6 +108,10 @@ def load() -> ctypes.CDLL:
         lib.il_kv_attend.restype = ci
         lib.il_kv_attend_scored.argtypes = [vp, vp, i64, vp, i64, i64, vp, i64, i64, ctypes.c_float, i64, vp, vp, i64, vp, vp]
         lib.il_kv_attend_scored.restype = ci
+        lib.il_kv_weigh.argtypes = [vp, vp, i64, vp, i64, i64, vp, i64, i64, ctypes.c_float, i64, vp, vp, vp, vp, vp, i64, i64, vp]
+        lib.il_kv_weigh.restype = ci
+        lib.il_kv_evict.argtypes = [vp, vp, i64, i64, vp, i64, i64, i64, i64, vp, vp, i64, i64, vp, vp, i64, i64, vp, i64, vp, vp]
+        lib.il_kv_evict.restype = ci
         lib.il_weight_is_gate_up.argtypes = [vp]
         lib.il_weight_is_gate_up.restype = ci
         lib.il_free_weight.argtypes = [vp]
@@ -539,6 +544,65 @@ def kv_attend(cache: KVCache, q, table, lens, out, lse=None, scale=None, window:
     else:
         rc = (_lib or load()).il_kv_attend_scored(cache._ref, qp, qs, tp, ts, tw, lp, n, heads, scale, window,
                                                   ctypes.addressof(score), op, os_, ep, stream)
+    if rc:
+        _check(rc)
+
+
+def _in_out(t, out, n: int, dtype, what: str):
+    """(address, address of the output, row stride, width) of a row a sequence that is updated, in place or beside."""
+    if t is None:
+        raise ILError(-1, f"{what} must not be None")
+    tp, ts, tw = _table(t, n, dtype, what)
+    if out is None or out is t:
+        return tp, tp, ts, tw
+    op, os_, ow = _table(out, n, dtype, what + "_out")
+    if ow != tw or (n > 1 and os_ != ts):
+        raise ILError(-2, f"{what}_out must have the shape and strides of {what}")
+    return tp, op, ts, tw
+
+
+def kv_weigh(cache: KVCache, q, table, lens, lse, weights, weights_out=None, add=None, scale=None, window: int = 0, stream=None,
+             cap: float = 0.0, slopes=None, starts=None, positions=None) -> None:
+    """``il_kv_weigh``: adds to ``weights`` fp32 ``[n_seq][width]`` (rows may be apart) what each cached token gets of
+    the attention of ``q`` over all query heads; ``weights_out`` defaults to ``weights`` itself.
+
+    ``lse`` is what :func:`kv_attend` gave for the same arguments; the last ``add`` (int32 ``[n_seq]``) tokens are
+    new and start from 0."""
+    import torch
+    if q.dim() != 3:
+        raise ILError(-1, "q must be [n_seq][n_q_heads][head_dim]")
+    n, heads, _ = q.shape
+    dim, f32, i32 = cache.head_dim, torch.float32, torch.int32
+    qp, qs = _rows(q, n, heads, dim, f32, "q")
+    tp, ts, tw = _table(table, n, i32)
+    if lse is None:
+        raise ILError(-1, "lse must not be None")
+    score = _score(n, heads, cap, slopes, starts, positions)
+    rc = (_lib or load()).il_kv_weigh(cache._ref, qp, qs, tp, ts, tw, _ptr(lens, i32, n, "lens"), n, heads,
+                                      dim ** -0.5 if scale is None else scale, window,
+                                      0 if score is None else ctypes.addressof(score), _ptr(lse, f32, n * heads, "lse"),
+                                      _ptr(add, i32, n, "add"), *_in_out(weights, weights_out, n, f32, "weights"), _stream_ptr(stream))
+    if rc:
+        _check(rc)
+
+
+def kv_evict(cache: KVCache, table, lens, weights, kept, drop, first: int = 0, recent: int = 0, weights_out=None, positions=None,
+             positions_out=None, stream=None) -> None:
+    """``il_kv_evict``: cuts each sequence to ``keep = kept.shape[1]`` tokens: those of the ``first`` and the ``recent``
+    positions and the heaviest of the others.  ``kept`` int32 ``[n_seq][keep]`` gets the old index of each token, ``drop`` int32
+    ``[n_seq]`` the changes of length, for :func:`kv_extend`.
+
+    ``weights`` fp32 and ``positions`` int32 (or None: positions are indices) ``[n_seq][width]`` are updated, in place or
+    into ``weights_out`` and ``positions_out``."""
+    import torch
+    i32 = torch.int32
+    n = lens.numel()
+    tp, ts, tw = _table(table, n, i32)
+    kp, ks, keep = _table(kept, n, i32, "kept")
+    places = (0, 0, 0, 0) if positions is None and positions_out is None else _in_out(positions, positions_out, n, i32, "positions")
+    rc = (_lib or load()).il_kv_evict(cache._ref, tp, ts, tw, _ptr(lens, i32, n, "lens"), n, keep, first, recent,
+                                      *_in_out(weights, weights_out, n, torch.float32, "weights"), *places, kp, ks,
+                                      _ptr(drop, i32, n, "drop"), _stream_ptr(stream))
     if rc:
         _check(rc)
 

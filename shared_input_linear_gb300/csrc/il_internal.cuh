@@ -413,6 +413,38 @@ struct KvAttendArgs {
   int64_t positions_stride, positions_width;
 };
 
+// il_kv_weigh: `attend` without out, whose lse is read.
+struct KvWeighArgs {
+  KvAttendArgs attend;
+  const int32_t* add;
+  const float* weights;
+  float* weights_out;
+  int64_t weights_stride, weights_width;
+};
+
+struct KvEvictArgs {
+  KvView kv;
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* lens;
+  int n_seq, cap;  // cap: a length is cut to it
+  int keep, first, recent;
+  const float* weights;
+  float* weights_out;
+  int64_t weights_stride;
+  const int32_t* positions;
+  int32_t* positions_out;
+  int64_t positions_stride;
+  int32_t* kept;
+  int64_t kept_stride;
+  int32_t* drop;
+  unsigned* status;
+};
+
+cudaError_t prepare_kv_weigh(const KvWeighArgs& a, int num_sms, Launch* out);
+// Two launches: the choice, then the rows.
+cudaError_t prepare_kv_evict(const KvEvictArgs& a, int num_sms, std::vector<Launch>* out);
+
 cudaError_t prepare_kv_extend(const KvExtendArgs& a, int num_sms, Launch* out);
 // write: fp32 rows into the cache; otherwise the cached values into the rows.
 cudaError_t prepare_kv_rows(bool write, const KvView& kv, float* k, int64_t k_stride, float* v, int64_t v_stride,

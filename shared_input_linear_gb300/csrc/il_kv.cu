@@ -1,5 +1,5 @@
 // il_kv.cu -- entry points of the paged K/V cache (include/il.h: il_kv_extend, il_kv_append,
-// il_kv_read, il_kv_attend, il_kv_attend_scored): every argument that the host can see is checked and the launch
+// il_kv_read, il_kv_attend, il_kv_attend_scored, il_kv_weigh, il_kv_evict): every argument that the host can see is checked and the launch
 // prepared before it is enqueued, as in the matmul entry points.
 #include <algorithm>
 #include <cstdio>
@@ -179,64 +179,81 @@ int check_score(const char* fn, const il_kv_score* score, float scale, int64_t n
   return IL_OK;
 }
 
-// score: nullptr, or what il_kv_attend_scored adds.
+// The arguments that il_kv_attend, il_kv_attend_scored and il_kv_weigh share, into `a`; score: nullptr or what it adds.  For n_seq = 0
+// (a no-op) the arrays are not looked at.
+int check_attended(const char* fn, const il_kv* kv, const float* q, int64_t q_stride, const int32_t* table, int64_t table_stride,
+                   int64_t table_width, const int32_t* lens, int64_t n_seq, int64_t n_q_heads, float scale, int64_t window,
+                   const il_kv_score* score, KvAttendArgs* a) {
+  memset(a, 0, sizeof *a);
+  int rc = check_cache(fn, kv, &a->kv);
+  if (rc != IL_OK) return rc;
+  if (n_seq < 0 || n_seq > kMaxKvSeqs) return bad(IL_ERR_ARG, fn, "n_seq out of range");
+  if (n_q_heads < 1 || n_q_heads > 32768 || n_q_heads % a->kv.n_heads != 0)
+    return bad(IL_ERR_SHAPE, fn, "n_q_heads must be a multiple of the cache's n_heads, at most 32768");
+  if (window < 0) return bad(IL_ERR_ARG, fn, "window is negative");
+  if (!(scale - scale == 0.0f)) return bad(IL_ERR_ARG, fn, "scale is not finite");
+  rc = check_score(fn, score, scale, n_seq, a);
+  if (rc != IL_OK || n_seq == 0) return rc;
+  if (q == nullptr || table == nullptr || lens == nullptr) return bad(IL_ERR_ARG, fn, "q, table and lens must not be NULL");
+  if (!aligned(q, 16)) return bad(IL_ERR_ARG, fn, "q is not 16-byte aligned");
+  if (!aligned(table, 4) || !aligned(lens, 4)) return bad(IL_ERR_ARG, fn, "table or lens is not 4-byte aligned");
+  if (n_seq > 1 && (q_stride < n_q_heads * a->kv.head_dim || q_stride % 4 != 0 || q_stride > INT64_MAX / 8 / n_seq))
+    return bad(IL_ERR_SHAPE, fn, "q_stride is smaller than a row or not a multiple of 4");
+  if (table_width < 1 || table_width > INT32_MAX || (n_seq > 1 && (table_stride < table_width || table_stride > INT32_MAX)))
+    return bad(IL_ERR_SHAPE, fn, "table_width or table_stride out of range");
+  a->q = q;
+  a->q_stride = n_seq > 1 ? q_stride : 0;
+  a->table = table;
+  a->table_stride = n_seq > 1 ? table_stride : 0;
+  a->table_width = table_width;
+  a->lens = lens;
+  a->n_seq = (int)n_seq;
+  a->n_q_heads = (int)n_q_heads;
+  a->scale = scale;
+  a->window = window;
+  return IL_OK;
+}
+
+// What a call of those arguments reads: q first.
+std::vector<Range> ranges_of(const KvAttendArgs& a) {
+  const int64_t n = a.n_seq, row = (int64_t)a.n_q_heads * a.kv.head_dim;
+  return {{a.q, 4 * ((n - 1) * a.q_stride + row), false},
+          {a.table, 4 * ((n - 1) * a.table_stride + a.table_width), false},
+          {a.lens, 4 * n, false},
+          {a.kv.k, extent_bytes(a.kv, false), false},
+          {a.kv.v, extent_bytes(a.kv, false), false},
+          {a.kv.k_scale, extent_bytes(a.kv, true), false},
+          {a.kv.v_scale, extent_bytes(a.kv, true), false},
+          {a.slopes, 4 * (int64_t)a.n_q_heads, false},
+          {a.starts, 4 * n, false},
+          {a.positions, 4 * ((n - 1) * a.positions_stride + a.positions_width), false}};
+}
+
 int attend_call(const char* fn, const il_kv* kv, const float* q, int64_t q_stride, const int32_t* table, int64_t table_stride,
                 int64_t table_width, const int32_t* lens, int64_t n_seq, int64_t n_q_heads, float scale, int64_t window,
                 const il_kv_score* score, float* out, int64_t out_stride, float* lse, void* stream) {
   NvtxRange range(fn);
   api_clear_error();
   KvAttendArgs a;
-  memset(&a, 0, sizeof a);
-  int rc = check_cache(fn, kv, &a.kv);
-  if (rc != IL_OK) return rc;
-  if (n_seq < 0 || n_seq > kMaxKvSeqs) return bad(IL_ERR_ARG, fn, "n_seq out of range");
-  if (n_q_heads < 1 || n_q_heads > 32768 || n_q_heads % a.kv.n_heads != 0)
-    return bad(IL_ERR_SHAPE, fn, "n_q_heads must be a multiple of the cache's n_heads, at most 32768");
-  if (window < 0) return bad(IL_ERR_ARG, fn, "window is negative");
-  if (!(scale - scale == 0.0f)) return bad(IL_ERR_ARG, fn, "scale is not finite");
-  rc = check_score(fn, score, scale, n_seq, &a);
+  int rc = check_attended(fn, kv, q, q_stride, table, table_stride, table_width, lens, n_seq, n_q_heads, scale, window, score, &a);
   if (rc != IL_OK || n_seq == 0) return rc;
-  if (q == nullptr || table == nullptr || lens == nullptr || out == nullptr)
-    return bad(IL_ERR_ARG, fn, "q, table, lens and out must not be NULL");
-  if (!aligned(q, 16) || !aligned(out, 16)) return bad(IL_ERR_ARG, fn, "q or out is not 16-byte aligned");
-  if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(lse, 4))
-    return bad(IL_ERR_ARG, fn, "table, lens or lse is not 4-byte aligned");
+  if (out == nullptr) return bad(IL_ERR_ARG, fn, "out must not be NULL");
+  if (!aligned(out, 16)) return bad(IL_ERR_ARG, fn, "out is not 16-byte aligned");
+  if (!aligned(lse, 4)) return bad(IL_ERR_ARG, fn, "lse is not 4-byte aligned");
   const int64_t row = n_q_heads * a.kv.head_dim;
-  if (n_seq > 1 && (q_stride < row || out_stride < row || q_stride % 4 != 0 || out_stride % 4 != 0 ||
-                    q_stride > INT64_MAX / 8 / n_seq || out_stride > INT64_MAX / 8 / n_seq))
-    return bad(IL_ERR_SHAPE, fn, "q_stride or out_stride is smaller than a row or not a multiple of 4");
-  if (table_width < 1 || table_width > INT32_MAX || (n_seq > 1 && (table_stride < table_width || table_stride > INT32_MAX)))
-    return bad(IL_ERR_SHAPE, fn, "table_width or table_stride out of range");
-  const int64_t qs = n_seq > 1 ? q_stride : 0, os = n_seq > 1 ? out_stride : 0, ts = n_seq > 1 ? table_stride : 0;
+  if (n_seq > 1 && (out_stride < row || out_stride % 4 != 0 || out_stride > INT64_MAX / 8 / n_seq))
+    return bad(IL_ERR_SHAPE, fn, "out_stride is smaller than a row or not a multiple of 4");
+  const int64_t os = n_seq > 1 ? out_stride : 0;
   const Range outs[] = {{out, 4 * ((n_seq - 1) * os + row), true}, {lse, 4 * n_seq * n_q_heads, true}};
-  const Range ins[] = {{q, 4 * ((n_seq - 1) * qs + row), false},
-                       {table, 4 * ((n_seq - 1) * ts + table_width), false},
-                       {lens, 4 * n_seq, false},
-                       {a.kv.k, extent_bytes(a.kv, false), false},
-                       {a.kv.v, extent_bytes(a.kv, false), false},
-                       {a.kv.k_scale, extent_bytes(a.kv, true), false},
-                       {a.kv.v_scale, extent_bytes(a.kv, true), false},
-                       {a.slopes, 4 * n_q_heads, false},
-                       {a.starts, 4 * n_seq, false},
-                       {a.positions, 4 * ((n_seq - 1) * a.positions_stride + a.positions_width), false}};
+  const std::vector<Range> ins = ranges_of(a);
   for (const Range& o : outs)
     for (const Range& i : ins)
-      if (clash(o, i) && !(&o == outs && &i == ins && side_by_side(out, os, q, qs, n_seq, row)))
+      if (clash(o, i) && !(&o == outs && &i == ins.data() && side_by_side(out, os, q, a.q_stride, n_seq, row)))
         return bad(IL_ERR_ARG, fn, "out and lse must not overlap q, table, lens, the score's arrays or the cache");
   if (clash(outs[0], outs[1])) return bad(IL_ERR_ARG, fn, "out and lse must not overlap");
   int num_sms = 0;
   const int dev = api_device(&num_sms, &a.status);
   if (dev < 0) return dev;
-  a.q = q;
-  a.q_stride = qs;
-  a.table = table;
-  a.table_stride = ts;
-  a.table_width = table_width;
-  a.lens = lens;
-  a.n_seq = (int)n_seq;
-  a.n_q_heads = (int)n_q_heads;
-  a.scale = scale;
-  a.window = window;
   a.out = out;
   a.out_stride = os;
   a.lse = lse;
@@ -247,6 +264,17 @@ int attend_call(const char* fn, const il_kv* kv, const float* q, int64_t q_strid
   const cudaError_t e = prepare_kv_attend(a, num_sms, ws, &L);
   if (e != cudaSuccess) return api_cuda_fail(e, fn);
   return enqueue(fn, L, stream);
+}
+
+constexpr int64_t kMaxWeightsRow = 1 << 30;
+
+// Rows of one number a token, [n_seq][width].
+int check_side(const char* fn, const void* in, const void* out, int64_t stride, int64_t width, int64_t n_seq, const char* what) {
+  char buf[96];
+  snprintf(buf, sizeof buf, "%s: NULL, not 4-byte aligned, or a width or stride out of range", what);
+  if (in == nullptr || out == nullptr || !aligned(in, 4) || !aligned(out, 4)) return bad(IL_ERR_ARG, fn, buf);
+  if (width < 1 || width > kMaxWeightsRow || (n_seq > 1 && (stride < width || stride > INT32_MAX))) return bad(IL_ERR_SHAPE, fn, buf);
+  return IL_OK;
 }
 
 }  // namespace
@@ -351,6 +379,124 @@ int il_kv_attend_scored(const il_kv* kv, const float* q, int64_t q_stride, const
                         int64_t window, const il_kv_score* score, float* out, int64_t out_stride, float* lse, void* stream) {
   return attend_call("il_kv_attend_scored", kv, q, q_stride, table, table_stride, table_width, lens, n_seq, n_q_heads, scale,
                      window, score, out, out_stride, lse, stream);
+}
+
+int il_kv_weigh(const il_kv* kv, const float* q, int64_t q_stride, const int32_t* table, int64_t table_stride,
+                int64_t table_width, const int32_t* lens, int64_t n_seq, int64_t n_q_heads, float scale, int64_t window,
+                const il_kv_score* score, const float* lse, const int32_t* add, const float* weights, float* weights_out,
+                int64_t weights_stride, int64_t weights_width, void* stream) {
+  const char* fn = "il_kv_weigh";
+  NvtxRange range(fn);
+  api_clear_error();
+  KvWeighArgs w;
+  KvAttendArgs& a = w.attend;
+  int rc = check_attended(fn, kv, q, q_stride, table, table_stride, table_width, lens, n_seq, n_q_heads, scale, window, score, &a);
+  if (rc != IL_OK || n_seq == 0) return rc;
+  if (lse == nullptr) return bad(IL_ERR_ARG, fn, "lse must not be NULL");
+  if (!aligned(lse, 4) || !aligned(add, 4)) return bad(IL_ERR_ARG, fn, "lse or add is not 4-byte aligned");
+  rc = check_side(fn, weights, weights_out, weights_stride, weights_width, n_seq, "weights, weights_out");
+  if (rc != IL_OK) return rc;
+  w.add = add;
+  w.weights = weights;
+  w.weights_out = weights_out;
+  w.weights_stride = n_seq > 1 ? weights_stride : 0;
+  w.weights_width = weights_width;
+  const int64_t bytes = 4 * ((n_seq - 1) * w.weights_stride + weights_width);
+  const Range o{weights_out, bytes, true};
+  std::vector<Range> ins = ranges_of(a);
+  ins.push_back({lse, 4 * n_seq * n_q_heads, false});
+  ins.push_back({add, 4 * n_seq, false});
+  if (weights != weights_out) ins.push_back({weights, bytes, false});
+  for (const Range& i : ins)
+    if (clash(o, i)) return bad(IL_ERR_ARG, fn, "weights_out must not overlap an input, but for weights itself");
+  int num_sms = 0;
+  const int dev = api_device(&num_sms, &a.status);
+  if (dev < 0) return dev;
+  a.lse = const_cast<float*>(lse);
+  Launch L;
+  const cudaError_t e = prepare_kv_weigh(w, num_sms, &L);
+  if (e != cudaSuccess) return api_cuda_fail(e, fn);
+  return enqueue(fn, L, stream);
+}
+
+int il_kv_evict(const il_kv* kv, const int32_t* table, int64_t table_stride, int64_t table_width, const int32_t* lens,
+                int64_t n_seq, int64_t keep, int64_t first, int64_t recent, const float* weights, float* weights_out,
+                int64_t weights_stride, int64_t weights_width, const int32_t* positions, int32_t* positions_out,
+                int64_t positions_stride, int64_t positions_width, int32_t* kept, int64_t kept_stride, int32_t* drop,
+                void* stream) {
+  const char* fn = "il_kv_evict";
+  NvtxRange range(fn);
+  api_clear_error();
+  KvEvictArgs a;
+  memset(&a, 0, sizeof a);
+  int rc = check_cache(fn, kv, &a.kv);
+  if (rc != IL_OK) return rc;
+  if (n_seq < 0 || n_seq > kMaxKvSeqs) return bad(IL_ERR_ARG, fn, "n_seq out of range");
+  if (keep < 1 || keep > kMaxWeightsRow || first < 0 || recent < 0 || first > keep || recent > keep - first)
+    return bad(IL_ERR_ARG, fn, "keep must be 1 to 2^30, first and recent not negative and together at most keep");
+  if (n_seq == 0) return IL_OK;
+  if (table == nullptr || lens == nullptr || kept == nullptr || drop == nullptr)
+    return bad(IL_ERR_ARG, fn, "table, lens, kept and drop must not be NULL");
+  if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(kept, 4) || !aligned(drop, 4))
+    return bad(IL_ERR_ARG, fn, "table, lens, kept or drop is not 4-byte aligned");
+  if (table_width < 1 || table_width > INT32_MAX || (n_seq > 1 && (table_stride < table_width || table_stride > INT32_MAX)))
+    return bad(IL_ERR_SHAPE, fn, "table_width or table_stride out of range");
+  if (n_seq > 1 && (kept_stride < keep || kept_stride > INT32_MAX)) return bad(IL_ERR_SHAPE, fn, "kept_stride out of range");
+  rc = check_side(fn, weights, weights_out, weights_stride, weights_width, n_seq, "weights, weights_out");
+  if (rc != IL_OK) return rc;
+  if (positions != nullptr || positions_out != nullptr) {
+    rc = check_side(fn, positions, positions_out, positions_stride, positions_width, n_seq, "positions, positions_out");
+    if (rc != IL_OK) return rc;
+    a.positions = positions;
+    a.positions_out = positions_out;
+    a.positions_stride = n_seq > 1 ? positions_stride : 0;
+  }
+  a.table = table;
+  a.table_stride = n_seq > 1 ? table_stride : 0;
+  a.lens = lens;
+  a.n_seq = (int)n_seq;
+  a.cap = (int)std::min({std::min<int64_t>(table_width * a.kv.page_size, INT32_MAX), weights_width,
+                         positions != nullptr ? positions_width : INT32_MAX});
+  a.keep = (int)keep;
+  a.first = (int)first;
+  a.recent = (int)recent;
+  a.weights = weights;
+  a.weights_out = weights_out;
+  a.weights_stride = n_seq > 1 ? weights_stride : 0;
+  a.kept = kept;
+  a.kept_stride = n_seq > 1 ? kept_stride : 0;
+  a.drop = drop;
+  const int64_t wb = 4 * ((n_seq - 1) * a.weights_stride + weights_width);
+  const int64_t pb = positions == nullptr ? 0 : 4 * ((n_seq - 1) * a.positions_stride + positions_width);
+  // the cache is read and written; weights and positions may be their own outputs
+  const std::vector<Range> rs = {{kept, 4 * ((n_seq - 1) * a.kept_stride + keep), true},
+                                 {drop, 4 * n_seq, true},
+                                 {weights_out, wb, true},
+                                 {positions_out, pb, true},
+                                 {a.kv.k, extent_bytes(a.kv, false), true},
+                                 {a.kv.v, extent_bytes(a.kv, false), true},
+                                 {a.kv.k_scale, extent_bytes(a.kv, true), true},
+                                 {a.kv.v_scale, extent_bytes(a.kv, true), true},
+                                 {weights == weights_out ? nullptr : weights, wb, false},
+                                 {positions == positions_out ? nullptr : positions, pb, false},
+                                 {table, 4 * ((n_seq - 1) * a.table_stride + table_width), false},
+                                 {lens, 4 * n_seq, false}};
+  for (size_t i = 0; i < rs.size(); ++i)
+    for (size_t j = i + 1; j < rs.size(); ++j) {
+      // K and V (and their scales) may be interleaved in one buffer
+      const bool pools = i >= 4 && j <= 7;
+      if (!pools && clash(rs[i], rs[j])) return bad(IL_ERR_ARG, fn, "the outputs and the cache must not overlap each other or an input");
+    }
+  int num_sms = 0;
+  const int dev = api_device(&num_sms, &a.status);
+  if (dev < 0) return dev;
+  std::vector<Launch> launches;
+  cudaError_t e = prepare_kv_evict(a, num_sms, &launches);
+  if (e == cudaSuccess) {
+    int n = 0;
+    e = run_launches(launches, static_cast<cudaStream_t>(stream), &n);
+  }
+  return e == cudaSuccess ? IL_OK : api_cuda_fail(e, fn);
 }
 
 }  // extern "C"

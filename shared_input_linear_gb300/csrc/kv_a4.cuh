@@ -69,17 +69,21 @@ __device__ __forceinline__ uint32_t split(float x) {
 // The {d, m} of one token: NB of them in shared memory, 4 NB-byte aligned.
 template <int NB>
 __device__ __forceinline__ void load_steps(uint32_t (&dm)[NB], uint32_t at) {
-  static_assert(NB == 2 || NB == 4, "heads of 64 or 128 columns");
-  if constexpr (NB == 4)
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(dm[0]), "=r"(dm[1]), "=r"(dm[2]), "=r"(dm[3]) : "r"(at));
-  else
+  if constexpr (NB == 2) {
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(dm[0]), "=r"(dm[1]) : "r"(at));
+  } else {
+#pragma unroll
+    for (int b = 0; b < NB; b += 4)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(dm[b]), "=r"(dm[b + 1]), "=r"(dm[b + 2]), "=r"(dm[b + 3])
+                   : "r"(at + 4 * b));
+  }
 }
 
-// Where chunk `b` (of one 32-element block, 16 bytes) of row `row` is in a tile: eight rows of one chunk cover the banks.
-template <int NB>
-__device__ __forceinline__ uint32_t chunk_at(int row, int b) {
-  return row * (16 * NB) + ((b ^ (NB == 4 ? (row >> 1) & 3 : (row >> 2) & 1)) << 4);
+// Where 16-byte chunk `c` of row `row` is in a tile whose rows have CPR of them: eight rows of one chunk cover the banks.
+template <int CPR>
+__device__ __forceinline__ uint32_t chunk_at(int row, int c) {
+  return row * (16 * CPR) + ((c ^ (CPR >= 8 ? row & 7 : CPR == 4 ? (row >> 1) & 3 : (row >> 2) & 1)) << 4);
 }
 
 // Query heads of 4 R columns as B operands, scaled so that the largest of a head becomes 2^13 .. 2^14.
