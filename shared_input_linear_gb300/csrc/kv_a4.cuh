@@ -5,10 +5,12 @@
 // times as large: x keeps 22 bits down to 2^-27 of the largest and is cut at 2^-49 of it.  With four heads a K/V head nothing of an
 // MMA is idle, a lane's accumulators are of one head (that of column pair q4 = lane % 4), and a softmax value is in one lane.
 //
-// Decoding costs 5 instructions for 8 elements: nibbles at bits 0-3 and 4-7 of a 16-bit half are fp16 subnormals as they stand,
-// u 2^-24 and 16 u 2^-24, exactly; one shift brings the other two there.  The factor 16 is taken from q, or from the sums
-// over p V at the end.  d multiplies a block's fp32 sum (K) or p (V); m meets the sum of q over the block, and sum p m is a
-// sum of its own, 8 FMAs for 16 tokens.
+// Decoding K costs 5 instructions for 8 elements: nibbles at bits 0-3 and 4-7 of a 16-bit half are fp16 subnormals as they
+// stand, u 2^-24 and 16 u 2^-24, exactly; one shift brings the other two there.  The factor 16 is taken from q.  d multiplies a
+// block's fp32 sum, m meets the sum of q over the block.  V is taken as d (u - 8) + (m + 8 d), d multiplying p: sums of d u and
+// of m over many tokens would each be far larger than the sum of V, and the MMAs' accumulators, which cut, lose it (1e-5 of the
+// result for 512 tokens; 6e-6 with sums that start at -8 times the weights').  u - 8 costs 9 instructions for 8
+// elements, the sum of p (m + 8 d) 8 FMAs for 16 tokens.
 #pragma once
 
 #include "il_internal.cuh"
@@ -44,6 +46,19 @@ __device__ __forceinline__ void nibbles(uint32_t w, uint32_t (&p)[4]) {
   p[3] = w & 0x00f000f0u;
 }
 
+// The same nibbles as fp16 pairs of u - 8: the bits 64uu are 1024 + u, 6400 + 16 u are 1024 + 16 u.
+__device__ __forceinline__ void nibbles_less_8(uint32_t w, uint32_t (&p)[4]) {
+  const __half2 low = __floats2half2_rn(-1032.f, -1032.f), high = __floats2half2_rn(-72.f, -72.f);
+  const __half2 sixteenth = __floats2half2_rn(0.0625f, 0.0625f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u = ((i < 2 ? w : w >> 8) & (i % 2 == 0 ? 0x000f000fu : 0x00f000f0u)) | 0x64006400u;
+    const __half2 h = *reinterpret_cast<const __half2*>(&u);
+    const __half2 v = i % 2 == 0 ? __hadd2(h, low) : __hfma2(h, sixteenth, high);
+    p[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
 __device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
@@ -58,6 +73,7 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 
 __device__ __forceinline__ float step_of(uint32_t dm) { return __uint_as_float(dm << 16); }
 __device__ __forceinline__ float least_of(uint32_t dm) { return __uint_as_float(dm & 0xffff0000u); }
+__device__ __forceinline__ float middle_of(uint32_t dm) { return fmaf(8.f, step_of(dm), least_of(dm)); }
 
 // {hi, lo 2^11} of x.
 __device__ __forceinline__ uint32_t split(float x) {

@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
     // and of query heads 8 r + 2 q4 + (x & 1).  A4: o[2 b + j][2 r + x] of element 32 b + 4 g + 2 j + x, head 4 r + q4
     float o[W / 16][OX], m[R], l[R];
     a4::Query<A4 ? NB : 1, A4 ? R : 1> aq;
-    float om[A4 ? R : 1][A4 ? NB : 1];  // A4: this lane's tokens' part of sum p m, of block b
+    float om[A4 ? R : 1][A4 ? NB : 1];  // A4: this lane's tokens' part of sum p (m + 8 d), of block b
     float slope[SCORED ? R : 1];        // of this lane's softmax rows, times log2(e)
     int newest = 0;                     // position of the row's last token
     // Q8: the largest s so far (m may lie below it), the biased exponent of the largest V scale so far, and that of
@@ -933,9 +933,9 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
         for (int r = 0; r < R; ++r) {
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            float sum = s[r][0] * a4::least_of(dm[0][b]);
+            float sum = s[r][0] * a4::middle_of(dm[0][b]);
 #pragma unroll
-            for (int c = 1; c < NV; ++c) sum = fmaf(s[r][c], a4::least_of(dm[c][b]), sum);
+            for (int c = 1; c < NV; ++c) sum = fmaf(s[r][c], a4::middle_of(dm[c][b]), sum);
             om[r][b] = fmaf(om[r][b], keep[r], sum);
           }
 #pragma unroll
@@ -972,17 +972,11 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
           uint32_t z[GR][4];
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            float c[2][R][4];  // MMA rows g, g + 8 of step j: elements 32 b + 4 g + 2 j, and (16 times) the next
+            uint32_t w[GR][R][2];
 #pragma unroll
-            for (int k = 0; k < GR; ++k) {
-              // tokens 2 q4, 2 q4 + 1 and 8 further of 16, elements 4 g .. 4 g + 3 of blocks b and b + 1
-              if (b % 2 == 0) a4::ldmatrix4_trans(z[k], fv + a4::chunk_at<NB>(16 * k + (lane & 15), b + (lane >> 4)));
-              uint32_t x[4], y[4];
-              a4::nibbles(z[k][2 * (b % 2)], x);
-              a4::nibbles(z[k][2 * (b % 2) + 1], y);
+            for (int k = 0; k < GR; ++k)
 #pragma unroll
-              for (int r = 0; r < R; ++r) {
-                uint32_t w[2];
+              for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   float v = s[r][2 * k + h] * a4::step_of(dm[2 * k + h][b]);
@@ -991,16 +985,25 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
                     const float size = fabsf(v);
                     v = size >= 1.f / 4096.f && (size < 16384.f || k26 == 0) ? v : 0.f;
                   }
-                  w[h] = a4::movmatrix(a4::split(v));
+                  w[k][r][h] = a4::movmatrix(a4::split(v));
                 }
+            float c[2][R][4];  // MMA rows g, g + 8 of step j: elements 32 b + 4 g + 2 j, and the next
+#pragma unroll
+            for (int k = 0; k < GR; ++k) {
+              // tokens 2 q4, 2 q4 + 1 and 8 further of 16, elements 4 g .. 4 g + 3 of blocks b and b + 1
+              if (b % 2 == 0) a4::ldmatrix4_trans(z[k], fv + a4::chunk_at<NB>(16 * k + (lane & 15), b + (lane >> 4)));
+              uint32_t x[4], y[4];
+              a4::nibbles_less_8(z[k][2 * (b % 2)], x);
+              a4::nibbles_less_8(z[k][2 * (b % 2) + 1], y);
+#pragma unroll
+              for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                   if (k == 0)
-                    a4::mma_first(c[j][r], x[2 * j], x[2 * j + 1], y[2 * j], y[2 * j + 1], w[0], w[1]);
+                    a4::mma_first(c[j][r], x[2 * j], x[2 * j + 1], y[2 * j], y[2 * j + 1], w[k][r][0], w[k][r][1]);
                   else
-                    a4::mma(c[j][r], x[2 * j], x[2 * j + 1], y[2 * j], y[2 * j + 1], w[0], w[1]);
+                    a4::mma(c[j][r], x[2 * j], x[2 * j + 1], y[2 * j], y[2 * j + 1], w[k][r][0], w[k][r][1]);
                 }
-              }
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -1202,7 +1205,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
           }
         }
         if constexpr (A4) {
-          const int exp = o_exp - 116, half = exp >> 1;  // the sums' unit is 2^exp, as two factors
+          const int exp = o_exp - 140, half = exp >> 1;  // the sums' unit is 2^exp, as two factors
           const float ua = pow2_biased(127 + half), ub = pow2_biased(127 + exp - half);
 #pragma unroll
           for (int r = 0; r < R; ++r) {
@@ -1227,7 +1230,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
             const float f = !alone ? 1.f : sum == 0.f ? 0.f : __fdividef(1.f, sum);
             float* const to = alone ? a.out + at.s * a.out_stride + ((int64_t)at.hk * P.group + of_group) * D + col0 : part + row * W;
             auto value = [&](int b, int e) {
-              return fmaf(o[2 * b + e / 2][2 * r + e % 2] * ua, e % 2 == 0 ? ub : ub * 0.0625f, om[r][b]) * f;
+              return fmaf(o[2 * b + e / 2][2 * r + e % 2] * ua, ub, om[r][b]) * f;
             };
 #pragma unroll
             for (int b = 0; b < NB; ++b)
