@@ -278,7 +278,7 @@ int il_centroid_head(const float* x, int64_t h, const il_weight* centroids, cons
  * page_size tokens.  A token's slot is page * page_size + its index in the page;
  * a sequence's block table lists its pages, so that its position p is in page
  * table[p / page_size].  All pointers are DEVICE pointers; every call is one
- * kernel launch (il_kv_evict two; none for an empty call), asynchronous on `stream`, and can be
+ * kernel launch (il_kv_evict one or two; none for an empty call), asynchronous on `stream`, and can be
  * captured in a CUDA graph.  Lengths, tables and slots live on the device and may
  * change between the replays of a graph.  Arguments that only the device can
  * see are checked there: a page or slot outside the cache is never accessed;
@@ -473,7 +473,7 @@ int il_kv_weigh(const il_kv* kv, const float* q, int64_t q_stride, const int32_t
  *   kept      : int32 [n_seq][keep], rows kept_stride apart: the index that a token now at i had, -1 from the new length on.
  *   drop      : int32 [n_seq]: the new length less the length.
  * The pages of a sequence that is cut must be its own.  Outputs must not overlap each other or an input, except
- * weights_out == weights and positions_out == positions.  Two launches; needs no workspace.
+ * weights_out == weights and positions_out == positions.  One launch where rows are at most keep + 64 wide, else two; needs no workspace.
  */
 int il_kv_evict(const il_kv* kv, const int32_t* table, int64_t table_stride, int64_t table_width, const int32_t* lens,
                 int64_t n_seq, int64_t keep, int64_t first, int64_t recent, const float* weights, float* weights_out,

@@ -124,13 +124,23 @@ def test_orders_of_weights(sil, kind, keep):
         Cut(sil, "bf16", [n, n - 1], kv=1, dim=8, weights=w, seed=keep).run(keep, 0, 1, in_place=in_place)
 
 
-@pytest.mark.parametrize("n,keep", [(5000, 4999), (20000, 1), (20000, 19000), (40000, 20000), (131072, 4096), (100001, 70000)])
+@pytest.mark.parametrize("n,keep", [(5000, 4999), (20000, 1), (20000, 19000), (40000, 20000), (131072, 4096), (100001, 70000),
+                                    (400000, 300), (400000, 250000)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_long(sil, n, keep, in_place):
     w = np.random.default_rng(n).random((2, n)).astype(np.float32) ** 8
     w[1, ::3] = 0.5
     first, recent = (4, min(64, keep - 4)) if keep > 4 else (0, 0)
     Cut(sil, "bf16", [n, n // 2], page=64, kv=1, dim=8, weights=w, seed=keep).run(keep, first, recent, in_place=in_place)
+
+
+@pytest.mark.parametrize("n_seq", [1, 7, 19, 30, 60, 100])
+def test_numbers_of_sequences(sil, n_seq):
+    """The CTAs that share a sequence go by the number of sequences and the rows' width."""
+    rng = np.random.default_rng(n_seq)
+    lens = [9000] + rng.integers(1, 9001, n_seq - 1).tolist()
+    w = rng.choice(np.float32([0, 0.5, 1, 2]), (n_seq, 9004)) * rng.choice(np.float32([1, 1, 1, 0.999]), (n_seq, 9004))
+    Cut(sil, "q8", lens, page=32, kv=1, dim=32, weights=w, seed=n_seq, positions=True).run(1777, 4, 100, in_place=n_seq % 2 == 0)
 
 
 def test_many_sequences(sil):
