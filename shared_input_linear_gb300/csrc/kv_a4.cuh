@@ -7,7 +7,7 @@
 //
 // Decoding K costs 5 instructions for 8 elements: nibbles at bits 0-3 and 4-7 of a 16-bit half are fp16 subnormals as they
 // stand, u 2^-24 and 16 u 2^-24, exactly; one shift brings the other two there.  The factor 16 is taken from q.  d multiplies a
-// block's fp32 sum, m meets the sum of q over the block.  V is taken as d (u - 8) + (m + 8 d), d multiplying p: sums of d u and
+// block's fp32 sum; the m of four blocks meet the sums of q over them, three bf16 parts each, in one MMA.  V is taken as d (u - 8) + (m + 8 d), d multiplying p: sums of d u and
 // of m over many tokens would each be far larger than the sum of V, and the MMAs' accumulators, which cut, lose it (1e-5 of the
 // result for 512 tokens; 6e-6 with sums that start at -8 times the weights').  u - 8 costs 9 instructions for 8
 // elements, the sum of p (m + 8 d) 8 FMAs for 16 tokens.
@@ -33,7 +33,7 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t at) {
 // Transpose of an 8 x 8 matrix of 16-bit elements, one row in the four lanes of a quad.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 
@@ -52,7 +52,8 @@ __device__ __forceinline__ void nibbles_less_8(uint32_t w, uint32_t (&p)[4]) {
   const __half2 sixteenth = __floats2half2_rn(0.0625f, 0.0625f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t u = ((i < 2 ? w : w >> 8) & (i % 2 == 0 ? 0x000f000fu : 0x00f000f0u)) | 0x64006400u;
+    uint32_t u;  // (w & mask) | 0x64006400
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(u) : "r"(i < 2 ? w : w >> 8), "r"(i % 2 == 0 ? 0x000f000fu : 0x00f000f0u), "r"(0x64006400u));
     const __half2 h = *reinterpret_cast<const __half2*>(&u);
     const __half2 v = i % 2 == 0 ? __hadd2(h, low) : __hfma2(h, sixteenth, high);
     p[i] = *reinterpret_cast<const uint32_t*>(&v);
@@ -71,15 +72,37 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// c = A B of bf16, or c += A B; A's rows g and g + 8 hold pairs x, y in columns 2 q4 and 2 q4 + 8.
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t x0, uint32_t x1, uint32_t y0, uint32_t y1, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(x0), "r"(x1), "r"(y0), "r"(y1), "r"(b0), "r"(b1));
+}
+
 __device__ __forceinline__ float step_of(uint32_t dm) { return __uint_as_float(dm << 16); }
 __device__ __forceinline__ float least_of(uint32_t dm) { return __uint_as_float(dm & 0xffff0000u); }
 __device__ __forceinline__ float middle_of(uint32_t dm) { return fmaf(8.f, step_of(dm), least_of(dm)); }
 
-// {hi, lo 2^11} of x.
-__device__ __forceinline__ uint32_t split(float x) {
-  const __half h = __float2half_rn(x);
-  const __half2 p = __halves2half2(h, __float2half_rn((x - __half2float(h)) * 2048.f));
-  return *reinterpret_cast<const uint32_t*>(&p);
+// Pairs of fp32 in one instruction each.
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(*reinterpret_cast<const uint64_t*>(&x)), "l"(*reinterpret_cast<const uint64_t*>(&y)));
+  return *reinterpret_cast<const float2*>(&r);
+}
+__device__ __forceinline__ float2 sub2(float2 x, float2 y) {
+  uint64_t r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(*reinterpret_cast<const uint64_t*>(&x)), "l"(*reinterpret_cast<const uint64_t*>(&y)));
+  return *reinterpret_cast<const float2*>(&r);
+}
+
+// u = {hi, lo 2^11} of x's first number, v of its second.
+__device__ __forceinline__ void split2(float2 x, uint32_t& u, uint32_t& v) {
+  const __half2 h = __floats2half2_rn(x.x, x.y);
+  const float2 rest = mul2(sub2(x, __half22float2(h)), make_float2(2048.f, 2048.f));
+  const __half2 l = __floats2half2_rn(rest.x, rest.y);
+  const uint32_t hi = *reinterpret_cast<const uint32_t*>(&h), lo = *reinterpret_cast<const uint32_t*>(&l);
+  u = __byte_perm(hi, lo, 0x5410);
+  v = __byte_perm(hi, lo, 0x7632);
 }
 
 // The {d, m} of one token: NB of them in shared memory, 4 NB-byte aligned.
@@ -106,7 +129,9 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
 template <int NB, int R>
 struct Query {
   uint32_t f[R][4 * NB];  // of head 4 r + g / 2, its hi (g even) or lo part: elements 8 q4 .. 8 q4 + 7 of each block
-  float sum[R][NB];       // of head 4 r + q4: the sum over a block, in the products' unit
+  // The sums over the blocks, in the products' unit, as a B operand whose rows are the same four blocks' times three bf16 parts (in the
+  // lanes of a quad; hi's column only): blocks 4 i, 4 i + 1 in [2 i], and the next two
+  uint32_t sum[R][(NB + 1) / 2];
   float back[R][2];       // of head 4 r + q4: the unit, as two factors
 
   // Elements x[b][0 .. 7] = 8 q4 .. of block b, of head 4 r + g / 2; `top`: their largest magnitude over the whole head.
@@ -121,31 +146,49 @@ struct Query {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {  // nibble j of both halves of the lane's word: elements j, j + 4
         const float y = x[b][j] * up, z = x[b][j + 4] * up, sixteenth = j % 2 == 0 ? 1.f : 0.0625f;
-        const uint32_t u = split(y * sixteenth), v = split(z * sixteenth);
+        uint32_t u, v;
+        split2(make_float2(y * sixteenth, z * sixteenth), u, v);
         f[r][4 * b + j] = lo_part ? __byte_perm(u, v, 0x7632) : __byte_perm(u, v, 0x5410);
         total += y + z;
       }
       total += __shfl_xor_sync(~0u, total, 1);
       total += __shfl_xor_sync(~0u, total, 2);
-      sum[r][b] = __shfl_sync(~0u, total, head_lane) * 5.9604644775390625e-08f;  // 2^-24
+      total *= 5.9604644775390625e-08f;  // 2^-24
+      float part = 0.f;                  // hi, mid or lo of it
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const float p = __bfloat162float(__float2bfloat16_rn(total));
+        if (k == q4) part = p;
+        total -= p;
+      }
+      const uint32_t bits = lo_part ? 0u : __float_as_uint(part);
+      sum[r][b / 2] = b % 2 == 0 ? bits >> 16 : sum[r][b / 2] | bits;
     }
     const int unit = __shfl_sync(~0u, e, head_lane) - 116, half = unit >> 1;  // 2^unit = 2^24 / up
     back[r][0] = __int_as_float((half + 127) << 23);
     back[r][1] = __int_as_float((unit - half + 127) << 23);
   }
 
-  // s[r][h]: the product of head 4 r + q4 with token 8 h + g of the 16 from `first` on in the tile of K at `tile`.
-  __device__ __forceinline__ void dot(float (&s)[R][2], uint32_t tile, uint32_t steps, int first, int lane) const {
+  // s[r][h]: the product of head 4 r + q4 with token 8 h + g of 16, whose rows of K are at `tile` and steps at `steps`;
+  // chunks[i]: where the lane's row of blocks 2 i and 2 i + 1 for ldmatrix lies from there, chunk_at(lane % 16, 2 i + lane / 16).
+  __device__ __forceinline__ void dot(float (&s)[R][2], uint32_t tile, uint32_t steps, const uint32_t (&chunks)[NB / 2], int lane) const {
     const int g = lane >> 2;
     uint32_t d[2][NB];
-    load_steps<NB>(d[0], steps + (first + g) * (4 * NB));
-    load_steps<NB>(d[1], steps + (first + 8 + g) * (4 * NB));
+    load_steps<NB>(d[0], steps + g * (4 * NB));
+    load_steps<NB>(d[1], steps + (8 + g) * (4 * NB));
+    auto pair = [&](int t, int b) { return b < NB ? __byte_perm(d[t][b], d[t][b + 1], 0x7632) : 0u; };  // {m, m}
 #pragma unroll
-    for (int r = 0; r < R; ++r) s[r][0] = s[r][1] = 0.f;
+    for (int r = 0; r < R; ++r) {
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int b = 0; b < NB; b += 4)
+        mma_bf16(c, pair(0, b), pair(1, b), pair(0, b + 2), pair(1, b + 2), sum[r][b / 2], b + 2 < NB ? sum[r][b / 2 + 1] : 0u);
+      s[r][0] = c[0], s[r][1] = c[2];
+    }
 #pragma unroll
     for (int i = 0; i < NB / 2; ++i) {
       uint32_t w[4];  // tokens g and g + 8 of blocks 2 i and 2 i + 1
-      ldmatrix4(w, tile + chunk_at<NB>(first + (lane & 15), 2 * i + (lane >> 4)));
+      ldmatrix4(w, tile + chunks[i]);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int b = 2 * i + h;
@@ -158,10 +201,7 @@ struct Query {
           mma_first(c, x[0], y[0], x[1], y[1], f[r][4 * b], f[r][4 * b + 1]);
           mma(c, x[2], y[2], x[3], y[3], f[r][4 * b + 2], f[r][4 * b + 3]);
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            s[r][t] = fmaf(fmaf(c[2 * t + 1], kLoUnit, c[2 * t]), step_of(d[t][b]), s[r][t]);
-            s[r][t] = fmaf(sum[r][b], least_of(d[t][b]), s[r][t]);
-          }
+          for (int t = 0; t < 2; ++t) s[r][t] = fmaf(fmaf(c[2 * t + 1], kLoUnit, c[2 * t]), step_of(d[t][b]), s[r][t]);
         }
       }
     }

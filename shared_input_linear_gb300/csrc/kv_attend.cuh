@@ -18,7 +18,7 @@
 // Stream.  Every warp owns a ring of stages, one tile of K and V each, filled with 16-byte
 // cp.async (any strides, any page size: a lane looks up its token's page one tile ahead) and zeros for
 // tokens outside the attended range.  Where pages hold whole groups of 16 tokens their addresses are one base and
-// constants of the lane.  No barrier other than the warp's own sits in the stream.  A head of more than 128
+// constants of the lane (A4: any pages, offsets of 32 bits that the lanes hand to one another).  No barrier other than the warp's own sits in the stream.  A head of more than 128
 // elements takes a pair of warps, half of its columns each: they trade their halves of s
 // through shared memory, with a barrier of the two.
 //
@@ -63,8 +63,8 @@ struct KvAttendPlan {
   float q_scale;          // scale * log2(e), or scale / cap
   float cap_log2;         // cap * log2(e); 0: none
   int simple;             // pages hold whole groups, the strides below fit, (Q8) scales allow the widest copies
-  uint32_t page_bytes, token_bytes, head_bytes;     // strides of k and v
-  uint32_t spage_bytes, stoken_bytes, shead_bytes;  // of the scales
+  uint32_t page_bytes, token_bytes, head_bytes;     // strides of k and v (A4: in 16 bytes)
+  uint32_t spage_bytes, stoken_bytes, shead_bytes;  // of the scales (A4: in pairs)
   unsigned* arrived;      // one counter a CTA, zero before and after
   float* parts;           // two parts a CTA
 };
@@ -91,14 +91,15 @@ struct Config {
   static constexpr int kPool = kTile * kRowBytes;                      // K or V of a tile
   static constexpr int kScales = F != IL_BF16 ? kTile * kBlocks * 4 : 0;  // its scales
   static constexpr int kStage = 2 * (kPool + kScales);
-  static constexpr int kWarps = kA4 ? (R == 1 ? 16 : R == 2 ? 12 : 8) : kQ8 && R == 1 && W == 64 ? 12 : 8;
+  // (A4: measured with 8, 12 and 16 warps, 64 ragged sequences, heads of 128 as they were then: 116, 102, 137 us; of 64: 133, 112, 97 us)
+  static constexpr int kWarps = kA4 ? (R == 2 ? (W == 64 ? 12 : 8) : W == 64 ? 16 : 12) : kQ8 && R == 1 && W == 64 ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kWorkers = kWarps / H;    // runs of tiles in a CTA
   static constexpr uint32_t kWhole = 2 * kWorkers;  // tiles of a row that is not cut over CTAs
   static constexpr int kFixed = kThreads * 8 + kWorkers * 48 + 32;
   // Two stages, one on its way while the other is used, are 70 KB in flight an SM.  More cost DRAM efficiency: with
   // three, 128 x 4096 tokens bf16 took 332 us instead of 317, heads of 64 92.3 instead of 89.5 (Q8 70.7, 69.1).
-  static constexpr int kStages = 2;
+  static constexpr int kStages = kA4 && W == 64 ? 4 : 2;
   static constexpr int kRing = kStages * kStage;
   static constexpr size_t kSmem = (size_t)kFixed + kWarps * (kPart * 4 + kRing);
   static_assert(kStages >= 2 && kSmem <= kSmemLimit, "the ring does not fit");
@@ -111,6 +112,17 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool use, ui
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(use ? 16 : 0),
                "l"(policy)
                : "memory");
+}
+// The same without a policy, which costs two instructions a copy.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool use) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(use ? 16 : 0) : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void cp_small(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 template <int BYTES>
 __device__ __forceinline__ void cp_small(uint32_t dst, const void* src, bool use, uint64_t policy) {
@@ -438,8 +450,18 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
 
     auto token_of = [&](const Walk& w) { return (w.q.first + w.tile) * T + (lane & (T - 1)); };
     auto column_of = [&](uint32_t t) { return P.by_page.of(t); };
+    // A4: of the tile to be copied next, this lane's token's place in its page (units of `fetch` below), and which tokens are wanted
+    uint32_t in_page_off = 0, in_page_soff = 0, wanted = 0;
     auto page_of = [&](const Walk& w) {  // page of this lane's token of the tile (of 16 tokens, lanes 16-31 repeat 0-15)
       const uint32_t t = token_of(w);
+      if constexpr (A4) {
+        const bool want = t >= w.q.begin && t < w.q.len;
+        const uint32_t col = column_of(t), in_page = t - col * (uint32_t)kv.page_size;
+        in_page_off = in_page * P.token_bytes + w.hk * P.head_bytes;
+        in_page_soff = in_page * P.stoken_bytes + w.hk * P.shead_bytes;
+        wanted = __ballot_sync(~0u, want);
+        return want ? a.table[(int64_t)w.s * (int)a.table_stride + col] : -1;
+      }
       return t >= w.q.begin && t < w.q.len ? a.table[w.s * a.table_stride + column_of(t)] : -1;
     };
     // Positions of the chunks of a row in shared memory, without bank conflicts in the reads below.
@@ -456,11 +478,33 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
     };
     // Copies the tile at `w`; gives the mask of its tokens that exist.
     auto fetch = [&](const Walk& w, int page, int stage) -> uint32_t {
+      if constexpr (A4) {
+        const uint32_t to = ring + stage * C::kStage;
+        if (P.simple && wanted == ~0u && __all_sync(~0u, (uint32_t)page < (uint32_t)kv.n_pages)) {
+          // offsets in units of 16 bytes (and of a pair of steps): 32 bits, computed for one token a lane
+          const uint32_t off = (uint32_t)page * P.page_bytes + in_page_off, soff = (uint32_t)page * P.spage_bytes + in_page_soff;
+          const uint8_t *const kb = kv.k + (col_bytes + chunk * 16), *const vb = kv.v + (col_bytes + chunk * 16);
+          const uint32_t at = to + a4::chunk_at<NB>(sub, chunk);  // rows PER further lie as far apart, whatever the chunk
+#pragma unroll
+          for (int i = 0; i < T / PER; ++i) {
+            const uint64_t o = (uint64_t)__shfl_sync(~0u, off, i * PER + sub) * 16;
+            cp16(at + i * 512, kb + o, in_row);
+            cp16(at + i * 512 + C::kPool, vb + o, in_row);
+          }
+          const uint32_t st = to + 2 * C::kPool + lane * NB * 4;
+#pragma unroll
+          for (int i = 0; i < NB * 4 / SB; ++i) {
+            cp_small<SB>(st + i * SB, reinterpret_cast<const uint8_t*>(kv.k_scale + soff) + col0 / 8 + i * SB);
+            cp_small<SB>(st + C::kScales + i * SB, reinterpret_cast<const uint8_t*>(kv.v_scale + soff) + col0 / 8 + i * SB);
+          }
+          return ~0u;
+        }
+      }
       const uint32_t t = token_of(w), t0 = t - (lane & (T - 1));
       const uint32_t to = ring + stage * C::kStage;
       const bool want = t >= w.q.begin && t < w.q.len, ok = want && (uint32_t)page < (uint32_t)kv.n_pages;
       const uint32_t mask = __ballot_sync(~0u, ok) & (uint32_t)((1ull << T) - 1);
-      if (P.simple && mask == (uint32_t)((1ull << T) - 1)) {
+      if (!A4 && P.simple && mask == (uint32_t)((1ull << T) - 1)) {
 #pragma unroll
         for (int k = 0; k < GR; ++k) {
           const uint32_t first = t0 + k * kGroup, pg = GR == 1 ? (uint32_t)page : (uint32_t)__shfl_sync(~0u, page, k * kGroup);
@@ -475,7 +519,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
             kp += row_step;
             vp += row_step;
           }
-          if constexpr (BLOCKED) {
+          if constexpr (Q8) {
             const uint8_t* const sc = reinterpret_cast<const uint8_t*>(lane < 16 ? kv.k_scale : kv.v_scale) +
                                       ((uint64_t)pg * P.spage_bytes + ((in_page + (lane & 15)) * P.stoken_bytes +
                                                                        w.hk * P.shead_bytes + col0 / 8));
@@ -521,6 +565,12 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
       if (a.positions == nullptr || !(t >= w.q.begin && t < w.q.len)) return (int)t;
       return (int)a.positions[w.s * a.positions_stride + t];
     };
+
+    uint32_t chunks[A4 ? NB / 2 : 1];  // A4: of ldmatrix's rows in 16 tokens, for blocks 2 i and 2 i + 1
+    if constexpr (A4) {
+#pragma unroll
+      for (int i = 0; i < NB / 2; ++i) chunks[i] = a4::chunk_at<NB>(lane & 15, 2 * i + (lane >> 4));
+    }
 
     int page = page_of(in);
     uint32_t masks[S];  // of the tiles in the ring, the tile being used first
@@ -684,7 +734,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
 #pragma unroll
           for (int k = 0; k < GR; ++k) {
             float c[R][2];
-            aq.dot(c, from, from + 2 * C::kPool, 16 * k, lane);
+            aq.dot(c, from + 16 * k * C::kRowBytes, from + 2 * C::kPool + 16 * k * NB * 4, chunks, lane);
 #pragma unroll
             for (int r = 0; r < R; ++r) s[r][2 * k] = c[r][0], s[r][2 * k + 1] = c[r][1];
           }
@@ -834,7 +884,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
       // ---- softmax: p = 2^(s - m) and the factor of what came before
       const uint32_t mk = masks[0];
       float low[R];
-      if constexpr (Q8) {
+      if constexpr (BLOCKED) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           low[r] = s[r][0];
@@ -878,6 +928,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
         } else if constexpr (A4) {
           highest[r] = fmaxf(highest[r], top[r]);
           next[r] = fmaxf(top[r], highest[r] - 24.f);
+          wide |= next[r] - low[r] > 26.f;
         } else {
           next[r] = fmaxf(m[r], top[r]);
         }
@@ -896,7 +947,6 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
           s[r][c] = exp2_fast(s[r][c] - base);
           s[r][c + 1] = exp2_fast(s[r][c + 1] - base);
           sum += s[r][c] + s[r][c + 1];
-          if (A4) wide |= (s[r][c] < 1.f / 67108864.f && s[r][c] > 0.f) || (s[r][c + 1] < 1.f / 67108864.f && s[r][c + 1] > 0.f);
         }
         l[r] = fmaf(l[r], keep[r], sum);
       }
@@ -915,11 +965,8 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
       };
       if constexpr (A4) {
         static_assert(!A4 || T == 32, "a lane looks at one token's steps");
-        const uint32_t sv = from + 2 * C::kPool + C::kScales;
-        uint32_t dm[NV][NB];  // {d, m} of the lane's tokens
-#pragma unroll
-        for (int c = 0; c < NV; ++c) a4::load_steps<NB>(dm[c], sv + (8 * c + g) * NB * 4);
-        uint32_t one[NB], most = 0;  // of one token
+        const uint32_t sv = from + 2 * C::kPool + C::kScales;  // V's steps
+        uint32_t one[NB], most = 0;  // steps of one token
         a4::load_steps<NB>(one, sv + lane * NB * 4);
 #pragma unroll
         for (int b = 0; b < NB; ++b) most = max(most, one[b] & 0x7fffu);
@@ -929,69 +976,50 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
         for (int b = 0; b < NB; ++b) wide |= (one[b] & 0x7fffu) < little && (one[b] & 0x7fffu) != 0;
         wide = __any_sync(~0u, wide);
         const float up = pow2_biased(267 - v_exp);  // the largest d becomes 2^13 .. 2^14
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
+        const uint32_t v_at = from + C::kPool, steps = sv + g * NB * 4;
+        float gap_up[NB];
+        // Products of weights p (ps: p up), with what came before times `keep`, and the sums' unit moved by `shift` too.
+        auto products = [&](auto is_wide, const float (&ps)[R][NV], const float (&p)[R][NV], float shift) {
+          constexpr bool WIDE = decltype(is_wide)::value;
+          uint32_t dm[NV][2], z[GR][4];
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            float sum = s[r][0] * a4::middle_of(dm[0][b]);
+            if (b % 2 == 0) {
+              // {d, m} of the lane's tokens, of blocks b and b + 1; V of tokens 2 q4, 2 q4 + 1 and 8 further of 16, elements 4 g .. 4 g + 3
 #pragma unroll
-            for (int c = 1; c < NV; ++c) sum = fmaf(s[r][c], a4::middle_of(dm[c][b]), sum);
-            om[r][b] = fmaf(om[r][b], keep[r], sum);
-          }
+              for (int c = 0; c < NV; ++c) lds64(dm[c][0], dm[c][1], steps + (8 * c * NB + b) * 4);
 #pragma unroll
-          for (int c = 0; c < NV; ++c) s[r][c] *= up;
-          kept[r] = keep[r];
-        }
-        // Weights w = p d up, at most 2^14, in classes of 2^26 where a tile has p below 2^-26 or a d below 2^-12 of the
-        // largest: class k, 2^(14 - 26 (k + 1)) <= w < 2^(14 - 26 k), is multiplied by 2^(26 k) and the sums' unit goes down as
-        // far until the last class is in; below 2^-90 w is 0.
-        uint32_t classes = 1;
-        if (wide) {
-          classes = 0;
+              for (int k = 0; k < GR; ++k) a4::ldmatrix4_trans(z[k], v_at + 16 * k * C::kRowBytes + chunks[b / 2]);
 #pragma unroll
-          for (int r = 0; r < R; ++r)
+              for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int c = 0; c < NV; ++c)
+                for (int x = 0; x < 2; ++x) {
+                  float sum = p[r][0] * a4::middle_of(dm[0][x]);
 #pragma unroll
-              for (int b = 0; b < NB; ++b) {
-                const float x = fabsf(s[r][c] * a4::step_of(dm[c][b]));
-                const int k = max(140 - (int)(__float_as_uint(x) >> 23), 0) / 26;
-                if (x > 0.f && k < 4) classes |= 1u << k;
+                  for (int c = 1; c < NV; ++c) sum = fmaf(p[r][c], a4::middle_of(dm[c][x]), sum);
+                  om[r][b + x] = fmaf(om[r][b + x], keep[r], sum);
+                }
+              if constexpr (WIDE) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                  for (int c = 0; c < NV; ++c) dm[c][x] = __float_as_uint(a4::step_of(dm[c][x]) * gap_up[b + x]) >> 16;
               }
-          classes = max(__reduce_or_sync(~0u, classes), 1u);  // one at least: what came before takes its factor there
-        }
-#pragma unroll 1
-        while (classes != 0) {
-          const int k26 = 26 * (31 - __clz(classes));
-          classes &= ~(1u << (k26 / 26));
-          const int change = o_exp - (v_exp - k26);
-          const float shift = change < -126 ? 0.f : pow2_biased(127 + change), class_up = pow2_biased(127 + k26);
-          o_exp = v_exp - k26;
-#pragma unroll
-          for (int r = 0; r < R; ++r) kept[r] *= shift;
-          uint32_t z[GR][4];
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
+            }
             uint32_t w[GR][R][2];
 #pragma unroll
             for (int k = 0; k < GR; ++k)
 #pragma unroll
-              for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  float v = s[r][2 * k + h] * a4::step_of(dm[2 * k + h][b]);
-                  if (wide) {
-                    v *= class_up;
-                    const float size = fabsf(v);
-                    v = size >= 1.f / 4096.f && (size < 16384.f || k26 == 0) ? v : 0.f;
-                  }
-                  w[k][r][h] = a4::movmatrix(a4::split(v));
-                }
+              for (int r = 0; r < R; ++r) {
+                a4::split2(a4::mul2(make_float2(ps[r][2 * k], ps[r][2 * k + 1]),
+                                    make_float2(a4::step_of(dm[2 * k][b % 2]), a4::step_of(dm[2 * k + 1][b % 2]))),
+                           w[k][r][0], w[k][r][1]);
+                w[k][r][0] = a4::movmatrix(w[k][r][0]);
+                w[k][r][1] = a4::movmatrix(w[k][r][1]);
+              }
             float c[2][R][4];  // MMA rows g, g + 8 of step j: elements 32 b + 4 g + 2 j, and the next
 #pragma unroll
             for (int k = 0; k < GR; ++k) {
-              // tokens 2 q4, 2 q4 + 1 and 8 further of 16, elements 4 g .. 4 g + 3 of blocks b and b + 1
-              if (b % 2 == 0) a4::ldmatrix4_trans(z[k], fv + a4::chunk_at<NB>(16 * k + (lane & 15), b + (lane >> 4)));
               uint32_t x[4], y[4];
               a4::nibbles_less_8(z[k][2 * (b % 2)], x);
               a4::nibbles_less_8(z[k][2 * (b % 2) + 1], y);
@@ -1005,26 +1033,80 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
                     a4::mma(c[j][r], x[2 * j], x[2 * j + 1], y[2 * j], y[2 * j + 1], w[k][r][0], w[k][r][1]);
                 }
             }
+            const float back = WIDE ? pow2_biased(254 - (int)(__float_as_uint(gap_up[b]) >> 23)) : 1.f;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-              for (int r = 0; r < R; ++r)
+              for (int r = 0; r < R; ++r) {
+                const float f = keep[r] * shift;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                  const float sum = fmaf(c[j][r][2 * x + 1], a4::kLoUnit, c[j][r][2 * x]);
-                  o[2 * b + j][2 * r + x] = fmaf(o[2 * b + j][2 * r + x], kept[r], sum);
+                  float sum = fmaf(c[j][r][2 * x + 1], a4::kLoUnit, c[j][r][2 * x]);
+                  if constexpr (WIDE) sum *= back;
+                  o[2 * b + j][2 * r + x] = fmaf(o[2 * b + j][2 * r + x], f, sum);
                 }
+              }
+          }
+        };
+        float ps[R][NV];
+        if (!wide) {
+          float shift = 1.f;
+          if (o_exp != v_exp) {
+            shift = o_exp - v_exp < -126 ? 0.f : pow2_biased(127 + o_exp - v_exp);
+            o_exp = v_exp;
           }
 #pragma unroll
-          for (int r = 0; r < R; ++r) kept[r] = 1.f;  // of a class still to come
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int c = 0; c < NV; ++c) ps[r][c] = s[r][c] * up;
+          products(std::false_type{}, ps, s, shift);
+        } else {
+          // A tile with p below 2^-26, or a d below 2^-12 of the largest, takes its products in classes of p, class k
+          // being 2^(-26 (k + 1)) <= p < 2^(-26 k) (p = 1 in class 0; p below 2^-104 is 0), and with each block's steps brought up to
+          // the largest.  Class k is multiplied by 2^(26 k), and the sums' unit goes down as far until the last class is in.
+          constexpr float kClass = 67108864.f;  // 2^26
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const int e = (int)(__reduce_max_sync(~0u, one[b] & 0x7fffu) >> 7);
+            gap_up[b] = pow2_biased(127 + min(v_exp - e, v_exp - 14));  // times up it stays a number
+          }
+          uint32_t classes = 0;
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int c = 0; c < NV; ++c) {
+              const int k = (126 - (int)(__float_as_uint(s[r][c]) >> 23)) / 26;
+              if (s[r][c] > 0.f && k < 4) classes |= 1u << k;
+            }
+          classes = max(__reduce_or_sync(~0u, classes), 1u);  // one at least: what came before takes its factor there
+#pragma unroll 1
+          while (classes != 0) {
+            const int k26 = 26 * (31 - __clz(classes));
+            classes &= ~(1u << (k26 / 26));
+            const int change = o_exp - (v_exp - k26);
+            o_exp = v_exp - k26;
+            const float class_up = pow2_biased(127 + k26);
+            float p[R][NV];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+              for (int c = 0; c < NV; ++c) {
+                const float x = s[r][c] * class_up;  // of a higher class: 2^26 or more above 1; of a lower: under 2^-26
+                const bool in_class = x >= 1.f / kClass && (x < 1.f || k26 == 0);
+                p[r][c] = in_class ? s[r][c] : 0.f, ps[r][c] = in_class ? x * up : 0.f;
+              }
+            products(std::true_type{}, ps, p, change < -126 ? 0.f : pow2_biased(127 + change));
+#pragma unroll
+            for (int r = 0; r < R; ++r) keep[r] = 1.f;  // of a class still to come
+          }
         }
         if (o_exp != v_exp) {
-          const float back = pow2_biased(127 + o_exp - v_exp);  // from the last class's unit
+          const float again = pow2_biased(127 + o_exp - v_exp);  // from the last class's unit
           o_exp = v_exp;
 #pragma unroll
           for (int k = 0; k < W / 16; ++k)
 #pragma unroll
-            for (int x = 0; x < OX; ++x) o[k][x] *= back;
+            for (int x = 0; x < OX; ++x) o[k][x] *= again;
         }
       } else if constexpr (Q8) {
         float d[2 * NN][NB];  // V's scales of the lane's tokens
@@ -1191,12 +1273,14 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
         if (!alone) {
           const long long row = u0 + i - at.tile;
           if (!begun_here) {
-            has0 = true, end0 = row_ends, left.s0 = at.s, left.hk0 = at.hk, left.block0 = at.block;
-            left.tiles0 = at.q.tiles, left.row0 = row;
+            Left& to = A4 ? s_left[worker] : left;  // (A4: not kept in registers meanwhile)
+            has0 = true, end0 = row_ends, to.s0 = at.s, to.hk0 = at.hk, to.block0 = at.block;
+            to.tiles0 = at.q.tiles, to.row0 = row;
             part = part_mem + warp * C::kPart;
           } else {  // the run's last tile: nothing is in flight into the ring any more
-            has1 = true, left.s1 = at.s, left.hk1 = at.hk, left.block1 = at.block;
-            left.tiles1 = at.q.tiles, left.row1 = row;
+            Left& to = A4 ? s_left[worker] : left;
+            has1 = true, to.s1 = at.s, to.hk1 = at.hk, to.block1 = at.block;
+            to.tiles1 = at.q.tiles, to.row1 = row;
             part = reinterpret_cast<float*>(ring_mem + (size_t)warp * C::kRing);
             cp_wait<0>();
             __syncwarp();
@@ -1284,7 +1368,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
     cp_wait<0>();
   }
   if (lane == 0 && col0 == 0) {
-    s_left[worker] = left;
+    if (!A4) s_left[worker] = left;
     if (has0) atomicOr(s_mask, 1u << worker);
     if (has0 && end0) atomicOr(s_mask + 1, 1u << worker);
     if (has1) atomicOr(s_mask + 2, 1u << worker);
@@ -1509,8 +1593,6 @@ template <int F, bool SCORED>
 cudaError_t prepare_format(const KvAttendPlan& p, int dim, int blocks, int ctas, Launch* out) {
   auto of = [&](auto w, auto h) {
     constexpr int W = decltype(w)::value, H = decltype(h)::value;
-    if constexpr (F == IL_A4)
-      if (blocks == 4) return prepare_variant<F, SCORED, W, 4, H>(p, ctas, out);
     return blocks == 2 ? prepare_variant<F, SCORED, W, 2, H>(p, ctas, out) : prepare_variant<F, SCORED, W, 1, H>(p, ctas, out);
   };
   using std::integral_constant;

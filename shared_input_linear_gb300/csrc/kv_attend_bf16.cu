@@ -12,11 +12,11 @@ namespace {
 
 int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
-// Blocks of 8 (A4: 4) query heads that a warp takes at once: 16 heads at most.
+// Blocks of 8 (A4: 4) query heads that a warp takes at once.  A4: 8 heads at most, of which K and V of larger groups are read again, from
+// L2; with 16 the sums do not fit the registers (128 heads on 8 of 128, 32 sequences of 4096: 143 us, two blocks of 8: below).
 int head_blocks(const KvAttendArgs& a) {
   const int group = a.n_q_heads / a.kv.n_heads;
-  if (a.kv.format != IL_A4) return group > 8 ? 2 : 1;
-  return group > 8 ? 4 : group > 4 ? 2 : 1;
+  return group > (a.kv.format == IL_A4 ? 4 : 8) ? 2 : 1;
 }
 
 }  // namespace
@@ -55,9 +55,21 @@ cudaError_t prepare_kv_attend(const KvAttendArgs& a, int num_sms, void* ws, Laun
   if (scaled && p.simple)
     p.simple = kv.head_dim == dim && fits(kv.spage * 4, kv.stoken * 4, kv.shead * 4) && bases % (4 * unit) == 0 &&
                even(kv.spage) && even(kv.stoken) && even(kv.shead);
+  if (kv.format == IL_A4) {
+    // offsets in 16 bytes and in pairs of steps fit 32 bits
+    const auto ends = [&](int64_t page, int64_t token, int64_t head) {
+      return (kv.n_pages - 1) * page + (kv.page_size - 1) * token + (kv.n_heads - 1) * head <= UINT32_MAX;
+    };
+    p.simple = kv.head_dim == dim && bases % (4 * unit) == 0 && even(kv.spage) && even(kv.stoken) && even(kv.shead) &&
+               ends(kv.page / 16, kv.token / 16, kv.head / 16) && ends(kv.spage, kv.stoken, kv.shead);
+  }
   p.page_bytes = (uint32_t)(kv.page * es), p.token_bytes = (uint32_t)(kv.token * es), p.head_bytes = (uint32_t)(kv.head * es);
   p.spage_bytes = (uint32_t)(kv.spage * 4), p.stoken_bytes = (uint32_t)(kv.stoken * 4);
   p.shead_bytes = (uint32_t)(kv.shead * 4);
+  if (kv.format == IL_A4) {
+    p.page_bytes = (uint32_t)(kv.page / 16), p.token_bytes = (uint32_t)(kv.token / 16), p.head_bytes = (uint32_t)(kv.head / 16);
+    p.spage_bytes = (uint32_t)kv.spage, p.stoken_bytes = (uint32_t)kv.stoken, p.shead_bytes = (uint32_t)kv.shead;
+  }
   p.arrived = static_cast<unsigned*>(ws);
   p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kKvCounterBytes);
   if (a.scored) {

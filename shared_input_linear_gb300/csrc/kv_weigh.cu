@@ -50,7 +50,7 @@ struct Heads;
 
 template <int NB>
 struct Heads<IL_A4, NB> {
-  static constexpr int kWords = 5 * NB + 2;
+  static constexpr int kWords = 4 * NB + NB / 2 + 2;
   a4::Query<NB, 1> q;
   template <class Load>
   __device__ __forceinline__ void take(const Load& load, int lane) {
@@ -65,11 +65,14 @@ struct Heads<IL_A4, NB> {
     q.take(0, x, quad_max(top), lane);
   }
   __device__ __forceinline__ uint32_t& word(int i) {
-    return i < 4 * NB ? q.f[0][i] : reinterpret_cast<uint32_t&>(i < 5 * NB ? q.sum[0][i - 4 * NB] : q.back[0][i - 5 * NB]);
+    return i < 4 * NB ? q.f[0][i] : i < 4 * NB + NB / 2 ? q.sum[0][i - 4 * NB] : reinterpret_cast<uint32_t&>(q.back[0][i - 4 * NB - NB / 2]);
   }
   __device__ __forceinline__ void dot(float (&s)[2], uint32_t tile, uint32_t steps, int first, int lane) const {
+    uint32_t chunks[NB / 2];
+#pragma unroll
+    for (int i = 0; i < NB / 2; ++i) chunks[i] = a4::chunk_at<NB>(lane & 15, 2 * i + (lane >> 4));
     float t[1][2];
-    q.dot(t, tile, steps, first, lane);
+    q.dot(t, tile + first * 16 * NB, steps + first * 4 * NB, chunks, lane);
     s[0] = t[0][0], s[1] = t[0][1];
   }
 };
@@ -102,7 +105,8 @@ struct Heads<IL_Q8, NB> {
 #pragma unroll
         for (int j = 0; j < 4; j += 2) {
           const float y = x[i][j] * up, z = x[i][j + 1] * up;
-          const uint32_t u = a4::split(y), v = a4::split(z);
+          uint32_t u, v;
+          a4::split2(make_float2(y, z), u, v);
           f[2 * i + j / 2] = lo_part ? __byte_perm(u, v, 0x7632) : __byte_perm(u, v, 0x5410);
           total += y + z;
         }
