@@ -1,6 +1,6 @@
 """Decode with a paged K/V cache: the attention block of a decoder layer for a batch of sequences.
 
-    python examples/decode_attention.py [--seqs 32] [--prompt 1000] [--steps 50] [--cache q8]
+    python examples/decode_attention.py [--seqs 32] [--prompt 1000] [--steps 50] [--cache q8] [--keep 512]
 
 Each step is six calls on one stream, captured once as a CUDA graph and replayed:
 
@@ -9,6 +9,12 @@ Each step is six calls on one stream, captured once as a CUDA graph and replayed
     kv_append                           k and v into the slots
     kv_attend                           q over each sequence's cache
     o = attention Wo^T                  the next batch
+
+With --keep N a sequence's cache is held at N tokens: before the output projection each step also takes
+
+    kv_weigh                            what each cached token got of the attention
+    kv_evict                            the tokens that got least make room, but for the first and the newest
+    kv_extend                           and their pages go back
 
 The lengths and the block table live on the GPU; the host does nothing between steps but
 replay.  Positions are not encoded (a model rotates q and k before the last three calls).
@@ -29,7 +35,8 @@ import shared_input_linear_gb300 as sil  # noqa: E402
 class AttentionBlock:
     """q/k/v and output projections of one layer, and the cache of up to ``n_seq`` sequences."""
 
-    def __init__(self, n_in=4096, heads=32, kv_heads=8, dim=128, n_seq=32, page=16, pages=4096, cache="q8", seed=0):
+    def __init__(self, n_in=4096, heads=32, kv_heads=8, dim=128, n_seq=32, page=16, pages=4096, cache="q8", seed=0,
+                 keep=0, first=4, recent=32):
         self.n_in, self.heads, self.kv_heads, self.dim, self.n_seq, self.page = n_in, heads, kv_heads, dim, n_seq, page
         gen = torch.Generator().manual_seed(seed)
 
@@ -53,6 +60,14 @@ class AttentionBlock:
         self.q, self.k, self.v = (torch.empty((n_seq, h * dim), **f32) for h in (heads, kv_heads, kv_heads))
         self.attention = torch.empty((n_seq, heads, dim), **f32)
         self.out = torch.empty((n_seq, n_in), **f32)
+        self.keep, self.first, self.recent = keep, min(first, keep), min(recent, keep - min(first, keep))
+        if keep:
+            width = self.table.shape[1] * page
+            self.lse = torch.empty((n_seq, heads), **f32)
+            self.weights = torch.zeros((n_seq, width), **f32)
+            self.positions, self.kept, self.drop = torch.zeros((n_seq, width), **i32), torch.empty((n_seq, keep), **i32), torch.empty(n_seq, **i32)
+            self.seen = torch.zeros(n_seq, **i32)  # tokens of each sequence so far, cached or not
+            self.no_slots = torch.empty(0, **i32)
 
     def prompt(self, x, lens):
         """The prompts' tokens, one sequence after the other ``[sum(lens)][n_in]``, into the cache."""
@@ -65,13 +80,24 @@ class AttentionBlock:
         if int(self.info[0]) != 0:
             raise RuntimeError(f"the cache has no room for the prompts: {self.info.tolist()}")
         sil.kv_append(self.cache, k, v, slots)
+        if self.keep:  # the prompts come before anything is evicted: a token's position is its index
+            self.positions.copy_(torch.arange(self.positions.shape[1], device="cuda", dtype=torch.int32).expand_as(self.positions))
+            self.seen.copy_(self.lens)
 
     def step(self):
         """One token of every sequence: reads ``x``, writes ``out``."""
         sil.matmul_batch(self.x, list(zip(self.dev, (self.q, self.k, self.v))))
         sil.kv_extend(self.lens, self.one, self.table, self.ring, self.cursor, self.page, self.slots, info=self.info)
         sil.kv_append(self.cache, self.k, self.v, self.slots)
-        sil.kv_attend(self.cache, self.q.view(self.n_seq, self.heads, self.dim), self.table, self.lens, self.attention)
+        q = self.q.view(self.n_seq, self.heads, self.dim)
+        sil.kv_attend(self.cache, q, self.table, self.lens, self.attention, lse=self.lse if self.keep else None)
+        if self.keep:
+            self.positions.scatter_(1, (self.lens - 1).long()[:, None], self.seen[:, None])
+            self.seen += 1
+            sil.kv_weigh(self.cache, q, self.table, self.lens, self.lse, self.weights, add=self.one)
+            sil.kv_evict(self.cache, self.table, self.lens, self.weights, self.kept, self.drop, first=self.first, recent=self.recent,
+                         positions=self.positions)
+            sil.kv_extend(self.lens, self.drop, self.table, self.ring, self.cursor, self.page, self.no_slots)
         sil.matmul_batch(self.attention.view(self.n_seq, -1), [(self.w_o, self.out)])
 
     def finish(self, which):
@@ -81,12 +107,14 @@ class AttentionBlock:
         sil.kv_extend(self.lens, add, self.table, self.ring, self.cursor, self.page, self.slots, info=self.info)
 
     def capture(self):
-        """A graph of :meth:`step`.  One step runs first, so that the library's workspaces exist, and is taken back."""
+        """A graph of :meth:`step`.  One step runs first, so that the library's workspaces exist, and is taken back (with ``keep``
+        it stays: what it evicted does not come back)."""
         stream = torch.cuda.Stream()
         stream.wait_stream(torch.cuda.current_stream())  # for the prompts' last kv_append, and x
         with torch.cuda.stream(stream):
             self.step()
-            sil.kv_extend(self.lens, -self.one, self.table, self.ring, self.cursor, self.page, self.slots)
+            if not self.keep:
+                sil.kv_extend(self.lens, -self.one, self.table, self.ring, self.cursor, self.page, self.slots)
             torch.cuda.synchronize()
             graph = torch.cuda.CUDAGraph()
             with torch.cuda.graph(graph, stream=stream):
@@ -99,11 +127,12 @@ def main(argv=None) -> dict:
     ap.add_argument("--seqs", type=int, default=32)
     ap.add_argument("--prompt", type=int, default=1000, help="longest prompt")
     ap.add_argument("--steps", type=int, default=50)
-    ap.add_argument("--cache", choices=("bf16", "q8"), default="q8")
+    ap.add_argument("--cache", choices=("bf16", "q8", "a4"), default="q8")
+    ap.add_argument("--keep", type=int, default=0, help="tokens that a sequence's cache is cut to (0: it grows)")
     a = ap.parse_args(argv)
     page = 16
     pages = a.seqs * (-(-(a.prompt + a.steps + 2) // page) + 1)
-    block = AttentionBlock(n_seq=a.seqs, page=page, pages=pages, cache=a.cache)
+    block = AttentionBlock(n_seq=a.seqs, page=page, pages=pages, cache=a.cache, keep=a.keep)
     gen = torch.Generator(device="cuda").manual_seed(1)
     lens = [a.prompt - (i * a.prompt) // (2 * a.seqs) for i in range(a.seqs)]
     for i in range(a.seqs):  # one prompt at a time, as they arrive
@@ -120,7 +149,8 @@ def main(argv=None) -> dict:
     end.record()
     torch.cuda.synchronize()
     sil.check_device_status()
-    if block.lens.tolist() != [n + a.steps for n in lens] or int(block.info[0]) != 0:
+    want = [min(n + a.steps + 1, a.keep) if a.keep else n + a.steps for n in lens]
+    if block.lens.tolist() != want or int(block.info[0]) != 0:
         raise RuntimeError("a step had no room in the cache")
     us = begin.elapsed_time(end) * 1e3 / a.steps
     print(f"{a.seqs} sequences of {min(lens)} to {max(lens)} tokens, {a.cache} cache: {us:.1f} us a step, "

@@ -471,7 +471,7 @@ int il_kv_weigh(const il_kv* kv, const float* q, int64_t q_stride, const int32_t
  *   positions, positions_out : int32 likewise [n_seq][positions_width], distinct in a sequence and the last token's the
  *               newest; both NULL: a token's position is its index.  A length is cut to their width.
  *   kept      : int32 [n_seq][keep], rows kept_stride apart: the index that a token now at i had, -1 from the new length on.
- *   drop      : int32 [n_seq]: the new length less the length.
+ *   drop      : int32 [n_seq]: the new length less lens[r] (of a length that was cut, all that is beyond goes too).
  * The pages of a sequence that is cut must be its own.  Outputs must not overlap each other or an input, except
  * weights_out == weights and positions_out == positions.  One launch where rows are at most keep + 64 wide, else two; needs no workspace.
  */

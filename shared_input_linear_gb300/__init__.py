@@ -413,6 +413,8 @@ def kv_cache(fmt, n_pages: int, page_size: int, n_heads: int, head_dim: int, dev
     f = KV_FORMATS.get(fmt, fmt) if isinstance(fmt, str) else fmt
     if f not in KV_FORMATS.values():
         raise ILError(-3, "the cache must be bf16, q8 or a4")
+    if f == IL_A4 and head_dim % 32:
+        raise ILError(-2, "head_dim of a 4-bit cache must be a multiple of 32")
 
     def pool(dtype, *last):
         return torch.zeros((n_pages, n_heads, page_size, *last), dtype=dtype, device=device).transpose(1, 2)
@@ -504,8 +506,8 @@ def kv_read(cache: KVCache, slots, k, v, stream=None) -> None:
 
 
 def _score(n: int, heads: int, cap: float, slopes, starts, positions):
-    """An ``il_kv_score``, or None where nothing of it is set."""
-    if not cap and slopes is None and starts is None:
+    """An ``il_kv_score``, or None where nothing of it is given."""
+    if not cap and slopes is None and starts is None and positions is None:
         return None
     import torch
     c = _Score(cap, _ptr(slopes, torch.float32, heads, "slopes"), _ptr(starts, torch.int32, n, "starts"), 0, 0, 0)

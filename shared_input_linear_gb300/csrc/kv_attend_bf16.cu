@@ -13,7 +13,7 @@ namespace {
 int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
 // Blocks of 8 (A4: 4) query heads that a warp takes at once.  A4: 8 heads at most, of which K and V of larger groups are read again, from
-// L2; with 16 the sums do not fit the registers (128 heads on 8 of 128, 32 sequences of 4096: 143 us, two blocks of 8: below).
+// L2; with 16 the sums do not fit the registers (128 heads on 8 of 128, 32 sequences of 4096: 143 us, two blocks of 8 117 us).
 int head_blocks(const KvAttendArgs& a) {
   const int group = a.n_q_heads / a.kv.n_heads;
   return group > (a.kv.format == IL_A4 ? 4 : 8) ? 2 : 1;

@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) kv_choose_long_kernel(const KvEvictA
     const int32_t* const positions = a.positions == nullptr ? nullptr : a.positions + s * a.positions_stride;
     int32_t* const positions_out = a.positions == nullptr ? nullptr : a.positions_out + s * a.positions_stride;
     int32_t* const kept = a.kept + s * a.kept_stride;
-    if (tid == 0) a.drop[s] = left - n;
+    if (tid == 0) a.drop[s] = left - max(a.lens[s], 0);
     for (int i = left + tid; i < a.keep; i += kThreads) kept[i] = -1;
     if (n == left) {
       for (int i = tid; i < n; i += kThreads) {
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads) kv_choose_kernel(const KvEvictArgs a
     const int32_t* const positions = a.positions == nullptr ? nullptr : a.positions + s * a.positions_stride;
     int32_t* const positions_out = a.positions == nullptr ? nullptr : a.positions_out + s * a.positions_stride;
     int32_t* const kept = a.kept + s * a.kept_stride;
-    if (tid == 0 && rank == 0) a.drop[s] = left - n;
+    if (tid == 0 && rank == 0) a.drop[s] = left - max(a.lens[s], 0);
     for (int i = left + rank * kThreads + tid; i < a.keep; i += ctas * kThreads) kept[i] = -1;
     if (n == left) {
       for (int i = rank * kThreads + tid; i < n; i += ctas * kThreads) {

@@ -6,9 +6,9 @@
 // token goes beside K.  Bound by HBM at bf16.
 //
 // Work.  Tiles of 32 tokens (16 of bf16 heads above 128) of all sequences form one list, of which every CTA takes an equal run.  A run's
-// piece of one sequence is worked off by the CTA's warps, a tile each at a time, over all K/V heads; where the call has fewer tiles than
-// warps, S warps share a tile, each S-th head one, and their sums are added in order.  Which warp does what depends on the lengths
-// alone: equal calls give equal bits.
+// piece of one sequence is worked off by the CTA's warps, a tile each at a time, over all K/V heads; of the last tiles of a piece,
+// fewer than the warps, each is shared by several warps that take every second, fourth or eighth head, and whose sums are added in
+// order.  Which warp does what depends on the lengths alone: equal calls give equal bits.
 //
 // q is split into the MMAs' parts once per sequence and CTA (by its warps, a K/V head each) and read from shared memory as
 // fragments; heads beyond what fits there are taken in batches.  Each warp has a ring of K tiles of its own, filled with
@@ -34,7 +34,10 @@ struct Plan {
   FastDiv by_page;
   int group, blocks;  // query heads of a K/V head, blocks of 4 of them
   float q_scale, cap_log2;
-  int whole;          // a token's scales can be copied as 16 bytes (8 for heads of 64)
+  int hks, cols;      // K/V heads, and blocks of each, whose q is in shared memory at a time
+  int whole;          // a token's scales can be copied as 16 bytes (8 for heads of 64), and offsets below fit 32 bits
+  uint32_t page, token;    // strides in 16 bytes
+  uint32_t spage, stoken;  // of the scales in words
 };
 
 // The largest of x over the four lanes of a quad.
@@ -202,13 +205,17 @@ struct Config {
   static constexpr int kPool = kTile * kRowBytes;
   static constexpr int kScales = F == IL_BF16 ? 0 : kTile * kBlocks * 4;
   static constexpr int kStage = kPool + kScales;
-  static constexpr int kWarps = 8;
+  // As many as the registers and the rings leave.  A4, 64 ragged sequences of heads of 128: 8 warps 63 us, 12 and 16 56 us; 8192 tokens of
+  // heads of 64: 68, 56, 53 us.  Q8 72 to 76 us with 8 or 12.
+  static constexpr int kWarps = F == IL_BF16 || W == 256 ? 8 : F == IL_A4 ? 16 : 12;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kStages = kStage > 5000 ? 2 : 4;
+  static constexpr int kStages = kStage > 5000 ? 2 : 3;
+  static constexpr int kRowsOf = kTile * kRowBytes / 512;  // copies of a lane, a row each
   static constexpr int kRing = kStages * kStage;
-  static constexpr int kWords = Heads<F, kBlocks>::kWords + 2;  // and of head q4 the lse, times log2(e), and the slope
-  static constexpr int kHeads = 128 * kWords;                   // bytes of four query heads
-  static constexpr int kFixed = kThreads * 8 + kWarps * 8 + 2 * kWarps * kTile * 4;
+  // Of a lane, in fours: the fragments, and of head q4 the lse, times log2(e), and the slope
+  static constexpr int kFours = (Heads<F, kBlocks>::kWords + 2 + 3) / 4;
+  static constexpr int kHeads = 512 * kFours;  // bytes of four query heads
+  static constexpr int kFixed = kThreads * 8 + kWarps * 8 + 2 * kWarps * kTile * 4 + kWarps * 32;
   static constexpr int kBatch = (kSmemLimit - kFixed - kWarps * kRing) / kHeads;  // fours of heads that fit
   static_assert(kBatch >= 1, "the ring leaves no room for q");
 };
@@ -246,15 +253,16 @@ __device__ __forceinline__ Seq seq_of(const Plan& P, int s) {
 }
 
 template <int F, bool SCORED, int W>
-__global__ void __launch_bounds__(Config<F, W>::kThreads, 1) kv_weigh_kernel(const Plan P, const int n_fours, const int batch) {
+__global__ void __launch_bounds__(Config<F, W>::kThreads, 1) kv_weigh_kernel(const Plan P) {
   using C = Config<F, W>;
   using Q = Heads<F, C::kBlocks>;
   constexpr int T = C::kTile, NB = C::kBlocks, NW = C::kWarps, NT = C::kThreads, S = C::kStages, NV = T / 8;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint32_t* const heads_mem = reinterpret_cast<uint32_t*>(smem + NW * C::kRing);
-  long long* const s_before = reinterpret_cast<long long*>(smem + NW * C::kRing + (size_t)batch * C::kHeads);
+  uint4* const heads_mem = reinterpret_cast<uint4*>(smem + NW * C::kRing);  // [four][kFours][lane]
+  long long* const s_before = reinterpret_cast<long long*>(smem + NW * C::kRing + (size_t)P.hks * P.cols * C::kHeads);
   long long* const s_warp = s_before + NT;
-  float* const s_sums = reinterpret_cast<float*>(s_warp + NW);  // [2][NW][T]
+  float* const s_sums = reinterpret_cast<float*>(s_warp + NW);             // [2][NW][T]
+  uint32_t* const s_seen = reinterpret_cast<uint32_t*>(s_sums + 2 * NW * T);  // [NW][8]: tokens seen, of a warp's latest tiles
 
   const KvAttendArgs& a = P.w.attend;
   const KvView& kv = a.kv;
@@ -302,9 +310,12 @@ __global__ void __launch_bounds__(Config<F, W>::kThreads, 1) kv_weigh_kernel(con
   // ---- this CTA's run of the list, and how many warps share a tile
   const long long from = total * blockIdx.x / gridDim.x, to = total * (blockIdx.x + 1) / gridDim.x;
   if (from == to) return;
-  int share = 1;
-  while (share < NW && 2 * share <= kv.n_heads && total * 2 * share <= (long long)gridDim.x * NW) share *= 2;
-  const int slots = NW / share, slot = warp / share, part = warp % share;  // this warp's tile, its share of the heads
+  // Of a piece's tiles whole rounds go a tile a warp; warps that the rest would leave idle share its tiles, each share-th head a warp
+  auto share_of = [&](uint32_t rest) {
+    int share = 1;
+    while (NW % (2 * share) == 0 && 2 * share <= kv.n_heads && rest * 2 * share <= NW) share *= 2;
+    return share;
+  };
 
   auto first_piece = [&]() {
     int lo = 0;
@@ -339,71 +350,96 @@ __global__ void __launch_bounds__(Config<F, W>::kThreads, 1) kv_weigh_kernel(con
   constexpr int ES = F == IL_BF16 ? 2 : 1;
   const uint32_t ring = smem_u32(smem) + warp * C::kRing;
   Piece ahead = first_piece();
-  uint32_t ahead_tile = slot;
-  int ahead_head = part;
+  uint32_t ahead_round = 0;  // first tile of the round
+  int ahead_head = 0, ahead_share = 1;
   bool more = true;
   long long off = 0, soff = 0;  // of this lane's token of that tile
-  bool ok = false;
-  auto locate = [&]() {  // behind the piece's last tile: on to the next piece that has one
-    while (more && ahead_tile >= ahead.count) {
-      more = next_piece(ahead);
-      ahead_tile = slot;
+  uint32_t rows[C::kRowsOf];    // and, where all tokens are there, of the rows that this lane copies, in 16 bytes
+  bool ok = false, all = false;
+  uint32_t located = 0;  // tiles so far
+  const int chunk = lane % CPR, sub = lane / CPR;
+  const bool in_row = chunk * C::kChunk < D;
+  auto locate = [&]() {  // this warp's tile of the round, or of the next that has one for it
+    uint32_t tile;
+    for (;; ahead_round += NW) {
+      while (ahead_round >= ahead.count) {
+        more = next_piece(ahead);
+        if (!more) return;
+        ahead_round = 0;
+      }
+      const uint32_t rest = ahead.count - ahead_round;
+      ahead_share = rest >= NW ? 1 : share_of(rest);
+      tile = ahead_round + warp / ahead_share;
+      ahead_head = warp % ahead_share;
+      if (tile < ahead.count) break;
     }
-    if (!more) return;
-    const uint32_t t = (ahead.q.first + ahead.tile0 + ahead_tile) * T + (lane & (T - 1));
+    const uint32_t t = (ahead.q.first + ahead.tile0 + tile) * T + (lane & (T - 1));
     const bool want = t >= ahead.q.begin && t < ahead.q.len;
     const uint32_t col = P.by_page.of(t);
     const uint32_t page = want ? (uint32_t)a.table[ahead.s * a.table_stride + col] : 0u;
     ok = want && page < (uint32_t)kv.n_pages;
     if (want && !ok) atomicOr(a.status, kStatusBadSlot);
-    const uint32_t in_page = t - col * P.by_page.d;
-    off = ok ? (page * kv.page + in_page * kv.token) * ES : 0;
-    soff = ok ? page * kv.spage + in_page * kv.stoken : 0;
+    const uint32_t seen = __ballot_sync(~0u, ok), in_page = t - col * P.by_page.d;
+    if (lane == 0) s_seen[warp * 8 + (located & 7)] = seen;
+    ++located;
+    all = P.whole && seen == ~0u;
+    if (all) {
+      const uint32_t o = page * P.page + in_page * P.token;
+#pragma unroll
+      for (int i = 0; i < C::kRowsOf; ++i) rows[i] = __shfl_sync(~0u, o, i * PER + sub);
+      soff = page * P.spage + in_page * P.stoken;
+    } else {
+      off = ok ? (page * kv.page + in_page * kv.token) * ES : 0;
+      soff = ok ? page * kv.spage + in_page * kv.stoken : 0;
+    }
   };
-  uint32_t seen = 0, seen_next = 0;  // masks of the tokens of the tile in use, and of the tile being copied
   int stage_in = 0;
   auto fetch = [&]() {
     if (more) {
-      const uint32_t to_smem = ring + stage_in * C::kStage;
-      const int chunk = lane % CPR, sub = lane / CPR;
-      const bool in_row = chunk * C::kChunk < D;
-      const long long head_off = (long long)ahead_head * kv.head * ES;
+      const uint32_t to_smem = ring + stage_in * C::kStage, st = to_smem + C::kPool + lane * NB * 4;
+      const uint8_t* const kb = kv.k + ((long long)ahead_head * kv.head * ES + chunk * 16);
+      const float* const sc = kv.k_scale + (soff + (long long)ahead_head * kv.shead);
+      if (all) {
 #pragma unroll
-      for (int i = 0; i < T * CPR / 32; ++i) {
-        const int row = CPR > 32 ? 0 : i * PER + sub;
-        const long long o = __shfl_sync(~0u, off, row);
-        const bool use = __shfl_sync(~0u, (int)ok, row) && in_row;
-        cp16(to_smem + a4::chunk_at<CPR>(row, chunk), kv.k + (use ? o + head_off + chunk * 16 : 0), use);
-      }
-      if constexpr (F != IL_BF16) {
-        const uint32_t st = to_smem + C::kPool + lane * NB * 4;
-        const float* const sc = kv.k_scale + (ok ? soff + (long long)ahead_head * kv.shead : 0);
-        if (P.whole) {
+        for (int i = 0; i < C::kRowsOf; ++i)
+          cp16(to_smem + a4::chunk_at<CPR>(i * PER + sub, chunk), kb + (uint64_t)rows[i] * 16, in_row);
+        if constexpr (F != IL_BF16) {
           constexpr int SB = NB == 2 ? 8 : 16;
 #pragma unroll
-          for (int i = 0; i < NB * 4 / SB; ++i) cp_small<SB>(st + i * SB, sc + i * (SB / 4), ok);
-        } else {
-#pragma unroll
-          for (int b = 0; b < NB; ++b) cp_small<4>(st + 4 * b, ok && 32 * b < D ? sc + b : kv.k_scale, ok && 32 * b < D);
+          for (int i = 0; i < NB * 4 / SB; ++i) cp_small<SB>(st + i * SB, sc + i * (SB / 4), true);
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < C::kRowsOf; ++i) {
+          const int row = i * PER + sub;
+          const long long o = __shfl_sync(~0u, off, row);
+          const bool use = __shfl_sync(~0u, (int)ok, row) && in_row;
+          cp16(to_smem + a4::chunk_at<CPR>(row, chunk), use ? kb + o : kv.k, use);
+        }
+        if constexpr (F != IL_BF16) {
+#pragma unroll 1
+          for (int b = 0; b < NB; ++b) {
+            const bool use = ok && 32 * b < D;
+            cp_small<4>(st + 4 * b, use ? sc + b : kv.k_scale, use);
+          }
         }
       }
-      ahead_head += share;
+      ahead_head += ahead_share;
       if (ahead_head >= kv.n_heads) {
-        ahead_head = part;
-        ahead_tile += slots;
+        ahead_round += NW;
         locate();
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     stage_in = stage_in + 1 == S ? 0 : stage_in + 1;
   };
-  (void)seen_next;
   locate();
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) fetch();
 
   // ---- the pieces
-  int stage = 0, staged_s = -1, staged_b = -1, parity = 0;
+  int stage = 0, staged_s = -1, staged_h = -1, staged_c = -1, parity = 0;
+  uint32_t used = 0;  // tiles of this warp so far
   Piece piece = first_piece();
   do {
     const int s = piece.s;
@@ -411,17 +447,18 @@ __global__ void __launch_bounds__(Config<F, W>::kThreads, 1) kv_weigh_kernel(con
     const int newest = !SCORED ? 0 : a.positions != nullptr ? a.positions[s * a.positions_stride + q.len - 1] : (int)q.len - 1;
     const uint32_t fresh = P.w.add == nullptr ? 0u : (uint32_t)min(max(P.w.add[s], 0), (int)q.len);
 #pragma unroll 1
-    for (uint32_t k0 = 0; k0 < piece.count; k0 += slots) {
-      const bool active = k0 + slot < piece.count;
-      const uint32_t t0 = (q.first + piece.tile0 + k0 + slot) * T;
-      float sums[NV], far[SCORED ? NV : 1];
+    for (uint32_t k0 = 0; k0 < piece.count; k0 += NW) {
+      const int share = piece.count - k0 >= NW ? 1 : share_of(piece.count - k0), part = warp % share;
+      const uint32_t tile_at = k0 + warp / share;
+      const bool active = tile_at < piece.count;
+      const uint32_t t0 = (q.first + piece.tile0 + tile_at) * T;
+      float sums[NV], far[SCORED ? NV : 1], had = 0.f;
       bool use[NV];
       if (active) {
-        // which of the tile's tokens are seen: in range, and on a page that exists
-        const uint32_t t = t0 + (lane & (T - 1));
-        bool there = t >= q.begin && t < q.len;
-        if (there) there = (uint32_t)a.table[s * a.table_stride + P.by_page.of(t)] < (uint32_t)kv.n_pages;
-        seen = __ballot_sync(~0u, there);
+        __syncwarp();
+        const uint32_t seen = s_seen[warp * 8 + (used++ & 7)], t = t0 + (lane & (T - 1));
+        const bool there = (seen >> lane) & 1;
+        if (part == 0 && t < q.len - fresh) had = P.w.weights[s * ws + t];
         int place = (int)t;
         if (SCORED && a.positions != nullptr && there) place = a.positions[s * a.positions_stride + t];
 #pragma unroll
@@ -432,63 +469,78 @@ __global__ void __launch_bounds__(Config<F, W>::kThreads, 1) kv_weigh_kernel(con
         }
       }
 #pragma unroll 1
-      for (int b0 = 0; b0 < n_fours; b0 += batch) {
-        const int b1 = min(b0 + batch, n_fours);
-        if (staged_s != s || staged_b != b0) {
-          __syncthreads();
-          // q as fragments, a warp four heads at a time
+      for (int h0 = 0; h0 < kv.n_heads; h0 += P.hks) {
 #pragma unroll 1
-          for (int four = b0 + warp; four < b1; four += NW) {
-            const int hk = four / P.blocks, block = four - hk * P.blocks, in_group = 4 * block + g / 2;
-            const int64_t head = (int64_t)hk * P.group + in_group;
-            const float* const src = a.q + s * a.q_stride + head * D;
-            Q h;
-            h.take([&](int e) { return in_group < P.group && e < D ? src[e] * P.q_scale : 0.f; }, lane);
-            uint32_t* const to_mem = heads_mem + (four - b0) * (C::kHeads / 4) + lane;
-#pragma unroll
-            for (int i = 0; i < Q::kWords; ++i) to_mem[i * 32] = h.word(i);
-            const int mine = 4 * block + q4;  // the head of this lane's logits; p = 0 beyond the last
-            const int64_t at = (int64_t)hk * P.group + mine;
-            to_mem[Q::kWords * 32] = __float_as_uint(mine < P.group ? a.lse[(int64_t)s * a.n_q_heads + at] * 1.4426950408889634f : INFINITY);
-            to_mem[(Q::kWords + 1) * 32] =
-                __float_as_uint(SCORED && a.slopes != nullptr && mine < P.group ? a.slopes[at] * 1.4426950408889634f : 0.f);
-          }
-          __syncthreads();
-          staged_s = s, staged_b = b0;
-        }
-        if (!active) continue;
+        for (int c0 = 0; c0 < P.blocks; c0 += P.cols) {
+          const int h1 = min(h0 + P.hks, kv.n_heads), c1 = min(c0 + P.cols, P.blocks), cols = c1 - c0;
+          if (staged_s != s || staged_h != h0 || staged_c != c0) {
+            __syncthreads();
+            // q as fragments, a warp four heads at a time
 #pragma unroll 1
-        for (int four = b0; four < b1; ++four) {
-          const int hk = four / P.blocks, block = four - hk * P.blocks;
-          if (hk % share != part) continue;
-          if (block == 0) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-            __syncwarp();
-            fetch();
-          }
-          const uint32_t* const from_mem = heads_mem + (four - b0) * (C::kHeads / 4) + lane;
-          Q h;
+            for (int four = warp; four < (h1 - h0) * cols; four += NW) {
+              const int hk = h0 + four / cols, block = c0 + four % cols, in_group = 4 * block + g / 2;
+              const float* const src = a.q + s * a.q_stride + ((int64_t)hk * P.group + in_group) * D;
+              const int mine = 4 * block + q4;  // the head of this lane's logits; p = 0 beyond the last
+              const int64_t at = (int64_t)hk * P.group + mine;
+              const bool exists = mine < P.group;
+              const float lse = exists ? a.lse[(int64_t)s * a.n_q_heads + at] * 1.4426950408889634f : INFINITY;
+              const float slope = SCORED && a.slopes != nullptr && exists ? a.slopes[at] * 1.4426950408889634f : 0.f;
+              Q h;
+              h.take([&](int e) { return in_group < P.group && e < D ? src[e] * P.q_scale : 0.f; }, lane);
+              uint4* const to_mem = heads_mem + four * (C::kFours * 32) + lane;
+              auto word = [&](int i) {
+                return i < Q::kWords ? h.word(i) : i == Q::kWords ? __float_as_uint(lse) : i == Q::kWords + 1 ? __float_as_uint(slope) : 0u;
+              };
 #pragma unroll
-          for (int i = 0; i < Q::kWords; ++i) h.word(i) = from_mem[i * 32];
-          const float lse = __uint_as_float(from_mem[Q::kWords * 32]), slope = __uint_as_float(from_mem[(Q::kWords + 1) * 32]);
-          const uint32_t tile = ring + stage * C::kStage;
-#pragma unroll
-          for (int k = 0; k < T / 16; ++k) {
-            float v[2];
-            h.dot(v, tile, tile + C::kPool, 16 * k, lane);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float x = v[c];
-              if constexpr (SCORED) {
-                if (P.cap_log2 > 0.f) x = P.cap_log2 * tanhf(x);
-                x = fmaf(slope, far[2 * k + c], x);
-              }
-              float p;
-              asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(x - lse));
-              sums[2 * k + c] += use[2 * k + c] ? p : 0.f;
+              for (int i = 0; i < C::kFours; ++i) to_mem[i * 32] = make_uint4(word(4 * i), word(4 * i + 1), word(4 * i + 2), word(4 * i + 3));
             }
+            __syncthreads();
+            staged_s = s, staged_h = h0, staged_c = c0;
           }
-          if (block == P.blocks - 1) stage = stage + 1 == S ? 0 : stage + 1;
+          if (!active) continue;
+#pragma unroll 1
+          for (int hk = h0 + ((part - h0) & (share - 1)); hk < h1; hk += share) {
+            if (c0 == 0) {
+              asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+              __syncwarp();
+              fetch();
+            }
+            const uint32_t tile = ring + stage * C::kStage;
+            const uint4* from_mem = heads_mem + (hk - h0) * cols * (C::kFours * 32) + lane;
+#pragma unroll 1
+            for (int block = c0; block < c1; ++block, from_mem += C::kFours * 32) {
+              Q h;
+              float lse = 0.f, slope = 0.f;
+#pragma unroll
+              for (int i = 0; i < C::kFours; ++i) {
+                const uint4 v = from_mem[i * 32];
+                const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  if (4 * i + j < Q::kWords) h.word(4 * i + j) = word[j];
+                  if (4 * i + j == Q::kWords) lse = __uint_as_float(word[j]);
+                  if (4 * i + j == Q::kWords + 1) slope = __uint_as_float(word[j]);
+                }
+              }
+#pragma unroll
+              for (int k = 0; k < T / 16; ++k) {
+                float v[2];
+                h.dot(v, tile, tile + C::kPool, 16 * k, lane);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  float x = v[c];
+                  if constexpr (SCORED) {
+                    if (P.cap_log2 > 0.f) x = P.cap_log2 * tanhf(x);
+                    x = fmaf(slope, far[2 * k + c], x);
+                  }
+                  float p;
+                  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(x - lse));
+                  sums[2 * k + c] += use[2 * k + c] ? p : 0.f;
+                }
+              }
+            }
+            if (c1 == P.blocks) stage = stage + 1 == S ? 0 : stage + 1;
+          }
         }
       }
       // ---- over the four lanes of a token, then over the warps of a tile
@@ -510,7 +562,6 @@ __global__ void __launch_bounds__(Config<F, W>::kThreads, 1) kv_weigh_kernel(con
         for (int w = 0; w < share; ++w) sum += shared[w * T + lane];
         const uint32_t t = t0 + lane;
         if (t < q.len) {
-          const float had = t >= q.len - fresh ? 0.f : P.w.weights[s * ws + t];
           P.w.weights_out[s * ws + t] = had + (t >= q.begin ? sum : 0.f);
         }
       }
@@ -524,9 +575,11 @@ template <int F, bool SCORED, int W>
 cudaError_t prepare(const Plan& p, int num_sms, Launch* out) {
   using C = Config<F, W>;
   const void* const fn = reinterpret_cast<const void*>(kv_weigh_kernel<F, SCORED, W>);
-  const int64_t fours = (int64_t)p.w.attend.kv.n_heads * p.blocks;
-  const int batch = (int)std::min<int64_t>(fours, C::kBatch);
-  const size_t smem = (size_t)C::kFixed + C::kWarps * C::kRing + (size_t)batch * C::kHeads;
+  // whole K/V heads where their blocks fit
+  Plan plan = p;
+  plan.cols = std::min(p.blocks, C::kBatch);
+  plan.hks = plan.cols < p.blocks ? 1 : std::min(p.w.attend.kv.n_heads, C::kBatch / p.blocks);
+  const size_t smem = (size_t)C::kFixed + C::kWarps * C::kRing + (size_t)plan.hks * plan.cols * C::kHeads;
   static std::atomic<unsigned long long> attr_set{0};  // one bit per device (setting it twice is harmless)
   int dev = 0;
   cudaGetDevice(&dev);
@@ -539,7 +592,7 @@ cudaError_t prepare(const Plan& p, int num_sms, Launch* out) {
   out->grid = dim3((unsigned)num_sms);
   out->block = dim3(C::kThreads);
   out->smem = smem;
-  if (!out->set_args(p, (int)fours, batch)) return cudaErrorMemoryAllocation;
+  if (!out->set_args(plan)) return cudaErrorMemoryAllocation;
   if (kUsePdl) out->allow_early_start();
   return cudaSuccess;
 }
@@ -567,8 +620,14 @@ cudaError_t prepare_kv_weigh(const KvWeighArgs& w, int num_sms, Launch* out) {
   p.q_scale = a.cap > 0.f ? a.scale / a.cap : a.scale * 1.4426950408889634f;
   p.cap_log2 = a.cap * 1.4426950408889634f;
   const int dim = kv.head_dim <= 64 ? 64 : kv.head_dim <= 128 ? 128 : 256, unit = dim == 64 ? 2 : 4;
-  p.whole = kv.head_dim == dim && reinterpret_cast<uintptr_t>(kv.k_scale) % (4 * unit) == 0 && kv.spage % unit == 0 &&
-            kv.stoken % unit == 0 && kv.shead % unit == 0;
+  const int64_t es = kv.format == IL_BF16 ? 2 : 1;
+  const auto ends = [&](int64_t page, int64_t token) { return (kv.n_pages - 1) * page + (kv.page_size - 1) * token <= UINT32_MAX; };
+  p.whole = ends(kv.page * es / 16, kv.token * es / 16);
+  if (kv.format != IL_BF16 && p.whole)
+    p.whole = kv.head_dim == dim && reinterpret_cast<uintptr_t>(kv.k_scale) % (4 * unit) == 0 && kv.spage % unit == 0 &&
+              kv.stoken % unit == 0 && kv.shead % unit == 0 && ends(kv.spage, kv.stoken);
+  p.page = (uint32_t)(kv.page * es / 16), p.token = (uint32_t)(kv.token * es / 16);
+  p.spage = (uint32_t)kv.spage, p.stoken = (uint32_t)kv.stoken;
   return kv.format == IL_BF16 ? weigh::prepare_format<IL_BF16>(p, num_sms, out)
          : kv.format == IL_Q8 ? weigh::prepare_format<IL_Q8>(p, num_sms, out)
                               : weigh::prepare_format<IL_A4>(p, num_sms, out);

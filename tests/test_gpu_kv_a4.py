@@ -286,7 +286,8 @@ def test_refusals(sil):
     for make in (lambda: sil.KVCache(k, k), lambda: sil.KVCache(k, k, s, None), lambda: sil.KVCache(k, k, s.float(), s.float()),
                  lambda: sil.KVCache(k, k, s[..., :1, :], s[..., :1, :]), lambda: sil.KVCache(k, k, s[..., 0], s[..., 0]),
                  lambda: sil.KVCache(k, k, s.transpose(3, 4), s.transpose(3, 4)), lambda: sil.KVCache(k, k, s, s.cpu()),
-                 lambda: sil.kv_cache("q4", 4, 16, 2, 64), lambda: sil.kv_cache("a8", 4, 16, 2, 64)):
+                 lambda: sil.kv_cache("q4", 4, 16, 2, 64), lambda: sil.kv_cache("a8", 4, 16, 2, 64),
+                 lambda: sil.kv_cache("a4", 4, 16, 2, 33), lambda: sil.kv_cache("a4", 4, 16, 2, 48)):
         with pytest.raises(sil.ILError):
             make()
     odd = z(4 * 16 * 2 * 5 + 8, dtype=torch.bfloat16).as_strided((4, 16, 2, 2, 2), (160, 10, 5, 2, 1))

@@ -70,12 +70,12 @@ class Cut:
         assert np.all(got[:, keep:] == -9) and torch.equal(lens.cpu(), torch.tensor(self.lens, dtype=torch.int32))
         want = [t.cpu().numpy() if t.dtype != torch.bfloat16 else t.view(torch.int16).cpu().numpy() for t in before]
         for r, length in enumerate(self.lens):
-            length = min(max(length, 0), width)
+            full, length = max(length, 0), min(max(length, 0), width)
             pos = np.arange(width) if self.positions is None else self.positions[r]
             entries = kl.evict(self.weights[r], pos, length, keep, first, recent)
             m = len(entries)
             assert got[r, :m].tolist() == entries and np.all(got[r, m:keep] == -1)
-            assert int(drop[r]) == m - length
+            assert int(drop[r]) == m - full
             expect = (self.weights[r] if in_place else np.full(width, -3, np.float32)).copy()
             expect[:m] = self.weights[r][entries]
             assert np.array_equal(got_w[r], expect, equal_nan=True)
@@ -160,7 +160,7 @@ def test_lengths_are_cut(sil):
     w[0, 60:] = -1
     sil.kv_evict(c.cache, torch.from_numpy(c.table).cuda(), lens, w, kept, drop)
     cap = c.table.shape[1] * 16
-    assert drop.tolist() == [8 - cap, 0] and kept[1].tolist() == [-1] * 8
+    assert drop.tolist() == [8 - (2**31 - 1), 0] and kept[1].tolist() == [-1] * 8 and 8 <= max(kept[0].tolist()) < cap
 
 
 def test_bad_pages_are_skipped_and_flagged(sil):
