@@ -18,8 +18,8 @@
 // Stream.  Every warp owns a ring of stages, one tile of K and V each, filled with 16-byte
 // cp.async (any strides, any page size: a lane looks up its token's page one tile ahead) and zeros for
 // tokens outside the attended range.  Where pages hold whole groups of 16 tokens their addresses are one base and
-// constants of the lane (A4: any pages, offsets of 32 bits that the lanes hand to one another).  No barrier other than the warp's own sits in the stream.  A head of more than 128
-// elements takes a pair of warps, half of its columns each: they trade their halves of s
+// constants of the lane (A4: any pages, offsets of 32 bits that the lanes hand to one another).  No barrier other than the
+// warp's own sits in the stream.  A head of more than 128 elements takes a pair of warps, half of its columns each: they trade their halves of s
 // through shared memory, with a barrier of the two.
 //
 // Arithmetic.  Query heads are the rows of m16n8k16 MMAs and tokens (then elements of V) the
@@ -985,7 +985,8 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             if (b % 2 == 0) {
-              // {d, m} of the lane's tokens, of blocks b and b + 1; V of tokens 2 q4, 2 q4 + 1 and 8 further of 16, elements 4 g .. 4 g + 3
+              // {d, m} of the lane's tokens, of blocks b and b + 1; V of tokens 2 q4, 2 q4 + 1 and 8 further of 16,
+              // elements 4 g .. 4 g + 3
 #pragma unroll
               for (int c = 0; c < NV; ++c) lds64(dm[c][0], dm[c][1], steps + (8 * c * NB + b) * 4);
 #pragma unroll

@@ -243,12 +243,13 @@ __global__ void __launch_bounds__(kThreads) kv_choose_long_kernel(const KvEvictA
 
 // Up to kMostKeys tokens a CTA: a cluster of 1 to 8 CTAs a sequence, the CTA of rank c with the c-th run of its tokens and their
 // keys in shared memory, read once.  Bound by latency (barriers, and 12 bytes a token from a few SMs): three passes of 11, 11 and 10
-// bits, whose histograms every CTA adds up through distributed shared memory, and one exchange of the numbers of movers and holes.
+// bits, whose histograms a warp of every CTA adds up through distributed shared memory, first sums of 32 bins, then the 32 bins that the
+// digit is among (all 2048 in each CTA took 1 to 1.5 us more a pass), and one exchange of the numbers of movers and holes.
 // Where no more than kFewRows rows of a sequence can move it moves them too, and there is no second launch.
 template <int CTAS, bool MOVE>
 __global__ void __launch_bounds__(kThreads) kv_choose_kernel(const KvEvictArgs a, const Rows R) {
   extern __shared__ uint32_t s_keys[];
-  __shared__ uint32_t s_count[2][2048], s_pick[2];
+  __shared__ uint32_t s_count[2][2048], s_coarse[2][64], s_pick[4];  // bins, and sums of 32 of them
   __shared__ unsigned long long s_warp[kWarps], s_total;
   __shared__ int s_last, s_moves, s_to[MOVE ? kFewRows : 1];
   constexpr int ctas = CTAS;
@@ -324,58 +325,74 @@ __global__ void __launch_bounds__(kThreads) kv_choose_kernel(const KvEvictArgs a
     }
 
     // ---- the smallest key that stays, and how many of that key do
-    uint32_t bar = 0, wanted = (uint32_t)a.keep, same_before = 0, same_here = 0;
+    uint32_t bar = 0, wanted = (uint32_t)a.keep;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 1 ? 21 : 10;
-      const int bins = pass == 2 ? 1024 : 2048;
-      uint32_t* const count = s_count[pass & 1];  // the other is still read by other CTAs
+      const uint32_t mask = pass == 2 ? 1023u : 2047u;
+      uint32_t *const count = s_count[pass & 1], *const coarse = s_coarse[pass & 1];  // the others are still read by other CTAs
       count[tid] = 0;
       count[tid + kThreads] = 0;
       __syncthreads();
-      for (int at = w0; at < w1; at += 32) {
-        const uint32_t key = at + lane < w1 ? s_keys[at + lane - i0] : 0u;
-        const bool in = at + lane < w1 && (pass == 0 || key >> above == bar >> above);
-        if (in) atomicAdd(&count[key >> shift & (bins - 1)], 1u);
+      for (int at = w0 + lane; at < w1; at += 32) {
+        const uint32_t key = s_keys[at - i0];
+        if (pass == 0 || key >> above == bar >> above) atomicAdd(&count[key >> shift & mask], 1u);
+      }
+      __syncthreads();
+      {
+        const uint2 two = *reinterpret_cast<const uint2*>(count + 2 * tid);
+        uint32_t sum = two.x + two.y;
+#pragma unroll
+        for (int by = 1; by < 16; by *= 2) sum += __shfl_xor_sync(~0u, sum, by);
+        if (lane % 16 == 0) coarse[tid / 16] = sum;
       }
       sync_all();
-      // from the largest digit down, two of them a thread
-      uint32_t high = 0, low = 0;
-      const int digit = bins - 2 - 2 * tid;
-      if (digit >= 0) {
-        uint2 v[CTAS];
+      if (warp == 0) {
+        // from the largest digit down: the 32 bins that it is in, two sums a lane, then the bin
+        auto before_of = [&](uint32_t mine) {
+          uint32_t incl = mine;
 #pragma unroll
-        for (int c = 0; c < CTAS; ++c) v[c] = *reinterpret_cast<const uint2*>(of_rank(count, c) + digit);
+          for (int by = 1; by < 32; by *= 2) {
+            const uint32_t o = __shfl_up_sync(~0u, incl, by);
+            if (lane >= by) incl += o;
+          }
+          return incl - mine;
+        };
+        uint2 two[CTAS];
+        uint32_t low = 0, high = 0, v[CTAS], sum = 0;
 #pragma unroll
-        for (int c = 0; c < CTAS; ++c) low += v[c].x, high += v[c].y;
-      }
-      uint32_t incl = high + low;
+        for (int c = 0; c < CTAS; ++c) two[c] = *reinterpret_cast<const uint2*>(of_rank(coarse, c) + 62 - 2 * lane);
 #pragma unroll
-      for (int by = 1; by < 32; by *= 2) {
-        const uint32_t o = __shfl_up_sync(~0u, incl, by);
-        if (lane >= by) incl += o;
-      }
-      unsigned long long all;
-      const uint32_t before = (uint32_t)sum_before(__shfl_sync(~0u, incl, 31), all) + incl - high - low;
-      if (before < wanted && wanted <= before + high + low) {
+        for (int c = 0; c < CTAS; ++c) low += two[c].x, high += two[c].y;
+        uint32_t before = before_of(low + high);
+        const int in = __ffs(__ballot_sync(~0u, before < wanted && wanted <= before + low + high)) - 1;
         const bool upper = wanted <= before + high;
-        s_pick[0] = digit + upper;
-        s_pick[1] = wanted - before - (upper ? 0 : high);
+        const int group = __shfl_sync(~0u, 62 - 2 * lane + upper, in);
+        const uint32_t rest = wanted - __shfl_sync(~0u, before + (upper ? 0u : high), in);
+        const int digit = 32 * group + 31 - lane;
+#pragma unroll
+        for (int c = 0; c < CTAS; ++c) v[c] = of_rank(count, c)[digit];
+#pragma unroll
+        for (int c = 0; c < CTAS; ++c) sum += v[c];
+        before = before_of(sum);
+        if (before < rest && rest <= before + sum) {
+          s_pick[0] = digit;
+          s_pick[1] = rest - before;
+          uint32_t lower = 0, here = 0;
+#pragma unroll
+          for (int c = 0; c < CTAS; ++c) {
+            if (c < rank) lower += v[c];
+            if (c == rank) here = v[c];
+          }
+          s_pick[2] = lower;
+          s_pick[3] = here;
+        }
       }
       __syncthreads();
       bar |= s_pick[0] << shift;
       wanted = s_pick[1];
-      if (pass == 2) {
-        uint32_t v[CTAS];
-#pragma unroll
-        for (int c = 0; c < CTAS; ++c) v[c] = of_rank(count, c)[s_pick[0]];
-#pragma unroll
-        for (int c = 0; c < CTAS; ++c) {
-          if (c < rank) same_before += v[c];
-          if (c == rank) same_here = v[c];
-        }
-      }
     }
+    const uint32_t same_before = s_pick[2], same_here = s_pick[3];  // tokens of that key in lower ranks, and here
 
     // ---- the index of the last token of that key that stays
     const uint32_t quota = wanted > same_before ? min(wanted - same_before, same_here) : 0u;
@@ -438,26 +455,43 @@ __global__ void __launch_bounds__(kThreads) kv_choose_kernel(const KvEvictArgs a
     sync_all();
 
     // ---- the entries: all of them read, then written
-    for (int at = w0; at < min(w1, mid); at += 32) {
-      const int i = at + lane;
-      const bool hit = i < w1 && i < mid && !stays(i);
-      const uint32_t hits = __ballot_sync(~0u, hit);
-      const uint32_t from = hit ? (uint32_t)list[hole + __popc(hits & ((1u << lane) - 1))] : (uint32_t)i;
-      if (i < w1 && i < mid) s_keys[i - i0] = from;
-      hole += __popc(hits);
+    const int end = min(w1, mid);
+    for (int at = w0; at < end; at += 128) {
+      uint32_t from[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = at + 32 * k + lane;
+        const bool hit = i < end && !stays(i);
+        const uint32_t hits = __ballot_sync(~0u, hit);
+        from[k] = hit ? (uint32_t)list[hole + __popc(hits & ((1u << lane) - 1))] : (uint32_t)i;
+        hole += __popc(hits);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (at + 32 * k + lane < end) s_keys[at + 32 * k + lane - i0] = from[k];
     }
     sync_all();
 #pragma unroll 1
-    for (int at = i0 + tid; at < mid; at += 2 * kThreads) {
+    for (int at = i0 + tid; at < mid; at += 4 * kThreads) {
+      float w[4];
+      int from[4], p[4];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < 4; ++k) {
+        const int i = at + k * kThreads;
+        from[k] = i < mid ? (int)s_keys[i - i0] : i;
+        const bool moves = from[k] != i;
+        w[k] = i < mid && (moves || weights_out != weights) ? weights[from[k]] : 0.f;
+        p[k] = i < mid && positions != nullptr && (moves || positions_out != positions) ? positions[from[k]] : 0;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
         const int i = at + k * kThreads;
         if (i >= mid) continue;
-        const int from = (int)s_keys[i - i0];
-        kept[i] = from;
-        if (from != i || weights_out != weights) weights_out[i] = weights[from];
-        if (positions != nullptr && (from != i || positions_out != positions)) positions_out[i] = positions[from];
-        if (MOVE && from != i) s_to[atomicAdd(&s_moves, 1)] = i;  // in any order: the rows lie apart
+        const bool moves = from[k] != i;
+        kept[i] = from[k];
+        if (moves || weights_out != weights) weights_out[i] = w[k];
+        if (positions != nullptr && (moves || positions_out != positions)) positions_out[i] = p[k];
+        if (MOVE && moves) s_to[atomicAdd(&s_moves, 1)] = i;  // in any order: the rows lie apart
       }
     }
     __syncthreads();

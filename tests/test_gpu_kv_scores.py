@@ -86,9 +86,18 @@ def test_long_sequences_split_and_join(sil, fmt):
 def test_nothing_set_is_the_plain_call(sil, fmt):
     c = kl.Case(sil, fmt, 8, 2, 128, 16, [70, 3, 0, 128], seed=2)
     plain = c.run()
-    c.starts = [0] * 4
+    c.starts = [0] * 4  # the scored kernel
     zeros = c.run()
     assert bool((plain[0] == zeros[0]).all()) and bool((plain[1] == zeros[1]).all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("slope", [0.05, 0.5, 5.0])
+def test_long_sequences_behind_a_steep_bias(sil, fmt, slope):
+    """Most tiles give nothing beside the newest, but each part of a row is first taken by itself; of positions in any order, any tile may count."""
+    for positions in (False, True):
+        _check(sil, fmt, 8, 2, 128, 64, [9001, 40, 3000], slopes=np.full(8, slope, np.float32), positions=positions, seed=7)
+        _check(sil, fmt, 9, 1, 256, 16, [2000], slopes=np.linspace(0, slope, 9, dtype=np.float32), positions=positions, seed=8)
 
 
 def test_a_length_is_cut_to_the_positions(sil):
