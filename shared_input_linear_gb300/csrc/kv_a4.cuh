@@ -1,9 +1,10 @@
-// kv_a4.cuh -- products with 4-bit rows of the cache (IL_A4: value d u + m, u of 0 .. 15) on m16n8k16 MMAs.
+// kv_a4.cuh -- products with 4-bit rows of the cache (IL_A4: value d u + m, u of 0 .. 15) on m16n8k16 MMAs, for il_kv_attend
+// (kv_attend.cuh) and il_kv_weigh.
 //
 // Tokens (for q K^T) or elements of V (for p V) are the rows of an MMA, and each query head has two columns: the hi and the lo
 // part of its fp32 operand, x = hi + lo 2^-11 in fp16.  The parts have accumulators of their own, so that lo is kept 2^11
-// times as large: x keeps 22 bits down to 2^-27 of the largest and is cut at 2^-49 of it.  With four heads a K/V head nothing of an
-// MMA is idle, a lane's accumulators are of one head (that of column pair q4 = lane % 4), and a softmax value is in one lane.
+// times as large: x keeps 22 bits down to 2^-27 of the largest and is cut at 2^-49 of it.  With four heads a K/V head nothing of
+// an MMA is idle, a lane's accumulators are of one head (that of column pair q4 = lane % 4), and a softmax value is in one lane.
 //
 // Decoding K costs 5 instructions for 8 elements: nibbles at bits 0-3 and 4-7 of a 16-bit half are fp16 subnormals as they
 // stand, u 2^-24 and 16 u 2^-24, exactly; one shift brings the other two there.  The factor 16 is taken from q.  d multiplies a

@@ -1,5 +1,5 @@
-// kv_attend.cuh -- attention of one new token per sequence over the paged cache (il_kv_attend):
-// the kernel, instantiated per cache format in kv_attend_bf16.cu and kv_attend_q8.cu.
+// kv_attend.cuh -- attention of one new token per sequence over the paged cache (il_kv_attend, il_kv_attend_scored):
+// the kernel, instantiated per cache format, plain and scored, in the six kv_attend_*.cu.
 //
 // For every sequence and K/V head, with G query heads reading that head:
 //   s = scale q K^T, p = exp(s - max), out = p V / sum p        ([G][len] by [len][D])
@@ -31,13 +31,18 @@
 // split costs one more MMA at bf16 and none at int8; with 9 to 16 heads (R = 2) every part is an MMA
 // of its own.  p V is computed transposed: the quad layout of s is that of a B operand, so p goes in as it is.
 // Each tile's product starts from zero accumulators and joins the running sum in fp32
-// FMAs (with the factor of the running maximum), which round to nearest.
+// FMAs (with the factor of the running maximum), which round to nearest.  A4 has the operands the other way round, query heads in
+// the columns (kv_a4.cuh), because its tiles are bound by instructions: 845 for 32 tokens of 128 columns, the loop and copies included.
+//
+// Scored (il_kv_attend_scored): logits are capped and biased between the two products, and a row may begin at a later token.
+// The plain kernels have none of it.
 //
 // Measured (GB300, 32 query heads on 8 K/V heads of 128, device time): bf16, 128 sequences of 4096 tokens 315 us, 6.8 TB/s
 // (the rate of a plain copy); 32 of 0 to 8192 86 us, 6.0 TB/s; one of 512 8.1 us.  Q8, 64 of 1 to 8192 106 us, 5.6 TB/s,
 // one of 131071 59 us, 5.2 TB/s.  What bounds it: HBM at bf16 (64 sequences of 8192: 317 us, 263 us with pages that stay in
-// L2); at Q8 no unit (207 us either way; issue slots 50 % used, ALU 44 %, tensor pipe 27 %, DRAM 65 %) but the chain of a tile
-// in a warp -- q K^T, maximum, exp2, split, p V -- at two warps a scheduler, about 520 instructions per 16 tokens; of
+// L2); A4, 64 of 1 to 8192 (another draw, 316,517 tokens) 94 us, 4.3 TB/s, one of 131071 45 us, one of 512 9.2 us: instructions (issue slots
+// 63 % used, ALU 52 %, tensor pipe 20 %, DRAM 54 %); at Q8 no unit (207 us either way; issue slots 50 % used, ALU 44 %, tensor pipe
+// 27 %, DRAM 65 %) but the chain of a tile in a warp -- q K^T, maximum, exp2, split, p V -- at two warps a scheduler, about 520 instructions per 16 tokens; of
 // a short call the latencies before the first tile and in the joins.
 #pragma once
 

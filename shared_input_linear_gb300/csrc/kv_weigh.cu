@@ -3,7 +3,12 @@
 //
 //   out[t] = (new ? 0 : w[t]) + sum_h exp(s_ht - lse_h)
 // K is read once and V not at all; the sum over the heads of a token is made where its K is, so that nothing but 8 bytes a
-// token goes beside K.  Bound by HBM at bf16.
+// token goes beside K.
+//
+// Measured (GB300, 32 query heads on 8 K/V heads of 128, device time): 64 sequences of 1 to 8192 tokens bf16 115 us, 5.7 TB/s, Q8 76 us,
+// 4.9 TB/s, A4 56 us, 3.7 TB/s; one of 131071 A4 25 us; one of 2048 bf16 9.0 us.  What bounds it: HBM at bf16; at A4 instructions
+// (410 for 32 tokens of a K/V head, issue slots 55 % used, ALU 48 %) and what the CTAs lose at the ends of pieces; of a short call the
+// latencies before the first tile.
 //
 // Work.  Tiles of 32 tokens (16 of bf16 heads above 128) of all sequences form one list, of which every CTA takes an equal run.  A run's
 // piece of one sequence is worked off by the CTA's warps, a tile each at a time, over all K/V heads; of the last tiles of a piece,
@@ -19,6 +24,7 @@
 // where the sums start), or three bf16 parts in two MMAs against bf16.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "il_internal.cuh"
 #include "il_ptx.cuh"
@@ -46,8 +52,8 @@ __device__ __forceinline__ float quad_max(float x) {
   return fmaxf(x, __shfl_xor_sync(~0u, x, 2));
 }
 
-// Four query heads against 16 tokens of a cache, per format.  load(e) gives element e of head g / 2 of the four, times the scale of the
-// logits; dot gives s[h] of head q4 with token 8 h + g.  kWords: registers of a lane, kept in shared memory between uses.
+// Four query heads against 16 tokens of a cache, per format.  load(e, x) gives elements e .. of head g / 2 of the four, times the scale of the
+// logits, four or two of them; dot gives s[h] of head q4 with token 8 h + g.  kWords: registers of a lane, kept in shared memory between uses.
 template <int F, int NB>
 struct Heads;
 
@@ -61,9 +67,11 @@ struct Heads<IL_A4, NB> {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x[b][j] = load(32 * b + 8 * (lane & 3) + j);
-        top = fmaxf(top, fabsf(x[b][j]));
+      for (int j = 0; j < 8; j += 4) {
+        float y[4];
+        load(32 * b + 8 * (lane & 3) + j, y);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[b][j + k] = y[k], top = fmaxf(top, fabsf(y[k]));
       }
     q.take(0, x, quad_max(top), lane);
   }
@@ -92,12 +100,11 @@ struct Heads<IL_Q8, NB> {
     const bool lo_part = (lane >> 2) & 1;
     float x[2 * NB][4], top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2 * NB; ++i)
+    for (int i = 0; i < 2 * NB; ++i) {
+      load(16 * i + 4 * q4, x[i]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[i][j] = load(16 * i + 4 * q4 + j);
-        top = fmaxf(top, fabsf(x[i][j]));
-      }
+      for (int j = 0; j < 4; ++j) top = fmaxf(top, fabsf(x[i][j]));
+    }
     const int e = max((int)(__float_as_uint(quad_max(top)) >> 23), 14);
     const float up = __int_as_float((267 - e) << 23);
 #pragma unroll
@@ -167,11 +174,14 @@ struct Heads<IL_BF16, NB> {
       const __nv_bfloat162 p = __floats2bfloat162_rn(u, v);
       return *reinterpret_cast<const uint32_t*>(&p);
     };
+    float all[2 * NB][2][2];
+#pragma unroll
+    for (int i = 0; i < 4 * NB; ++i) load(16 * (i / 2) + 2 * q4 + 8 * (i % 2), all[i / 2][i % 2]);
 #pragma unroll
     for (int i = 0; i < 2 * NB; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float x = load(16 * i + 2 * q4 + 8 * j), y = load(16 * i + 2 * q4 + 8 * j + 1);
+        float x = all[i][j][0], y = all[i][j][1];
         const uint32_t hi = pack(x, y);
         x -= bf16_lo(hi), y -= bf16_hi(hi);
         const uint32_t mid = pack(x, y);
@@ -486,7 +496,18 @@ __global__ void __launch_bounds__(Config<F, W>::kThreads, 1) kv_weigh_kernel(con
               const float lse = exists ? a.lse[(int64_t)s * a.n_q_heads + at] * 1.4426950408889634f : INFINITY;
               const float slope = SCORED && a.slopes != nullptr && exists ? a.slopes[at] * 1.4426950408889634f : 0.f;
               Q h;
-              h.take([&](int e) { return in_group < P.group && e < D ? src[e] * P.q_scale : 0.f; }, lane);
+              // (rows of q are 16-byte aligned, and D a multiple of 8)
+              h.take(
+                  [&](int e, auto& x) {
+                    constexpr int N = sizeof(x) / 4;
+                    using Vec = typename std::conditional<N == 4, float4, float2>::type;
+                    Vec v = {};
+                    if (in_group < P.group && e < D) v = *reinterpret_cast<const Vec*>(src + e);
+                    const float* const f = reinterpret_cast<const float*>(&v);
+#pragma unroll
+                    for (int k = 0; k < N; ++k) x[k] = f[k] * P.q_scale;
+                  },
+                  lane);
               uint4* const to_mem = heads_mem + four * (C::kFours * 32) + lane;
               auto word = [&](int i) {
                 return i < Q::kWords ? h.word(i) : i == Q::kWords ? __float_as_uint(lse) : i == Q::kWords + 1 ? __float_as_uint(slope) : 0u;
@@ -600,9 +621,13 @@ cudaError_t prepare(const Plan& p, int num_sms, Launch* out) {
 template <int F>
 cudaError_t prepare_format(const Plan& p, int num_sms, Launch* out) {
   const int dim = p.w.attend.kv.head_dim;
-  if (p.w.attend.scored)
-    return dim <= 64 ? prepare<F, true, 64>(p, num_sms, out) : dim <= 128 ? prepare<F, true, 128>(p, num_sms, out) : prepare<F, true, 256>(p, num_sms, out);
-  return dim <= 64 ? prepare<F, false, 64>(p, num_sms, out) : dim <= 128 ? prepare<F, false, 128>(p, num_sms, out) : prepare<F, false, 256>(p, num_sms, out);
+  const auto of = [&](auto scored) {
+    constexpr bool SCORED = decltype(scored)::value;
+    return dim <= 64    ? prepare<F, SCORED, 64>(p, num_sms, out)
+           : dim <= 128 ? prepare<F, SCORED, 128>(p, num_sms, out)
+                        : prepare<F, SCORED, 256>(p, num_sms, out);
+  };
+  return p.w.attend.scored ? of(std::true_type{}) : of(std::false_type{});
 }
 
 }  // namespace weigh
