@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThreads) kv_choose_kernel(const KvEvictArgs a
   extern __shared__ uint32_t s_keys[];
   __shared__ uint32_t s_count[2][2048], s_coarse[2][64], s_pick[4];  // bins, and sums of 32 of them
   __shared__ unsigned long long s_warp[kWarps], s_total;
-  __shared__ int s_last, s_moves, s_to[MOVE ? kFewRows : 1];
+  __shared__ int s_whole, s_last, s_moves, s_to[MOVE ? kFewRows : 1];
   constexpr int ctas = CTAS;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = CTAS == 1 ? 0 : (int)cluster.block_rank();
@@ -389,13 +389,17 @@ __global__ void __launch_bounds__(kThreads) kv_choose_kernel(const KvEvictArgs a
             if (c < rank) lower += v[c];
             if (c == rank) here = v[c];
           }
-          s_pick[2] = lower;
-          s_pick[3] = here;
+          // where all of the bin stay, every key from its least on does, and the lower bits need not be looked at
+          const bool whole = rest - before == sum;
+          s_pick[2] = whole ? 0u : lower;
+          s_pick[3] = whole ? 0u : here;
+          s_whole = whole;
         }
       }
       __syncthreads();
       bar |= s_pick[0] << shift;
       wanted = s_pick[1];
+      if (s_whole) break;
     }
     const uint32_t same_before = s_pick[2], same_here = s_pick[3];  // tokens of that key in lower ranks, and here
 
