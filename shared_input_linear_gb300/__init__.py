@@ -235,12 +235,21 @@ def weight_bytes(w: Weight) -> int:
     return int(load().il_weight_bytes(w.handle))
 
 
+_raw = None  # (raw current stream of a device, current device), once CUDA is up
+
+
 def _stream_ptr(stream) -> int:
+    global _raw
     if stream is None:
-        import torch
+        if _raw is None:
+            import torch
+            raw, device = (getattr(torch._C, name, None) for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+            if raw is None or device is None:
+                return torch.cuda.current_stream().cuda_stream
+            torch.cuda.current_device()
+            _raw = raw, device
         # the handle of torch.cuda.current_stream() without the object (3 us on the host)
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        return torch.cuda.current_stream().cuda_stream if raw is None else raw(torch.cuda.current_device())
+        return _raw[0](_raw[1]())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -350,6 +359,17 @@ def dequantize_weight(w: Weight, out, stream=None) -> None:
 # ---------------------------------------------------------------------------
 # Paged K/V cache
 # ---------------------------------------------------------------------------
+_dtypes = None
+
+
+def _types():
+    """float32, int32, int64 (an import statement a call takes 0.3 us)."""
+    global _dtypes
+    import torch
+    _dtypes = torch.float32, torch.int32, torch.int64
+    return _dtypes
+
+
 def _steps(t):
     """Strides of ``t``; 0 for a dimension of one entry, whose stride means nothing."""
     return [st if n > 1 else 0 for n, st in zip(t.shape, t.stride())]
@@ -464,8 +484,7 @@ def kv_extend(lens, add, table, ring, cursor, page_size: int, slots, lens_out=No
     ``positions`` int32 ``[max_slots]``; ``first`` int32 ``[n_seq + 1]``; ``info`` int64 ``[4]``.
     ``lens_out`` and ``cursor_out`` default to ``lens`` and ``cursor`` themselves.
     """
-    import torch
-    i32, i64 = torch.int32, torch.int64
+    _, i32, i64 = _dtypes or _types()
     n, most = lens.numel(), slots.numel()
     tp, ts, tw = _table(table, n, i32)
     size = ring.numel()
@@ -483,11 +502,11 @@ def kv_extend(lens, add, table, ring, cursor, page_size: int, slots, lens_out=No
 def kv_append(cache: KVCache, k, v, slots, stream=None) -> None:
     """``il_kv_append``: fp32 rows ``k``, ``v`` ``[n][n_heads][head_dim]`` into the cache's ``slots``
     (int32 ``[n]``; a negative one is skipped).  The rows may be columns of a wider tensor."""
-    import torch
-    n, heads, dim, f32 = slots.numel(), cache.n_heads, cache.head_dim, torch.float32
+    f32, i32, _ = _dtypes or _types()
+    n, heads, dim = slots.numel(), cache.n_heads, cache.head_dim
     kp, ks = _rows(k, n, heads, dim, f32, "k")
     vp, vs = _rows(v, n, heads, dim, f32, "v")
-    rc = (_lib or load()).il_kv_append(cache._ref, kp, ks, vp, vs, _ptr(slots, torch.int32, n, "slots"), n,
+    rc = (_lib or load()).il_kv_append(cache._ref, kp, ks, vp, vs, _ptr(slots, i32, n, "slots"), n,
                                        _stream_ptr(stream))
     if rc:
         _check(rc)
@@ -495,11 +514,11 @@ def kv_append(cache: KVCache, k, v, slots, stream=None) -> None:
 
 def kv_read(cache: KVCache, slots, k, v, stream=None) -> None:
     """``il_kv_read``: the cached values of ``slots`` as fp32 into ``k`` and ``v`` (as for :func:`kv_append`)."""
-    import torch
-    n, heads, dim, f32 = slots.numel(), cache.n_heads, cache.head_dim, torch.float32
+    f32, i32, _ = _dtypes or _types()
+    n, heads, dim = slots.numel(), cache.n_heads, cache.head_dim
     kp, ks = _rows(k, n, heads, dim, f32, "k")
     vp, vs = _rows(v, n, heads, dim, f32, "v")
-    rc = (_lib or load()).il_kv_read(cache._ref, _ptr(slots, torch.int32, n, "slots"), n, kp, ks, vp, vs,
+    rc = (_lib or load()).il_kv_read(cache._ref, _ptr(slots, i32, n, "slots"), n, kp, ks, vp, vs,
                                      _stream_ptr(stream))
     if rc:
         _check(rc)
@@ -509,10 +528,10 @@ def _score(n: int, heads: int, cap: float, slopes, starts, positions):
     """An ``il_kv_score``, or None where nothing of it is given."""
     if not cap and slopes is None and starts is None and positions is None:
         return None
-    import torch
-    c = _Score(cap, _ptr(slopes, torch.float32, heads, "slopes"), _ptr(starts, torch.int32, n, "starts"), 0, 0, 0)
+    f32, i32, _ = _dtypes or _types()
+    c = _Score(cap, _ptr(slopes, f32, heads, "slopes"), _ptr(starts, i32, n, "starts"), 0, 0, 0)
     if positions is not None:
-        c.positions, c.positions_stride, c.positions_width = _table(positions, n, torch.int32, "positions")
+        c.positions, c.positions_stride, c.positions_width = _table(positions, n, i32, "positions")
     return c
 
 
@@ -530,11 +549,10 @@ def kv_attend(cache: KVCache, q, table, lens, out, lse=None, scale=None, window:
 
     A captured call uses the workspace of the stream it was captured on: graphs of one capture stream, and calls
     on that stream, must not run side by side."""
-    import torch
+    f32, i32, _ = _dtypes or _types()
     if q.dim() != 3:
         raise ILError(-1, "q must be [n_seq][n_q_heads][head_dim]")
-    n, heads, _ = q.shape
-    dim, f32, i32 = cache.head_dim, torch.float32, torch.int32
+    (n, heads, _), dim = q.shape, cache.head_dim
     qp, qs = _rows(q, n, heads, dim, f32, "q")
     op, os_ = _rows(out, n, heads, dim, f32, "out")
     tp, ts, tw = _table(table, n, i32)
@@ -557,6 +575,8 @@ def _in_out(t, out, n: int, dtype, what: str):
     tp, ts, tw = _table(t, n, dtype, what)
     if out is None or out is t:
         return tp, tp, ts, tw
+    if out.dtype is dtype and out.is_cuda and out.shape == t.shape and out.stride() == t.stride():
+        return tp, out.data_ptr(), ts, tw
     op, os_, ow = _table(out, n, dtype, what + "_out")
     if ow != tw or (n > 1 and os_ != ts):
         raise ILError(-2, f"{what}_out must have the shape and strides of {what}")
@@ -570,11 +590,10 @@ def kv_weigh(cache: KVCache, q, table, lens, lse, weights, weights_out=None, add
 
     ``lse`` is what :func:`kv_attend` gave for the same arguments; the last ``add`` (int32 ``[n_seq]``) tokens are
     new and start from 0."""
-    import torch
+    f32, i32, _ = _dtypes or _types()
     if q.dim() != 3:
         raise ILError(-1, "q must be [n_seq][n_q_heads][head_dim]")
-    n, heads, _ = q.shape
-    dim, f32, i32 = cache.head_dim, torch.float32, torch.int32
+    (n, heads, _), dim = q.shape, cache.head_dim
     qp, qs = _rows(q, n, heads, dim, f32, "q")
     tp, ts, tw = _table(table, n, i32)
     if lse is None:
@@ -596,14 +615,13 @@ def kv_evict(cache: KVCache, table, lens, weights, kept, drop, first: int = 0, r
 
     ``weights`` fp32 and ``positions`` int32 (or None: positions are indices) ``[n_seq][width]`` are updated, in place or
     into ``weights_out`` and ``positions_out``."""
-    import torch
-    i32 = torch.int32
+    f32, i32, _ = _dtypes or _types()
     n = lens.numel()
     tp, ts, tw = _table(table, n, i32)
     kp, ks, keep = _table(kept, n, i32, "kept")
     places = (0, 0, 0, 0) if positions is None and positions_out is None else _in_out(positions, positions_out, n, i32, "positions")
     rc = (_lib or load()).il_kv_evict(cache._ref, tp, ts, tw, _ptr(lens, i32, n, "lens"), n, keep, first, recent,
-                                      *_in_out(weights, weights_out, n, torch.float32, "weights"), *places, kp, ks,
+                                      *_in_out(weights, weights_out, n, f32, "weights"), *places, kp, ks,
                                       _ptr(drop, i32, n, "drop"), _stream_ptr(stream))
     if rc:
         _check(rc)

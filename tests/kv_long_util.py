@@ -86,10 +86,11 @@ def logits(q, keys, kmag, scale, cap=0.0, slopes=None, far=None):
     return s, tol
 
 
-def attend(q, keys, values_, kmag, vmag, scale, **score):
+def attend(q, keys, values_, kmag, vmag, scale, floor=0.0, **score):
     """One sequence's seen tokens: q [H][D], keys, values [T][Hk][D] -> out, lse and bounds of their error (see
     kv_util.attend): a weight is off by a factor e^(2 tol), the sum of the weights by the mean of those; the exponential, the
-    rounding of p and the division add 16 u, the sums over the tokens (T / 16 + 64) u."""
+    rounding of p and the division add 16 u, the sums over the tokens (T / 16 + 64) u.  floor: what every weight may be off by
+    beside that, of the largest."""
     H, D = q.shape
     T = keys.shape[0]
     out, lse = np.zeros((H, D)), np.full(H, -np.inf)
@@ -107,7 +108,7 @@ def attend(q, keys, values_, kmag, vmag, scale, **score):
         out[h] = p @ values_[:, h // G]
         lse[h] = m + math.log(e.sum())
         mag = p @ vmag[:, h // G]
-        out_tol[h] += off @ vmag[:, h // G] + (off.sum() + 16 * U + steps) * mag
+        out_tol[h] += off @ vmag[:, h // G] + (off.sum() + 16 * U + steps) * mag + floor * p.max() * vmag[:, h // G].sum(0)
         lse_tol[h] = off.sum() + 16 * U + steps + 4 * U * abs(lse[h])
     return out, lse, out_tol, lse_tol
 
@@ -227,7 +228,10 @@ class Case:
         scale = self.dim ** -0.5 if scale is None else scale
         for r in range(len(self.lens)) if rows is None else rows:
             k, v, km, vm = self.rows[r]
-            o, l, ot, lt = attend(self.q[r], k, v, km, vm, scale, **self.plain_score(r))
+            # of Q8 the header states that p d is kept to 2^-26 d where 22 bits of it are less, p relative to the largest: a token's
+            # part of out is off by 2^-26 d |q| = 2^-26 |v| of the largest weight then.  A bias makes such weights common, and a
+            # V of exactly 0 in the largest one's place makes them count.
+            o, l, ot, lt = attend(self.q[r], k, v, km, vm, scale, floor=2.0**-26 if self.fmt == "q8" else 0.0, **self.plain_score(r))
             assert np.all(np.isfinite(out[r])), (r, self.lens[r])
             worst = float(np.max(np.abs(out[r] - o) / ot))
             assert worst <= 1, f"sequence {r} of length {self.lens[r]}: out is {worst:.3g} x its bound"
