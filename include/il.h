@@ -400,7 +400,7 @@ int il_kv_read(const il_kv* kv, const int32_t* slots, int64_t n, float* k, int64
  * or 32 tokens; p below is relative to the tile's largest, or to 2^-24 of the sequence's largest so
  * far where that is more.  p d keeps 22 bits, or 2^-26 d where that is coarser.  In a tile with p below
  * 2^-26 or d below 2^-12 of the sequence's largest so far, the second bound is 2^-12 of p times the
- * tile's largest d of the same 32 columns instead, and p below 2^-104 counts as 0.  Over an A4 cache an element of q
+ * tile's largest d of the same 32 columns instead, and p below 2^-104 counts as 0.  Over an A4 cache, and with il_kv_attend_scored over a Q8 one, an element of q
  * keeps 22 bits, or 2^-49 of its head's largest where that is coarser, and p d keeps 22 bits, or 2^-49 of the sequence's
  * largest so far; in a tile with p below 2^-26 or d below 2^-12 of those, 22 bits down to 2^-104 of it, where it counts as 0.
  * Workspace: il_kv_extend and il_kv_attend share one of about 5 MB per (device, stream), owned by the library,

@@ -1,5 +1,5 @@
 // kv_a4.cuh -- products with 4-bit rows of the cache (IL_A4: value d u + m, u of 0 .. 15) on m16n8k16 MMAs, for il_kv_attend
-// (kv_attend.cuh) and il_kv_weigh.
+// (kv_attend.cuh) and il_kv_weigh; with 8-bit rows for il_kv_attend_scored and il_kv_weigh.
 //
 // Tokens (for q K^T) or elements of V (for p V) are the rows of an MMA, and each query head has two columns: the hi and the lo
 // part of its fp32 operand, x = hi + lo 2^-11 in fp16.  The parts have accumulators of their own, so that lo is kept 2^11
@@ -204,6 +204,81 @@ struct Query {
 #pragma unroll
           for (int t = 0; t < 2; ++t) s[r][t] = fmaf(fmaf(c[2 * t + 1], kLoUnit, c[2 * t]), step_of(d[t][b]), s[r][t]);
         }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) s[r][t] = s[r][t] * back[r][0] * back[r][1];
+  }
+};
+
+// V's 8-bit elements 2 g and 2 g + 1 of a token pair (its bytes 0, 1 and 2, 3) as fp16 pairs over the tokens, exactly q.
+__device__ __forceinline__ void bytes_of_pairs(uint32_t w, uint32_t& even, uint32_t& odd) {
+  const uint32_t u = w ^ 0x80808080u;  // q + 128; the bits 64uu are 1024 + u
+  const __half2 low = __floats2half2_rn(-1152.f, -1152.f);
+  const uint32_t a = __byte_perm(u, 0x64646464u, 0x4240), b = __byte_perm(u, 0x64646464u, 0x4341);
+  const __half2 x = __hadd2(*reinterpret_cast<const __half2*>(&a), low), y = __hadd2(*reinterpret_cast<const __half2*>(&b), low);
+  even = *reinterpret_cast<const uint32_t*>(&x);
+  odd = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+// The same for 8-bit rows (IL_Q8: value d q), whose bytes u = q + 128 are fp16 subnormals u 2^-24 as they stand; the products with
+// the 128 are taken off by where the sums start.
+template <int NB, int R>
+struct Query8 {
+  uint32_t f[R][4 * NB];  // of head 4 r + g / 2, its hi or lo part: of 16-element chunk i elements 4 q4, 4 q4 + 1 in [2 i], the next two
+  float start[R][NB];     // of head 4 r + q4: -128 times the sum over a block, in the products' unit
+  float back[R][2];
+
+  // Elements x[b][0 .. 3] = 4 q4 .. of the first chunk of block b, x[b][4 .. 7] of the second.
+  __device__ __forceinline__ void take(int r, const float (&x)[NB][8], float top, int lane) {
+    const int q4 = lane & 3, head_lane = q4 * 8;
+    const bool lo_part = (lane >> 2) & 1;
+    const int e = max((int)(__float_as_uint(top) >> 23), 14);
+    const float up = __int_as_float((267 - e) << 23);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      float total = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float y = x[b][2 * j] * up, z = x[b][2 * j + 1] * up;
+        uint32_t u, v;
+        split2(make_float2(y, z), u, v);
+        f[r][4 * b + j] = lo_part ? __byte_perm(u, v, 0x7632) : __byte_perm(u, v, 0x5410);
+        total += y + z;
+      }
+      total += __shfl_xor_sync(~0u, total, 1);
+      total += __shfl_xor_sync(~0u, total, 2);
+      start[r][b] = __shfl_sync(~0u, total, head_lane) * -7.62939453125e-06f;  // -128 2^-24
+    }
+    const int unit = __shfl_sync(~0u, e, head_lane) - 116, half = unit >> 1;  // 2^unit = 2^24 / up
+    back[r][0] = __int_as_float((half + 127) << 23);
+    back[r][1] = __int_as_float((unit - half + 127) << 23);
+  }
+
+  __device__ __forceinline__ void dot(float (&s)[R][2], uint32_t tile, uint32_t steps, const uint32_t (&chunks)[NB], int lane) const {
+    const int g = lane >> 2;
+    uint32_t d[2][NB];
+    load_steps<NB>(d[0], steps + g * (4 * NB));
+    load_steps<NB>(d[1], steps + (8 + g) * (4 * NB));
+#pragma unroll
+    for (int r = 0; r < R; ++r) s[r][0] = s[r][1] = 0.f;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      uint32_t w[4];  // tokens g and g + 8 of chunk 2 b, then of 2 b + 1
+      ldmatrix4(w, tile + chunks[b]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] ^= 0x80808080u;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float c[4] = {start[r][b], 0.f, start[r][b], 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          mma(c, __byte_perm(w[2 * h], 0u, 0x4140), __byte_perm(w[2 * h + 1], 0u, 0x4140), __byte_perm(w[2 * h], 0u, 0x4342),
+              __byte_perm(w[2 * h + 1], 0u, 0x4342), f[r][4 * b + 2 * h], f[r][4 * b + 2 * h + 1]);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) s[r][t] = fmaf(fmaf(c[2 * t + 1], kLoUnit, c[2 * t]), __uint_as_float(d[t][b]), s[r][t]);
       }
     }
 #pragma unroll

@@ -79,25 +79,26 @@ namespace attend {
 constexpr int kGroup = 16;          // tokens of a product's step; pages of whole groups are copied the simple way
 constexpr int kSmemLimit = 232448;  // 227 KB
 constexpr int kMaxCtas = 256;       // of a grid, one an SM
+constexpr int kQ8Columns = 16 + IL_Q8;  // IL_Q8 with query heads in the MMAs' columns, as A4 has them
 
-// F: format of the cache.  W columns of a head in a warp, H warps a head (H * W >= head_dim), R blocks of 8 (A4: of 4) query
-// heads.
+// F: format of the cache, or kQ8Columns.  W columns of a head in a warp, H warps a head (H * W >= head_dim), R blocks of 8
+// (heads in columns: of 4) query heads.
 template <int F, int W, int R, int H>
 struct Config {
-  static constexpr bool kA4 = F == IL_A4, kQ8 = F == IL_Q8;
-  static constexpr int kRows = (kA4 ? 4 : 8) * R;  // query heads of a block
+  static constexpr bool kA4 = F == IL_A4, kQ8 = F == IL_Q8, kCols = kA4 || F == kQ8Columns;
+  static constexpr int kRows = (kCols ? 4 : 8) * R;  // query heads of a block
   static constexpr int kBlocks = W / 32;           // 32-element blocks of a warp's columns
   static constexpr int kPart = kRows * (W + 2);    // floats of a part: sums, maxima, sums of p
   // Tokens of a tile: 32 where a row is short in bytes, so that what a tile costs beside its bytes counts half
-  static constexpr int kTile = kA4 || (R == 1 && (kQ8 || W == 64)) ? 32 : 16;
-  static constexpr int kValues = kTile / (kA4 ? 8 : 4);  // of s, of a softmax row in a lane
-  static constexpr int kRowBytes = kA4 ? W / 2 : kQ8 ? W : 2 * W;
+  static constexpr int kTile = kCols || (R == 1 && (kQ8 || W == 64)) ? 32 : 16;
+  static constexpr int kValues = kTile / (kCols ? 8 : 4);  // of s, of a softmax row in a lane
+  static constexpr int kRowBytes = kA4 ? W / 2 : F == IL_BF16 ? 2 * W : W;
   static constexpr int kChunk = 16 * W / kRowBytes;                    // elements of 16 bytes
   static constexpr int kPool = kTile * kRowBytes;                      // K or V of a tile
   static constexpr int kScales = F != IL_BF16 ? kTile * kBlocks * 4 : 0;  // its scales
   static constexpr int kStage = 2 * (kPool + kScales);
   // (A4: measured with 8, 12 and 16 warps, 64 ragged sequences, heads of 128 as they were then: 116, 102, 137 us; of 64: 133, 112, 97 us)
-  static constexpr int kWarps = kA4 ? (R == 2 ? (W == 64 ? 12 : 8) : W == 64 ? 16 : 12) : kQ8 && R == 1 && W == 64 ? 12 : 8;
+  static constexpr int kWarps = kA4 ? (R == 2 ? (W == 64 ? 12 : 8) : W == 64 ? 16 : 12) : F != IL_BF16 && R == 1 && W == 64 ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kWorkers = kWarps / H;    // runs of tiles in a CTA
   static constexpr uint32_t kWhole = 2 * kWorkers;  // tiles of a row that is not cut over CTAs
@@ -310,7 +311,7 @@ static_assert(sizeof(Left) == 48, "see Config::kFixed");
 template <int F, bool SCORED, int W, int R, int H>
 __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_kernel(const KvAttendPlan P) {
   using C = Config<F, W, R, H>;
-  constexpr bool Q8 = C::kQ8, A4 = C::kA4, BLOCKED = Q8 || A4;  // scales of 32 elements
+  constexpr bool Q8 = C::kQ8, A4 = C::kA4, COLS = C::kCols, BLOCKED = F != IL_BF16;  // scales of 32 elements
   constexpr int NV = C::kValues;
   constexpr int T = C::kTile, NN = T / 8, GR = T / kGroup;  // tokens of a tile, in eights, in groups
   constexpr int NB = C::kBlocks, NT = C::kThreads, NW = C::kWarps, NK = C::kWorkers, S = C::kStages, ROWS = C::kRows;
@@ -455,11 +456,11 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
 
     auto token_of = [&](const Walk& w) { return (w.q.first + w.tile) * T + (lane & (T - 1)); };
     auto column_of = [&](uint32_t t) { return P.by_page.of(t); };
-    // A4: of the tile to be copied next, this lane's token's place in its page (units of `fetch` below), and which tokens are wanted
+    // Heads in columns: of the tile to be copied next, this lane's token's place in its page (units of `fetch` below), and which tokens are wanted
     uint32_t in_page_off = 0, in_page_soff = 0, wanted = 0;
     auto page_of = [&](const Walk& w) {  // page of this lane's token of the tile (of 16 tokens, lanes 16-31 repeat 0-15)
       const uint32_t t = token_of(w);
-      if constexpr (A4) {
+      if constexpr (COLS) {
         const bool want = t >= w.q.begin && t < w.q.len;
         const uint32_t col = column_of(t), in_page = t - col * (uint32_t)kv.page_size;
         in_page_off = in_page * P.token_bytes + w.hk * P.head_bytes;
@@ -471,30 +472,32 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
     };
     // Positions of the chunks of a row in shared memory, without bank conflicts in the reads below.
     auto k_at = [&](int row) {
-      if (A4) return (int)a4::chunk_at<NB>(row, chunk);
+      if (COLS) return (int)a4::chunk_at<CPR>(row, chunk);
       return row * C::kRowBytes +
              ((Q8 ? chunk ^ ((W == 64 ? (row >> 1) & 1 : row & 3) << 1) : chunk ^ ((row & 1) << 2)) << 4);
     };
     auto v_at = [&](int row) {
-      if (A4) return (int)a4::chunk_at<NB>(row, chunk);
+      if (COLS) return (int)a4::chunk_at<CPR>(row, chunk);
       if (!Q8) return row * C::kRowBytes + ((chunk ^ (row & 7)) << 4);
       if (W == 64) row = (row & ~15) | ((row >> 1) & 7) | ((row & 1) << 3);
       return row * C::kRowBytes + ((chunk ^ (((row >> 1) & (W == 64 ? 1 : 3)) << 1)) << 4);
     };
     // Copies the tile at `w`; gives the mask of its tokens that exist.
     auto fetch = [&](const Walk& w, int page, int stage) -> uint32_t {
-      if constexpr (A4) {
+      if constexpr (COLS) {
         const uint32_t to = ring + stage * C::kStage;
         if (P.simple && wanted == ~0u && __all_sync(~0u, (uint32_t)page < (uint32_t)kv.n_pages)) {
           // offsets in units of 16 bytes (and of a pair of steps): 32 bits, computed for one token a lane
           const uint32_t off = (uint32_t)page * P.page_bytes + in_page_off, soff = (uint32_t)page * P.spage_bytes + in_page_soff;
           const uint8_t *const kb = kv.k + (col_bytes + chunk * 16), *const vb = kv.v + (col_bytes + chunk * 16);
-          const uint32_t at = to + a4::chunk_at<NB>(sub, chunk);  // rows PER further lie as far apart, whatever the chunk
+          const uint32_t first = to + a4::chunk_at<CPR>(sub, chunk);
 #pragma unroll
           for (int i = 0; i < T / PER; ++i) {
             const uint64_t o = (uint64_t)__shfl_sync(~0u, off, i * PER + sub) * 16;
-            cp16(at + i * 512, kb + o, in_row);
-            cp16(at + i * 512 + C::kPool, vb + o, in_row);
+            // A4: rows PER further lie as far apart, whatever the chunk
+            const uint32_t at = A4 ? first + i * 512 : to + a4::chunk_at<CPR>(i * PER + sub, chunk);
+            cp16(at, kb + o, in_row);
+            cp16(at + C::kPool, vb + o, in_row);
           }
           const uint32_t st = to + 2 * C::kPool + lane * NB * 4;
 #pragma unroll
@@ -509,7 +512,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
       const uint32_t to = ring + stage * C::kStage;
       const bool want = t >= w.q.begin && t < w.q.len, ok = want && (uint32_t)page < (uint32_t)kv.n_pages;
       const uint32_t mask = __ballot_sync(~0u, ok) & (uint32_t)((1ull << T) - 1);
-      if (!A4 && P.simple && mask == (uint32_t)((1ull << T) - 1)) {
+      if (!COLS && P.simple && mask == (uint32_t)((1ull << T) - 1)) {
 #pragma unroll
         for (int k = 0; k < GR; ++k) {
           const uint32_t first = t0 + k * kGroup, pg = GR == 1 ? (uint32_t)page : (uint32_t)__shfl_sync(~0u, page, k * kGroup);
@@ -571,10 +574,10 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
       return (int)a.positions[w.s * a.positions_stride + t];
     };
 
-    uint32_t chunks[A4 ? NB / 2 : 1];  // A4: of ldmatrix's rows in 16 tokens, for blocks 2 i and 2 i + 1
-    if constexpr (A4) {
+    uint32_t chunks[CPR / 2];  // heads in columns: of ldmatrix's rows in 16 tokens, for chunks 2 i and 2 i + 1
+    if constexpr (COLS) {
 #pragma unroll
-      for (int i = 0; i < NB / 2; ++i) chunks[i] = a4::chunk_at<NB>(lane & 15, 2 * i + (lane >> 4));
+      for (int i = 0; i < CPR / 2; ++i) chunks[i] = a4::chunk_at<CPR>(lane & 15, 2 * i + (lane >> 4));
     }
 
     int page = page_of(in);
@@ -582,15 +585,16 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
     int place = SCORED ? position_of(in) : 0, places[SCORED ? S : 1];
 
     // ---- the row being worked on
-    constexpr int QR = A4 ? 1 : Q8 ? 4 * R : 6 * R;  // registers of q for 16 elements
-    constexpr int OX = A4 ? 2 * R : 4 * R;
+    constexpr int QR = COLS ? 1 : Q8 ? 4 * R : 6 * R;  // registers of q for 16 elements
+    constexpr int OX = COLS ? 2 * R : 4 * R;
     uint32_t qf[2 * NB][QR];
     float q_back[R];      // Q8: what s is to be multiplied by for the scaling of q and the bytes' unit; -2^-64 times it if above 2^127
     float q_start[R][NB];  // Q8: -128 units times the sum of q over a block
     // sums of p V, transposed: o[i][4 r + x] of MMA rows (columns of the head) g (x = 0, 1) or g + 8 (2, 3) of step i
-    // and of query heads 8 r + 2 q4 + (x & 1).  A4: o[2 b + j][2 r + x] of element 32 b + 4 g + 2 j + x, head 4 r + q4
+    // and of query heads 8 r + 2 q4 + (x & 1).  Heads in columns: o[2 b + j][2 r + x] of head 4 r + q4,
+    // element 32 b + 4 g + 2 j + x (A4) or 32 b + 16 j + 2 g + x (Q8)
     float o[W / 16][OX], m[R], l[R];
-    a4::Query<A4 ? NB : 1, A4 ? R : 1> aq;
+    typename std::conditional<A4, a4::Query<A4 ? NB : 1, R>, a4::Query8<COLS ? NB : 1, R>>::type cq;
     float om[A4 ? R : 1][A4 ? NB : 1];  // A4: this lane's tokens' part of sum p (m + 8 d), of block b
     float slope[SCORED ? R : 1];        // of this lane's softmax rows, times log2(e)
     int newest = 0;                     // position of the row's last token
@@ -600,26 +604,28 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
     int v_exp = 14, o_exp = 14;
 
     auto load_q = [&]() {
+      // this lane's eight elements of a block: 8 q4 .., or (Q8 in columns) 4 q4 .. of both its chunks
+      constexpr bool CHUNKS = COLS && !A4;
       if constexpr (SCORED) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          const int in_group = at.block * ROWS + (A4 ? 4 * r + q4 : 8 * r + g);
+          const int in_group = at.block * ROWS + (COLS ? 4 * r + q4 : 8 * r + g);
           slope[r] = a.slopes != nullptr && in_group < P.group ? a.slopes[(int64_t)at.hk * P.group + in_group] * 1.4426950408889634f : 0.f;
         }
         newest = a.positions != nullptr ? a.positions[at.s * a.positions_stride + at.q.len - 1] : (int)at.q.len - 1;
       }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int in_group = at.block * ROWS + (A4 ? r * 4 + g / 2 : r * 8 + g);
+        const int in_group = at.block * ROWS + (COLS ? r * 4 + g / 2 : r * 8 + g);
         const bool use = in_group < P.group;
-        const float* src = a.q + at.s * a.q_stride + (int64_t)(at.hk * P.group + in_group) * D + col0 + 8 * q4;
+        const float* src = a.q + at.s * a.q_stride + (int64_t)(at.hk * P.group + in_group) * D + col0 + (CHUNKS ? 4 : 8) * q4;
         float x[NB][8];
         float top = 0.f;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const bool here = use && col0 + 32 * b + 8 * q4 < D;
           const float4 u = here ? *reinterpret_cast<const float4*>(src + 32 * b) : make_float4(0.f, 0.f, 0.f, 0.f);
-          const float4 v = here ? *reinterpret_cast<const float4*>(src + 32 * b + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 v = here ? *reinterpret_cast<const float4*>(src + 32 * b + (CHUNKS ? 16 : 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
           x[b][0] = u.x, x[b][1] = u.y, x[b][2] = u.z, x[b][3] = u.w;
           x[b][4] = v.x, x[b][5] = v.y, x[b][6] = v.z, x[b][7] = v.w;
 #pragma unroll
@@ -632,10 +638,11 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
           top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
           top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
         }
-        if constexpr (A4) {
-          aq.take(r, x, top, lane);
+        if constexpr (COLS) {
+          cq.take(r, x, top, lane);
+          if constexpr (A4)
 #pragma unroll
-          for (int b = 0; b < NB; ++b) om[r][b] = 0.f;
+            for (int b = 0; b < NB; ++b) om[r][b] = 0.f;
         } else if constexpr (Q8) {
           const int e = max((int)(__float_as_uint(top) >> 23), 14);
           const float up = pow2_biased(267 - e);  // the row's largest |q| becomes 2^13 .. 2^14
@@ -731,15 +738,15 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
       }
       const uint32_t from = ring + stage * C::kStage;
 
-      // ---- s = q K^T: s[r][2 nt + c] of head row g + 8 r, token 8 nt + 2 q4 + c (A4: s[r][c] of head 4 r + q4, token 8 c + g)
+      // ---- s = q K^T: s[r][2 nt + c] of head row g + 8 r, token 8 nt + 2 q4 + c (in columns: s[r][c] of head 4 r + q4, token 8 c + g)
       float s[R][NV];
-      auto token_at = [&](int c) { return A4 ? 8 * c + g : 8 * (c / 2) + 2 * q4 + c % 2; };
+      auto token_at = [&](int c) { return COLS ? 8 * c + g : 8 * (c / 2) + 2 * q4 + c % 2; };
       if (H == 1 || i >= 0) {
-        if constexpr (A4) {
+        if constexpr (COLS) {
 #pragma unroll
           for (int k = 0; k < GR; ++k) {
             float c[R][2];
-            aq.dot(c, from + 16 * k * C::kRowBytes, from + 2 * C::kPool + 16 * k * NB * 4, chunks, lane);
+            cq.dot(c, from + 16 * k * C::kRowBytes, from + 2 * C::kPool + 16 * k * NB * 4, chunks, lane);
 #pragma unroll
             for (int r = 0; r < R; ++r) s[r][2 * k] = c[r][0], s[r][2 * k + 1] = c[r][1];
           }
@@ -910,7 +917,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
         top[r] = s[r][0];
 #pragma unroll
         for (int c = 1; c < NV; ++c) top[r] = fmaxf(top[r], s[r][c]);
-        if constexpr (A4) {
+        if constexpr (COLS) {
           top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 4));
           top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 8));
           top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 16));
@@ -930,7 +937,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
           highest[r] = fmaxf(highest[r], top[r]);
           next[r] = fmaxf(top[r], highest[r] - 24.f);
           wide |= next[r] - low[r] > 26.f;
-        } else if constexpr (A4) {
+        } else if constexpr (COLS) {
           highest[r] = fmaxf(highest[r], top[r]);
           next[r] = fmaxf(top[r], highest[r] - 24.f);
           wide |= next[r] - low[r] > 26.f;
@@ -960,7 +967,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
       const uint32_t fv = from + C::kPool;
       float kept[2 * R];  // keep of the heads that this lane's sums are of
 #pragma unroll
-      for (int r = 0; r < (A4 ? 0 : R); ++r) {
+      for (int r = 0; r < (COLS ? 0 : R); ++r) {
         kept[2 * r] = __shfl_sync(~0u, keep[r], 8 * q4);
         kept[2 * r + 1] = __shfl_sync(~0u, keep[r], 8 * q4 + 4);
       }
@@ -968,17 +975,20 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
 #pragma unroll
         for (int x = 0; x < 4 * R; ++x) acc[x] = fmaf(acc[x], kept[2 * (x / 4) + x % 2], c[x / 4][x % 4]);
       };
-      if constexpr (A4) {
-        static_assert(!A4 || T == 32, "a lane looks at one token's steps");
+      if constexpr (COLS) {
+        static_assert(!COLS || T == 32, "a lane looks at one token's steps");
         const uint32_t sv = from + 2 * C::kPool + C::kScales;  // V's steps
         uint32_t one[NB], most = 0;  // steps of one token
         a4::load_steps<NB>(one, sv + lane * NB * 4);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) most = max(most, one[b] & 0x7fffu);
-        v_exp = max(v_exp, (int)(__reduce_max_sync(~0u, most) >> 7));
-        const uint32_t little = (uint32_t)(v_exp - 12) << 7;
+        for (int b = 0; b < NB; ++b) {
+          one[b] = A4 ? (one[b] & 0x7fffu) << 16 : one[b] & 0x7fffffffu;  // |d| as the bits of a float
+          most = max(most, one[b]);
+        }
+        v_exp = max(v_exp, (int)(__reduce_max_sync(~0u, most) >> 23));
+        const uint32_t little = (uint32_t)(v_exp - 12) << 23;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) wide |= (one[b] & 0x7fffu) < little && (one[b] & 0x7fffu) != 0;
+        for (int b = 0; b < NB; ++b) wide |= one[b] < little && one[b] != 0;
         wide = __any_sync(~0u, wide);
         const float up = pow2_biased(267 - v_exp);  // the largest d becomes 2^13 .. 2^14
         const uint32_t v_at = from + C::kPool, steps = sv + g * NB * 4;
@@ -987,9 +997,19 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
         auto products = [&](auto is_wide, const float (&ps)[R][NV], const float (&p)[R][NV], float shift) {
           constexpr bool WIDE = decltype(is_wide)::value;
           uint32_t dm[NV][2], z[GR][4];
+          float d[NV];  // of block b
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            if (b % 2 == 0) {
+            if constexpr (!A4) {
+              // V of tokens 2 q4, 2 q4 + 1 and 8 further of 16, bytes 2 g and 2 g + 1 of the block's two chunks
+#pragma unroll
+              for (int c = 0; c < NV; ++c) {
+                d[c] = __uint_as_float(lds32(steps + (8 * c * NB + b) * 4));
+                if constexpr (WIDE) d[c] *= gap_up[b];
+              }
+#pragma unroll
+              for (int k = 0; k < GR; ++k) a4::ldmatrix4_trans(z[k], v_at + 16 * k * C::kRowBytes + chunks[b]);
+            } else if (b % 2 == 0) {
               // {d, m} of the lane's tokens, of blocks b and b + 1; V of tokens 2 q4, 2 q4 + 1 and 8 further of 16,
               // elements 4 g .. 4 g + 3
 #pragma unroll
@@ -1012,23 +1032,32 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
                   for (int c = 0; c < NV; ++c) dm[c][x] = __float_as_uint(a4::step_of(dm[c][x]) * gap_up[b + x]) >> 16;
               }
             }
+            if constexpr (A4)
+#pragma unroll
+              for (int c = 0; c < NV; ++c) d[c] = a4::step_of(dm[c][b % 2]);
             uint32_t w[GR][R][2];
 #pragma unroll
             for (int k = 0; k < GR; ++k)
 #pragma unroll
               for (int r = 0; r < R; ++r) {
-                a4::split2(a4::mul2(make_float2(ps[r][2 * k], ps[r][2 * k + 1]),
-                                    make_float2(a4::step_of(dm[2 * k][b % 2]), a4::step_of(dm[2 * k + 1][b % 2]))),
-                           w[k][r][0], w[k][r][1]);
+                a4::split2(a4::mul2(make_float2(ps[r][2 * k], ps[r][2 * k + 1]), make_float2(d[2 * k], d[2 * k + 1])), w[k][r][0], w[k][r][1]);
                 w[k][r][0] = a4::movmatrix(w[k][r][0]);
                 w[k][r][1] = a4::movmatrix(w[k][r][1]);
               }
-            float c[2][R][4];  // MMA rows g, g + 8 of step j: elements 32 b + 4 g + 2 j, and the next
+            float c[2][R][4];  // MMA rows g, g + 8 of step j: elements as in o
 #pragma unroll
             for (int k = 0; k < GR; ++k) {
               uint32_t x[4], y[4];
-              a4::nibbles_less_8(z[k][2 * (b % 2)], x);
-              a4::nibbles_less_8(z[k][2 * (b % 2) + 1], y);
+              if constexpr (A4) {
+                a4::nibbles_less_8(z[k][2 * (b % 2)], x);
+                a4::nibbles_less_8(z[k][2 * (b % 2) + 1], y);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  a4::bytes_of_pairs(z[k][2 * j], x[2 * j], x[2 * j + 1]);
+                  a4::bytes_of_pairs(z[k][2 * j + 1], y[2 * j], y[2 * j + 1]);
+                }
+              }
 #pragma unroll
               for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -1073,7 +1102,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
           constexpr float kClass = 67108864.f;  // 2^26
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            const int e = (int)(__reduce_max_sync(~0u, one[b] & 0x7fffu) >> 7);
+            const int e = (int)(__reduce_max_sync(~0u, one[b]) >> 23);
             gap_up[b] = pow2_biased(127 + min(v_exp - e, v_exp - 14));  // times up it stays a number
           }
           uint32_t classes = 0;
@@ -1266,7 +1295,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
       // ---- the row's or the run's end
       const bool row_ends = at.tile + 1 == at.q.tiles;
       if (row_ends || i + 1 == n) {
-        float unit = Q8 ? pow2_biased(o_exp - 13) : 1.f;  // (A4: below)
+        float unit = Q8 ? pow2_biased(o_exp - 13) : 1.f;  // (in columns: below)
         if (Q8 && o_exp < 80) {  // unit / sum may be below 2^-126: two factors
 #pragma unroll
           for (int k = 0; k < W / 16; ++k)
@@ -1279,12 +1308,12 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
         if (!alone) {
           const long long row = u0 + i - at.tile;
           if (!begun_here) {
-            Left& to = A4 ? s_left[worker] : left;  // (A4: not kept in registers meanwhile)
+            Left& to = COLS ? s_left[worker] : left;  // (in columns: not kept in registers meanwhile)
             has0 = true, end0 = row_ends, to.s0 = at.s, to.hk0 = at.hk, to.block0 = at.block;
             to.tiles0 = at.q.tiles, to.row0 = row;
             part = part_mem + warp * C::kPart;
           } else {  // the run's last tile: nothing is in flight into the ring any more
-            Left& to = A4 ? s_left[worker] : left;
+            Left& to = COLS ? s_left[worker] : left;
             has1 = true, to.s1 = at.s, to.hk1 = at.hk, to.block1 = at.block;
             to.tiles1 = at.q.tiles, to.row1 = row;
             part = reinterpret_cast<float*>(ring_mem + (size_t)warp * C::kRing);
@@ -1294,7 +1323,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
             if (H == 2) asm volatile("bar.sync %0, 64;" ::"r"(worker + 1) : "memory");
           }
         }
-        if constexpr (A4) {
+        if constexpr (COLS) {
           const int exp = o_exp - 140, half = exp >> 1;  // the sums' unit is 2^exp, as two factors
           const float ua = pow2_biased(127 + half), ub = pow2_biased(127 + exp - half);
 #pragma unroll
@@ -1303,8 +1332,9 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
 #pragma unroll
             for (int by = 4; by < 32; by *= 2) {
               sum += __shfl_xor_sync(~0u, sum, by);
+              if constexpr (A4)
 #pragma unroll
-              for (int b = 0; b < NB; ++b) om[r][b] += __shfl_xor_sync(~0u, om[r][b], by);
+                for (int b = 0; b < NB; ++b) om[r][b] += __shfl_xor_sync(~0u, om[r][b], by);
             }
             const int row = 4 * r + q4, of_group = at.block * ROWS + row;
             if (of_group >= P.group) continue;
@@ -1320,16 +1350,24 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
             const float f = !alone ? 1.f : sum == 0.f ? 0.f : __fdividef(1.f, sum);
             float* const to = alone ? a.out + at.s * a.out_stride + ((int64_t)at.hk * P.group + of_group) * D + col0 : part + row * W;
             auto value = [&](int b, int e) {
-              return fmaf(o[2 * b + e / 2][2 * r + e % 2] * ua, ub, om[r][b]) * f;
+              const float x = o[2 * b + e / 2][2 * r + e % 2] * ua;
+              if constexpr (A4) return fmaf(x, ub, om[r][b]) * f;
+              return x * ub * f;
             };
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
-              if (col0 + 32 * b < D)
+            for (int b = 0; b < NB; ++b) {
+              if (col0 + 32 * b >= D) continue;
+              if constexpr (A4) {
                 *reinterpret_cast<float4*>(to + 32 * b + 4 * g) = make_float4(value(b, 0), value(b, 1), value(b, 2), value(b, 3));
+              } else {
+                *reinterpret_cast<float2*>(to + 32 * b + 2 * g) = make_float2(value(b, 0), value(b, 1));
+                *reinterpret_cast<float2*>(to + 32 * b + 16 + 2 * g) = make_float2(value(b, 2), value(b, 3));
+              }
+            }
           }
         }
 #pragma unroll
-        for (int r = 0; r < (A4 ? 0 : R); ++r) {
+        for (int r = 0; r < (COLS ? 0 : R); ++r) {
           float sum = l[r];
           sum += __shfl_xor_sync(~0u, sum, 1);
           sum += __shfl_xor_sync(~0u, sum, 2);
@@ -1374,7 +1412,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
     cp_wait<0>();
   }
   if (lane == 0 && col0 == 0) {
-    if (!A4) s_left[worker] = left;
+    if (!COLS) s_left[worker] = left;
     if (has0) atomicOr(s_mask, 1u << worker);
     if (has0 && end0) atomicOr(s_mask + 1, 1u << worker);
     if (has1) atomicOr(s_mask + 2, 1u << worker);
@@ -1594,7 +1632,7 @@ cudaError_t prepare_variant(const KvAttendPlan& p, int ctas, Launch* out) {
 }
 
 // The variant of a cache: heads of up to 64, 128 or (a pair of warps) 256 elements, in blocks of kRows query heads (R blocks of 8
-// or, A4, of 4).
+// or, in columns, of 4).
 template <int F, bool SCORED>
 cudaError_t prepare_format(const KvAttendPlan& p, int dim, int blocks, int ctas, Launch* out) {
   auto of = [&](auto w, auto h) {

@@ -12,11 +12,15 @@ namespace {
 
 int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
-// Blocks of 8 (A4: 4) query heads that a warp takes at once.  A4: 8 heads at most, of which K and V of larger groups are read again, from
+// Whether query heads are in the MMAs' columns: A4, and Q8 with scores (one query head a K/V head, biased: with 8 rows for it 85 us, in
+// columns below).  Plain Q8 keeps the order that its bits came from.
+bool in_columns(const KvAttendArgs& a) { return a.kv.format == IL_A4 || (a.kv.format == IL_Q8 && a.scored); }
+
+// Blocks of 8 (in columns: 4) query heads that a warp takes at once.  In columns 8 heads at most, of which K and V of larger groups are read again, from
 // L2; with 16 the sums do not fit the registers (128 heads on 8 of 128, 32 sequences of 4096: 143 us, two blocks of 8 117 us).
 int head_blocks(const KvAttendArgs& a) {
   const int group = a.n_q_heads / a.kv.n_heads;
-  return group > (a.kv.format == IL_A4 ? 4 : 8) ? 2 : 1;
+  return group > (in_columns(a) ? 4 : 8) ? 2 : 1;
 }
 
 }  // namespace
@@ -28,7 +32,7 @@ size_t kv_workspace_bytes(int num_sms) { return kKvCounterBytes + (size_t)num_sm
 cudaError_t prepare_kv_attend(const KvAttendArgs& a, int num_sms, void* ws, Launch* out) {
   static_assert(attend::kMaxCtas * sizeof(unsigned) <= kKvCounterBytes, "a counter for each CTA");
   num_sms = std::min(num_sms, attend::kMaxCtas);
-  const int per_warp = head_blocks(a), rows = per_warp * (a.kv.format == IL_A4 ? 4 : 8);
+  const int per_warp = head_blocks(a), rows = per_warp * (in_columns(a) ? 4 : 8);
   KvAttendPlan p{};
   p.a = a;
   p.cap = (int)std::min<int64_t>(a.table_width * a.kv.page_size, INT32_MAX);
@@ -55,7 +59,7 @@ cudaError_t prepare_kv_attend(const KvAttendArgs& a, int num_sms, void* ws, Laun
   if (scaled && p.simple)
     p.simple = kv.head_dim == dim && fits(kv.spage * 4, kv.stoken * 4, kv.shead * 4) && bases % (4 * unit) == 0 &&
                even(kv.spage) && even(kv.stoken) && even(kv.shead);
-  if (kv.format == IL_A4) {
+  if (in_columns(a)) {
     // offsets in 16 bytes and in pairs of steps fit 32 bits
     const auto ends = [&](int64_t page, int64_t token, int64_t head) {
       return (kv.n_pages - 1) * page + (kv.page_size - 1) * token + (kv.n_heads - 1) * head <= UINT32_MAX;
@@ -66,7 +70,7 @@ cudaError_t prepare_kv_attend(const KvAttendArgs& a, int num_sms, void* ws, Laun
   p.page_bytes = (uint32_t)(kv.page * es), p.token_bytes = (uint32_t)(kv.token * es), p.head_bytes = (uint32_t)(kv.head * es);
   p.spage_bytes = (uint32_t)(kv.spage * 4), p.stoken_bytes = (uint32_t)(kv.stoken * 4);
   p.shead_bytes = (uint32_t)(kv.shead * 4);
-  if (kv.format == IL_A4) {
+  if (in_columns(a)) {
     p.page_bytes = (uint32_t)(kv.page / 16), p.token_bytes = (uint32_t)(kv.token / 16), p.head_bytes = (uint32_t)(kv.head / 16);
     p.spage_bytes = (uint32_t)kv.spage, p.stoken_bytes = (uint32_t)kv.stoken, p.shead_bytes = (uint32_t)kv.shead;
   }

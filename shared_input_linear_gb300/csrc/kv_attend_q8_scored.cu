@@ -4,7 +4,7 @@
 namespace il {
 
 cudaError_t prepare_kv_attend_q8_scored(const KvAttendPlan& p, int dim, int blocks, int ctas, Launch* out) {
-  return attend::prepare_format<IL_Q8, true>(p, dim, blocks, ctas, out);
+  return attend::prepare_format<attend::kQ8Columns, true>(p, dim, blocks, ctas, out);
 }
 
 }  // namespace il

@@ -91,68 +91,31 @@ struct Heads<IL_A4, NB> {
 template <int NB>
 struct Heads<IL_Q8, NB> {
   static constexpr int kWords = 5 * NB + 2;
-  uint32_t f[4 * NB];  // of 16-element chunk i: elements 16 i + 4 q4, + 1 and + 2, + 3
-  float start[NB];     // of head q4: -128 times the sum of q over a block, in the products' unit
-  float back[2];
+  a4::Query8<NB, 1> q;
   template <class Load>
   __device__ __forceinline__ void take(const Load& load, int lane) {
-    const int q4 = lane & 3, head_lane = 8 * q4;
-    const bool lo_part = (lane >> 2) & 1;
-    float x[2 * NB][4], top = 0.f;
+    float x[NB][8], top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2 * NB; ++i) {
-      load(16 * i + 4 * q4, x[i]);
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) top = fmaxf(top, fabsf(x[i][j]));
-    }
-    const int e = max((int)(__float_as_uint(quad_max(top)) >> 23), 14);
-    const float up = __int_as_float((267 - e) << 23);
+      for (int j = 0; j < 8; j += 4) {
+        float y[4];
+        load(32 * b + 4 * j + 4 * (lane & 3), y);
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      float total = 0.f;
-#pragma unroll
-      for (int i = 2 * b; i < 2 * b + 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-          const float y = x[i][j] * up, z = x[i][j + 1] * up;
-          uint32_t u, v;
-          a4::split2(make_float2(y, z), u, v);
-          f[2 * i + j / 2] = lo_part ? __byte_perm(u, v, 0x7632) : __byte_perm(u, v, 0x5410);
-          total += y + z;
-        }
-      total += __shfl_xor_sync(~0u, total, 1);
-      total += __shfl_xor_sync(~0u, total, 2);
-      start[b] = __shfl_sync(~0u, total, head_lane) * -7.62939453125e-06f;  // -128 2^-24
-    }
-    const int unit = __shfl_sync(~0u, e, head_lane) - 116, half = unit >> 1;
-    back[0] = __int_as_float((half + 127) << 23);
-    back[1] = __int_as_float((unit - half + 127) << 23);
+        for (int k = 0; k < 4; ++k) x[b][j + k] = y[k], top = fmaxf(top, fabsf(y[k]));
+      }
+    q.take(0, x, quad_max(top), lane);
   }
   __device__ __forceinline__ uint32_t& word(int i) {
-    return i < 4 * NB ? f[i] : reinterpret_cast<uint32_t&>(i < 5 * NB ? start[i - 4 * NB] : back[i - 5 * NB]);
+    return i < 4 * NB ? q.f[0][i] : reinterpret_cast<uint32_t&>(i < 5 * NB ? q.start[0][i - 4 * NB] : q.back[0][i - 5 * NB]);
   }
   __device__ __forceinline__ void dot(float (&s)[2], uint32_t tile, uint32_t steps, int first, int lane) const {
-    const int g = lane >> 2;
-    uint32_t d[2][NB];
-    a4::load_steps<NB>(d[0], steps + (first + g) * (4 * NB));
-    a4::load_steps<NB>(d[1], steps + (first + 8 + g) * (4 * NB));
-    s[0] = s[1] = 0.f;
+    uint32_t chunks[NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      uint32_t w[4];  // tokens g and g + 8 of chunk 2 b, then of 2 b + 1
-      a4::ldmatrix4(w, tile + a4::chunk_at<2 * NB>(first + (lane & 15), 2 * b + (lane >> 4)));
-      float c[4] = {start[b], 0.f, start[b], 0.f};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t x = w[2 * h] ^ 0x80808080u, y = w[2 * h + 1] ^ 0x80808080u;
-        a4::mma(c, __byte_perm(x, 0u, 0x4140), __byte_perm(y, 0u, 0x4140), __byte_perm(x, 0u, 0x4342), __byte_perm(y, 0u, 0x4342),
-                f[4 * b + 2 * h], f[4 * b + 2 * h + 1]);
-      }
-#pragma unroll
-      for (int t = 0; t < 2; ++t) s[t] = fmaf(fmaf(c[2 * t + 1], a4::kLoUnit, c[2 * t]), __uint_as_float(d[t][b]), s[t]);
-    }
-#pragma unroll
-    for (int t = 0; t < 2; ++t) s[t] = s[t] * back[0] * back[1];
+    for (int i = 0; i < NB; ++i) chunks[i] = a4::chunk_at<2 * NB>(lane & 15, 2 * i + (lane >> 4));
+    float t[1][2];
+    q.dot(t, tile + first * 32 * NB, steps + first * 4 * NB, chunks, lane);
+    s[0] = t[0][0], s[1] = t[0][1];
   }
 };
 

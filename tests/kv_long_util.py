@@ -229,9 +229,11 @@ class Case:
         for r in range(len(self.lens)) if rows is None else rows:
             k, v, km, vm = self.rows[r]
             # of Q8 the header states that p d is kept to 2^-26 d where 22 bits of it are less, p relative to the largest: a token's
-            # part of out is off by 2^-26 d |q| = 2^-26 |v| of the largest weight then.  A bias makes such weights common, and a
-            # V of exactly 0 in the largest one's place makes them count.
-            o, l, ot, lt = attend(self.q[r], k, v, km, vm, scale, floor=2.0**-26 if self.fmt == "q8" else 0.0, **self.plain_score(r))
+            # part of out is off by 2^-26 d |q| = 2^-26 |v| of the largest weight then, which counts where a V of exactly 0 is in the
+            # largest one's place.
+            # (With scores the header promises more.)
+            plain = self.cap == 0 and self.slopes is None and self.starts is None
+            o, l, ot, lt = attend(self.q[r], k, v, km, vm, scale, floor=2.0**-26 if self.fmt == "q8" and plain else 0.0, **self.plain_score(r))
             assert np.all(np.isfinite(out[r])), (r, self.lens[r])
             worst = float(np.max(np.abs(out[r] - o) / ot))
             assert worst <= 1, f"sequence {r} of length {self.lens[r]}: out is {worst:.3g} x its bound"
