@@ -274,7 +274,7 @@ __device__ __forceinline__ unsigned long long divide(unsigned long long a, uint3
   return a >> 32 == 0 ? (unsigned long long)((uint32_t)a / b) : divide_wide(a, b);
 }
 
-template <int T, bool SCORED>
+template <int T, bool SCORED, int LEAD>
 __device__ __forceinline__ Seq seq_of(const KvAttendPlan& P, int s) {
   Seq q;
   const int len = min(max(P.a.lens[s], 0), P.cap);
@@ -282,11 +282,11 @@ __device__ __forceinline__ Seq seq_of(const KvAttendPlan& P, int s) {
   q.begin = P.window > 0 ? (uint32_t)max(len - P.window, 0) : 0u;
   if (SCORED && P.a.starts != nullptr) q.begin = max(q.begin, (uint32_t)min(max(P.a.starts[s], 0), len));
   q.first = q.begin / T;
-  q.tiles = len == 0 || (SCORED && q.begin == q.len) ? 0u : (q.len + T - 1) / T - q.first;
+  q.tiles = len == 0 || (SCORED && q.begin == q.len) ? 0u : (q.len + T - 1) / T - q.first + LEAD;
   return q;
 }
 
-template <int T, bool SCORED>
+template <int T, bool SCORED, int LEAD>
 __device__ __forceinline__ void advance(Walk& w, const KvAttendPlan& P) {
   if (++w.tile < w.q.tiles) return;
   w.tile = 0;
@@ -294,7 +294,7 @@ __device__ __forceinline__ void advance(Walk& w, const KvAttendPlan& P) {
   w.block = 0;
   if (++w.hk < P.a.kv.n_heads) return;
   w.hk = 0;
-  do w.q = seq_of<T, SCORED>(P, ++w.s);
+  do w.q = seq_of<T, SCORED, LEAD>(P, ++w.s);
   while (w.q.tiles == 0 && w.s + 1 < P.a.n_seq);
 }
 
@@ -313,6 +313,10 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
   using C = Config<F, W, R, H>;
   constexpr bool Q8 = C::kQ8, A4 = C::kA4, COLS = C::kCols, BLOCKED = F != IL_BF16;  // scales of 32 elements
   constexpr int NV = C::kValues;
+  // Empty tiles before each row's, for what its start and end cost beside its tiles (q, parts, result).  One: 1024 biased Q8 rows of 1
+  // to 108 tiles 78.9 -> 60.5 us (two 61.5, four 65.3), 64 ragged A4 sequences 94.0 -> 93.4, 256 of 50 to 150 tokens 20.8 -> 19.9.  Not
+  // where rows of few bytes or pairs of warps lose: A4 heads of 64 90.3 -> 94.4, capped heads of 256 83.0 -> 84.0.
+  constexpr int LEAD = H == 1 && (SCORED || (A4 && W == 128)) ? 1 : 0;  // (a pair of warps meets at every tile's barrier: none may be empty)
   constexpr int T = C::kTile, NN = T / 8, GR = T / kGroup;  // tokens of a tile, in eights, in groups
   constexpr int NB = C::kBlocks, NT = C::kThreads, NW = C::kWarps, NK = C::kWorkers, S = C::kStages, ROWS = C::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -350,7 +354,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
   for (int k = 0; k < run; ++k) {
     const int s = tid * run + k;
     const bool in = s < a.n_seq;
-    const Seq q = in ? seq_of<T, SCORED>(P, s) : Seq{0, 0, 0, 0};
+    const Seq q = in ? seq_of<T, SCORED, LEAD>(P, s) : Seq{0, 0, 0, 0};
     mine += q.tiles;
     short_rows |= q.tiles - 1 < C::kWhole;
     unsigned none = __ballot_sync(~0u, in && q.tiles == 0 && s % gridDim.x == blockIdx.x);
@@ -419,10 +423,10 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
     const int lo = runs - 1;
     long long off = target - s_before[lo] * rows_per_seq;
     in.s = lo * run;
-    in.q = seq_of<T, SCORED>(P, in.s);
+    in.q = seq_of<T, SCORED, LEAD>(P, in.s);
     while (off >= (long long)in.q.tiles * rows_per_seq && in.s + 1 < a.n_seq) {
       off -= (long long)in.q.tiles * rows_per_seq;
-      in.q = seq_of<T, SCORED>(P, ++in.s);
+      in.q = seq_of<T, SCORED, LEAD>(P, ++in.s);
     }
     const int row = (int)divide(off, in.q.tiles);
     in.tile = (uint32_t)(off - (long long)row * in.q.tiles);
@@ -454,12 +458,14 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
     // scales: the widest copy of a token's scales; a lane copies K's (lanes 0-15) or V's
     constexpr int SB = NB * 4 > 16 ? 16 : NB * 4;
 
-    auto token_of = [&](const Walk& w) { return (w.q.first + w.tile) * T + (lane & (T - 1)); };
+    auto token_of = [&](const Walk& w) { return (w.q.first + w.tile - LEAD) * T + (lane & (T - 1)); };
+    auto empty = [&](const Walk& w) { return LEAD > 0 && w.tile < LEAD; };
     auto column_of = [&](uint32_t t) { return P.by_page.of(t); };
     // Heads in columns: of the tile to be copied next, this lane's token's place in its page (units of `fetch` below), and which tokens are wanted
     uint32_t in_page_off = 0, in_page_soff = 0, wanted = 0;
     auto page_of = [&](const Walk& w) {  // page of this lane's token of the tile (of 16 tokens, lanes 16-31 repeat 0-15)
       const uint32_t t = token_of(w);
+      if (empty(w)) return -1;
       if constexpr (COLS) {
         const bool want = t >= w.q.begin && t < w.q.len;
         const uint32_t col = column_of(t), in_page = t - col * (uint32_t)kv.page_size;
@@ -484,6 +490,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
     };
     // Copies the tile at `w`; gives the mask of its tokens that exist.
     auto fetch = [&](const Walk& w, int page, int stage) -> uint32_t {
+      if (empty(w)) return 0u;
       if constexpr (COLS) {
         const uint32_t to = ring + stage * C::kStage;
         if (P.simple && wanted == ~0u && __all_sync(~0u, (uint32_t)page < (uint32_t)kv.n_pages)) {
@@ -570,7 +577,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
     // Position of this lane's token of the tile, for the bias by distance.
     auto position_of = [&](const Walk& w) {
       const uint32_t t = token_of(w);
-      if (a.positions == nullptr || !(t >= w.q.begin && t < w.q.len)) return (int)t;
+      if (a.positions == nullptr || empty(w) || !(t >= w.q.begin && t < w.q.len)) return (int)t;
       return (int)a.positions[w.s * a.positions_stride + t];
     };
 
@@ -716,7 +723,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
           masks[S - 1] = fetch(in, page, ahead);
           if (SCORED) places[S - 1] = place;
           if (i + S < n) {
-            advance<T, SCORED>(in, P);
+            advance<T, SCORED, LEAD>(in, P);
             page = page_of(in);
             if (SCORED) place = position_of(in);
           }
@@ -741,7 +748,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
       // ---- s = q K^T: s[r][2 nt + c] of head row g + 8 r, token 8 nt + 2 q4 + c (in columns: s[r][c] of head 4 r + q4, token 8 c + g)
       float s[R][NV];
       auto token_at = [&](int c) { return COLS ? 8 * c + g : 8 * (c / 2) + 2 * q4 + c % 2; };
-      if (H == 1 || i >= 0) {
+      if ((H == 1 || i >= 0) && !empty(at)) {
         if constexpr (COLS) {
 #pragma unroll
           for (int k = 0; k < GR; ++k) {
@@ -875,420 +882,422 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
         if (i < 0) continue;
       }
 
-      // ---- capped and biased
-      if constexpr (SCORED) {
-        if (P.cap_log2 > 0.f) {
+      if (!empty(at)) {
+        // ---- capped and biased
+        if constexpr (SCORED) {
+          if (P.cap_log2 > 0.f) {
 #pragma unroll
-          for (int r = 0; r < R; ++r)
+            for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int c = 0; c < NV; ++c) s[r][c] = P.cap_log2 * tanhf(s[r][c]);
-        }
-        if (a.slopes != nullptr) {
-#pragma unroll
-          for (int c = 0; c < NV; ++c) {
-            const float far = (float)(__shfl_sync(~0u, places[0], token_at(c)) - newest);
-#pragma unroll
-            for (int r = 0; r < R; ++r) s[r][c] = fmaf(slope[r], far, s[r][c]);
+              for (int c = 0; c < NV; ++c) s[r][c] = P.cap_log2 * tanhf(s[r][c]);
           }
-        }
-      }
-
-      // ---- softmax: p = 2^(s - m) and the factor of what came before
-      const uint32_t mk = masks[0];
-      float low[R];
-      if constexpr (BLOCKED) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          low[r] = s[r][0];
-#pragma unroll
-          for (int c = 1; c < NV; ++c) low[r] = fminf(low[r], s[r][c]);
-        }
-      }
-      if (mk != (uint32_t)((1ull << T) - 1)) {
-#pragma unroll
-        for (int c = 0; c < NV; ++c)
-          if (!((mk >> token_at(c)) & 1))
-#pragma unroll
-            for (int r = 0; r < R; ++r) s[r][c] = -INFINITY;
-      }
-      float top[R];
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        top[r] = s[r][0];
-#pragma unroll
-        for (int c = 1; c < NV; ++c) top[r] = fmaxf(top[r], s[r][c]);
-        if constexpr (COLS) {
-          top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 4));
-          top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 8));
-          top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 16));
-        } else {
-          top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
-          top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
-        }
-      }
-      // bf16 parts of p have fp32's range: m is the maximum so far.  fp16 parts keep 12 bits or more of p only
-      // above 2^-26, so that m follows the tile's own maximum, down to 2^-24 of the largest p; a tile with
-      // smaller p all the same (`wide`) takes its products in classes of 2^-26 (below).
-      bool wide = false;
-      float next[R];
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if constexpr (Q8) {
-          highest[r] = fmaxf(highest[r], top[r]);
-          next[r] = fmaxf(top[r], highest[r] - 24.f);
-          wide |= next[r] - low[r] > 26.f;
-        } else if constexpr (COLS) {
-          highest[r] = fmaxf(highest[r], top[r]);
-          next[r] = fmaxf(top[r], highest[r] - 24.f);
-          wide |= next[r] - low[r] > 26.f;
-        } else {
-          next[r] = fmaxf(m[r], top[r]);
-        }
-      }
-      if (Q8) wide = __any_sync(~0u, wide);
-      float keep[R];
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (Q8 && wide) next[r] = highest[r];
-        const float base = next[r] == -INFINITY ? 0.f : next[r];
-        keep[r] = exp2_fast(m[r] - base);
-        m[r] = next[r];
-        float sum = 0.f;
-#pragma unroll
-        for (int c = 0; c < NV; c += 2) {
-          s[r][c] = exp2_fast(s[r][c] - base);
-          s[r][c + 1] = exp2_fast(s[r][c + 1] - base);
-          sum += s[r][c] + s[r][c + 1];
-        }
-        l[r] = fmaf(l[r], keep[r], sum);
-      }
-
-      // ---- o^T = o^T keep + V^T p^T: p is the B operand as it stands, its parts add up in the accumulators
-      const uint32_t fv = from + C::kPool;
-      float kept[2 * R];  // keep of the heads that this lane's sums are of
-#pragma unroll
-      for (int r = 0; r < (COLS ? 0 : R); ++r) {
-        kept[2 * r] = __shfl_sync(~0u, keep[r], 8 * q4);
-        kept[2 * r + 1] = __shfl_sync(~0u, keep[r], 8 * q4 + 4);
-      }
-      auto join = [&](float (&acc)[OX], const float (&c)[R][4]) {
-#pragma unroll
-        for (int x = 0; x < 4 * R; ++x) acc[x] = fmaf(acc[x], kept[2 * (x / 4) + x % 2], c[x / 4][x % 4]);
-      };
-      if constexpr (COLS) {
-        static_assert(!COLS || T == 32, "a lane looks at one token's steps");
-        const uint32_t sv = from + 2 * C::kPool + C::kScales;  // V's steps
-        uint32_t one[NB], most = 0;  // steps of one token
-        a4::load_steps<NB>(one, sv + lane * NB * 4);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          one[b] = A4 ? (one[b] & 0x7fffu) << 16 : one[b] & 0x7fffffffu;  // |d| as the bits of a float
-          most = max(most, one[b]);
-        }
-        v_exp = max(v_exp, (int)(__reduce_max_sync(~0u, most) >> 23));
-        const uint32_t little = (uint32_t)(v_exp - 12) << 23;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) wide |= one[b] < little && one[b] != 0;
-        wide = __any_sync(~0u, wide);
-        const float up = pow2_biased(267 - v_exp);  // the largest d becomes 2^13 .. 2^14
-        const uint32_t v_at = from + C::kPool, steps = sv + g * NB * 4;
-        float gap_up[NB];
-        // Products of weights p (ps: p up), with what came before times `keep`, and the sums' unit moved by `shift` too.
-        auto products = [&](auto is_wide, const float (&ps)[R][NV], const float (&p)[R][NV], float shift) {
-          constexpr bool WIDE = decltype(is_wide)::value;
-          uint32_t dm[NV][2], z[GR][4];
-          float d[NV];  // of block b
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            if constexpr (!A4) {
-              // V of tokens 2 q4, 2 q4 + 1 and 8 further of 16, bytes 2 g and 2 g + 1 of the block's two chunks
-#pragma unroll
-              for (int c = 0; c < NV; ++c) {
-                d[c] = __uint_as_float(lds32(steps + (8 * c * NB + b) * 4));
-                if constexpr (WIDE) d[c] *= gap_up[b];
-              }
-#pragma unroll
-              for (int k = 0; k < GR; ++k) a4::ldmatrix4_trans(z[k], v_at + 16 * k * C::kRowBytes + chunks[b]);
-            } else if (b % 2 == 0) {
-              // {d, m} of the lane's tokens, of blocks b and b + 1; V of tokens 2 q4, 2 q4 + 1 and 8 further of 16,
-              // elements 4 g .. 4 g + 3
-#pragma unroll
-              for (int c = 0; c < NV; ++c) lds64(dm[c][0], dm[c][1], steps + (8 * c * NB + b) * 4);
-#pragma unroll
-              for (int k = 0; k < GR; ++k) a4::ldmatrix4_trans(z[k], v_at + 16 * k * C::kRowBytes + chunks[b / 2]);
-#pragma unroll
-              for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  float sum = p[r][0] * a4::middle_of(dm[0][x]);
-#pragma unroll
-                  for (int c = 1; c < NV; ++c) sum = fmaf(p[r][c], a4::middle_of(dm[c][x]), sum);
-                  om[r][b + x] = fmaf(om[r][b + x], keep[r], sum);
-                }
-              if constexpr (WIDE) {
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                  for (int c = 0; c < NV; ++c) dm[c][x] = __float_as_uint(a4::step_of(dm[c][x]) * gap_up[b + x]) >> 16;
-              }
-            }
-            if constexpr (A4)
-#pragma unroll
-              for (int c = 0; c < NV; ++c) d[c] = a4::step_of(dm[c][b % 2]);
-            uint32_t w[GR][R][2];
-#pragma unroll
-            for (int k = 0; k < GR; ++k)
-#pragma unroll
-              for (int r = 0; r < R; ++r) {
-                a4::split2(a4::mul2(make_float2(ps[r][2 * k], ps[r][2 * k + 1]), make_float2(d[2 * k], d[2 * k + 1])), w[k][r][0], w[k][r][1]);
-                w[k][r][0] = a4::movmatrix(w[k][r][0]);
-                w[k][r][1] = a4::movmatrix(w[k][r][1]);
-              }
-            float c[2][R][4];  // MMA rows g, g + 8 of step j: elements as in o
-#pragma unroll
-            for (int k = 0; k < GR; ++k) {
-              uint32_t x[4], y[4];
-              if constexpr (A4) {
-                a4::nibbles_less_8(z[k][2 * (b % 2)], x);
-                a4::nibbles_less_8(z[k][2 * (b % 2) + 1], y);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  a4::bytes_of_pairs(z[k][2 * j], x[2 * j], x[2 * j + 1]);
-                  a4::bytes_of_pairs(z[k][2 * j + 1], y[2 * j], y[2 * j + 1]);
-                }
-              }
-#pragma unroll
-              for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  if (k == 0)
-                    a4::mma_first(c[j][r], x[2 * j], x[2 * j + 1], y[2 * j], y[2 * j + 1], w[k][r][0], w[k][r][1]);
-                  else
-                    a4::mma(c[j][r], x[2 * j], x[2 * j + 1], y[2 * j], y[2 * j + 1], w[k][r][0], w[k][r][1]);
-                }
-            }
-            const float back = WIDE ? pow2_biased(254 - (int)(__float_as_uint(gap_up[b]) >> 23)) : 1.f;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int r = 0; r < R; ++r) {
-                const float f = keep[r] * shift;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  float sum = fmaf(c[j][r][2 * x + 1], a4::kLoUnit, c[j][r][2 * x]);
-                  if constexpr (WIDE) sum *= back;
-                  o[2 * b + j][2 * r + x] = fmaf(o[2 * b + j][2 * r + x], f, sum);
-                }
-              }
-          }
-        };
-        float ps[R][NV];
-        if (!wide) {
-          float shift = 1.f;
-          if (o_exp != v_exp) {
-            shift = o_exp - v_exp < -126 ? 0.f : pow2_biased(127 + o_exp - v_exp);
-            o_exp = v_exp;
-          }
-#pragma unroll
-          for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int c = 0; c < NV; ++c) ps[r][c] = s[r][c] * up;
-          products(std::false_type{}, ps, s, shift);
-        } else {
-          // A tile with p below 2^-26, or a d below 2^-12 of the largest, takes its products in classes of p, class k
-          // being 2^(-26 (k + 1)) <= p < 2^(-26 k) (p = 1 in class 0; p below 2^-104 is 0), and with each block's steps brought up to
-          // the largest.  Class k is multiplied by 2^(26 k), and the sums' unit goes down as far until the last class is in.
-          constexpr float kClass = 67108864.f;  // 2^26
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const int e = (int)(__reduce_max_sync(~0u, one[b]) >> 23);
-            gap_up[b] = pow2_biased(127 + min(v_exp - e, v_exp - 14));  // times up it stays a number
-          }
-          uint32_t classes = 0;
-#pragma unroll
-          for (int r = 0; r < R; ++r)
+          if (a.slopes != nullptr) {
 #pragma unroll
             for (int c = 0; c < NV; ++c) {
-              const int k = (126 - (int)(__float_as_uint(s[r][c]) >> 23)) / 26;
-              if (s[r][c] > 0.f && k < 4) classes |= 1u << k;
+              const float far = (float)(__shfl_sync(~0u, places[0], token_at(c)) - newest);
+#pragma unroll
+              for (int r = 0; r < R; ++r) s[r][c] = fmaf(slope[r], far, s[r][c]);
             }
-          classes = max(__reduce_or_sync(~0u, classes), 1u);  // one at least: what came before takes its factor there
-#pragma unroll 1
-          while (classes != 0) {
-            const int k26 = 26 * (31 - __clz(classes));
-            classes &= ~(1u << (k26 / 26));
-            const int change = o_exp - (v_exp - k26);
-            o_exp = v_exp - k26;
-            const float class_up = pow2_biased(127 + k26);
-            float p[R][NV];
+          }
+        }
+
+        // ---- softmax: p = 2^(s - m) and the factor of what came before
+        const uint32_t mk = masks[0];
+        float low[R];
+        if constexpr (BLOCKED) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            low[r] = s[r][0];
+#pragma unroll
+            for (int c = 1; c < NV; ++c) low[r] = fminf(low[r], s[r][c]);
+          }
+        }
+        if (mk != (uint32_t)((1ull << T) - 1)) {
+#pragma unroll
+          for (int c = 0; c < NV; ++c)
+            if (!((mk >> token_at(c)) & 1))
+#pragma unroll
+              for (int r = 0; r < R; ++r) s[r][c] = -INFINITY;
+        }
+        float top[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          top[r] = s[r][0];
+#pragma unroll
+          for (int c = 1; c < NV; ++c) top[r] = fmaxf(top[r], s[r][c]);
+          if constexpr (COLS) {
+            top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 4));
+            top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 8));
+            top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 16));
+          } else {
+            top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
+            top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
+          }
+        }
+        // bf16 parts of p have fp32's range: m is the maximum so far.  fp16 parts keep 12 bits or more of p only
+        // above 2^-26, so that m follows the tile's own maximum, down to 2^-24 of the largest p; a tile with
+        // smaller p all the same (`wide`) takes its products in classes of 2^-26 (below).
+        bool wide = false;
+        float next[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          if constexpr (Q8) {
+            highest[r] = fmaxf(highest[r], top[r]);
+            next[r] = fmaxf(top[r], highest[r] - 24.f);
+            wide |= next[r] - low[r] > 26.f;
+          } else if constexpr (COLS) {
+            highest[r] = fmaxf(highest[r], top[r]);
+            next[r] = fmaxf(top[r], highest[r] - 24.f);
+            wide |= next[r] - low[r] > 26.f;
+          } else {
+            next[r] = fmaxf(m[r], top[r]);
+          }
+        }
+        if (Q8) wide = __any_sync(~0u, wide);
+        float keep[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          if (Q8 && wide) next[r] = highest[r];
+          const float base = next[r] == -INFINITY ? 0.f : next[r];
+          keep[r] = exp2_fast(m[r] - base);
+          m[r] = next[r];
+          float sum = 0.f;
+#pragma unroll
+          for (int c = 0; c < NV; c += 2) {
+            s[r][c] = exp2_fast(s[r][c] - base);
+            s[r][c + 1] = exp2_fast(s[r][c + 1] - base);
+            sum += s[r][c] + s[r][c + 1];
+          }
+          l[r] = fmaf(l[r], keep[r], sum);
+        }
+
+        // ---- o^T = o^T keep + V^T p^T: p is the B operand as it stands, its parts add up in the accumulators
+        const uint32_t fv = from + C::kPool;
+        float kept[2 * R];  // keep of the heads that this lane's sums are of
+#pragma unroll
+        for (int r = 0; r < (COLS ? 0 : R); ++r) {
+          kept[2 * r] = __shfl_sync(~0u, keep[r], 8 * q4);
+          kept[2 * r + 1] = __shfl_sync(~0u, keep[r], 8 * q4 + 4);
+        }
+        auto join = [&](float (&acc)[OX], const float (&c)[R][4]) {
+#pragma unroll
+          for (int x = 0; x < 4 * R; ++x) acc[x] = fmaf(acc[x], kept[2 * (x / 4) + x % 2], c[x / 4][x % 4]);
+        };
+        if constexpr (COLS) {
+          static_assert(!COLS || T == 32, "a lane looks at one token's steps");
+          const uint32_t sv = from + 2 * C::kPool + C::kScales;  // V's steps
+          uint32_t one[NB], most = 0;  // steps of one token
+          a4::load_steps<NB>(one, sv + lane * NB * 4);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            one[b] = A4 ? (one[b] & 0x7fffu) << 16 : one[b] & 0x7fffffffu;  // |d| as the bits of a float
+            most = max(most, one[b]);
+          }
+          v_exp = max(v_exp, (int)(__reduce_max_sync(~0u, most) >> 23));
+          const uint32_t little = (uint32_t)(v_exp - 12) << 23;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) wide |= one[b] < little && one[b] != 0;
+          wide = __any_sync(~0u, wide);
+          const float up = pow2_biased(267 - v_exp);  // the largest d becomes 2^13 .. 2^14
+          const uint32_t v_at = from + C::kPool, steps = sv + g * NB * 4;
+          float gap_up[NB];
+          // Products of weights p (ps: p up), with what came before times `keep`, and the sums' unit moved by `shift` too.
+          auto products = [&](auto is_wide, const float (&ps)[R][NV], const float (&p)[R][NV], float shift) {
+            constexpr bool WIDE = decltype(is_wide)::value;
+            uint32_t dm[NV][2], z[GR][4];
+            float d[NV];  // of block b
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              if constexpr (!A4) {
+                // V of tokens 2 q4, 2 q4 + 1 and 8 further of 16, bytes 2 g and 2 g + 1 of the block's two chunks
+#pragma unroll
+                for (int c = 0; c < NV; ++c) {
+                  d[c] = __uint_as_float(lds32(steps + (8 * c * NB + b) * 4));
+                  if constexpr (WIDE) d[c] *= gap_up[b];
+                }
+#pragma unroll
+                for (int k = 0; k < GR; ++k) a4::ldmatrix4_trans(z[k], v_at + 16 * k * C::kRowBytes + chunks[b]);
+              } else if (b % 2 == 0) {
+                // {d, m} of the lane's tokens, of blocks b and b + 1; V of tokens 2 q4, 2 q4 + 1 and 8 further of 16,
+                // elements 4 g .. 4 g + 3
+#pragma unroll
+                for (int c = 0; c < NV; ++c) lds64(dm[c][0], dm[c][1], steps + (8 * c * NB + b) * 4);
+#pragma unroll
+                for (int k = 0; k < GR; ++k) a4::ldmatrix4_trans(z[k], v_at + 16 * k * C::kRowBytes + chunks[b / 2]);
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                  for (int x = 0; x < 2; ++x) {
+                    float sum = p[r][0] * a4::middle_of(dm[0][x]);
+#pragma unroll
+                    for (int c = 1; c < NV; ++c) sum = fmaf(p[r][c], a4::middle_of(dm[c][x]), sum);
+                    om[r][b + x] = fmaf(om[r][b + x], keep[r], sum);
+                  }
+                if constexpr (WIDE) {
+#pragma unroll
+                  for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int c = 0; c < NV; ++c) dm[c][x] = __float_as_uint(a4::step_of(dm[c][x]) * gap_up[b + x]) >> 16;
+                }
+              }
+              if constexpr (A4)
+#pragma unroll
+                for (int c = 0; c < NV; ++c) d[c] = a4::step_of(dm[c][b % 2]);
+              uint32_t w[GR][R][2];
+#pragma unroll
+              for (int k = 0; k < GR; ++k)
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                  a4::split2(a4::mul2(make_float2(ps[r][2 * k], ps[r][2 * k + 1]), make_float2(d[2 * k], d[2 * k + 1])), w[k][r][0], w[k][r][1]);
+                  w[k][r][0] = a4::movmatrix(w[k][r][0]);
+                  w[k][r][1] = a4::movmatrix(w[k][r][1]);
+                }
+              float c[2][R][4];  // MMA rows g, g + 8 of step j: elements as in o
+#pragma unroll
+              for (int k = 0; k < GR; ++k) {
+                uint32_t x[4], y[4];
+                if constexpr (A4) {
+                  a4::nibbles_less_8(z[k][2 * (b % 2)], x);
+                  a4::nibbles_less_8(z[k][2 * (b % 2) + 1], y);
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 2; ++j) {
+                    a4::bytes_of_pairs(z[k][2 * j], x[2 * j], x[2 * j + 1]);
+                    a4::bytes_of_pairs(z[k][2 * j + 1], y[2 * j], y[2 * j + 1]);
+                  }
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                  for (int j = 0; j < 2; ++j) {
+                    if (k == 0)
+                      a4::mma_first(c[j][r], x[2 * j], x[2 * j + 1], y[2 * j], y[2 * j + 1], w[k][r][0], w[k][r][1]);
+                    else
+                      a4::mma(c[j][r], x[2 * j], x[2 * j + 1], y[2 * j], y[2 * j + 1], w[k][r][0], w[k][r][1]);
+                  }
+              }
+              const float back = WIDE ? pow2_biased(254 - (int)(__float_as_uint(gap_up[b]) >> 23)) : 1.f;
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                  const float f = keep[r] * shift;
+#pragma unroll
+                  for (int x = 0; x < 2; ++x) {
+                    float sum = fmaf(c[j][r][2 * x + 1], a4::kLoUnit, c[j][r][2 * x]);
+                    if constexpr (WIDE) sum *= back;
+                    o[2 * b + j][2 * r + x] = fmaf(o[2 * b + j][2 * r + x], f, sum);
+                  }
+                }
+            }
+          };
+          float ps[R][NV];
+          if (!wide) {
+            float shift = 1.f;
+            if (o_exp != v_exp) {
+              shift = o_exp - v_exp < -126 ? 0.f : pow2_biased(127 + o_exp - v_exp);
+              o_exp = v_exp;
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+              for (int c = 0; c < NV; ++c) ps[r][c] = s[r][c] * up;
+            products(std::false_type{}, ps, s, shift);
+          } else {
+            // A tile with p below 2^-26, or a d below 2^-12 of the largest, takes its products in classes of p, class k
+            // being 2^(-26 (k + 1)) <= p < 2^(-26 k) (p = 1 in class 0; p below 2^-104 is 0), and with each block's steps brought up to
+            // the largest.  Class k is multiplied by 2^(26 k), and the sums' unit goes down as far until the last class is in.
+            constexpr float kClass = 67108864.f;  // 2^26
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              const int e = (int)(__reduce_max_sync(~0u, one[b]) >> 23);
+              gap_up[b] = pow2_biased(127 + min(v_exp - e, v_exp - 14));  // times up it stays a number
+            }
+            uint32_t classes = 0;
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
               for (int c = 0; c < NV; ++c) {
-                const float x = s[r][c] * class_up;  // of a higher class: 2^26 or more above 1; of a lower: under 2^-26
-                const bool in_class = x >= 1.f / kClass && (x < 1.f || k26 == 0);
-                p[r][c] = in_class ? s[r][c] : 0.f, ps[r][c] = in_class ? x * up : 0.f;
+                const int k = (126 - (int)(__float_as_uint(s[r][c]) >> 23)) / 26;
+                if (s[r][c] > 0.f && k < 4) classes |= 1u << k;
               }
-            products(std::true_type{}, ps, p, change < -126 ? 0.f : pow2_biased(127 + change));
+            classes = max(__reduce_or_sync(~0u, classes), 1u);  // one at least: what came before takes its factor there
+#pragma unroll 1
+            while (classes != 0) {
+              const int k26 = 26 * (31 - __clz(classes));
+              classes &= ~(1u << (k26 / 26));
+              const int change = o_exp - (v_exp - k26);
+              o_exp = v_exp - k26;
+              const float class_up = pow2_biased(127 + k26);
+              float p[R][NV];
 #pragma unroll
-            for (int r = 0; r < R; ++r) keep[r] = 1.f;  // of a class still to come
+              for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int c = 0; c < NV; ++c) {
+                  const float x = s[r][c] * class_up;  // of a higher class: 2^26 or more above 1; of a lower: under 2^-26
+                  const bool in_class = x >= 1.f / kClass && (x < 1.f || k26 == 0);
+                  p[r][c] = in_class ? s[r][c] : 0.f, ps[r][c] = in_class ? x * up : 0.f;
+                }
+              products(std::true_type{}, ps, p, change < -126 ? 0.f : pow2_biased(127 + change));
+#pragma unroll
+              for (int r = 0; r < R; ++r) keep[r] = 1.f;  // of a class still to come
+            }
           }
-        }
-        if (o_exp != v_exp) {
-          const float again = pow2_biased(127 + o_exp - v_exp);  // from the last class's unit
-          o_exp = v_exp;
+          if (o_exp != v_exp) {
+            const float again = pow2_biased(127 + o_exp - v_exp);  // from the last class's unit
+            o_exp = v_exp;
 #pragma unroll
-          for (int k = 0; k < W / 16; ++k)
+            for (int k = 0; k < W / 16; ++k)
 #pragma unroll
-            for (int x = 0; x < OX; ++x) o[k][x] *= again;
-        }
-      } else if constexpr (Q8) {
-        float d[2 * NN][NB];  // V's scales of the lane's tokens
-        const uint32_t sv = from + 2 * C::kPool + C::kScales + 2 * q4 * NB * 4;
-        float vs[NB], most = 0.f;  // of one token
-        lds_floats(vs, from + 2 * C::kPool + C::kScales + (lane & (T - 1)) * NB * 4);
+              for (int x = 0; x < OX; ++x) o[k][x] *= again;
+          }
+        } else if constexpr (Q8) {
+          float d[2 * NN][NB];  // V's scales of the lane's tokens
+          const uint32_t sv = from + 2 * C::kPool + C::kScales + 2 * q4 * NB * 4;
+          float vs[NB], most = 0.f;  // of one token
+          lds_floats(vs, from + 2 * C::kPool + C::kScales + (lane & (T - 1)) * NB * 4);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) most = fmaxf(most, fabsf(vs[b]));
-        v_exp = max(v_exp, (int)(__reduce_max_sync(~0u, __float_as_uint(most)) >> 23));
-        // fp16 parts of p d keep 2^-38 of the largest scale: 2^-26 of one that lies 2^12 below it.  A tile with smaller
-        // ones takes its products in classes too, with each block's scales brought up to the largest (64 x 8192 tokens whose
-        // blocks lie further apart: 267 us, else 207).
-        const float little = pow2_biased(v_exp - 12);
+          for (int b = 0; b < NB; ++b) most = fmaxf(most, fabsf(vs[b]));
+          v_exp = max(v_exp, (int)(__reduce_max_sync(~0u, __float_as_uint(most)) >> 23));
+          // fp16 parts of p d keep 2^-38 of the largest scale: 2^-26 of one that lies 2^12 below it.  A tile with smaller
+          // ones takes its products in classes too, with each block's scales brought up to the largest (64 x 8192 tokens whose
+          // blocks lie further apart: 267 us, else 207).
+          const float little = pow2_biased(v_exp - 12);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) wide |= fabsf(vs[b]) < little && vs[b] != 0.f;
-        wide = __any_sync(~0u, wide);
+          for (int b = 0; b < NB; ++b) wide |= fabsf(vs[b]) < little && vs[b] != 0.f;
+          wide = __any_sync(~0u, wide);
 #pragma unroll
-        for (int c = 0; c < 2 * NN; ++c) lds_floats(d[c], sv + (8 * (c / 2) + c % 2) * NB * 4);
-        const float up = pow2_biased(267 - v_exp);  // the largest scale becomes 2^13 .. 2^14
-        // Products of weights w, with the sums' unit moved to the biased exponent `unit`; back(b) undoes what d[.][b] was
-        // multiplied by.
-        auto products = [&](const float (&w)[R][2 * NN], int unit, auto back) {
-          const int change = o_exp - unit;
-          const float shift = change < -126 ? 0.f : pow2_biased(127 + change);
-          o_exp = unit;
+          for (int c = 0; c < 2 * NN; ++c) lds_floats(d[c], sv + (8 * (c / 2) + c % 2) * NB * 4);
+          const float up = pow2_biased(267 - v_exp);  // the largest scale becomes 2^13 .. 2^14
+          // Products of weights w, with the sums' unit moved to the biased exponent `unit`; back(b) undoes what d[.][b] was
+          // multiplied by.
+          auto products = [&](const float (&w)[R][2 * NN], int unit, auto back) {
+            const int change = o_exp - unit;
+            const float shift = change < -126 ? 0.f : pow2_biased(127 + change);
+            o_exp = unit;
 #pragma unroll
-          for (int x = 0; x < 2 * R; ++x) kept[x] *= shift;
+            for (int x = 0; x < 2 * R; ++x) kept[x] *= shift;
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            float c[2][R][4];  // MMA rows g, g + 8 of step j: elements 32 b + 4 g + 2 j, and the next
+            for (int b = 0; b < NB; ++b) {
+              float c[2][R][4];  // MMA rows g, g + 8 of step j: elements 32 b + 4 g + 2 j, and the next
 #pragma unroll
-            for (int k = 0; k < GR; ++k) {
-              uint32_t f[2][4];  // V of tokens (2 q4, 2 q4 + 1) and 8 further, elements 32 b + 4 g + 0..3
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                auto word = [&](int t) {
-                  const int vrow = W == 64 ? (t & ~15) | ((t >> 1) & 7) | ((t & 1) << 3) : t;
-                  const int seg = b ^ ((vrow >> 1) & (W == 64 ? 1 : 3));
-                  return lds32(fv + vrow * C::kRowBytes + seg * 32 + g * 4) ^ 0x80808080u;
-                };
-                const uint32_t x = word(16 * k + 8 * h + 2 * q4), y = word(16 * k + 8 * h + 2 * q4 + 1);
-                q8_word_to_f16x2(__byte_perm(x, y, 0x5140), f[h][0], f[h][1]);
-                q8_word_to_f16x2(__byte_perm(x, y, 0x7362), f[h][2], f[h][3]);
-              }
-#pragma unroll
-              for (int r = 0; r < R; ++r) {
-                uint32_t hi[2], lo[2];
+              for (int k = 0; k < GR; ++k) {
+                uint32_t f[2][4];  // V of tokens (2 q4, 2 q4 + 1) and 8 further, elements 32 b + 4 g + 0..3
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  const int t = 4 * k + 2 * h;
-                  split2(w[r][t] * d[t][b], w[r][t + 1] * d[t + 1][b], hi[h], lo[h]);
+                  auto word = [&](int t) {
+                    const int vrow = W == 64 ? (t & ~15) | ((t >> 1) & 7) | ((t & 1) << 3) : t;
+                    const int seg = b ^ ((vrow >> 1) & (W == 64 ? 1 : 3));
+                    return lds32(fv + vrow * C::kRowBytes + seg * 32 + g * 4) ^ 0x80808080u;
+                  };
+                  const uint32_t x = word(16 * k + 8 * h + 2 * q4), y = word(16 * k + 8 * h + 2 * q4 + 1);
+                  q8_word_to_f16x2(__byte_perm(x, y, 0x5140), f[h][0], f[h][1]);
+                  q8_word_to_f16x2(__byte_perm(x, y, 0x7362), f[h][2], f[h][3]);
                 }
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  if (k == 0)
-                    mma_first<true>(c[j][r], f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1], hi[0], hi[1]);
-                  else
-                    mma<true>(c[j][r], f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1], hi[0], hi[1]);
-                  mma<true>(c[j][r], f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1], lo[0], lo[1]);
+                for (int r = 0; r < R; ++r) {
+                  uint32_t hi[2], lo[2];
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    const int t = 4 * k + 2 * h;
+                    split2(w[r][t] * d[t][b], w[r][t + 1] * d[t + 1][b], hi[h], lo[h]);
+                  }
+#pragma unroll
+                  for (int j = 0; j < 2; ++j) {
+                    if (k == 0)
+                      mma_first<true>(c[j][r], f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1], hi[0], hi[1]);
+                    else
+                      mma<true>(c[j][r], f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1], hi[0], hi[1]);
+                    mma<true>(c[j][r], f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1], lo[0], lo[1]);
+                  }
                 }
               }
+#pragma unroll
+              for (int x = 0; x < 8 * R; ++x) c[x / (4 * R)][x / 4 % R][x % 4] *= back(b);
+              join(o[2 * b], c[0]);
+              join(o[2 * b + 1], c[1]);
             }
+          };
+          float w[R][2 * NN];
+          if (!wide) {
 #pragma unroll
-            for (int x = 0; x < 8 * R; ++x) c[x / (4 * R)][x / 4 % R][x % 4] *= back(b);
-            join(o[2 * b], c[0]);
-            join(o[2 * b + 1], c[1]);
-          }
-        };
-        float w[R][2 * NN];
-        if (!wide) {
+            for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int r = 0; r < R; ++r)
+              for (int c = 0; c < 2 * NN; ++c) w[r][c] = s[r][c] * up;
+            products(w, v_exp, [](int) { return 1.f; });
+          } else {
+            // Classes of p, class k being 2^(-26 (k + 1)) <= p < 2^(-26 k) (p = 1 in class 0); p below 2^-104 is 0.  Class k is
+            // multiplied by 2^(26 k), and the sums' unit goes down as far, until the last class is in.
+            constexpr float kClass = 67108864.f;  // 2^26
+            float back[NB];
 #pragma unroll
-            for (int c = 0; c < 2 * NN; ++c) w[r][c] = s[r][c] * up;
-          products(w, v_exp, [](int) { return 1.f; });
-        } else {
-          // Classes of p, class k being 2^(-26 (k + 1)) <= p < 2^(-26 k) (p = 1 in class 0); p below 2^-104 is 0.  Class k is
-          // multiplied by 2^(26 k), and the sums' unit goes down as far, until the last class is in.
-          constexpr float kClass = 67108864.f;  // 2^26
-          float back[NB];
+            for (int b = 0; b < NB; ++b) {
+              const int e = (int)(__reduce_max_sync(~0u, __float_as_uint(fabsf(vs[b]))) >> 23);
+              const int gap = min(max(v_exp - e, 0), 120);  // (a NaN's e is 255)
+              back[b] = pow2_biased(127 - gap);
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const int e = (int)(__reduce_max_sync(~0u, __float_as_uint(fabsf(vs[b]))) >> 23);
-            const int gap = min(max(v_exp - e, 0), 120);  // (a NaN's e is 255)
-            back[b] = pow2_biased(127 - gap);
-#pragma unroll
-            for (int c = 0; c < 2 * NN; ++c) d[c][b] *= pow2_biased(127 + gap);
-          }
-          uint32_t classes = 0;
-#pragma unroll
-          for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int c = 0; c < 2 * NN; ++c) {
-              const int k = (126 - (int)(__float_as_uint(s[r][c]) >> 23)) / 26;
-              if (s[r][c] > 0.f && k < 4) classes |= 1u << k;
+              for (int c = 0; c < 2 * NN; ++c) d[c][b] *= pow2_biased(127 + gap);
             }
-          classes = max(__reduce_or_sync(~0u, classes), 1u);  // one at least: what came before takes its factor there
-#pragma unroll 1
-          while (classes != 0) {
-            const int k = 31 - __clz(classes);
-            classes ^= 1u << k;
-            float factor = 1.f;
-            for (int i26 = 0; i26 < k; ++i26) factor *= kClass;
+            uint32_t classes = 0;
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
               for (int c = 0; c < 2 * NN; ++c) {
-                const float x = s[r][c] * factor;  // of a higher class: 2^26 or more above 1; of a lower: under 2^-26
-                w[r][c] = x >= 1.f / kClass && (x < 1.f || k == 0) ? x * up : 0.f;
+                const int k = (126 - (int)(__float_as_uint(s[r][c]) >> 23)) / 26;
+                if (s[r][c] > 0.f && k < 4) classes |= 1u << k;
               }
-            products(w, v_exp - 26 * k, [&](int b) { return back[b]; });
+            classes = max(__reduce_or_sync(~0u, classes), 1u);  // one at least: what came before takes its factor there
+#pragma unroll 1
+            while (classes != 0) {
+              const int k = 31 - __clz(classes);
+              classes ^= 1u << k;
+              float factor = 1.f;
+              for (int i26 = 0; i26 < k; ++i26) factor *= kClass;
 #pragma unroll
-            for (int x = 0; x < 2 * R; ++x) kept[x] = 1.f;  // of a class still to come
-          }
-          const float up_again = pow2_biased(127 + o_exp - v_exp);  // from the last class's unit
-          o_exp = v_exp;
+              for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int k = 0; k < W / 16; ++k)
+                for (int c = 0; c < 2 * NN; ++c) {
+                  const float x = s[r][c] * factor;  // of a higher class: 2^26 or more above 1; of a lower: under 2^-26
+                  w[r][c] = x >= 1.f / kClass && (x < 1.f || k == 0) ? x * up : 0.f;
+                }
+              products(w, v_exp - 26 * k, [&](int b) { return back[b]; });
 #pragma unroll
-            for (int x = 0; x < 4 * R; ++x) o[k][x] *= up_again;
-        }
-      } else {
-        uint32_t hi[R][NN], mid[R][NN], lo[R][NN];  // of tokens 8 nt + 2 q4, and the next
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int nt = 0; nt < NN; ++nt)
-            split3(s[r][2 * nt], s[r][2 * nt + 1], hi[r][nt], mid[r][nt], lo[r][nt]);
-#pragma unroll
-        for (int i16 = 0; i16 < W / 16; ++i16) {  // MMA rows g, g + 8: elements 16 i16 + g, and 8 further
-          float c[R][4];
-#pragma unroll
-          for (int k = 0; k < GR; ++k) {
-            uint32_t w[4];
-            const int t = 16 * k + (lane & 15);
-            ldmatrix4_trans(w, fv + t * C::kRowBytes + (((2 * i16 + (lane >> 4)) ^ (t & 7)) << 4));
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-              if (k == 0)
-                mma_first<false>(c[r], w[0], w[2], w[1], w[3], hi[r][0], hi[r][1]);
-              else
-                mma<false>(c[r], w[0], w[2], w[1], w[3], hi[r][2 * k], hi[r][2 * k + 1]);
-              mma<false>(c[r], w[0], w[2], w[1], w[3], mid[r][2 * k], mid[r][2 * k + 1]);
-              mma<false>(c[r], w[0], w[2], w[1], w[3], lo[r][2 * k], lo[r][2 * k + 1]);
+              for (int x = 0; x < 2 * R; ++x) kept[x] = 1.f;  // of a class still to come
             }
+            const float up_again = pow2_biased(127 + o_exp - v_exp);  // from the last class's unit
+            o_exp = v_exp;
+#pragma unroll
+            for (int k = 0; k < W / 16; ++k)
+#pragma unroll
+              for (int x = 0; x < 4 * R; ++x) o[k][x] *= up_again;
           }
-          join(o[i16], c);
+        } else {
+          uint32_t hi[R][NN], mid[R][NN], lo[R][NN];  // of tokens 8 nt + 2 q4, and the next
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int nt = 0; nt < NN; ++nt)
+              split3(s[r][2 * nt], s[r][2 * nt + 1], hi[r][nt], mid[r][nt], lo[r][nt]);
+#pragma unroll
+          for (int i16 = 0; i16 < W / 16; ++i16) {  // MMA rows g, g + 8: elements 16 i16 + g, and 8 further
+            float c[R][4];
+#pragma unroll
+            for (int k = 0; k < GR; ++k) {
+              uint32_t w[4];
+              const int t = 16 * k + (lane & 15);
+              ldmatrix4_trans(w, fv + t * C::kRowBytes + (((2 * i16 + (lane >> 4)) ^ (t & 7)) << 4));
+#pragma unroll
+              for (int r = 0; r < R; ++r) {
+                if (k == 0)
+                  mma_first<false>(c[r], w[0], w[2], w[1], w[3], hi[r][0], hi[r][1]);
+                else
+                  mma<false>(c[r], w[0], w[2], w[1], w[3], hi[r][2 * k], hi[r][2 * k + 1]);
+                mma<false>(c[r], w[0], w[2], w[1], w[3], mid[r][2 * k], mid[r][2 * k + 1]);
+                mma<false>(c[r], w[0], w[2], w[1], w[3], lo[r][2 * k], lo[r][2 * k + 1]);
+              }
+            }
+            join(o[i16], c);
+          }
         }
       }
 
@@ -1405,7 +1414,7 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
       }
       stage = stage + 1 == S ? 0 : stage + 1;
       if (i + 1 < n) {
-        advance<T, SCORED>(at, P);
+        advance<T, SCORED, LEAD>(at, P);
         if (at.tile == 0) begun_here = fresh = true;
       }
     }
