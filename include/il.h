@@ -278,8 +278,8 @@ int il_centroid_head(const float* x, int64_t h, const il_weight* centroids, cons
  * page_size tokens.  A token's slot is page * page_size + its index in the page;
  * a sequence's block table lists its pages, so that its position p is in page
  * table[p / page_size].  All pointers are DEVICE pointers; every call is one
- * kernel launch (il_kv_evict one or two; none for an empty call), asynchronous on `stream`, and can be
- * captured in a CUDA graph.  Lengths, tables and slots live on the device and may
+ * kernel launch (il_kv_evict one or two; none for an empty call), asynchronous on `stream`,
+ * and can be captured in a CUDA graph.  Lengths, tables and slots live on the device and may
  * change between the replays of a graph.  Arguments that only the device can
  * see are checked there: a page or slot outside the cache is never accessed;
  * it is skipped and flagged, and il_check_device_status then returns IL_ERR_ARG.
@@ -288,9 +288,10 @@ int il_centroid_head(const float* x, int64_t h, const il_weight* centroids, cons
 
 /* A paged cache.
  *   format   : IL_BF16, or IL_Q8 as the weights have it: int8 q and one fp32 scale
- *              d per 32 elements of head_dim, value fp32(d*q), or IL_A4: u of 0 .. 15, two per byte,
- *              element 2k in bits 0-3 of byte k, and one pair of bf16 {d, m} per 32 elements, value
- *              fp32(d*u + m).  (The weights' Q4 has no offset; the channels of K seldom lie about 0.)
+ *              d per 32 elements of head_dim, value fp32(d*q), or IL_A4: u of 0 .. 15, two per
+ *              byte, element 2k in bits 0-3 of byte k, and one pair of bf16 {d, m} per 32 elements,
+ *              value fp32(d*u + m).  (The weights' Q4 has no offset; the channels of K seldom lie
+ *              about 0.)
  *   page_size: tokens per page, 1 .. 2^20.      n_pages: 1 .., n_pages * page_size < 2^31.
  *   n_heads  : K/V heads, 1 .. 1024.
  *   head_dim : 8 .. 256, a multiple of 8 (IL_BF16) or of 32 (IL_Q8, IL_A4).
@@ -299,8 +300,8 @@ int il_centroid_head(const float* x, int64_t h, const il_weight* centroids, cons
  *              bytes, and i / 2).  Any order of the three strides (64-bit offsets); 16-byte aligned
  *              rows: base address and strides times the element size are multiples of 16.
  *   k_scale, v_scale : IL_Q8: fp32 scales, (page, token, head, i / 32) likewise with
- *              the scale_ strides, in floats (4-byte alignment); IL_A4: the pairs, 4 bytes each with d in the
- *              lower half, in their place; NULL for IL_BF16.
+ *              the scale_ strides, in floats (4-byte alignment); IL_A4: the pairs, 4 bytes each
+ *              with d in the lower half, in their place; NULL for IL_BF16.
  * Strides of a dimension of extent 1 are not used; the others are at least a
  * row (head_dim, IL_A4 head_dim / 2; scales: head_dim / 32).  Elements must not overlap. */
 typedef struct {
@@ -361,10 +362,11 @@ int il_kv_extend(int64_t n_seq, int64_t page_size, const int32_t* lens, const in
  * bf16 rounds to nearest even.  Q8: d = max|w| / 127 over the 32 elements, q = w / d
  * rounded to nearest even (IEEE divisions, as the weights' test quantiser); a block of
  * zeros has d = 0, q = 0; a block with a NaN or an infinity reads back as NaN.
- * IL_A4: m is the least of the 32 elements rounded down to bf16, d = (max - m) / 15 rounded up to bf16,
- * u = (w - m) / d rounded to nearest even and cut to 0 .. 15 (IEEE single operations each); u = 0 where
- * d = 0, and a block with a NaN, an infinity or a range beyond bf16 reads back as NaN.  A value is off by
- * at most d / 2 and a rounding; d is at most (1 + 2^-7) ((max - min) + 2^-7 |min|) / 15.
+ * IL_A4: m is the least of the 32 elements rounded down to bf16, d = (max - m) / 15 rounded up
+ * to bf16, u = (w - m) / d rounded to nearest even and cut to 0 .. 15 (IEEE single operations
+ * each); u = 0 where d = 0, and a block with a NaN, an infinity or a range beyond bf16 reads back
+ * as NaN.  A value is off by at most d / 2 and a rounding; d is at most
+ * (1 + 2^-7) ((max - min) + 2^-7 |min|) / 15.
  */
 int il_kv_append(const il_kv* kv, const float* k, int64_t k_stride, const float* v, int64_t v_stride,
                  const int32_t* slots, int64_t n, void* stream);
@@ -400,9 +402,11 @@ int il_kv_read(const il_kv* kv, const int32_t* slots, int64_t n, float* k, int64
  * or 32 tokens; p below is relative to the tile's largest, or to 2^-24 of the sequence's largest so
  * far where that is more.  p d keeps 22 bits, or 2^-26 d where that is coarser.  In a tile with p below
  * 2^-26 or d below 2^-12 of the sequence's largest so far, the second bound is 2^-12 of p times the
- * tile's largest d of the same 32 columns instead, and p below 2^-104 counts as 0.  Over an A4 cache, and with il_kv_attend_scored over a Q8 one, an element of q
- * keeps 22 bits, or 2^-49 of its head's largest where that is coarser, and p d keeps 22 bits, or 2^-49 of the sequence's
- * largest so far; in a tile with p below 2^-26 or d below 2^-12 of those, 22 bits down to 2^-104 of it, where it counts as 0.
+ * tile's largest d of the same 32 columns instead, and p below 2^-104 counts as 0.  Over an A4 cache,
+ * and with il_kv_attend_scored over a Q8 one, an element of q keeps 22 bits, or 2^-49 of its head's
+ * largest where that is coarser, and p d keeps 22 bits, or 2^-49 of the sequence's largest so far; in
+ * a tile with p below 2^-26 or d below 2^-12 of those, 22 bits down to 2^-104 of it, where it counts
+ * as 0.
  * Workspace: il_kv_extend and il_kv_attend share one of about 5 MB per (device, stream), owned by the library,
  * allocated (stream-ordered) by the first of these calls on the stream and never moved: run one before
  * capturing the stream (IL_ERR_UNSUPPORTED otherwise).  il_release_scratch frees it.  A graph keeps using
@@ -414,13 +418,14 @@ int il_kv_attend(const il_kv* kv, const float* q, int64_t q_stride, const int32_
 
 /* What il_kv_attend_scored does to a logit, scale q_h . k_t at first; all of it zero or NULL: nothing.
  *   cap       : > 0: s = cap tanh(s / cap).
- *   slopes    : fp32 [n_q_heads] or NULL: then s += slopes[h] (pos_t - pos_last), a bias that grows with the
- *               distance from the sequence's last token.
- *   starts    : int32 [n_seq] or NULL: tokens before starts[r] are not seen (the first token of the document that
- *               the new token belongs to); negative: all are, len or more: none is.
- *   positions : int32 [n_seq][positions_width], rows positions_stride apart, or NULL (a token's position is its index):
- *               positions of the tokens where il_kv_evict has moved them.  A length is cut to positions_width.
- * cap, scale / cap and slopes must be finite. */
+ *   slopes    : fp32 [n_q_heads] or NULL: then s += slopes[h] (pos_t - pos_last), a bias that grows
+ *               with the distance from the sequence's last token.
+ *   starts    : int32 [n_seq] or NULL: tokens of index below starts[r] are not seen (the first token
+ *               of the document that the new token belongs to); negative: all are, len or more: none is.
+ *   positions : int32 [n_seq][positions_width], rows positions_stride apart, or NULL (a token's
+ *               position is its index): positions of the tokens where il_kv_evict has moved them.
+ *               A length is cut to positions_width.
+ * cap is 0 or 2^-100 to 2^100; scale / cap, an element of q times that, and slopes must be finite. */
 typedef struct {
   float cap;
   const float* slopes;
@@ -430,50 +435,58 @@ typedef struct {
 } il_kv_score;
 
 /*
- * il_kv_attend_scored -- il_kv_attend with capped and biased logits and sequences that begin later.  The window
- * counts by index; with starts, a token is seen that both allow.  A sequence of which no token is seen gives out = 0 and
- * lse = -inf.  The cap and the bias are fp32: a logit's error is that of tanhf times cap, and a rounding of the bias.
+ * il_kv_attend_scored -- il_kv_attend with capped and biased logits and sequences that begin later.
+ * The window counts by index; with starts, a token is seen that both allow.  A sequence of which no
+ * token is seen gives out = 0 and lse = -inf.  The cap and the bias are fp32: a logit's error is that
+ * of tanhf times cap, and a rounding of the bias.
  */
 int il_kv_attend_scored(const il_kv* kv, const float* q, int64_t q_stride, const int32_t* table, int64_t table_stride,
                         int64_t table_width, const int32_t* lens, int64_t n_seq, int64_t n_q_heads, float scale,
-                        int64_t window, const il_kv_score* score, float* out, int64_t out_stride, float* lse, void* stream);
+                        int64_t window, const il_kv_score* score, float* out, int64_t out_stride, float* lse,
+                        void* stream);
 
 /*
  * il_kv_weigh -- what each cached token collects of one new token's attention, over all query heads:
  *     weights_out[r][t] = (t is new ? 0 : weights[r][t]) + sum_h exp(s_t - lse_h)
- * for t < lens[r], with s as il_kv_attend (or, with score, il_kv_attend_scored) has it; tokens that are not seen add
- * nothing.  Call it with the same arguments, and that call's lse.  K is read, V is not.
+ * for t < lens[r], with s as il_kv_attend (or, with score, il_kv_attend_scored) has it; tokens that
+ * are not seen add nothing.  Call it with the same arguments, and that call's lse.  K is read, V is not.
  *   q .. score : as for il_kv_attend_scored; score may be NULL.
  *   lse       : fp32 [n_seq][n_q_heads].
- *   add       : int32 [n_seq] or NULL: the last add[r] tokens are new, whatever weights holds there (il_kv_extend's
- *               add; all of them for a new sequence; negative: none).
- *   weights, weights_out : fp32 [n_seq][weights_width], rows weights_stride apart; may be the same.  A length is cut to
- *               weights_width (at most 2^30).  Entries from the length on are left as they are.
- * Sums are fp32, in an order that depends on the lengths only: equal calls give equal bits.  K, q and lse that are read must
- * be finite.  Needs no workspace.
+ *   add       : int32 [n_seq] or NULL: the last add[r] tokens are new, whatever weights holds there
+ *               (il_kv_extend's add; all of them for a new sequence; negative: none).
+ *   weights, weights_out : fp32 [n_seq][weights_width], rows weights_stride apart; may be the same.
+ *               A length is cut to weights_width (at most 2^30).  Entries from the length on are left
+ *               as they are.
+ * Sums are fp32, in an order that depends on the lengths only: equal calls give equal bits.  K, q and
+ * lse that are read must be finite.  Needs no workspace.
  */
 int il_kv_weigh(const il_kv* kv, const float* q, int64_t q_stride, const int32_t* table, int64_t table_stride,
-                int64_t table_width, const int32_t* lens, int64_t n_seq, int64_t n_q_heads, float scale, int64_t window,
-                const il_kv_score* score, const float* lse, const int32_t* add, const float* weights, float* weights_out,
-                int64_t weights_stride, int64_t weights_width, void* stream);
+                int64_t table_width, const int32_t* lens, int64_t n_seq, int64_t n_q_heads, float scale,
+                int64_t window, const il_kv_score* score, const float* lse, const int32_t* add, const float* weights,
+                float* weights_out, int64_t weights_stride, int64_t weights_width, void* stream);
 
 /*
- * il_kv_evict -- cuts sequences longer than `keep` to that many tokens: those at the first positions, the most recent
- * ones and, of the others, those of the largest weight (of equal ones those of the lower index; NaN counts as the least).
- * Kept tokens of index keep and more move to the places of tokens before it that go, the i-th to the i-th; the others stay
- * where they are, so that a token's index no longer tells its position (hence `positions`).
- * Sequences of up to `keep` tokens stay as they are.  lens, table and the free pages stay too: drop holds the
- * changes of length for il_kv_extend's add, which gives the pages back -- once, where the caches of several
- * layers share a table and each has been cut by a call of its own.
- *   keep      : 1 to 2^30.     first, recent : tokens of position below first, or above that of the last token less
- *               recent, stay whatever their weight; first + recent <= keep.
+ * il_kv_evict -- cuts sequences longer than `keep` to that many tokens: those at the first positions,
+ * the most recent ones and, of the others, those of the largest weight (of equal ones those of the
+ * lower index; NaN counts as the least).  Kept tokens of index keep and more move to the places of
+ * tokens before it that go, the i-th to the i-th; the others stay where they are, so that a token's
+ * index no longer tells its position (hence `positions`).  Sequences of up to `keep` tokens stay as
+ * they are.  lens, table and the free pages stay too: drop holds the changes of length for
+ * il_kv_extend's add, which gives the pages back -- once, where the caches of several layers share a
+ * table and each has been cut by a call of its own.
+ *   keep      : 1 to 2^30.     first, recent : tokens of position below first, or above that of the
+ *               last token less recent, stay whatever their weight; first + recent <= keep.
  *   weights, weights_out : as for il_kv_weigh; the weights move with their tokens.
- *   positions, positions_out : int32 likewise [n_seq][positions_width], distinct in a sequence and the last token's the
- *               newest; both NULL: a token's position is its index.  A length is cut to their width.
- *   kept      : int32 [n_seq][keep], rows kept_stride apart: the index that a token now at i had, -1 from the new length on.
- *   drop      : int32 [n_seq]: the new length less lens[r] (of a length that was cut, all that is beyond goes too).
- * The pages of a sequence that is cut must be its own.  Outputs must not overlap each other or an input, except
- * weights_out == weights and positions_out == positions.  One launch where rows are at most keep + 64 wide, else two; needs no workspace.
+ *   positions, positions_out : int32 likewise [n_seq][positions_width], distinct in a sequence and
+ *               the last token's the newest; both NULL: a token's position is its index.  A length is
+ *               cut to their width.
+ *   kept      : int32 [n_seq][keep], rows kept_stride apart: the index that a token now at i had, -1
+ *               from the new length on.
+ *   drop      : int32 [n_seq]: the new length less lens[r] (of a length that was cut, all that is
+ *               beyond goes too).
+ * The pages of a sequence that is cut must be its own.  Outputs must not overlap each other or an
+ * input, except weights_out == weights and positions_out == positions.  One launch where rows are at
+ * most keep + 64 wide, else two; needs no workspace.
  */
 int il_kv_evict(const il_kv* kv, const int32_t* table, int64_t table_stride, int64_t table_width, const int32_t* lens,
                 int64_t n_seq, int64_t keep, int64_t first, int64_t recent, const float* weights, float* weights_out,

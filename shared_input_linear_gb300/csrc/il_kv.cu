@@ -1,10 +1,11 @@
-// il_kv.cu -- entry points of the paged K/V cache (include/il.h: il_kv_extend, il_kv_append,
-// il_kv_read, il_kv_attend, il_kv_attend_scored, il_kv_weigh, il_kv_evict): every argument that the host can see is checked and the launch
-// prepared before it is enqueued, as in the matmul entry points.
+// il_kv.cu -- entry points of the paged K/V cache (include/il.h: il_kv_extend, il_kv_append, il_kv_read,
+// il_kv_attend, il_kv_attend_scored, il_kv_weigh, il_kv_evict): every argument that the host can see is checked and
+// the launch prepared before it is enqueued, as in the matmul entry points.
 #include <algorithm>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <new>
 #include <vector>
 
 #include <nvtx3/nvToolsExt.h>
@@ -159,7 +160,8 @@ int rows_call(const char* fn, bool write, const il_kv* kv, float* k, int64_t k_s
 int check_score(const char* fn, const il_kv_score* score, float scale, int64_t n_seq, KvAttendArgs* a) {
   if (score == nullptr) return IL_OK;
   const il_kv_score& c = *score;
-  if (!(c.cap >= 0.0f) || !(c.cap - c.cap == 0.0f)) return bad(IL_ERR_ARG, fn, "cap is negative or not finite");
+  // (beyond these, cap log2(e) or q scale / cap leaves fp32 where the logit itself does not)
+  if (!(c.cap == 0.0f || (c.cap >= 0x1p-100f && c.cap <= 0x1p100f))) return bad(IL_ERR_ARG, fn, "cap must be 0, or 2^-100 to 2^100");
   if (c.cap > 0.0f && !(scale / c.cap - scale / c.cap == 0.0f)) return bad(IL_ERR_ARG, fn, "scale / cap is not finite");
   if (!aligned(c.slopes, 4) || !aligned(c.starts, 4) || !aligned(c.positions, 4))
     return bad(IL_ERR_ARG, fn, "slopes, starts or positions is not 4-byte aligned");
@@ -215,18 +217,21 @@ int check_attended(const char* fn, const il_kv* kv, const float* q, int64_t q_st
 }
 
 // What a call of those arguments reads: q first.
-std::vector<Range> ranges_of(const KvAttendArgs& a) {
+struct Ranges {
+  Range r[10];
+};
+Ranges ranges_of(const KvAttendArgs& a) {
   const int64_t n = a.n_seq, row = (int64_t)a.n_q_heads * a.kv.head_dim;
-  return {{a.q, 4 * ((n - 1) * a.q_stride + row), false},
-          {a.table, 4 * ((n - 1) * a.table_stride + a.table_width), false},
-          {a.lens, 4 * n, false},
-          {a.kv.k, extent_bytes(a.kv, false), false},
-          {a.kv.v, extent_bytes(a.kv, false), false},
-          {a.kv.k_scale, extent_bytes(a.kv, true), false},
-          {a.kv.v_scale, extent_bytes(a.kv, true), false},
-          {a.slopes, 4 * (int64_t)a.n_q_heads, false},
-          {a.starts, 4 * n, false},
-          {a.positions, 4 * ((n - 1) * a.positions_stride + a.positions_width), false}};
+  return {{{a.q, 4 * ((n - 1) * a.q_stride + row), false},
+           {a.table, 4 * ((n - 1) * a.table_stride + a.table_width), false},
+           {a.lens, 4 * n, false},
+           {a.kv.k, extent_bytes(a.kv, false), false},
+           {a.kv.v, extent_bytes(a.kv, false), false},
+           {a.kv.k_scale, extent_bytes(a.kv, true), false},
+           {a.kv.v_scale, extent_bytes(a.kv, true), false},
+           {a.slopes, 4 * (int64_t)a.n_q_heads, false},
+           {a.starts, 4 * n, false},
+           {a.positions, 4 * ((n - 1) * a.positions_stride + a.positions_width), false}}};
 }
 
 int attend_call(const char* fn, const il_kv* kv, const float* q, int64_t q_stride, const int32_t* table, int64_t table_stride,
@@ -245,10 +250,10 @@ int attend_call(const char* fn, const il_kv* kv, const float* q, int64_t q_strid
     return bad(IL_ERR_SHAPE, fn, "out_stride is smaller than a row or not a multiple of 4");
   const int64_t os = n_seq > 1 ? out_stride : 0;
   const Range outs[] = {{out, 4 * ((n_seq - 1) * os + row), true}, {lse, 4 * n_seq * n_q_heads, true}};
-  const std::vector<Range> ins = ranges_of(a);
+  const Ranges ins = ranges_of(a);
   for (const Range& o : outs)
-    for (const Range& i : ins)
-      if (clash(o, i) && !(&o == outs && &i == ins.data() && side_by_side(out, os, q, a.q_stride, n_seq, row)))
+    for (const Range& i : ins.r)
+      if (clash(o, i) && !(&o == outs && &i == ins.r && side_by_side(out, os, q, a.q_stride, n_seq, row)))
         return bad(IL_ERR_ARG, fn, "out and lse must not overlap q, table, lens, the score's arrays or the cache");
   if (clash(outs[0], outs[1])) return bad(IL_ERR_ARG, fn, "out and lse must not overlap");
   int num_sms = 0;
@@ -284,7 +289,7 @@ extern "C" {
 int il_kv_extend(int64_t n_seq, int64_t page_size, const int32_t* lens, const int32_t* add, int32_t* table,
                  int64_t table_stride, int64_t table_width, int32_t* ring, int64_t ring_size, const int64_t* cursor,
                  int32_t* lens_out, int64_t* cursor_out, int32_t* slots, int64_t max_slots, int32_t* positions,
-                 int32_t* first, int64_t* info, void* stream) {
+                 int32_t* first, int64_t* info, void* stream) try {
   const char* fn = "il_kv_extend";
   NvtxRange range(fn);
   api_clear_error();
@@ -354,37 +359,47 @@ int il_kv_extend(int64_t n_seq, int64_t page_size, const int32_t* lens, const in
   const cudaError_t e = prepare_kv_extend(a, num_sms, &L);
   if (e != cudaSuccess) return api_cuda_fail(e, fn);
   return enqueue(fn, L, stream);
+} catch (const std::bad_alloc&) {  // of the launch lists
+  return api_cuda_fail(cudaErrorMemoryAllocation, "il_kv_extend");
 }
 
 int il_kv_append(const il_kv* kv, const float* k, int64_t k_stride, const float* v, int64_t v_stride,
-                 const int32_t* slots, int64_t n, void* stream) {
+                 const int32_t* slots, int64_t n, void* stream) try {
   return rows_call("il_kv_append", true, kv, const_cast<float*>(k), k_stride, const_cast<float*>(v), v_stride, slots, n,
                    stream);
+} catch (const std::bad_alloc&) {  // of the launch lists
+  return api_cuda_fail(cudaErrorMemoryAllocation, "il_kv_append");
 }
 
 int il_kv_read(const il_kv* kv, const int32_t* slots, int64_t n, float* k, int64_t k_stride, float* v, int64_t v_stride,
-               void* stream) {
+               void* stream) try {
   return rows_call("il_kv_read", false, kv, k, k_stride, v, v_stride, slots, n, stream);
+} catch (const std::bad_alloc&) {  // of the launch lists
+  return api_cuda_fail(cudaErrorMemoryAllocation, "il_kv_read");
 }
 
 int il_kv_attend(const il_kv* kv, const float* q, int64_t q_stride, const int32_t* table, int64_t table_stride,
                  int64_t table_width, const int32_t* lens, int64_t n_seq, int64_t n_q_heads, float scale, int64_t window,
-                 float* out, int64_t out_stride, float* lse, void* stream) {
+                 float* out, int64_t out_stride, float* lse, void* stream) try {
   return attend_call("il_kv_attend", kv, q, q_stride, table, table_stride, table_width, lens, n_seq, n_q_heads, scale, window,
                      nullptr, out, out_stride, lse, stream);
+} catch (const std::bad_alloc&) {  // of the launch lists
+  return api_cuda_fail(cudaErrorMemoryAllocation, "il_kv_attend");
 }
 
 int il_kv_attend_scored(const il_kv* kv, const float* q, int64_t q_stride, const int32_t* table, int64_t table_stride,
                         int64_t table_width, const int32_t* lens, int64_t n_seq, int64_t n_q_heads, float scale,
-                        int64_t window, const il_kv_score* score, float* out, int64_t out_stride, float* lse, void* stream) {
+                        int64_t window, const il_kv_score* score, float* out, int64_t out_stride, float* lse, void* stream) try {
   return attend_call("il_kv_attend_scored", kv, q, q_stride, table, table_stride, table_width, lens, n_seq, n_q_heads, scale,
                      window, score, out, out_stride, lse, stream);
+} catch (const std::bad_alloc&) {  // of the launch lists
+  return api_cuda_fail(cudaErrorMemoryAllocation, "il_kv_attend_scored");
 }
 
 int il_kv_weigh(const il_kv* kv, const float* q, int64_t q_stride, const int32_t* table, int64_t table_stride,
                 int64_t table_width, const int32_t* lens, int64_t n_seq, int64_t n_q_heads, float scale, int64_t window,
                 const il_kv_score* score, const float* lse, const int32_t* add, const float* weights, float* weights_out,
-                int64_t weights_stride, int64_t weights_width, void* stream) {
+                int64_t weights_stride, int64_t weights_width, void* stream) try {
   const char* fn = "il_kv_weigh";
   NvtxRange range(fn);
   api_clear_error();
@@ -403,12 +418,13 @@ int il_kv_weigh(const il_kv* kv, const float* q, int64_t q_stride, const int32_t
   w.weights_width = weights_width;
   const int64_t bytes = 4 * ((n_seq - 1) * w.weights_stride + weights_width);
   const Range o{weights_out, bytes, true};
-  std::vector<Range> ins = ranges_of(a);
-  ins.push_back({lse, 4 * n_seq * n_q_heads, false});
-  ins.push_back({add, 4 * n_seq, false});
-  if (weights != weights_out) ins.push_back({weights, bytes, false});
-  for (const Range& i : ins)
-    if (clash(o, i)) return bad(IL_ERR_ARG, fn, "weights_out must not overlap an input, but for weights itself");
+  const Range more[] = {{lse, 4 * n_seq * n_q_heads, false},
+                        {add, 4 * n_seq, false},
+                        {weights == weights_out ? nullptr : weights, bytes, false}};
+  bool apart = true;
+  for (const Range& i : ranges_of(a).r) apart &= !clash(o, i);
+  for (const Range& i : more) apart &= !clash(o, i);
+  if (!apart) return bad(IL_ERR_ARG, fn, "weights_out must not overlap an input, but for weights itself");
   int num_sms = 0;
   const int dev = api_device(&num_sms, &a.status);
   if (dev < 0) return dev;
@@ -417,13 +433,15 @@ int il_kv_weigh(const il_kv* kv, const float* q, int64_t q_stride, const int32_t
   const cudaError_t e = prepare_kv_weigh(w, num_sms, &L);
   if (e != cudaSuccess) return api_cuda_fail(e, fn);
   return enqueue(fn, L, stream);
+} catch (const std::bad_alloc&) {  // of the launch lists
+  return api_cuda_fail(cudaErrorMemoryAllocation, "il_kv_weigh");
 }
 
 int il_kv_evict(const il_kv* kv, const int32_t* table, int64_t table_stride, int64_t table_width, const int32_t* lens,
                 int64_t n_seq, int64_t keep, int64_t first, int64_t recent, const float* weights, float* weights_out,
                 int64_t weights_stride, int64_t weights_width, const int32_t* positions, int32_t* positions_out,
                 int64_t positions_stride, int64_t positions_width, int32_t* kept, int64_t kept_stride, int32_t* drop,
-                void* stream) {
+                void* stream) try {
   const char* fn = "il_kv_evict";
   NvtxRange range(fn);
   api_clear_error();
@@ -469,20 +487,21 @@ int il_kv_evict(const il_kv* kv, const int32_t* table, int64_t table_stride, int
   const int64_t wb = 4 * ((n_seq - 1) * a.weights_stride + weights_width);
   const int64_t pb = positions == nullptr ? 0 : 4 * ((n_seq - 1) * a.positions_stride + positions_width);
   // the cache is read and written; weights and positions may be their own outputs
-  const std::vector<Range> rs = {{kept, 4 * ((n_seq - 1) * a.kept_stride + keep), true},
-                                 {drop, 4 * n_seq, true},
-                                 {weights_out, wb, true},
-                                 {positions_out, pb, true},
-                                 {a.kv.k, extent_bytes(a.kv, false), true},
-                                 {a.kv.v, extent_bytes(a.kv, false), true},
-                                 {a.kv.k_scale, extent_bytes(a.kv, true), true},
-                                 {a.kv.v_scale, extent_bytes(a.kv, true), true},
-                                 {weights == weights_out ? nullptr : weights, wb, false},
-                                 {positions == positions_out ? nullptr : positions, pb, false},
-                                 {table, 4 * ((n_seq - 1) * a.table_stride + table_width), false},
-                                 {lens, 4 * n_seq, false}};
-  for (size_t i = 0; i < rs.size(); ++i)
-    for (size_t j = i + 1; j < rs.size(); ++j) {
+  const Range rs[] = {{kept, 4 * ((n_seq - 1) * a.kept_stride + keep), true},
+                      {drop, 4 * n_seq, true},
+                      {weights_out, wb, true},
+                      {positions_out, pb, true},
+                      {a.kv.k, extent_bytes(a.kv, false), true},
+                      {a.kv.v, extent_bytes(a.kv, false), true},
+                      {a.kv.k_scale, extent_bytes(a.kv, true), true},
+                      {a.kv.v_scale, extent_bytes(a.kv, true), true},
+                      {weights == weights_out ? nullptr : weights, wb, false},
+                      {positions == positions_out ? nullptr : positions, pb, false},
+                      {table, 4 * ((n_seq - 1) * a.table_stride + table_width), false},
+                      {lens, 4 * n_seq, false}};
+  const int n_ranges = (int)(sizeof rs / sizeof rs[0]);
+  for (int i = 0; i < n_ranges; ++i)
+    for (int j = i + 1; j < n_ranges; ++j) {
       // K and V (and their scales) may be interleaved in one buffer
       const bool pools = i >= 4 && j <= 7;
       if (!pools && clash(rs[i], rs[j])) return bad(IL_ERR_ARG, fn, "the outputs and the cache must not overlap each other or an input");
@@ -497,6 +516,8 @@ int il_kv_evict(const il_kv* kv, const int32_t* table, int64_t table_stride, int
     e = run_launches(launches, static_cast<cudaStream_t>(stream), &n);
   }
   return e == cudaSuccess ? IL_OK : api_cuda_fail(e, fn);
+} catch (const std::bad_alloc&) {  // of the launch lists
+  return api_cuda_fail(cudaErrorMemoryAllocation, "il_kv_evict");
 }
 
 }  // extern "C"

@@ -74,6 +74,17 @@ def test_scores_are_refused(libil):
     assert call(n=0, cap=2.0) == {0}   # a no-op
 
 
+@pytest.mark.parametrize("cap,scale", [(1e31, 1.0), (3e38, 1.0), (3e38, 1e30), (7e-31, 1.0), (1e-45, 1e-45)])
+def test_caps_beyond_fp32_are_refused(libil, cap, scale):
+    """cap log2(e), or q scale / cap, would be infinite or lose bits where the logit is an ordinary number."""
+    import shared_input_linear_gb300 as sil
+    kv, score = _kv(), sil._Score(cap, None, None, None, 0, 0)
+    p, c = ctypes.addressof(kv), ctypes.addressof(score)
+    assert libil.il_kv_attend_scored(p, 16, 128, 4, 1, 1, 4, 2, 2, scale, 0, c, 1 << 16, 128, None, None) == -1
+    assert libil.il_kv_weigh(p, 16, 128, 4, 1, 1, 4, 2, 2, scale, 0, c, 4, None, 1 << 25, 1 << 25, 64, 64, None) == -1
+    assert b"cap" in libil.il_last_error()
+
+
 def test_weigh_and_evict_are_refused(libil):
     kv = _kv()
     p = ctypes.addressof(kv)
