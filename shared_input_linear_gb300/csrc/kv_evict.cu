@@ -2,12 +2,11 @@
 //
 // Of n > keep tokens the first, the recent and the heaviest stay.  Those of them at `keep` and behind (movers) go to the places
 // of those before it that do not (holes), the i-th mover to the i-th hole: there are as many of either, no row is both read
-// of those before it that do not (holes), the i-th mover to the i-th hole: there are as many of either, no row is both read
 // and written, and what need not move stays.  A compaction in order would move nearly every row.
 //
-// Measured (GB300, 8 heads of 128, device time): 64 sequences of 1025 bf16 tokens cut to 1024 8.3 us; one of 32768 cut to 4096 21.5 us, of
-// which about 14 choose (8 CTAs, by time stamps: load 1.6, the bar 6.4, movers and holes 2.2, their list 1.4, entries 2.8) and
-// 8 move 3584 rows (29 MB read and written); 32 of 500 to 8192 Q8 tokens cut to 2048 about 45 us.
+// Measured (GB300, 8 heads of 128, device time): 64 sequences of 1025 bf16 tokens cut to 1024 8.4 us; one of 32768 cut to 4096
+// 18.2 us, of which about 12 choose (8 CTAs: barriers of the cluster, exchanges, L2 latencies) and 6 move 3584 rows (29 MB
+// read and written); 32 of 500 to 8192 Q8 tokens cut to 2048 about 45 us.
 #include <algorithm>
 #include <atomic>
 
@@ -57,9 +56,10 @@ __device__ __forceinline__ Place place_of(const KvEvictArgs& a, const Rows& R, i
           page < (uint32_t)a.kv.n_pages};
 }
 
-// K and V of all heads, 16 bytes a lane of the warp, and the scales, 4 bytes a lane, from f, sf to t, st: all loads before the stores
-// where a token has up to 64 chunks.
-__device__ __forceinline__ void copy_token(const KvView& kv, const Rows& R, long long t, long long f, long long st, long long sf, int lane) {
+// K and V of all heads, 16 bytes a lane of the warp, and the scales, 4 bytes a lane, from f, sf to t, st: all loads before the
+// stores where a token has up to 64 chunks.
+__device__ __forceinline__ void copy_token(const KvView& kv, const Rows& R, long long t, long long f, long long st, long long sf,
+                                           int lane) {
   long long soff = 0;  // of the lane's first scale
   float ks = 0.f, vs = 0.f;
   if (lane < R.scales) {
@@ -99,11 +99,11 @@ __device__ __forceinline__ void copy_token(const KvView& kv, const Rows& R, long
   }
 }
 
-// The choice, in both kernels below: the keep-th largest key digit by digit, from the highest (a histogram of the keys that match so
-// far); among equal keys those of the lowest index, up to the last one taken; then the list of movers, which is put at the
-// end of the sequence's row of `kept`; then the entries from it.  Of the list's M places the j-th lies behind the j-th hole, and an entry
-// that is no hole lies before every place that a later hole needs: filling the entries in order, each read before it is
-// written, loses nothing.
+// The choice, in both kernels below: the keep-th largest key digit by digit, from the highest (a histogram of the keys that
+// match so far); among equal keys those of the lowest index, up to the last one taken; then the list of movers, which is put
+// at the end of the sequence's row of `kept`; then the entries from it.  Of the list's M places the j-th lies at the j-th hole
+// or behind it, and an entry that is no hole lies before every place that a later hole needs: filling the entries in order,
+// each read before it is written, loses nothing.
 
 // Any length: a CTA a sequence, keys computed again in each pass.
 __global__ void __launch_bounds__(kThreads) kv_choose_long_kernel(const KvEvictArgs a) {
@@ -246,11 +246,12 @@ __global__ void __launch_bounds__(kThreads) kv_choose_long_kernel(const KvEvictA
   }
 }
 
-// Up to kMostKeys tokens a CTA: a cluster of 1 to 8 CTAs a sequence, the CTA of rank c with the c-th run of its tokens and their
-// keys in shared memory, read once.  Bound by latency (barriers, and 12 bytes a token from a few SMs): three passes of 11, 11 and 10
-// bits, whose histograms a warp of every CTA adds up through distributed shared memory, first sums of 32 bins, then the 32 bins that the
-// digit is among (all 2048 in each CTA took 1 to 1.5 us more a pass), and one exchange of the numbers of movers and holes.
-// Where no more than kFewRows rows of a sequence can move it moves them too, and there is no second launch.
+// Up to kMostKeys tokens a CTA: a cluster of 1 to 8 CTAs a sequence, the CTA of rank c with the c-th run of its tokens and
+// their keys in shared memory, read once.  Bound by latency (barriers, and 12 bytes a token from a few SMs): up to three passes
+// of 11, 11 and 10 bits (the last ones are left where all of a bin stay), whose histograms a warp of every CTA adds up
+// through distributed shared memory, first sums of 32 bins, then the 32 bins that the digit is among (all 2048 in each CTA took
+// 1 to 1.5 us more a pass), and one exchange of the numbers of movers and holes.  Where no more than kFewRows rows of a
+// sequence can move it moves them too, and there is no second launch.
 template <int CTAS, bool MOVE>
 __global__ void __launch_bounds__(kThreads) kv_choose_kernel(const KvEvictArgs a, const Rows R) {
   extern __shared__ uint32_t s_keys[];
@@ -519,9 +520,11 @@ __global__ void __launch_bounds__(kThreads) kv_choose_kernel(const KvEvictArgs a
 }
 
 constexpr int kMoveThreads = 256;
+constexpr int kMoveCtas = 4;  // an SM
 
-// The rows, a warp an entry; a lane looks up one of the warp's next 32 entries.  Bound by HBM where many rows move.
-__global__ void __launch_bounds__(kMoveThreads, 6) kv_move_kernel(const KvEvictArgs a, const Rows R) {
+// The rows, a warp an entry; a lane looks up one of the warp's next 32 entries.  Bound by HBM where many rows move.  Four CTAs an
+// SM, all at once: with six (40 registers, which spill) 3584 of 4096 rows took 2.2 us more, with five 0.5, with three 1.6.
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtas) kv_move_kernel(const KvEvictArgs a, const Rows R) {
   const int lane = threadIdx.x & 31;
   const long long warps = (long long)gridDim.x * (kMoveThreads / 32), total = (long long)a.n_seq * a.keep;
   grid_dep_launch();
@@ -554,7 +557,8 @@ namespace {
 
 template <int CTAS>
 const void* choose_fn(bool move) {
-  return move ? reinterpret_cast<const void*>(kv_choose_kernel<CTAS, true>) : reinterpret_cast<const void*>(kv_choose_kernel<CTAS, false>);
+  return move ? reinterpret_cast<const void*>(kv_choose_kernel<CTAS, true>)
+              : reinterpret_cast<const void*>(kv_choose_kernel<CTAS, false>);
 }
 
 }  // namespace
@@ -573,7 +577,8 @@ cudaError_t prepare_kv_evict(const KvEvictArgs& a, int num_sms, std::vector<Laun
   Launch& choose = (*out)[0];
   choose.block = dim3(kThreads);
   const bool any_length = a.cap > kMostCtas * kMostKeys;
-  // A sequence's own CTAs move its rows where few can move: one launch less (64 sequences of 1025 tokens cut to 1024: 12.5 -> 7.9 us)
+  // A sequence's own CTAs move its rows where few can move: one launch less (64 sequences of 1025 tokens cut to 1024: 12.5 ->
+  // 7.9 us)
   const bool move = !any_length && a.cap - a.keep <= kFewRows;
   if (any_length) {
     choose.fn = reinterpret_cast<const void*>(kv_choose_long_kernel);
@@ -605,7 +610,7 @@ cudaError_t prepare_kv_evict(const KvEvictArgs& a, int num_sms, std::vector<Laun
   Launch& rows = (*out)[1];
   rows.fn = reinterpret_cast<const void*>(kv_move_kernel);
   const int64_t entries = (int64_t)a.n_seq * a.keep, per_cta = kMoveThreads / 32;
-  rows.grid = dim3((unsigned)std::min<int64_t>((entries + per_cta - 1) / per_cta, (int64_t)num_sms * 8));
+  rows.grid = dim3((unsigned)std::min<int64_t>((entries + per_cta - 1) / per_cta, (int64_t)num_sms * kMoveCtas));
   rows.block = dim3(kMoveThreads);
   if (!rows.set_args(a, R)) return cudaErrorMemoryAllocation;
   if (kUsePdl) rows.allow_early_start();
