@@ -602,7 +602,8 @@ def kv_weigh(cache: KVCache, q, table, lens, lse, weights, weights_out=None, add
     rc = (_lib or load()).il_kv_weigh(cache._ref, qp, qs, tp, ts, tw, _ptr(lens, i32, n, "lens"), n, heads,
                                       dim ** -0.5 if scale is None else scale, window,
                                       0 if score is None else ctypes.addressof(score), _ptr(lse, f32, n * heads, "lse"),
-                                      _ptr(add, i32, n, "add"), *_in_out(weights, weights_out, n, f32, "weights"), _stream_ptr(stream))
+                                      _ptr(add, i32, n, "add"), *_in_out(weights, weights_out, n, f32, "weights"),
+                                      _stream_ptr(stream))
     if rc:
         _check(rc)
 

@@ -6,12 +6,14 @@
 // times as large: x keeps 22 bits down to 2^-27 of the largest and is cut at 2^-49 of it.  With four heads a K/V head nothing of
 // an MMA is idle, a lane's accumulators are of one head (that of column pair q4 = lane % 4), and a softmax value is in one lane.
 //
-// Decoding K costs 5 instructions for 8 elements: nibbles at bits 0-3 and 4-7 of a 16-bit half are fp16 subnormals as they
-// stand, u 2^-24 and 16 u 2^-24, exactly; one shift brings the other two there.  The factor 16 is taken from q.  d multiplies a
-// block's fp32 sum; the m of four blocks meet the sums of q over them, three bf16 parts each, in one MMA.  V is taken as d (u - 8) + (m + 8 d), d multiplying p: sums of d u and
-// of m over many tokens would each be far larger than the sum of V, and the MMAs' accumulators, which cut, lose it (1e-5 of the
-// result for 512 tokens; 6e-6 with sums that start at -8 times the weights').  u - 8 costs 9 instructions for 8
-// elements, the sum of p (m + 8 d) 8 FMAs for 16 tokens.
+// Decoding K costs 6 instructions for 8 elements: nibbles at bits 2-5 and 6-9 of a 16-bit half are fp16 subnormals, 4 u 2^-24
+// and 64 u 2^-24, exactly; two shifts bring all four there.  The factor 16 is taken from q.  (One shift would do for bits 0-3 and
+// 4-7, but the MMAs line products up by the exponents as written and cut 25 bits below the largest: what subnormals lead with in
+// zeros is lost.  A logit was off by 1e-6, now by 3e-7; higher bits gain nothing more, since q has 22.)  d multiplies a
+// block's fp32 sum; the m of four blocks meet the sums of q over them, three bf16 parts each, in one MMA.
+// V is taken as d (u - 8) + (m + 8 d), d multiplying p: sums of d u and of m over many tokens would each be far larger than the
+// sum of V, and lose it (1e-5 of the result for 512 tokens; 6e-6 with sums that start at -8 times the weights').  u - 8
+// costs 9 instructions for 8 elements, the sum of p (m + 8 d) 8 FMAs for 16 tokens.
 #pragma once
 
 #include "il_internal.cuh"
@@ -38,13 +40,13 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   return r;
 }
 
-// Nibbles 0, 1, 2, 3 of both halves of w, as fp16 pairs of u 2^-24 (even) and 16 u 2^-24 (odd).
+// Nibbles 0, 1, 2, 3 of both halves of w, as fp16 pairs of u 2^-22 (even) and 16 u 2^-22 (odd).
 __device__ __forceinline__ void nibbles(uint32_t w, uint32_t (&p)[4]) {
-  p[0] = w & 0x000f000fu;
-  p[1] = w & 0x00f000f0u;
-  w >>= 8;
-  p[2] = w & 0x000f000fu;
-  p[3] = w & 0x00f000f0u;
+  const uint32_t low = w << 2, high = w >> 6;
+  p[0] = low & 0x003c003cu;
+  p[1] = low & 0x03c003c0u;
+  p[2] = high & 0x003c003cu;
+  p[3] = high & 0x03c003c0u;
 }
 
 // The same nibbles as fp16 pairs of u - 8: the bits 64uu are 1024 + u, 6400 + 16 u are 1024 + 16 u.
@@ -54,7 +56,9 @@ __device__ __forceinline__ void nibbles_less_8(uint32_t w, uint32_t (&p)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint32_t u;  // (w & mask) | 0x64006400
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(u) : "r"(i < 2 ? w : w >> 8), "r"(i % 2 == 0 ? 0x000f000fu : 0x00f000f0u), "r"(0x64006400u));
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
+        : "=r"(u)
+        : "r"(i < 2 ? w : w >> 8), "r"(i % 2 == 0 ? 0x000f000fu : 0x00f000f0u), "r"(0x64006400u));
     const __half2 h = *reinterpret_cast<const __half2*>(&u);
     const __half2 v = i % 2 == 0 ? __hadd2(h, low) : __hfma2(h, sixteenth, high);
     p[i] = *reinterpret_cast<const uint32_t*>(&v);
@@ -127,12 +131,14 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
 }
 
 // Query heads of 4 R columns as B operands, scaled so that the largest of a head becomes 2^13 .. 2^14.
-template <int NB, int R>
+// FMAS: m by FMAs, 2 NB a head block, and not by an MMA.  What is faster depends on the kernel around it: il_kv_weigh, 64 ragged
+// sequences, 45.7 us (by MMA 47.4), il_kv_attend 93.7 (93.1), two blocks of 4 heads 122.7 (117.3).
+template <int NB, int R, bool FMAS = false>
 struct Query {
   uint32_t f[R][4 * NB];  // of head 4 r + g / 2, its hi (g even) or lo part: elements 8 q4 .. 8 q4 + 7 of each block
-  // The sums over the blocks, in the products' unit, as a B operand whose rows are the same four blocks' times three bf16 parts (in the
-  // lanes of a quad; hi's column only): blocks 4 i, 4 i + 1 in [2 i], and the next two
-  uint32_t sum[R][(NB + 1) / 2];
+  // The sums over the blocks, in the products' unit.  FMAS: of head 4 r + q4.  Else as a B operand whose rows are the same four
+  // blocks' times three bf16 parts (in the lanes of a quad; hi's column only): blocks 4 i, 4 i + 1 in [2 i], and the next two
+  uint32_t sum[R][FMAS ? NB : (NB + 1) / 2];
   float back[R][2];       // of head 4 r + q4: the unit, as two factors
 
   // Elements x[b][0 .. 7] = 8 q4 .. of block b, of head 4 r + g / 2; `top`: their largest magnitude over the whole head.
@@ -154,25 +160,30 @@ struct Query {
       }
       total += __shfl_xor_sync(~0u, total, 1);
       total += __shfl_xor_sync(~0u, total, 2);
-      total *= 5.9604644775390625e-08f;  // 2^-24
-      float part = 0.f;                  // hi, mid or lo of it
+      total *= 2.384185791015625e-07f;  // 2^-22
+      if constexpr (FMAS) {
+        sum[r][b] = __float_as_uint(__shfl_sync(~0u, total, head_lane));
+      } else {
+        float part = 0.f;  // hi, mid or lo of it
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const float p = __bfloat162float(__float2bfloat16_rn(total));
-        if (k == q4) part = p;
-        total -= p;
+        for (int k = 0; k < 3; ++k) {
+          const float p = __bfloat162float(__float2bfloat16_rn(total));
+          if (k == q4) part = p;
+          total -= p;
+        }
+        const uint32_t bits = lo_part ? 0u : __float_as_uint(part);
+        sum[r][b / 2] = b % 2 == 0 ? bits >> 16 : sum[r][b / 2] | bits;
       }
-      const uint32_t bits = lo_part ? 0u : __float_as_uint(part);
-      sum[r][b / 2] = b % 2 == 0 ? bits >> 16 : sum[r][b / 2] | bits;
     }
-    const int unit = __shfl_sync(~0u, e, head_lane) - 116, half = unit >> 1;  // 2^unit = 2^24 / up
+    const int unit = __shfl_sync(~0u, e, head_lane) - 118, half = unit >> 1;  // 2^unit = 2^22 / up
     back[r][0] = __int_as_float((half + 127) << 23);
     back[r][1] = __int_as_float((unit - half + 127) << 23);
   }
 
   // s[r][h]: the product of head 4 r + q4 with token 8 h + g of 16, whose rows of K are at `tile` and steps at `steps`;
   // chunks[i]: where the lane's row of blocks 2 i and 2 i + 1 for ldmatrix lies from there, chunk_at(lane % 16, 2 i + lane / 16).
-  __device__ __forceinline__ void dot(float (&s)[R][2], uint32_t tile, uint32_t steps, const uint32_t (&chunks)[NB / 2], int lane) const {
+  __device__ __forceinline__ void dot(float (&s)[R][2], uint32_t tile, uint32_t steps, const uint32_t (&chunks)[NB / 2],
+                                      int lane) const {
     const int g = lane >> 2;
     uint32_t d[2][NB];
     load_steps<NB>(d[0], steps + g * (4 * NB));
@@ -180,11 +191,20 @@ struct Query {
     auto pair = [&](int t, int b) { return b < NB ? __byte_perm(d[t][b], d[t][b + 1], 0x7632) : 0u; };  // {m, m}
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float c[4] = {0.f, 0.f, 0.f, 0.f};
+      if constexpr (FMAS) {
 #pragma unroll
-      for (int b = 0; b < NB; b += 4)
-        mma_bf16(c, pair(0, b), pair(1, b), pair(0, b + 2), pair(1, b + 2), sum[r][b / 2], b + 2 < NB ? sum[r][b / 2 + 1] : 0u);
-      s[r][0] = c[0], s[r][1] = c[2];
+        for (int t = 0; t < 2; ++t) {
+          s[r][t] = 0.f;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) s[r][t] = fmaf(__uint_as_float(sum[r][b]), least_of(d[t][b]), s[r][t]);
+        }
+      } else {
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int b = 0; b < NB; b += 4)
+          mma_bf16(c, pair(0, b), pair(1, b), pair(0, b + 2), pair(1, b + 2), sum[r][b / 2], b + 2 < NB ? sum[r][b / 2 + 1] : 0u);
+        s[r][0] = c[0], s[r][1] = c[2];
+      }
     }
 #pragma unroll
     for (int i = 0; i < NB / 2; ++i) {
@@ -227,7 +247,8 @@ __device__ __forceinline__ void bytes_of_pairs(uint32_t w, uint32_t& even, uint3
 // the 128 are taken off by where the sums start.
 template <int NB, int R>
 struct Query8 {
-  uint32_t f[R][4 * NB];  // of head 4 r + g / 2, its hi or lo part: of 16-element chunk i elements 4 q4, 4 q4 + 1 in [2 i], the next two
+  // Of head 4 r + g / 2, its hi or lo part: of 16-element chunk i elements 4 q4, 4 q4 + 1 in [2 i], then the next two
+  uint32_t f[R][4 * NB];
   float start[R][NB];     // of head 4 r + q4: -128 times the sum over a block, in the products' unit
   float back[R][2];
 

@@ -18,9 +18,9 @@
 // Stream.  Every warp owns a ring of stages, one tile of K and V each, filled with 16-byte
 // cp.async (any strides, any page size: a lane looks up its token's page one tile ahead) and zeros for
 // tokens outside the attended range.  Where pages hold whole groups of 16 tokens their addresses are one base and
-// constants of the lane (A4: any pages, offsets of 32 bits that the lanes hand to one another).  No barrier other than the
-// warp's own sits in the stream.  A head of more than 128 elements takes a pair of warps, half of its columns each: they trade their halves of s
-// through shared memory, with a barrier of the two.
+// constants of the lane (heads in columns: any pages, offsets of 32 bits that the lanes hand to one another).  No barrier
+// other than the warp's own sits in the stream.  A head of more than 128 elements takes a pair of warps, half of its columns
+// each: they trade their halves of s through shared memory, with a barrier of the two.
 //
 // Arithmetic.  Query heads are the rows of m16n8k16 MMAs and tokens (then elements of V) the
 // columns; a softmax row lives in the four lanes of a quad.  q and p are fp32 and are split
@@ -31,8 +31,9 @@
 // split costs one more MMA at bf16 and none at int8; with 9 to 16 heads (R = 2) every part is an MMA
 // of its own.  p V is computed transposed: the quad layout of s is that of a B operand, so p goes in as it is.
 // Each tile's product starts from zero accumulators and joins the running sum in fp32
-// FMAs (with the factor of the running maximum), which round to nearest.  A4 has the operands the other way round, query heads in
-// the columns (kv_a4.cuh), because its tiles are bound by instructions: 845 for 32 tokens of 128 columns, the loop and copies included.
+// FMAs (with the factor of the running maximum), which round to nearest.  A4, and Q8 where it is scored, have the operands
+// the other way round, query heads in the columns (kv_a4.cuh), because their tiles are bound by instructions: 875 of A4 for
+// 32 tokens of 128 columns, the loop and copies included.
 //
 // Scored (il_kv_attend_scored): logits are capped and biased between the two products, and a row may begin at a later token.
 // The plain kernels have none of it.
@@ -40,10 +41,12 @@
 // Measured (GB300, 32 query heads on 8 K/V heads of 128, device time): bf16, 128 sequences of 4096 tokens 315 us, 6.8 TB/s
 // (the rate of a plain copy); 32 of 0 to 8192 86 us, 6.0 TB/s; one of 512 8.1 us.  Q8, 64 of 1 to 8192 106 us, 5.6 TB/s,
 // one of 131071 59 us, 5.2 TB/s.  What bounds it: HBM at bf16 (64 sequences of 8192: 317 us, 263 us with pages that stay in
-// L2); A4, 64 of 1 to 8192 (another draw, 316,517 tokens) 94 us, 4.3 TB/s, one of 131071 45 us, one of 512 9.2 us: instructions (issue slots
-// 63 % used, ALU 52 %, tensor pipe 20 %, DRAM 54 %); at Q8 no unit (207 us either way; issue slots 50 % used, ALU 44 %, tensor pipe
-// 27 %, DRAM 65 %) but the chain of a tile in a warp -- q K^T, maximum, exp2, split, p V -- at two warps a scheduler, about 520 instructions per 16 tokens; of
-// a short call the latencies before the first tile and in the joins.
+// L2); A4, 64 of 1 to 8192 (another draw, 316,517 tokens) 94 us, 4.4 TB/s, one of 131071 45 us, one of 512 9.0 us:
+// instructions (issue slots 64 % used, ALU 54 %, tensor pipe 20 %, DRAM 53 %); at Q8 no unit (207 us either way; issue slots
+// 50 % used, ALU 44 %, tensor pipe 27 %, DRAM 65 %) but the chain of a tile in a warp -- q K^T, maximum, exp2, split, p V -- at
+// two warps a scheduler, about 520 instructions per 16 tokens; of a short call the latencies before the first tile and in
+// the joins.  Scored: bf16, 16 of 1000 to 16384 under a window of 4096, 16 heads of 256 on 8, 83 us, 5.7 TB/s; Q8, 32 of up to
+// 4096, 32 heads on 32, 61 us, 3.8 TB/s.
 #pragma once
 
 #include <algorithm>
@@ -97,7 +100,8 @@ struct Config {
   static constexpr int kPool = kTile * kRowBytes;                      // K or V of a tile
   static constexpr int kScales = F != IL_BF16 ? kTile * kBlocks * 4 : 0;  // its scales
   static constexpr int kStage = 2 * (kPool + kScales);
-  // (A4: measured with 8, 12 and 16 warps, 64 ragged sequences, heads of 128 as they were then: 116, 102, 137 us; of 64: 133, 112, 97 us)
+  // (A4, measured with 8, 12 and 16 warps, 64 ragged sequences as the kernel was then: heads of 128 116, 102, 137 us, of 64
+  // 133, 112, 97 us)
   static constexpr int kWarps = kA4 ? (R == 2 ? (W == 64 ? 12 : 8) : W == 64 ? 16 : 12) : F != IL_BF16 && R == 1 && W == 64 ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kWorkers = kWarps / H;    // runs of tiles in a CTA
@@ -313,10 +317,11 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
   using C = Config<F, W, R, H>;
   constexpr bool Q8 = C::kQ8, A4 = C::kA4, COLS = C::kCols, BLOCKED = F != IL_BF16;  // scales of 32 elements
   constexpr int NV = C::kValues;
-  // Empty tiles before each row's, for what its start and end cost beside its tiles (q, parts, result).  One: 1024 biased Q8 rows of 1
-  // to 108 tiles 78.9 -> 60.5 us (two 61.5, four 65.3), 64 ragged A4 sequences 94.0 -> 93.4, 256 of 50 to 150 tokens 20.8 -> 19.9.  Not
-  // where rows of few bytes or pairs of warps lose: A4 heads of 64 90.3 -> 94.4, capped heads of 256 83.0 -> 84.0.
-  constexpr int LEAD = H == 1 && (SCORED || (A4 && W == 128)) ? 1 : 0;  // (a pair of warps meets at every tile's barrier: none may be empty)
+  // Empty tiles before each row's, for what its start and end cost beside its tiles (q, parts, result).  One: 1024 biased Q8
+  // rows of 1 to 108 tiles 78.9 -> 60.5 us (two 61.5, four 65.3), 64 ragged A4 sequences 94.0 -> 93.4, 256 of 50 to 150
+  // tokens 20.8 -> 19.9.  Not where rows of few bytes or pairs of warps lose: A4 heads of 64 90.3 -> 94.4, capped heads of
+  // 256 83.0 -> 84.0.  (A pair of warps meets at every tile's barrier: none of its tiles may be empty.)
+  constexpr int LEAD = H == 1 && (SCORED || (A4 && W == 128)) ? 1 : 0;
   constexpr int T = C::kTile, NN = T / 8, GR = T / kGroup;  // tokens of a tile, in eights, in groups
   constexpr int NB = C::kBlocks, NT = C::kThreads, NW = C::kWarps, NK = C::kWorkers, S = C::kStages, ROWS = C::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -461,7 +466,8 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
     auto token_of = [&](const Walk& w) { return (w.q.first + w.tile - LEAD) * T + (lane & (T - 1)); };
     auto empty = [&](const Walk& w) { return LEAD > 0 && w.tile < LEAD; };
     auto column_of = [&](uint32_t t) { return P.by_page.of(t); };
-    // Heads in columns: of the tile to be copied next, this lane's token's place in its page (units of `fetch` below), and which tokens are wanted
+    // Heads in columns: of the tile to be copied next, this lane's token's place in its page (units of `fetch` below),
+    // and which tokens are wanted
     uint32_t in_page_off = 0, in_page_soff = 0, wanted = 0;
     auto page_of = [&](const Walk& w) {  // page of this lane's token of the tile (of 16 tokens, lanes 16-31 repeat 0-15)
       const uint32_t t = token_of(w);
@@ -617,7 +623,9 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const int in_group = at.block * ROWS + (COLS ? 4 * r + q4 : 8 * r + g);
-          slope[r] = a.slopes != nullptr && in_group < P.group ? a.slopes[(int64_t)at.hk * P.group + in_group] * 1.4426950408889634f : 0.f;
+          slope[r] = a.slopes != nullptr && in_group < P.group
+                         ? a.slopes[(int64_t)at.hk * P.group + in_group] * 1.4426950408889634f
+                         : 0.f;
         }
         newest = a.positions != nullptr ? a.positions[at.s * a.positions_stride + at.q.len - 1] : (int)at.q.len - 1;
       }
@@ -745,7 +753,8 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
       }
       const uint32_t from = ring + stage * C::kStage;
 
-      // ---- s = q K^T: s[r][2 nt + c] of head row g + 8 r, token 8 nt + 2 q4 + c (in columns: s[r][c] of head 4 r + q4, token 8 c + g)
+      // ---- s = q K^T: s[r][2 nt + c] of head row g + 8 r, token 8 nt + 2 q4 + c (in columns: s[r][c] of head 4 r + q4,
+      // token 8 c + g)
       float s[R][NV];
       auto token_at = [&](int c) { return COLS ? 8 * c + g : 8 * (c / 2) + 2 * q4 + c % 2; };
       if ((H == 1 || i >= 0) && !empty(at)) {
@@ -1048,7 +1057,8 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
               for (int k = 0; k < GR; ++k)
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                  a4::split2(a4::mul2(make_float2(ps[r][2 * k], ps[r][2 * k + 1]), make_float2(d[2 * k], d[2 * k + 1])), w[k][r][0], w[k][r][1]);
+                  a4::split2(a4::mul2(make_float2(ps[r][2 * k], ps[r][2 * k + 1]), make_float2(d[2 * k], d[2 * k + 1])),
+                             w[k][r][0], w[k][r][1]);
                   w[k][r][0] = a4::movmatrix(w[k][r][0]);
                   w[k][r][1] = a4::movmatrix(w[k][r][1]);
                 }

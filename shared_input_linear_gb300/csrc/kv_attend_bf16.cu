@@ -12,12 +12,13 @@ namespace {
 
 int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
-// Whether query heads are in the MMAs' columns: A4, and Q8 with scores (one query head a K/V head, biased: with 8 rows for it 85 us, in
-// columns below).  Plain Q8 keeps the order that its bits came from.
+// Whether query heads are in the MMAs' columns: A4, and Q8 with scores (one query head a K/V head, biased, 32 sequences
+// of up to 4096 tokens: with 8 rows for it 85.4 us, in columns 78.6).  Plain Q8 keeps the order that its bits came from.
 bool in_columns(const KvAttendArgs& a) { return a.kv.format == IL_A4 || (a.kv.format == IL_Q8 && a.scored); }
 
-// Blocks of 8 (in columns: 4) query heads that a warp takes at once.  In columns 8 heads at most, of which K and V of larger groups are read again, from
-// L2; with 16 the sums do not fit the registers (128 heads on 8 of 128, 32 sequences of 4096: 143 us, two blocks of 8 117 us).
+// Blocks of 8 (in columns: 4) query heads that a warp takes at once.  In columns 8 heads at most: larger groups read K and V
+// again, from L2, where 16 heads' sums would not fit the registers (128 heads on 8 of 128, 32 sequences of 4096: 143 us,
+// two blocks of 8 117 us).
 int head_blocks(const KvAttendArgs& a) {
   const int group = a.n_q_heads / a.kv.n_heads;
   return group > (in_columns(a) ? 4 : 8) ? 2 : 1;

@@ -5,23 +5,23 @@
 // K is read once and V not at all; the sum over the heads of a token is made where its K is, so that nothing but 8 bytes a
 // token goes beside K.
 //
-// Measured (GB300, 32 query heads on 8 K/V heads of 128, device time): 64 sequences of 1 to 8192 tokens bf16 115 us, 5.7 TB/s, Q8 76 us,
-// 4.9 TB/s, A4 56 us, 3.7 TB/s; one of 131071 A4 25 us; one of 2048 bf16 9.0 us.  What bounds it: HBM at bf16; at A4 instructions
-// (410 for 32 tokens of a K/V head, issue slots 55 % used, ALU 48 %) and what the CTAs lose at the ends of pieces; of a short call the
-// latencies before the first tile.
+// Measured (GB300, 32 query heads on 8 K/V heads of 128, device time): 64 sequences of 1 to 8192 tokens bf16 104 us, 6.3 TB/s,
+// Q8 66 us, 5.6 TB/s, A4 51 us, 4.1 TB/s; one of 131071 A4 24 us; one of 2048 bf16 6.3 us.  What bounds it: HBM at bf16; at A4
+// instructions (343 for 32 tokens of a K/V head, issue slots 62 % used, ALU 52 %) and what the CTAs lose at the ends of pieces;
+// of a short call the latencies before the first tile.
 //
-// Work.  Tiles of 32 tokens (16 of bf16 heads above 128) of all sequences form one list, of which every CTA takes an equal run.  A run's
-// piece of one sequence is worked off by the CTA's warps, a tile each at a time, over all K/V heads; of the last tiles of a piece,
-// fewer than the warps, each is shared by several warps that take every second, fourth or eighth head, and whose sums are added in
-// order.  Which warp does what depends on the lengths alone: equal calls give equal bits.
+// Work.  Tiles of 32 tokens (16 of bf16 heads above 128) of all sequences form one list, of which every CTA takes an equal
+// run.  A run's piece of one sequence is worked off by the CTA's warps, a tile each at a time, over all K/V heads; of the last
+// tiles of a piece, fewer than the warps, each is shared by several warps that take every second, fourth or eighth head, and
+// whose sums are added in order.  Which warp does what depends on the lengths alone: equal calls give equal bits.
 //
 // q is split into the MMAs' parts once per sequence and CTA (by its warps, a K/V head each) and read from shared memory as
 // fragments; heads beyond what fits there are taken in batches.  Each warp has a ring of K tiles of its own, filled with
 // cp.async ahead of use across heads, tiles and sequences.
 //
-// Arithmetic.  Tokens are the rows of m16n8k16 MMAs and query heads the columns, two for each of four heads, as in kv_a4.cuh: the hi and lo
-// parts of q in fp16 against 4-bit and 8-bit integers (K's bytes u = q + 128 as subnormals, the products with the 128 taken off by
-// where the sums start), or three bf16 parts in two MMAs against bf16.
+// Arithmetic.  Tokens are the rows of m16n8k16 MMAs and query heads the columns, two for each of four heads, as in
+// kv_a4.cuh: the hi and lo parts of q in fp16 against 4-bit and 8-bit integers (K's bytes u = q + 128 as subnormals, the
+// products with the 128 taken off by where the sums start), or three bf16 parts in two MMAs against bf16.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -52,15 +52,16 @@ __device__ __forceinline__ float quad_max(float x) {
   return fmaxf(x, __shfl_xor_sync(~0u, x, 2));
 }
 
-// Four query heads against 16 tokens of a cache, per format.  load(e, x) gives elements e .. of head g / 2 of the four, times the scale of the
-// logits, four or two of them; dot gives s[h] of head q4 with token 8 h + g.  kWords: registers of a lane, kept in shared memory between uses.
+// Four query heads against 16 tokens of a cache, per format.  load(e, x) gives elements e .. of head g / 2 of the four, times
+// the scale of the logits, four or two of them; dot gives s[h] of head q4 with token 8 h + g.  kWords: registers of a lane,
+// kept in shared memory between uses.
 template <int F, int NB>
 struct Heads;
 
 template <int NB>
 struct Heads<IL_A4, NB> {
-  static constexpr int kWords = 4 * NB + NB / 2 + 2;
-  a4::Query<NB, 1> q;
+  static constexpr int kWords = 5 * NB + 2;
+  a4::Query<NB, 1, true> q;
   template <class Load>
   __device__ __forceinline__ void take(const Load& load, int lane) {
     float x[NB][8], top = 0.f;
@@ -76,7 +77,7 @@ struct Heads<IL_A4, NB> {
     q.take(0, x, quad_max(top), lane);
   }
   __device__ __forceinline__ uint32_t& word(int i) {
-    return i < 4 * NB ? q.f[0][i] : i < 4 * NB + NB / 2 ? q.sum[0][i - 4 * NB] : reinterpret_cast<uint32_t&>(q.back[0][i - 4 * NB - NB / 2]);
+    return i < 4 * NB ? q.f[0][i] : i < 5 * NB ? q.sum[0][i - 4 * NB] : reinterpret_cast<uint32_t&>(q.back[0][i - 5 * NB]);
   }
   __device__ __forceinline__ void dot(float (&s)[2], uint32_t tile, uint32_t steps, int first, int lane) const {
     uint32_t chunks[NB / 2];
@@ -178,8 +179,8 @@ struct Config {
   static constexpr int kPool = kTile * kRowBytes;
   static constexpr int kScales = F == IL_BF16 ? 0 : kTile * kBlocks * 4;
   static constexpr int kStage = kPool + kScales;
-  // As many as the registers and the rings leave.  A4, 64 ragged sequences of heads of 128: 8 warps 63 us, 12 and 16 56 us; 8192 tokens of
-  // heads of 64: 68, 56, 53 us.  Q8 72 to 76 us with 8 or 12.
+  // As many as the registers and the rings leave.  A4, 64 ragged sequences of heads of 128: 8 warps 63 us, 12 and 16 56 us;
+  // 8192 tokens of heads of 64: 68, 56, 53 us.  Q8 72 to 76 us with 8 or 12.
   static constexpr int kWarps = F == IL_BF16 || W == 256 ? 8 : F == IL_A4 ? 16 : 12;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kStages = kStage > 5000 ? 2 : 3;
@@ -283,7 +284,8 @@ __global__ void __launch_bounds__(Config<F, W>::kThreads, 1) kv_weigh_kernel(con
   // ---- this CTA's run of the list, and how many warps share a tile
   const long long from = total * blockIdx.x / gridDim.x, to = total * (blockIdx.x + 1) / gridDim.x;
   if (from == to) return;
-  // Of a piece's tiles whole rounds go a tile a warp; warps that the rest would leave idle share its tiles, each share-th head a warp
+  // Of a piece's tiles whole rounds go a tile a warp; warps that the rest would leave idle share its tiles, each share-th
+  // head a warp
   auto share_of = [&](uint32_t rest) {
     int share = 1;
     while (NW % (2 * share) == 0 && 2 * share <= kv.n_heads && rest * 2 * share <= NW) share *= 2;
@@ -473,10 +475,14 @@ __global__ void __launch_bounds__(Config<F, W>::kThreads, 1) kv_weigh_kernel(con
                   lane);
               uint4* const to_mem = heads_mem + four * (C::kFours * 32) + lane;
               auto word = [&](int i) {
-                return i < Q::kWords ? h.word(i) : i == Q::kWords ? __float_as_uint(lse) : i == Q::kWords + 1 ? __float_as_uint(slope) : 0u;
+                return i < Q::kWords        ? h.word(i)
+                       : i == Q::kWords     ? __float_as_uint(lse)
+                       : i == Q::kWords + 1 ? __float_as_uint(slope)
+                                            : 0u;
               };
 #pragma unroll
-              for (int i = 0; i < C::kFours; ++i) to_mem[i * 32] = make_uint4(word(4 * i), word(4 * i + 1), word(4 * i + 2), word(4 * i + 3));
+              for (int i = 0; i < C::kFours; ++i)
+                to_mem[i * 32] = make_uint4(word(4 * i), word(4 * i + 1), word(4 * i + 2), word(4 * i + 3));
             }
             __syncthreads();
             staged_s = s, staged_h = h0, staged_c = c0;
@@ -545,9 +551,7 @@ __global__ void __launch_bounds__(Config<F, W>::kThreads, 1) kv_weigh_kernel(con
         float sum = 0.f;
         for (int w = 0; w < share; ++w) sum += shared[w * T + lane];
         const uint32_t t = t0 + lane;
-        if (t < q.len) {
-          P.w.weights_out[s * ws + t] = had + (t >= q.begin ? sum : 0.f);
-        }
+        if (t < q.len) P.w.weights_out[s * ws + t] = had + (t >= q.begin ? sum : 0.f);
       }
       parity ^= 1;
     }
@@ -600,7 +604,8 @@ cudaError_t prepare_kv_weigh(const KvWeighArgs& w, int num_sms, Launch* out) {
   const KvView& kv = a.kv;
   weigh::Plan p{};
   p.w = w;
-  p.cap = (int)std::min<int64_t>({a.table_width * kv.page_size, w.weights_width, a.positions != nullptr ? a.positions_width : INT32_MAX});
+  p.cap = (int)std::min<int64_t>({a.table_width * kv.page_size, w.weights_width,
+                                  a.positions != nullptr ? a.positions_width : INT32_MAX});
   p.window = (int)std::min<int64_t>(a.window, INT32_MAX);
   p.by_page = FastDiv((uint32_t)kv.page_size);
   p.group = a.n_q_heads / kv.n_heads;
