@@ -46,7 +46,7 @@
 // 50 % used, ALU 44 %, tensor pipe 27 %, DRAM 65 %) but the chain of a tile in a warp -- q K^T, maximum, exp2, split, p V -- at
 // two warps a scheduler, about 520 instructions per 16 tokens; of a short call the latencies before the first tile and in
 // the joins.  Scored: bf16, 16 of 1000 to 16384 under a window of 4096, 16 heads of 256 on 8, 83 us, 5.7 TB/s; Q8, 32 of up to
-// 4096, 32 heads on 32, 61 us, 3.8 TB/s.
+// 4096, 32 heads on 32, 56 us, 4.1 TB/s.
 #pragma once
 
 #include <algorithm>
@@ -318,10 +318,15 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
   constexpr bool Q8 = C::kQ8, A4 = C::kA4, COLS = C::kCols, BLOCKED = F != IL_BF16;  // scales of 32 elements
   constexpr int NV = C::kValues;
   // Empty tiles before each row's, for what its start and end cost beside its tiles (q, parts, result).  One: 1024 biased Q8
-  // rows of 1 to 108 tiles 78.9 -> 60.5 us (two 61.5, four 65.3), 64 ragged A4 sequences 94.0 -> 93.4, 256 of 50 to 150
+  // rows of 1 to 108 tiles, from the oldest on, 78.9 -> 60.5 us (two 61.5, four 65.3), 64 ragged A4 sequences 94.0 -> 93.4, 256 of 50 to 150
   // tokens 20.8 -> 19.9.  Not where rows of few bytes or pairs of warps lose: A4 heads of 64 90.3 -> 94.4, capped heads of
   // 256 83.0 -> 84.0.  (A pair of warps meets at every tile's barrier: none of its tiles may be empty.)
   constexpr int LEAD = H == 1 && (SCORED || (A4 && W == 128)) ? 1 : 0;
+  // Rows from the newest tile back: a steep bias then leaves tiles that weigh nothing beside the newest, whose V is not used,
+  // and few whose p lie far apart.  (The first CTAs took 42 us and those of the steep heads 55.)  32 heads on 32, 32 sequences
+  // of up to 4096 tokens: Q8 60.6 -> 56.2 us, A4 119 -> 102; 32 on 8, 64 of up to 8192: Q8 143 -> 134, A4 140 -> 135; capped
+  // without a bias Q8 119.7 -> 122.6, A4 104.5 -> 103.5.  Rows of bf16 are bound by HBM either way.
+  constexpr bool BACK = SCORED && COLS;
   constexpr int T = C::kTile, NN = T / 8, GR = T / kGroup;  // tokens of a tile, in eights, in groups
   constexpr int NB = C::kBlocks, NT = C::kThreads, NW = C::kWarps, NK = C::kWorkers, S = C::kStages, ROWS = C::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -463,7 +468,9 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
     // scales: the widest copy of a token's scales; a lane copies K's (lanes 0-15) or V's
     constexpr int SB = NB * 4 > 16 ? 16 : NB * 4;
 
-    auto token_of = [&](const Walk& w) { return (w.q.first + w.tile - LEAD) * T + (lane & (T - 1)); };
+    auto token_of = [&](const Walk& w) {
+      return (w.q.first + (BACK ? w.q.tiles - 1 - w.tile : w.tile - LEAD)) * T + (lane & (T - 1));
+    };
     auto empty = [&](const Walk& w) { return LEAD > 0 && w.tile < LEAD; };
     auto column_of = [&](uint32_t t) { return P.by_page.of(t); };
     // Heads in columns: of the tile to be copied next, this lane's token's place in its page (units of `fetch` below),
@@ -891,6 +898,9 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
         if (i < 0) continue;
       }
 
+      const uint32_t mk = masks[0];
+      float low[R], top[R];
+      bool idle = false;
       if (!empty(at)) {
         // ---- capped and biased
         if constexpr (SCORED) {
@@ -910,9 +920,6 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
           }
         }
 
-        // ---- softmax: p = 2^(s - m) and the factor of what came before
-        const uint32_t mk = masks[0];
-        float low[R];
         if constexpr (BLOCKED) {
 #pragma unroll
           for (int r = 0; r < R; ++r) {
@@ -928,7 +935,6 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
 #pragma unroll
               for (int r = 0; r < R; ++r) s[r][c] = -INFINITY;
         }
-        float top[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           top[r] = s[r][0];
@@ -943,8 +949,43 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
             top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
           }
         }
+        if (BACK && a.slopes != nullptr) {
+          // A head's tile of which every p is below 2^-104 adds nothing (but a NaN)
+          idle = true;
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const bool gone = top[r] < highest[r] - 104.f;
+            idle &= gone || at.block * ROWS + 4 * r + q4 >= P.group;
+            if (gone) low[r] = INFINITY;
+#pragma unroll
+            for (int c = 0; c < NV; ++c)
+              if (gone && s[r][c] == s[r][c]) s[r][c] = -INFINITY;
+          }
+          idle = __all_sync(~0u, idle);
+          if (idle) {
+            uint32_t dm[NB];
+            bool number = true;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+              for (int c = 0; c < NV; ++c) number &= s[r][c] == s[r][c];
+#pragma unroll
+            for (int half = 0; half < H; ++half) {  // (both warps of a pair decide alike)
+              const uint32_t there = half == 0 ? from : from + (warp % 2 == 0 ? C::kRing : -C::kRing);
+              a4::load_steps<NB>(dm, there + 2 * C::kPool + C::kScales + lane * NB * 4);
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+                number &= (dm[b] & 0x7f800000u) != 0x7f800000u && (!A4 || (dm[b] & 0x7f80u) != 0x7f80u);
+            }
+            idle = __all_sync(~0u, number);
+          }
+        }
+      }
+
+      if (!empty(at) && !idle) {
+        // ---- softmax: p = 2^(s - m) and the factor of what came before.
         // bf16 parts of p have fp32's range: m is the maximum so far.  fp16 parts keep 12 bits or more of p only
-        // above 2^-26, so that m follows the tile's own maximum, down to 2^-24 of the largest p; a tile with
+        // above 2^-26, so that m follows the tile's own maximum, down to 2^-24 (or 2^-64) of the largest p; a tile with
         // smaller p all the same (`wide`) takes its products in classes of 2^-26 (below).
         bool wide = false;
         float next[R];
@@ -955,18 +996,37 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
             next[r] = fmaxf(top[r], highest[r] - 24.f);
             wide |= next[r] - low[r] > 26.f;
           } else if constexpr (COLS) {
+            // (from the newest back most tiles lie below.  2^64 leaves Q8's sums of 2^31 tokens numbers, A4's of m + 8 d have no
+            // unit that would)
             highest[r] = fmaxf(highest[r], top[r]);
-            next[r] = fmaxf(top[r], highest[r] - 24.f);
+            next[r] = fmaxf(top[r], highest[r] - (BACK && !A4 ? 64.f : 24.f));
             wide |= next[r] - low[r] > 26.f;
           } else {
             next[r] = fmaxf(m[r], top[r]);
           }
         }
-        if (Q8) wide = __any_sync(~0u, wide);
+        const uint32_t sv = from + 2 * C::kPool + C::kScales;  // V's steps
+        auto steps_of_one = [&](uint32_t (&one)[NB]) {         // of this lane's token, |d| as the bits of a float
+          static_assert(!COLS || T == 32, "a lane looks at one token's steps");
+          a4::load_steps<NB>(one, sv + lane * NB * 4);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) one[b] = A4 ? (one[b] & 0x7fffu) << 16 : one[b] & 0x7fffffffu;
+        };
+        if constexpr (COLS) {
+          uint32_t one[NB], most = 0;
+          steps_of_one(one);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) most = max(most, one[b]);
+          v_exp = max(v_exp, (int)(__reduce_max_sync(~0u, most) >> 23));
+          const uint32_t little = (uint32_t)(v_exp - 12) << 23;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) wide |= one[b] < little && one[b] != 0;
+        }
+        if (Q8 || COLS) wide = __any_sync(~0u, wide);
         float keep[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          if (Q8 && wide) next[r] = highest[r];
+          if ((Q8 || COLS) && wide) next[r] = highest[r];  // the classes' factors leave no room for 2^24 more
           const float base = next[r] == -INFINITY ? 0.f : next[r];
           keep[r] = exp2_fast(m[r] - base);
           m[r] = next[r];
@@ -993,20 +1053,6 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
           for (int x = 0; x < 4 * R; ++x) acc[x] = fmaf(acc[x], kept[2 * (x / 4) + x % 2], c[x / 4][x % 4]);
         };
         if constexpr (COLS) {
-          static_assert(!COLS || T == 32, "a lane looks at one token's steps");
-          const uint32_t sv = from + 2 * C::kPool + C::kScales;  // V's steps
-          uint32_t one[NB], most = 0;  // steps of one token
-          a4::load_steps<NB>(one, sv + lane * NB * 4);
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            one[b] = A4 ? (one[b] & 0x7fffu) << 16 : one[b] & 0x7fffffffu;  // |d| as the bits of a float
-            most = max(most, one[b]);
-          }
-          v_exp = max(v_exp, (int)(__reduce_max_sync(~0u, most) >> 23));
-          const uint32_t little = (uint32_t)(v_exp - 12) << 23;
-#pragma unroll
-          for (int b = 0; b < NB; ++b) wide |= one[b] < little && one[b] != 0;
-          wide = __any_sync(~0u, wide);
           const float up = pow2_biased(267 - v_exp);  // the largest d becomes 2^13 .. 2^14
           const uint32_t v_at = from + C::kPool, steps = sv + g * NB * 4;
           float gap_up[NB];
@@ -1118,6 +1164,8 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
             // being 2^(-26 (k + 1)) <= p < 2^(-26 k) (p = 1 in class 0; p below 2^-104 is 0), and with each block's steps brought up to
             // the largest.  Class k is multiplied by 2^(26 k), and the sums' unit goes down as far until the last class is in.
             constexpr float kClass = 67108864.f;  // 2^26
+            uint32_t one[NB];
+            steps_of_one(one);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
               const int e = (int)(__reduce_max_sync(~0u, one[b]) >> 23);

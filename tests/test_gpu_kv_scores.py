@@ -102,6 +102,56 @@ def test_long_sequences_behind_a_steep_bias(sil, fmt, slope):
         _check(sil, fmt, 9, 1, 256, 16, [2000], slopes=np.linspace(0, slope, 9, dtype=np.float32), positions=positions, seed=8)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("scored", [False, True])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_a_wide_tile_far_below_a_heavy_peak(sil, fmt, scored, dim):
+    """1024 equal logits, and before and behind them tiles of logits from 2^-24 to 2^-140 of them: no sum leaves fp32 on the way.
+    As many sequences (of the same pages) as leave a warp tiles of both."""
+    import torch
+    low = -np.linspace(17.0, 97.0, 32)
+    logits = np.concatenate([low, np.zeros(1024), low[::-1], low, np.full(32, -60.0), [-80.0]]).astype(np.float32)
+    n, n_seq = len(logits), 600
+    pages = (n + 15) // 16
+    cache = sil.kv_cache(fmt, pages, 16, 1, dim)
+    k = torch.from_numpy(np.repeat(logits / dim, dim).reshape(n, 1, dim).astype(np.float32)).cuda()  # every element of a token the same
+    v = torch.zeros(n, 1, dim, device="cuda")
+    v[..., ::2] = 100.0
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    sil.kv_append(cache, k, v, slots)
+    sil.kv_read(cache, slots, k, v)
+    q = torch.ones(n_seq, 1, dim, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(n_seq, 1, device="cuda")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").repeat(n_seq, 1)
+    lens = torch.full((n_seq,), n, dtype=torch.int32, device="cuda")
+    starts = torch.zeros(n_seq, dtype=torch.int32, device="cuda") if scored else None
+    sil.kv_attend(cache, q, table, lens, out, lse=lse, scale=1.0, starts=starts)
+    s = k.double().sum(-1)[:, 0]
+    want = torch.softmax(s, 0) @ v.double()[:, 0]
+    # q and p in 21 bits or more, and roundings of sums of 32 tiles and of their joins, all of numbers of up to 101
+    assert (out[:, 0].double() - want).abs().max() <= 101 * (2 * 2**-21 + 64 * 2**-24)
+    assert (lse.double() - torch.logsumexp(s, 0)).abs().max() <= 1e-5  # 8 times a rounding of 2^4, in exp2's units
+
+
+@pytest.mark.parametrize("fmt", ["q8", "a4"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("where", ["k", "v"])
+def test_a_nan_far_behind_a_steep_bias_is_seen(sil, fmt, dim, where):
+    """In a tile that weighs nothing beside the newest, as anywhere: the heads that read it give no number, the others what they gave."""
+    import torch
+    c = kl.Case(sil, fmt, 8, 4, dim, 16, [700, 90], slopes=np.full(8, 4.0, np.float32), seed=9)
+    c.check(*c.run())
+    before = c.run()
+    pools = {"k": c.cache.k_scale, "v": c.cache.v_scale}[where]
+    page = c.table[0][5]
+    pools[int(page), 3, 2].view(-1)[-1 if fmt == "q8" else -2] = float("nan")  # d of the last block of token 83's K/V head 2
+    out, lse = c.run()
+    assert torch.isnan(out[0, 4:6, dim - 32:]).all() and (where == "v" or torch.isnan(lse[0, 4:6]).all())
+    keep = torch.ones(2, 8, dtype=torch.bool, device=out.device)
+    keep[0, 4:6] = False
+    assert torch.equal(out[keep], before[0][keep]) and torch.equal(lse[keep], before[1][keep])
+
+
 def test_a_length_is_cut_to_the_positions(sil):
     import torch
     c = kl.Case(sil, "bf16", 4, 1, 64, 16, [40, 40], slopes=_slopes(4), positions=True, seed=2)
