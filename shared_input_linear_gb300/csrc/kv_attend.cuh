@@ -1395,7 +1395,9 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
           const float ua = pow2_biased(127 + half), ub = pow2_biased(127 + exp - half);
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            float sum = l[r];
+            // from m to the maximum: m may lie 2^64 below it, and the warps of a pair, whose V differ, have one only of that
+            const float down = highest[r] == -INFINITY ? 1.f : exp2_fast(m[r] - highest[r]);
+            float sum = l[r] * down;
 #pragma unroll
             for (int by = 4; by < 32; by *= 2) {
               sum += __shfl_xor_sync(~0u, sum, by);
@@ -1407,19 +1409,19 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
             if (of_group >= P.group) continue;
             if (g == 0) {
               if (!alone) {
-                part[ROWS * W + row] = m[r];
+                part[ROWS * W + row] = highest[r];
                 part[ROWS * W + ROWS + row] = sum;
               } else if (a.lse != nullptr && col0 == 0) {
                 a.lse[(int64_t)at.s * a.n_q_heads + (int64_t)at.hk * P.group + of_group] =
-                    sum == 0.f ? -INFINITY : (m[r] + __log2f(sum)) * 0.6931471805599453f;
+                    sum == 0.f ? -INFINITY : (highest[r] + __log2f(sum)) * 0.6931471805599453f;
               }
             }
-            const float f = !alone ? 1.f : sum == 0.f ? 0.f : __fdividef(1.f, sum);
+            const float f = !alone ? down : sum == 0.f ? 0.f : __fdividef(down, sum);
             float* const to = alone ? a.out + at.s * a.out_stride + ((int64_t)at.hk * P.group + of_group) * D + col0 : part + row * W;
             auto value = [&](int b, int e) {
-              const float x = o[2 * b + e / 2][2 * r + e % 2] * ua;
-              if constexpr (A4) return fmaf(x, ub, om[r][b]) * f;
-              return x * ub * f;
+              const float x = o[2 * b + e / 2][2 * r + e % 2] * f * ua;
+              if constexpr (A4) return fmaf(x, ub, om[r][b] * f);
+              return x * ub;
             };
 #pragma unroll
             for (int b = 0; b < NB; ++b) {

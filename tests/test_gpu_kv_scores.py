@@ -133,6 +133,33 @@ def test_a_wide_tile_far_below_a_heavy_peak(sil, fmt, scored, dim):
     assert (lse.double() - torch.logsumexp(s, 0)).abs().max() <= 1e-5  # 8 times a rounding of 2^4, in exp2's units
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("scored", [False, True])
+@pytest.mark.parametrize("half", [0, 1])
+def test_v_of_two_sizes_in_one_half_of_a_wide_head(sil, fmt, scored, half):
+    """The warps of a head above 128 elements see V of different ranges; their parts are joined across CTAs by one maximum."""
+    import torch
+    n, dim, heads = 100003, 256, 3
+    g = torch.Generator().manual_seed(5)
+    pages = (n + 63) // 64
+    cache = sil.kv_cache(fmt, pages, 64, 1, dim)
+    k, v = (torch.randn(n, 1, dim, generator=g).cuda() for _ in range(2))
+    v[::2, :, 128 * half:128 * half + 128] *= 2.0**-20
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    sil.kv_append(cache, k, v, slots)
+    sil.kv_read(cache, slots, k, v)
+    q = torch.randn(1, heads, dim, generator=g).cuda()
+    out, lse = torch.empty_like(q), torch.empty(1, heads, device="cuda")
+    table, lens = torch.arange(pages, dtype=torch.int32, device="cuda")[None], torch.tensor([n], dtype=torch.int32, device="cuda")
+    starts = torch.zeros(1, dtype=torch.int32, device="cuda") if scored else None
+    sil.kv_attend(cache, q, table, lens, out, lse=lse, starts=starts)
+    s = q[0].double() @ k[:, 0].double().T / 16
+    want = torch.softmax(s, 1) @ v[:, 0].double()
+    # a logit: 22 bits of q, up to 40 in sum |q k| / 16; p: 21 bits; roundings of sums of 5 tiles and two joins, of numbers of up to 5
+    assert (out[0].double() - want).abs().max() <= 5 * (40 * 2**-22 + 2**-21 + 32 * 2**-24)
+    assert (lse[0].double() - torch.logsumexp(s, 1)).abs().max() <= 40 * 2**-22 + 8 * 2**-20
+
+
 @pytest.mark.parametrize("fmt", ["q8", "a4"])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("where", ["k", "v"])
