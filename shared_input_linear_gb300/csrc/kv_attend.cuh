@@ -1169,7 +1169,8 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
               const int e = (int)(__reduce_max_sync(~0u, one[b]) >> 23);
-              gap_up[b] = pow2_biased(127 + min(v_exp - e, v_exp - 14));  // times up it stays a number
+              // (up to 2^120, so that it and its inverse are numbers, for steps of 0 too; below 2^-104 p d counts as 0 anyway)
+              gap_up[b] = pow2_biased(127 + min(max(min(v_exp - e, v_exp - 14), 0), 120));
             }
             uint32_t classes = 0;
 #pragma unroll
