@@ -393,7 +393,8 @@ int il_kv_read(const il_kv* kv, const int32_t* slots, int64_t n, float* k, int64
  *   window : tokens seen, counted from the end; 0: all.
  * A sequence of length 0 gives out = 0 and lse = -inf.  Cached values outside the
  * attended range are never used, NaN or not.  q, K and V that are attended must be finite:
- * where one is not, that sequence's heads that read it give NaN or infinity.  Work is split
+ * where one is not, that sequence's heads that read it give NaN or infinity, of V in its column
+ * (Q8, A4: in its block's 32) alone.  Work is split
  * over the length and joined in an order that depends on the lengths only, so that equal
  * calls give equal bits.
  * Rounding: sums and softmax statistics are fp32.  Over a bf16 cache q and the weights p keep

@@ -1006,21 +1006,25 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
           }
         }
         const uint32_t sv = from + 2 * C::kPool + C::kScales;  // V's steps
-        auto steps_of_one = [&](uint32_t (&one)[NB]) {         // of this lane's token, |d| as the bits of a float
+        // Of this lane's token, |d| as the bits of a float and 2^23 more: infinities and NaN, which are for their own 32 columns and
+        // set no unit for the others, become negative.
+        constexpr int kOne = 1 << 23;
+        auto steps_of_one = [&](int (&one)[NB]) {
           static_assert(!COLS || T == 32, "a lane looks at one token's steps");
-          a4::load_steps<NB>(one, sv + lane * NB * 4);
+          uint32_t step[NB];
+          a4::load_steps<NB>(step, sv + lane * NB * 4);
 #pragma unroll
-          for (int b = 0; b < NB; ++b) one[b] = A4 ? (one[b] & 0x7fffu) << 16 : one[b] & 0x7fffffffu;
+          for (int b = 0; b < NB; ++b) one[b] = (int)((A4 ? (step[b] & 0x7fffu) * 65536u : step[b] & 0x7fffffffu) + kOne);
         };
         if constexpr (COLS) {
-          uint32_t one[NB], most = 0;
+          int one[NB], most = 0;
           steps_of_one(one);
 #pragma unroll
           for (int b = 0; b < NB; ++b) most = max(most, one[b]);
-          v_exp = max(v_exp, (int)(__reduce_max_sync(~0u, most) >> 23));
-          const uint32_t little = (uint32_t)(v_exp - 12) << 23;
+          v_exp = max(v_exp, (__reduce_max_sync(~0u, most) >> 23) - 1);
+          const int little = (v_exp - 12) * kOne;
 #pragma unroll
-          for (int b = 0; b < NB; ++b) wide |= one[b] < little && one[b] != 0;
+          for (int b = 0; b < NB; ++b) wide |= one[b] > kOne && one[b] < little + kOne;
         }
         if (Q8 || COLS) wide = __any_sync(~0u, wide);
         float keep[R];
@@ -1164,13 +1168,13 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
             // being 2^(-26 (k + 1)) <= p < 2^(-26 k) (p = 1 in class 0; p below 2^-104 is 0), and with each block's steps brought up to
             // the largest.  Class k is multiplied by 2^(26 k), and the sums' unit goes down as far until the last class is in.
             constexpr float kClass = 67108864.f;  // 2^26
-            uint32_t one[NB];
+            int one[NB];
             steps_of_one(one);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-              const int e = (int)(__reduce_max_sync(~0u, one[b]) >> 23);
-              // (up to 2^120, so that it and its inverse are numbers, for steps of 0 too; below 2^-104 p d counts as 0 anyway)
-              gap_up[b] = pow2_biased(127 + min(max(min(v_exp - e, v_exp - 14), 0), 120));
+              const int e = (__reduce_max_sync(~0u, one[b]) >> 23) - 1;
+              // (e is at most v_exp.  Up to 2^120, so that it and its inverse are numbers, for steps of 0 too; p d below 2^-104 is 0 anyway)
+              gap_up[b] = pow2_biased(127 + min(v_exp - max(e, 14), 120));
             }
             uint32_t classes = 0;
 #pragma unroll

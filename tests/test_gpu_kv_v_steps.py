@@ -53,3 +53,29 @@ def test_a_block_of_zeros_beside_large_steps(sil, fmt, scored, dim, exponent):
     off = (out.double().view(n_seq, -1, 32) - want).abs()
     assert bool((off <= 2 * most * (2 * 2**-21 + 64 * 2**-24)).all()), (off / most.clamp(min=1e-300)).amax((0, 2)).tolist()
     assert (lse.double() - torch.logsumexp(s, 0)).abs().max() <= 1e-5
+
+
+@pytest.mark.parametrize("fmt,scored", LAYOUTS)
+@pytest.mark.parametrize("heads,kv,dim", [(8, 4, 64), (8, 4, 128), (32, 4, 128), (8, 4, 256)])
+@pytest.mark.parametrize("what", ["nan", "inf", "nan in a wide tile"])
+def test_a_step_that_is_no_number_stays_in_its_columns(sil, fmt, scored, heads, kv, dim, what):
+    """The heads that read it give no number in the 32 columns of the step and what they should in all others."""
+    import torch
+    c = kl.Case(sil, fmt, heads, kv, dim, 16, [700, 90, 33], starts=[0, 0, 0] if scored else None, seed=9,
+                spread=40.0 if "wide" in what else 1.0)
+    c.check(*c.run())
+    bad = float(what[:3])
+    tokens, head, block = {0: [83, 84, 600], 1: [0]}, 2, dim // 32 - 1 if dim != 128 else 1
+    for r, ts in tokens.items():
+        for t in ts:
+            scales = c.cache.v_scale[int(c.table[r][t // 16]), t % 16, head]
+            scales[block, ...][0 if fmt == "a4" else ...] = bad
+    out, lse = c.run()
+    hs = slice(head * heads // kv, (head + 1) * heads // kv)
+    columns = slice(32 * block, 32 * block + 32)
+    for r in (0, 1):
+        assert bool((~torch.isfinite(out[r, hs, columns])).all())
+    out[:, hs, columns] = 0.0
+    for row in c.rows:  # the other columns against the same bounds
+        row[1][:, head, columns] = 0.0
+    c.check(out, lse)
