@@ -1217,11 +1217,12 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
         } else if constexpr (Q8) {
           float d[2 * NN][NB];  // V's scales of the lane's tokens
           const uint32_t sv = from + 2 * C::kPool + C::kScales + 2 * q4 * NB * 4;
-          float vs[NB], most = 0.f;  // of one token
+          float vs[NB];  // of one token
+          int most = 0;  // as in steps_of_one: an infinity sets no unit
           lds_floats(vs, from + 2 * C::kPool + C::kScales + (lane & (T - 1)) * NB * 4);
 #pragma unroll
-          for (int b = 0; b < NB; ++b) most = fmaxf(most, fabsf(vs[b]));
-          v_exp = max(v_exp, (int)(__reduce_max_sync(~0u, __float_as_uint(most)) >> 23));
+          for (int b = 0; b < NB; ++b) most = max(most, (int)(__float_as_uint(fabsf(vs[b])) + kOne));
+          v_exp = max(v_exp, (__reduce_max_sync(~0u, most) >> 23) - 1);
           // fp16 parts of p d keep 2^-38 of the largest scale: 2^-26 of one that lies 2^12 below it.  A tile with smaller
           // ones takes its products in classes too, with each block's scales brought up to the largest (64 x 8192 tokens whose
           // blocks lie further apart: 267 us, else 207).

@@ -79,3 +79,31 @@ def test_a_step_that_is_no_number_stays_in_its_columns(sil, fmt, scored, heads, 
     for row in c.rows:  # the other columns against the same bounds
         row[1][:, head, columns] = 0.0
     c.check(out, lse)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "q8", "a4"])
+@pytest.mark.parametrize("scored", [False, True])
+def test_an_appended_infinity_of_v_stays_in_its_columns(sil, fmt, scored):
+    """As kv_append leaves it: of bf16 in one column, else in 32.  Rows enough for several tiles a warp before and behind it."""
+    import torch
+    n, dim, n_seq = 600, 128, 400
+    pages = (n + 15) // 16
+    g = torch.Generator().manual_seed(3)
+    cache = sil.kv_cache(fmt, pages, 16, 1, dim)
+    k, v = (torch.randn(n, 1, dim, generator=g).cuda() for _ in range(2))
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    v[301, 0, 40] = float("inf")
+    sil.kv_append(cache, k, v, slots)
+    sil.kv_read(cache, slots, k, v)
+    q = torch.randn(1, 4, dim, generator=g).cuda().repeat(n_seq, 1, 1)
+    out, lse = torch.empty_like(q), torch.empty(n_seq, 4, device="cuda")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").repeat(n_seq, 1)
+    lens = torch.full((n_seq,), n, dtype=torch.int32, device="cuda")
+    sil.kv_attend(cache, q, table, lens, out, lse=lse, starts=torch.zeros_like(lens) if scored else None)
+    s = q[0].double() @ k[:, 0].double().T / dim ** 0.5
+    want = torch.softmax(s, 1) @ v[:, 0].double()
+    good = torch.isfinite(v[:, 0]).all(0)
+    assert int((~good).sum()) == (1 if fmt == "bf16" else 32)
+    assert not torch.isfinite(out[:, :, ~good]).any()
+    # a logit: 22 bits of q, up to 40 in sum |q k| / 11; p: 21 bits; roundings of sums of 19 tiles and two joins, of numbers of up to 5
+    assert (out.double() - want)[:, :, good].abs().max() <= 5 * (40 * 2**-22 + 2**-21 + 32 * 2**-24)
