@@ -9,6 +9,7 @@
 // read and written); 32 of 500 to 8192 Q8 tokens cut to 2048 about 45 us.
 #include <algorithm>
 #include <atomic>
+#include <cstddef>
 
 #include <cooperative_groups.h>
 
@@ -246,6 +247,13 @@ __global__ void __launch_bounds__(kThreads) kv_choose_long_kernel(const KvEvictA
   }
 }
 
+// The histogram of a digit.
+struct alignas(16) Digits {
+  uint32_t bins[2048], sums[64];  // sums: of 32 bins each
+};
+static_assert(alignof(Digits) % sizeof(uint2) == 0 && offsetof(Digits, sums) % sizeof(uint2) == 0 && sizeof(Digits) % sizeof(uint2) == 0,
+              "bins and sums are read in pairs");
+
 // Up to kMostKeys tokens a CTA: a cluster of 1 to 8 CTAs a sequence, the CTA of rank c with the c-th run of its tokens and
 // their keys in shared memory, read once.  Bound by latency (barriers, and 12 bytes a token from a few SMs): up to three passes
 // of 11, 11 and 10 bits (the last ones are left where all of a bin stay), whose histograms a warp of every CTA adds up
@@ -255,7 +263,8 @@ __global__ void __launch_bounds__(kThreads) kv_choose_long_kernel(const KvEvictA
 template <int CTAS, bool MOVE>
 __global__ void __launch_bounds__(kThreads) kv_choose_kernel(const KvEvictArgs a, const Rows R) {
   extern __shared__ uint32_t s_keys[];
-  __shared__ uint32_t s_count[2][2048], s_coarse[2][64], s_pick[4];  // bins, and sums of 32 of them
+  __shared__ Digits s_digits[2];
+  __shared__ uint32_t s_pick[4];
   __shared__ unsigned long long s_warp[kWarps], s_total;
   __shared__ int s_whole, s_last, s_moves, s_to[MOVE ? kFewRows : 1];
   constexpr int ctas = CTAS;
@@ -336,7 +345,7 @@ __global__ void __launch_bounds__(kThreads) kv_choose_kernel(const KvEvictArgs a
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 1 ? 21 : 10;
       const uint32_t mask = pass == 2 ? 1023u : 2047u;
-      uint32_t *const count = s_count[pass & 1], *const coarse = s_coarse[pass & 1];  // the others are still read by other CTAs
+      uint32_t *const count = s_digits[pass & 1].bins, *const coarse = s_digits[pass & 1].sums;  // the others are still read by other CTAs
       count[tid] = 0;
       count[tid + kThreads] = 0;
       __syncthreads();
