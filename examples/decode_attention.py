@@ -76,13 +76,16 @@ class AttentionBlock:
         sil.matmul_batch(x, [(self.dev[1], k), (self.dev[2], v)])
         slots = torch.empty(n, dtype=torch.int32, device="cuda")
         add = torch.tensor(lens, dtype=torch.int32, device="cuda")
-        sil.kv_extend(self.lens, add, self.table, self.ring, self.cursor, self.page, slots, info=self.info)
+        before, index = self.lens.clone(), torch.empty_like(slots)
+        sil.kv_extend(self.lens, add, self.table, self.ring, self.cursor, self.page, slots, positions=index, info=self.info)
         if int(self.info[0]) != 0:
             raise RuntimeError(f"the cache has no room for the prompts: {self.info.tolist()}")
         sil.kv_append(self.cache, k, v, slots)
-        if self.keep:  # the prompts come before anything is evicted: a token's position is its index
-            self.positions.copy_(torch.arange(self.positions.shape[1], device="cuda", dtype=torch.int32).expand_as(self.positions))
-            self.seen.copy_(self.lens)
+        if self.keep:  # positions go on from what each sequence has seen, which is more than its length once something was evicted
+            row, at = torch.repeat_interleave(add).long(), index.long()
+            self.positions[row, at] = index + (self.seen - before)[row]
+            self.weights[row, at] = 0
+            self.seen += add
 
     def step(self):
         """One token of every sequence: reads ``x``, writes ``out``."""
@@ -92,9 +95,12 @@ class AttentionBlock:
         q = self.q.view(self.n_seq, self.heads, self.dim)
         sil.kv_attend(self.cache, q, self.table, self.lens, self.attention, lse=self.lse if self.keep else None)
         if self.keep:
-            self.positions.scatter_(1, (self.lens - 1).long()[:, None], self.seen[:, None])
-            self.seen += 1
-            sil.kv_weigh(self.cache, q, self.table, self.lens, self.lse, self.weights, add=self.one)
+            # the new tokens' positions, where there was room for them
+            grown, last = self.info[:1] == 0, (self.lens - 1).clamp(min=0).long()[:, None]
+            new = self.one * grown
+            self.positions.scatter_(1, last, torch.where(grown, self.seen[:, None], self.positions.gather(1, last)))
+            self.seen += new
+            sil.kv_weigh(self.cache, q, self.table, self.lens, self.lse, self.weights, add=new)
             sil.kv_evict(self.cache, self.table, self.lens, self.weights, self.kept, self.drop, first=self.first, recent=self.recent,
                          positions=self.positions)
             sil.kv_extend(self.lens, self.drop, self.table, self.ring, self.cursor, self.page, self.no_slots)
@@ -105,6 +111,8 @@ class AttentionBlock:
         add = torch.zeros(self.n_seq, dtype=torch.int32, device="cuda")
         add[list(which)] = -2**31
         sil.kv_extend(self.lens, add, self.table, self.ring, self.cursor, self.page, self.slots, info=self.info)
+        if self.keep:
+            self.seen[list(which)] = 0
 
     def capture(self):
         """A graph of :meth:`step`.  One step runs first, so that the library's workspaces exist, and is taken back (with ``keep``
