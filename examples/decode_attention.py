@@ -65,7 +65,9 @@ class AttentionBlock:
             width = self.table.shape[1] * page
             self.lse = torch.empty((n_seq, heads), **f32)
             self.weights = torch.zeros((n_seq, width), **f32)
-            self.positions, self.kept, self.drop = torch.zeros((n_seq, width), **i32), torch.empty((n_seq, keep), **i32), torch.empty(n_seq, **i32)
+            self.places = torch.zeros((n_seq, width + 1), **i32)  # and a last column for tokens that found no room
+            self.positions, self.kept, self.drop = self.places[:, :width], torch.empty((n_seq, keep), **i32), torch.empty(n_seq, **i32)
+            self.index = torch.empty(n_seq, **i32)  # of the new tokens in their sequences
             self.seen = torch.zeros(n_seq, **i32)  # tokens of each sequence so far, cached or not
             self.no_slots = torch.empty(0, **i32)
 
@@ -90,15 +92,15 @@ class AttentionBlock:
     def step(self):
         """One token of every sequence: reads ``x``, writes ``out``."""
         sil.matmul_batch(self.x, list(zip(self.dev, (self.q, self.k, self.v))))
-        sil.kv_extend(self.lens, self.one, self.table, self.ring, self.cursor, self.page, self.slots, info=self.info)
+        sil.kv_extend(self.lens, self.one, self.table, self.ring, self.cursor, self.page, self.slots,
+                      positions=self.index if self.keep else None, info=self.info)
         sil.kv_append(self.cache, self.k, self.v, self.slots)
         q = self.q.view(self.n_seq, self.heads, self.dim)
         sil.kv_attend(self.cache, q, self.table, self.lens, self.attention, lse=self.lse if self.keep else None)
         if self.keep:
-            # the new tokens' positions, where there was room for them
-            grown, last = self.info[:1] == 0, (self.lens - 1).clamp(min=0).long()[:, None]
-            new = self.one * grown
-            self.positions.scatter_(1, last, torch.where(grown, self.seen[:, None], self.positions.gather(1, last)))
+            # the new tokens' positions; without room there is none, and the index is -1
+            self.places.scatter_(1, self.index.long().remainder_(self.places.shape[1])[:, None], self.seen[:, None])
+            new = (self.index >= 0).int()
             self.seen += new
             sil.kv_weigh(self.cache, q, self.table, self.lens, self.lse, self.weights, add=new)
             sil.kv_evict(self.cache, self.table, self.lens, self.weights, self.kept, self.drop, first=self.first, recent=self.recent,
