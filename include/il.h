@@ -291,7 +291,8 @@ int il_centroid_head(const float* x, int64_t h, const il_weight* centroids, cons
  *              d per 32 elements of head_dim, value fp32(d*q), or IL_A4: u of 0 .. 15, two per
  *              byte, element 2k in bits 0-3 of byte k, and one pair of bf16 {d, m} per 32 elements,
  *              value fp32(d*u + m).  (The weights' Q4 has no offset; the channels of K seldom lie
- *              about 0.)
+ *              about 0.)  Half the bytes of IL_Q8 are not half the time: with up to 4 query heads a K/V
+ *              head attention takes 0.73 to 0.77 of it, with 8 or 16 it takes 1.05 to 1.19 times as long.
  *   page_size: tokens per page, 1 .. 2^20.      n_pages: 1 .., n_pages * page_size < 2^31.
  *   n_heads  : K/V heads, 1 .. 1024.
  *   head_dim : 8 .. 256, a multiple of 8 (IL_BF16) or of 32 (IL_Q8, IL_A4).
@@ -394,7 +395,8 @@ int il_kv_read(const il_kv* kv, const int32_t* slots, int64_t n, float* k, int64
  * A sequence of length 0 gives out = 0 and lse = -inf.  Cached values outside the
  * attended range are never used, NaN or not.  q, K and V that are attended must be finite:
  * where one is not, that sequence's heads that read it give NaN or infinity, of V in its column
- * (Q8, A4: in its block's 32) alone.  Work is split
+ * (Q8, A4: in its block's 32) alone.  Nor may len times the largest |V| reach 2^127 (A4: 2^103, since
+ * its sums may be kept 2^24 times as large): the sums of p V are divided at the end.  Work is split
  * over the length and joined in an order that depends on the lengths only, so that equal
  * calls give equal bits.
  * Rounding: sums and softmax statistics are fp32.  Over a bf16 cache q and the weights p keep
@@ -425,7 +427,9 @@ int il_kv_attend(const il_kv* kv, const float* q, int64_t q_stride, const int32_
  *               of the document that the new token belongs to); negative: all are, len or more: none is.
  *   positions : int32 [n_seq][positions_width], rows positions_stride apart, or NULL (a token's
  *               position is its index): positions of the tokens where il_kv_evict has moved them.
- *               A length is cut to positions_width.
+ *               A length is cut to positions_width.  Only the bias goes by them: window and starts count
+ *               indices, which say nothing about a token's place once something was evicted.  Do not
+ *               combine those with an eviction; its `recent` stands in for a window.
  * cap is 0 or 2^-100 to 2^100; scale / cap, an element of q times that, and slopes must be finite. */
 typedef struct {
   float cap;
@@ -439,7 +443,7 @@ typedef struct {
  * il_kv_attend_scored -- il_kv_attend with capped and biased logits and sequences that begin later.
  * The window counts by index; with starts, a token is seen that both allow.  A sequence of which no
  * token is seen gives out = 0 and lse = -inf.  The cap and the bias are fp32: a logit's error is that
- * of tanhf times cap, and a rounding of the bias.
+ * of tanhf and three roundings times cap, and three of the bias (log2(e), the slope times it, the sum).
  */
 int il_kv_attend_scored(const il_kv* kv, const float* q, int64_t q_stride, const int32_t* table, int64_t table_stride,
                         int64_t table_width, const int32_t* lens, int64_t n_seq, int64_t n_q_heads, float scale,
@@ -475,12 +479,16 @@ int il_kv_weigh(const il_kv* kv, const float* q, int64_t q_stride, const int32_t
  * they are.  lens, table and the free pages stay too: drop holds the changes of length for
  * il_kv_extend's add, which gives the pages back -- once, where the caches of several layers share a
  * table and each has been cut by a call of its own.
+ * What goes by index goes wrong once tokens were moved: a window and starts (il_kv_score), and an add below 0
+ * for a rejected draft, which drops the last indices -- take drafts back before the eviction.
  *   keep      : 1 to 2^30.     first, recent : tokens of position below first, or above that of the
  *               last token less recent, stay whatever their weight; first + recent <= keep.
  *   weights, weights_out : as for il_kv_weigh; the weights move with their tokens.
- *   positions, positions_out : int32 likewise [n_seq][positions_width], distinct in a sequence and
- *               the last token's the newest; both NULL: a token's position is its index.  A length is
- *               cut to their width.
+ *   positions, positions_out : int32 likewise [n_seq][positions_width], not negative, distinct in a
+ *               sequence and the last token's the newest; both NULL: a token's position is its index
+ *               (right until something was evicted).  A length is cut to their width.  The caller writes those of new tokens (il_kv_extend's
+ *               positions are indices).  After an eviction the last token is seldom the newest: cut a sequence
+ *               again only when a new token has come.
  *   kept      : int32 [n_seq][keep], rows kept_stride apart: the index that a token now at i had, -1
  *               from the new length on.
  *   drop      : int32 [n_seq]: the new length less lens[r] (of a length that was cut, all that is

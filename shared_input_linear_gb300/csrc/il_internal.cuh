@@ -442,7 +442,7 @@ struct KvEvictArgs {
 };
 
 cudaError_t prepare_kv_weigh(const KvWeighArgs& a, int num_sms, Launch* out);
-// Two launches: the choice, then the rows.
+// One launch where few rows of a sequence can move, else two: the choice, then the rows.
 cudaError_t prepare_kv_evict(const KvEvictArgs& a, int num_sms, std::vector<Launch>* out);
 
 cudaError_t prepare_kv_extend(const KvExtendArgs& a, int num_sms, Launch* out);

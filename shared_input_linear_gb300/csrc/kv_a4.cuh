@@ -49,7 +49,8 @@ __device__ __forceinline__ void nibbles(uint32_t w, uint32_t (&p)[4]) {
   p[3] = high & 0x03c003c0u;
 }
 
-// The same nibbles as fp16 pairs of u - 8: the bits 64uu are 1024 + u, 6400 + 16 u are 1024 + 16 u.
+// The same nibbles as fp16 pairs of u - 8, by the known way with the exponent of 1024: the bits 64uu are 1024 + u, 6400 + 16 u are
+// 1024 + 16 u.
 __device__ __forceinline__ void nibbles_less_8(uint32_t w, uint32_t (&p)[4]) {
   const __half2 low = __floats2half2_rn(-1032.f, -1032.f), high = __floats2half2_rn(-72.f, -72.f);
   const __half2 sixteenth = __floats2half2_rn(0.0625f, 0.0625f);
@@ -132,7 +133,7 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
 
 // Query heads of 4 R columns as B operands, scaled so that the largest of a head becomes 2^13 .. 2^14.
 // FMAS: m by FMAs, 2 NB a head block, and not by an MMA.  What is faster depends on the kernel around it: il_kv_weigh, 64 ragged
-// sequences, 45.7 us (by MMA 47.4), il_kv_attend 93.7 (93.1), two blocks of 4 heads 122.7 (117.3).
+// sequences, 45.7 us (by MMA 47.4), il_kv_attend 93.7 (93.1), two blocks of 4 heads 122.7 (117.3 when it was chosen, 123 now).
 template <int NB, int R, bool FMAS = false>
 struct Query {
   uint32_t f[R][4 * NB];  // of head 4 r + g / 2, its hi (g even) or lo part: elements 8 q4 .. 8 q4 + 7 of each block

@@ -32,8 +32,8 @@
 // of its own.  p V is computed transposed: the quad layout of s is that of a B operand, so p goes in as it is.
 // Each tile's product starts from zero accumulators and joins the running sum in fp32
 // FMAs (with the factor of the running maximum), which round to nearest.  A4, and Q8 where it is scored, have the operands
-// the other way round, query heads in the columns (kv_a4.cuh), because their tiles are bound by instructions: 875 of A4 for
-// 32 tokens of 128 columns, the loop and copies included.
+// the other way round, query heads in the columns (kv_a4.cuh), which takes fewer instructions: 875 of A4 for 32 tokens of 128
+// columns, the loop and copies included.
 //
 // Scored (il_kv_attend_scored): logits are capped and biased between the two products, and a row may begin at a later token.
 // The plain kernels have none of it.
@@ -41,11 +41,13 @@
 // Measured (GB300, 32 query heads on 8 K/V heads of 128, device time): bf16, 128 sequences of 4096 tokens 315 us, 6.8 TB/s
 // (the rate of a plain copy); 32 of 0 to 8192 86 us, 6.0 TB/s; one of 512 8.1 us.  Q8, 64 of 1 to 8192 106 us, 5.6 TB/s,
 // one of 131071 59 us, 5.2 TB/s.  What bounds it: HBM at bf16 (64 sequences of 8192: 317 us, 263 us with pages that stay in
-// L2); A4, 64 of 1 to 8192 (another draw, 316,517 tokens) 94 us, 4.4 TB/s, one of 131071 45 us, one of 512 9.0 us:
-// instructions (issue slots 64 % used, ALU 54 %, tensor pipe 20 %, DRAM 53 %); at Q8 no unit (207 us either way; issue slots
+// L2); at Q8 no unit (207 us either way; issue slots
 // 50 % used, ALU 44 %, tensor pipe 27 %, DRAM 65 %) but the chain of a tile in a warp -- q K^T, maximum, exp2, split, p V -- at
-// two warps a scheduler, about 520 instructions per 16 tokens; of a short call the latencies before the first tile and in
-// the joins.  Scored: bf16, 16 of 1000 to 16384 under a window of 4096, 16 heads of 256 on 8, 83 us, 5.7 TB/s; Q8, 32 of up to
+// two warps a scheduler, about 520 instructions per 16 tokens; A4, 64 of 1 to 8192 (another draw, 316,517 tokens) 94 us, 4.3 TB/s, one of
+// 131071 45 us, one of 512 9.0 us: the same chain at three warps a scheduler, which use 64 % of the issue slots (ALU 54 %, tensor
+// pipe 20 %, DRAM 53 %); at HBM's rate a tile would have 848 slots for its 875 instructions.  With two blocks of 4 heads A4 has two warps a
+// scheduler and twice the splits and products: 8 heads on one of 256, 64 of 8192, 79 us (Q8 66), 64 on 8 of 128, 64 of 4096, 123 us
+// (Q8 110).  Of a short call the latencies before the first tile and in the joins.  Scored: bf16, 16 of 1000 to 16384 under a window of 4096, 16 heads of 256 on 8, 83 us, 5.7 TB/s; Q8, 32 of up to
 // 4096, 32 heads on 32, 56 us, 4.1 TB/s.
 #pragma once
 
@@ -324,7 +326,8 @@ __global__ void __launch_bounds__(Config<F, W, R, H>::kThreads, 1) kv_attend_ker
   constexpr int LEAD = H == 1 && (SCORED || (A4 && W == 128)) ? 1 : 0;
   // Rows from the newest tile back: a steep bias then leaves tiles that weigh nothing beside the newest, whose V is not used,
   // and few whose p lie far apart.  (The first CTAs took 42 us and those of the steep heads 55.)  32 heads on 32, 32 sequences
-  // of up to 4096 tokens: Q8 60.6 -> 56.2 us, A4 119 -> 102; 32 on 8, 64 of up to 8192: Q8 143 -> 134, A4 140 -> 135; capped
+  // of up to 4096 tokens: Q8 with document starts, 25,000 tokens seen, 60.6 -> 56.2 us, A4 without, 59,000 seen, 119 -> 102; 32 on 8,
+  // 64 of up to 8192: Q8 143 -> 134, A4 140 -> 135; capped
   // without a bias Q8 119.7 -> 122.6, A4 104.5 -> 103.5.  Rows of bf16 are bound by HBM either way.
   constexpr bool BACK = SCORED && COLS;
   constexpr int T = C::kTile, NN = T / 8, GR = T / kGroup;  // tokens of a tile, in eights, in groups

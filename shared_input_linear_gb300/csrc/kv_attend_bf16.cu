@@ -17,8 +17,8 @@ int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 bool in_columns(const KvAttendArgs& a) { return a.kv.format == IL_A4 || (a.kv.format == IL_Q8 && a.scored); }
 
 // Blocks of 8 (in columns: 4) query heads that a warp takes at once.  In columns 8 heads at most: larger groups read K and V
-// again, from L2, where 16 heads' sums would not fit the registers (128 heads on 8 of 128, 32 sequences of 4096: 143 us,
-// two blocks of 8 117 us).
+// again, from L2, where 16 heads' sums would not fit the registers (128 heads on 8 of 128, 32 sequences of 4096: 143 us;
+// two blocks of 8 117 us then, 123 after the steps that followed).
 int head_blocks(const KvAttendArgs& a) {
   const int group = a.n_q_heads / a.kv.n_heads;
   return group > (in_columns(a) ? 4 : 8) ? 2 : 1;

@@ -232,8 +232,9 @@ __global__ void __launch_bounds__(kExtendThreads) kv_extend_kernel(const KvExten
 //   division, so that d and q are the definition's bit for bit.
 // - A4 takes its u from (w - m) / d in the same way, with the least and the largest of the block by four shuffles.
 // Measured (8 heads of 128, device time): append of 16384 tokens bf16 30.4 us, 6.6 TB/s, Q8 31.3 us, 5.5 TB/s; of 4097 Q8
-// 10.0 us; append and read of 4097 A4 together 19.0 us; read of 16384 bf16 32.9 us, 6.1 TB/s, Q8 28.8 us, 6.0 TB/s, of
-// 4097 Q8 9.2 us; append of one token 1.3 us.
+// 10.0 us; A4 append of 16384 35 us, 4.4 TB/s, of 4097 10.7 us (its quantiser spills, 32 B stored and 52 loaded at 48 registers; issue
+// slots 63 %); read of 16384 bf16 32.9 us, 6.1 TB/s, Q8 28.8 us, 6.0 TB/s, A4 27.8 us, 5.6 TB/s, of
+// 4097 Q8 9.2 us, A4 8.9; append of one token 1.3 us.
 constexpr int kRowThreads = 256;
 // Units of a thread at a time: two, all loads first, but for Q8's quantiser, where more warps hide its chains
 // better (when it was chosen, 4097 tokens of 8 x 128: 13.0 us with two, 11.0 us with one; bf16 append 9.6 and 9.2,

@@ -6,9 +6,10 @@
 // token goes beside K.
 //
 // Measured (GB300, 32 query heads on 8 K/V heads of 128, device time): 64 sequences of 1 to 8192 tokens bf16 104 us, 6.3 TB/s,
-// Q8 66 us, 5.6 TB/s, A4 51 us, 4.1 TB/s; one of 131071 A4 24 us; one of 2048 bf16 6.3 us.  What bounds it: HBM at bf16; at A4
-// instructions (343 for 32 tokens of a K/V head, issue slots 62 % used, ALU 52 %) and what the CTAs lose at the ends of pieces;
-// of a short call the latencies before the first tile.
+// Q8 66 us, 5.6 TB/s, A4 51 us, 4.1 TB/s; one of 131071 A4 24 us; one of 2048 bf16 6.3 us.  A4 in other layouts, 64 sequences: 64
+// heads on 8 of 128, 4096 tokens, 62 us, 2.8 TB/s; 8192 tokens of 32 on 8 of 64 52 us, 3.3 TB/s, of 8 on one of 256 46 us, 1.9 TB/s.
+// What bounds it: HBM at bf16; at A4 issue (343 instructions for 32 tokens of a K/V head, about as many as there are slots at HBM's rate, of
+// which 62 % are used; ALU 52 %) and what the CTAs lose at the ends of pieces; of a short call the latencies before the first tile.
 //
 // Work.  Tiles of 32 tokens (16 of bf16 heads above 128) of all sequences form one list, of which every CTA takes an equal
 // run.  A run's piece of one sequence is worked off by the CTA's warps, a tile each at a time, over all K/V heads; of the last
