@@ -545,7 +545,8 @@ def kv_attend(cache: KVCache, q, table, lens, out, lse=None, scale=None, window:
 
     ``il_kv_attend_scored`` with one of these: ``cap``: logits are ``cap * tanh(s / cap)``; ``slopes`` fp32
     ``[n_q_heads]``: a bias of ``slopes[h]`` times the distance from the last token (a negative number), by index or by
-    ``positions`` int32 ``[n_seq][width]``; ``starts`` int32 ``[n_seq]``: the first token seen.
+    ``positions`` int32 ``[n_seq][width]``; ``starts`` int32 ``[n_seq]``: the first token seen.  ``window`` and ``starts`` count
+    indices: not for sequences that :func:`kv_evict` has cut.
 
     A captured call uses the workspace of the stream it was captured on: graphs of one capture stream, and calls
     on that stream, must not run side by side."""
@@ -615,7 +616,8 @@ def kv_evict(cache: KVCache, table, lens, weights, kept, drop, first: int = 0, r
     ``[n_seq]`` the changes of length, for :func:`kv_extend`.
 
     ``weights`` fp32 and ``positions`` int32 (or None: positions are indices) ``[n_seq][width]`` are updated, in place or
-    into ``weights_out`` and ``positions_out``."""
+    into ``weights_out`` and ``positions_out``.  The caller writes the position of each new token, the newest of its sequence,
+    before the next call; a sequence is not cut twice without a new token in between."""
     f32, i32, _ = _dtypes or _types()
     n = lens.numel()
     tp, ts, tw = _table(table, n, i32)
